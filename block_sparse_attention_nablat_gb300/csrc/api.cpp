@@ -30,6 +30,56 @@ bool valid_dtype(nabla_dtype dt) { return dt == NABLA_F32 || dt == NABLA_BF16; }
 
 nabla_status from_cuda(cudaError_t e) { return e == cudaSuccess ? NABLA_OK : NABLA_ERR_CUDA; }
 
+// ---- tensors given by strides (nabla_strides)
+
+// A [B, S, h, D] tensor's rows: the caller's strides, or the dense ones.
+struct Rows {
+  const void *p;
+  nabla_strides st;
+  int h;
+};
+
+Rows rows_of(const void *p, const nabla_strides *st, int B, int S, int h, int D) {
+  Rows r{p, {(int64_t)S * h * D, (int64_t)h * D}, h};
+  if (st) {
+    if (B > 1) r.st.batch = st->batch;
+    if (S > 1) r.st.token = st->token;
+  }
+  return r;
+}
+
+bool valid_rows(const Rows &r, int B, int S, int D, size_t esz) {
+  if (!r.p || !aligned(r.p, 16)) return false;
+  const int64_t row = (int64_t)r.h * D, most = (int64_t)1 << 40;
+  if (r.st.token < row || r.st.token > most || r.st.batch > most) return false;
+  if (B > 1 && r.st.batch < (S - 1) * r.st.token + row) return false;
+  return r.st.token * esz % 16 == 0 && r.st.batch * esz % 16 == 0;
+}
+
+// Bytes from the tensor's first element to behind its last.
+uintptr_t extent(const Rows &r, int B, int S, int D, size_t esz) {
+  return (uintptr_t)((B - 1) * r.st.batch + (S - 1) * r.st.token + (int64_t)r.h * D) * esz;
+}
+
+bool ranges_meet(const void *a, uintptr_t an, const void *b, uintptr_t bn) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + bn && b0 < a0 + an;
+}
+
+// Whether two written tensors share elements: they do not if their ranges are apart,
+// or if they are columns of one larger tensor (the same strides, batches a whole number
+// of tokens apart) that stay apart within the token.
+bool rows_collide(const Rows &a, const Rows &b, int B, int S, int D, size_t esz) {
+  if (!ranges_meet(a.p, extent(a, B, S, D, esz), b.p, extent(b, B, S, D, esz))) return false;
+  if (S > 1 && a.st.token != b.st.token) return true;
+  if (B > 1 && a.st.batch != b.st.batch) return true;
+  const int64_t pitch = S > 1 ? a.st.token : a.st.batch;
+  if (S > 1 && B > 1 && a.st.batch % a.st.token != 0) return true;
+  const int64_t off = ((const char *)b.p - (const char *)a.p) / (int64_t)esz;
+  const int64_t d = ((off % pitch) + pitch) % pitch;
+  return d < (int64_t)a.h * D || d + (int64_t)b.h * D > pitch;
+}
+
 }  // namespace
 
 MaskWorkspace mask_workspace_layout(const Shape &s) {
@@ -244,6 +294,125 @@ nabla_status nabla_sta_mask(int T, int H, int W, int wt, int wh, int ww, uint8_t
   if ((long)T * H * W > nabla::kMaxBlocks) return NABLA_ERR_INVALID_ARG;
   return nabla::from_cuda(
       nabla::launch_sta(T, H, W, wt, wh, ww, sta, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Checks and call of nabla_qk_norm_rope (dz all null) and its backward.
+static nabla_status qk_norm_call(const void *const (&x)[2], const nabla_strides *const (&x_st)[2],
+                                 const void *const (&dz)[2], const nabla_strides *const (&dz_st)[2],
+                                 void *const (&out)[2], const nabla_strides *const (&out_st)[2],
+                                 bool bwd, nabla_dtype dt, int B, int S, int hq, int hk, int D,
+                                 const void *const (&w)[2], void *const (&dw)[2], nabla_dtype wdt,
+                                 const float *cos_t, const float *sin_t, int rope_rows, int R,
+                                 int interleaved, const int32_t *pos, float eps, void *workspace,
+                                 size_t ws_bytes, nabla_stream_t stream) {
+  using namespace nabla;
+  if (!valid_dtype(dt) || !valid_dtype(wdt)) return NABLA_ERR_INVALID_ARG;
+  if (B < 1 || S < 1 || hq < 1 || hk < 0 || (D != 64 && D != 128)) return NABLA_ERR_INVALID_ARG;
+  if ((hk == 0) != (x[1] == nullptr)) return NABLA_ERR_INVALID_ARG;
+  if ((double)B * S * ((double)hq + hk) * D > 4.0e12) return NABLA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return NABLA_ERR_INVALID_ARG;
+  if (R < 0 || R > D || R % 16 != 0) return NABLA_ERR_INVALID_ARG;
+  if (R > 0) {
+    if (!cos_t || !sin_t || !aligned(cos_t, 16) || !aligned(sin_t, 16) || rope_rows < 1)
+      return NABLA_ERR_INVALID_ARG;
+    if (pos ? !aligned(pos, 4) : rope_rows < S) return NABLA_ERR_INVALID_ARG;
+  }
+  const size_t esz = dt == NABLA_BF16 ? 2 : 4, wsz = wdt == NABLA_BF16 ? 2 : 4;
+  const int h[2] = {hq, hk}, sides = hk > 0 ? 2 : 1;
+  QkNormArgs a{};
+  Rows rx[2], rz[2], ro[2];
+  for (int i = 0; i < sides; ++i) {
+    rx[i] = rows_of(x[i], x_st[i], B, S, h[i], D);
+    ro[i] = rows_of(out[i], out_st[i], B, S, h[i], D);
+    if (!valid_rows(rx[i], B, S, D, esz) || !valid_rows(ro[i], B, S, D, esz))
+      return NABLA_ERR_INVALID_ARG;
+    if (bwd) {
+      rz[i] = rows_of(dz[i], dz_st[i], B, S, h[i], D);
+      if (!valid_rows(rz[i], B, S, D, esz)) return NABLA_ERR_INVALID_ARG;
+    }
+    if (!aligned(w[i], 16) || !aligned(dw[i], wsz)) return NABLA_ERR_INVALID_ARG;
+    a.x[i] = x[i];
+    a.dz[i] = dz[i];
+    a.w[i] = w[i];
+    a.out[i] = out[i];
+    a.dw[i] = dw[i];
+    a.x_st[i] = rx[i].st;
+    a.out_st[i] = ro[i].st;
+    if (bwd) a.dz_st[i] = rz[i].st;
+    a.h[i] = h[i];
+  }
+  for (int i = 0; i < sides; ++i) {  // what is written overlaps nothing else
+    const uintptr_t n = extent(ro[i], B, S, D, esz);
+    for (int j = 0; j < sides; ++j) {
+      if (ranges_meet(ro[i].p, n, rx[j].p, extent(rx[j], B, S, D, esz)) ||
+          (bwd && ranges_meet(ro[i].p, n, rz[j].p, extent(rz[j], B, S, D, esz))))
+        return NABLA_ERR_INVALID_ARG;
+      const size_t row = (size_t)D * wsz;
+      if (w[j] && (ranges_meet(ro[i].p, n, w[j], row) ||
+                   (dw[i] && ranges_meet(dw[i], row, w[j], row))))
+        return NABLA_ERR_INVALID_ARG;
+      if (dw[j] && ranges_meet(ro[i].p, n, dw[j], row)) return NABLA_ERR_INVALID_ARG;
+    }
+  }
+  if (sides == 2 && rows_collide(ro[0], ro[1], B, S, D, esz)) return NABLA_ERR_INVALID_ARG;
+  if (bwd && (dw[0] || dw[1])) {
+    if (dw[0] && dw[1] && ranges_meet(dw[0], (size_t)D * wsz, dw[1], (size_t)D * wsz))
+      return NABLA_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || ws_bytes < qk_norm_bwd_workspace(D))
+      return NABLA_ERR_INVALID_ARG;
+  }
+  a.dt = dt;
+  a.wdt = wdt;
+  a.B = B;
+  a.S = S;
+  a.D = D;
+  a.R = R;
+  a.rope_rows = rope_rows;
+  a.interleaved = interleaved != 0;
+  a.cos_t = cos_t;
+  a.sin_t = sin_t;
+  a.pos = R > 0 ? pos : nullptr;
+  a.eps = eps;
+  a.workspace = workspace;
+  cudaError_t e;
+  a.status = device_status_ptr(&e);
+  if (!a.status) return NABLA_ERR_CUDA;
+  return from_cuda(launch_qk_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nabla_status nabla_qk_norm_rope(const void *q, const nabla_strides *q_st, const void *k,
+                                const nabla_strides *k_st, nabla_dtype dt, int B, int S, int hq,
+                                int hk, int D, const void *wq, const void *wk, nabla_dtype wdt,
+                                const float *cos_t, const float *sin_t, int rope_rows, int R,
+                                int interleaved, const int32_t *pos, float eps, void *q_out,
+                                const nabla_strides *qo_st, void *k_out,
+                                const nabla_strides *ko_st, nabla_stream_t stream) {
+  const void *x[2] = {q, k}, *none[2] = {}, *w[2] = {wq, wk};
+  const nabla_strides *x_st[2] = {q_st, k_st}, *no_st[2] = {}, *out_st[2] = {qo_st, ko_st};
+  void *out[2] = {q_out, k_out}, *dw[2] = {};
+  return qk_norm_call(x, x_st, none, no_st, out, out_st, false, dt, B, S, hq, hk, D, w, dw, wdt,
+                      cos_t, sin_t, rope_rows, R, interleaved, pos, eps, nullptr, 0, stream);
+}
+
+size_t nabla_qk_norm_rope_bwd_workspace_bytes(int D) {
+  return D == 64 || D == 128 ? nabla::qk_norm_bwd_workspace(D) : 0;
+}
+
+nabla_status nabla_qk_norm_rope_bwd(
+    const void *q, const nabla_strides *q_st, const void *k, const nabla_strides *k_st,
+    nabla_dtype dt, int B, int S, int hq, int hk, int D, const void *wq, const void *wk,
+    nabla_dtype wdt, const float *cos_t, const float *sin_t, int rope_rows, int R,
+    int interleaved, const int32_t *pos, float eps, const void *dq_out,
+    const nabla_strides *dqo_st, const void *dk_out, const nabla_strides *dko_st, void *dq,
+    const nabla_strides *dq_st, void *dk, const nabla_strides *dk_st, void *dwq, void *dwk,
+    void *workspace, size_t ws_bytes, nabla_stream_t stream) {
+  const void *x[2] = {q, k}, *dz[2] = {dq_out, dk_out}, *w[2] = {wq, wk};
+  const nabla_strides *x_st[2] = {q_st, k_st}, *dz_st[2] = {dqo_st, dko_st},
+                      *out_st[2] = {dq_st, dk_st};
+  void *out[2] = {dq, dk}, *dw[2] = {dwq, dwk};
+  return qk_norm_call(x, x_st, dz, dz_st, out, out_st, true, dt, B, S, hq, hk, D, w, dw, wdt,
+                      cos_t, sin_t, rope_rows, R, interleaved, pos, eps, workspace, ws_bytes,
+                      stream);
 }
 
 nabla_status nabla_selftest_bounded_wait(nabla_stream_t stream) {

@@ -92,4 +92,24 @@ cudaError_t launch_attn_simt(const void *q, const void *k, const void *v, nabla_
                              const Shape &s, const int32_t *kv_nb, const int32_t *kv_inds,
                              float scale, void *o, float *lse, int *status, cudaStream_t st);
 
+// K8: per-head RMS norm and rotation of q (index 0) and k (index 1, h = 0: none), or
+// its gradient where dz is given.  Arguments are checked by the caller; every stride
+// is set (dense ones filled in).
+struct QkNormArgs {
+  const void *x[2], *dz[2], *w[2];
+  void *out[2], *dw[2];
+  nabla_strides x_st[2], dz_st[2], out_st[2];
+  int h[2];
+  nabla_dtype dt, wdt;
+  int B, S, D, R, rope_rows;
+  bool interleaved;
+  const float *cos_t, *sin_t;
+  const int32_t *pos;
+  float eps;
+  void *workspace;  // backward: qk_norm_bwd_workspace(D) bytes of partial sums
+  int *status;
+};
+size_t qk_norm_bwd_workspace(int D);
+cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);
+
 }  // namespace nabla

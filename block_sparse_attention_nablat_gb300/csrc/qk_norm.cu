@@ -1,0 +1,415 @@
+// K8 -- RMS norm of queries and keys per head with the position rotation in the
+// same pass, and its gradient.
+//
+// A row x (one head of one token, D columns) becomes z = Rot(y), y = w x r with
+// r = 1 / sqrt(mean(x^2) + eps); Rot turns the first R columns in pairs (a, b) ->
+// (a c - b s, a s + b c) by the token's angles.  With dy = Rot^T dz and g = w dy:
+//   dx = r (g - x r^2 mean(g x)),   dw = sum over all rows of dy x r.
+// Everything between the load and the one rounding at the store is fp32.
+//
+// HBM-bound: a row is read once and written once (backward: x and dz read, dx
+// written).  A lane holds 8 adjacent columns (one 16-byte load of bf16), D / 8
+// lanes hold a row and a warp 32 / (D / 8) rows at a time, so the norm's sum is
+// log2(D / 8) shuffles and no shared memory is touched.  A warp's item is a run of
+// one token's heads, so the token's angles and the weights are read once per item
+// and stay in registers.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "pdl.cuh"
+
+namespace nabla {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  const float4 b = *reinterpret_cast<const float4 *>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4 *>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Weights of this lane's columns (1 where the caller gave none).
+__device__ __forceinline__ void load_weight(const void *w, nabla_dtype wdt, int col,
+                                            float (&v)[8]) {
+  if (!w) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 1.f;
+  } else if (wdt == NABLA_BF16) {
+    load8(static_cast<const __nv_bfloat16 *>(w) + col, v);
+  } else {
+    load8(static_cast<const float *>(w) + col, v);
+  }
+}
+
+// The rotation of one lane's 8 columns.  Pairs: c[j], s[j] (j < 4) turn columns 2j
+// and 2j + 1.  Halves: column j of this lane pairs with column j of lane `partner`
+// (R / 2 columns on), and the sign of the second product is folded into s.  Lanes
+// beyond R keep c = 1, s = 0, with themselves as partner.  R is a multiple of 16, so
+// a lane lies wholly in the first half, the second half or beyond.
+struct Turn {
+  float c[8], s[8];
+  int partner;
+};
+
+template <bool kPairs>
+__device__ __forceinline__ Turn load_turn(const float *cos_t, const float *sin_t, long at, int R,
+                                          int col, int lane, bool on) {
+  Turn t;
+  t.partner = lane;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    t.c[j] = 1.f;
+    t.s[j] = 0.f;
+  }
+  const int half = R >> 1;
+  if (!kPairs && col < R) t.partner = col < half ? lane + (half >> 3) : lane - (half >> 3);
+  if (!on || col >= R) return t;
+  if (kPairs) {
+    const float4 c = *reinterpret_cast<const float4 *>(cos_t + at * half + (col >> 1));
+    const float4 s = *reinterpret_cast<const float4 *>(sin_t + at * half + (col >> 1));
+    t.c[0] = c.x, t.c[1] = c.y, t.c[2] = c.z, t.c[3] = c.w;
+    t.s[0] = s.x, t.s[1] = s.y, t.s[2] = s.z, t.s[3] = s.w;
+  } else {
+    const bool second = col >= half;
+    const long i = at * half + (second ? col - half : col);
+    load8(cos_t + i, t.c);
+    load8(sin_t + i, t.s);
+    if (!second)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t.s[j] = -t.s[j];
+  }
+  return t;
+}
+
+// kBack: the transpose (the angles negated).
+template <bool kPairs, bool kBack>
+__device__ __forceinline__ void turn8(float (&y)[8], const Turn &t) {
+  if (kPairs) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = y[2 * j], b = y[2 * j + 1], s = kBack ? -t.s[j] : t.s[j];
+      y[2 * j] = fmaf(a, t.c[j], -(b * s));
+      y[2 * j + 1] = fmaf(a, s, b * t.c[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float o = __shfl_sync(0xffffffffu, y[j], t.partner);
+      y[j] = fmaf(y[j], t.c[j], o * (kBack ? -t.s[j] : t.s[j]));
+    }
+  }
+}
+
+template <int kLanes>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Side {  // q or k
+  const void *x, *dz;
+  void *out;  // z, or dx
+  const void *w;
+  int64_t xb, xt, ob, ot, zb, zt;  // batch and token strides of x, out and dz (elements)
+  int h, chunks;                   // heads, items per token
+};
+
+struct QkParams {
+  Side side[2];
+  nabla_dtype wdt;
+  const float *cos_t, *sin_t;
+  const int32_t *pos;
+  long tokens, items;  // B * S; tokens * (chunks of both sides)
+  int S, rows, R, heads_per_item;
+  float eps;
+  float *partial;  // backward: [grid][2][D] column sums
+  int *status;
+};
+
+struct Item {
+  int side, h0, h1;
+  long b, s, at;
+  bool turn;
+};
+
+// The item's token, its run of heads and its row of the rotation table.
+__device__ __forceinline__ Item decode_item(const QkParams &P, long i) {
+  const int per = P.side[0].chunks + P.side[1].chunks;
+  const long t = i / per;
+  int c = (int)(i - t * per);
+  Item it;
+  it.side = c >= P.side[0].chunks;
+  if (it.side) c -= P.side[0].chunks;
+  it.h0 = c * P.heads_per_item;
+  it.h1 = min(it.h0 + P.heads_per_item, P.side[it.side].h);
+  it.b = t / P.S;
+  it.s = t - it.b * P.S;
+  it.at = P.pos && P.R ? P.pos[t] : it.s;
+  it.turn = P.R > 0;
+  if (P.pos && P.R && (it.at < 0 || it.at >= P.rows)) {  // normed, not rotated, and reported
+    if ((threadIdx.x & 31) == 0) atomicCAS(P.status, kDevOk, kDevBadIndex);
+    it.turn = false;
+  }
+  return it;
+}
+
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads) qk_norm_kernel(QkParams P) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 4;
+  const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long stride = (long)gridDim.x * kWarps;
+  for (long i = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < P.items; i += stride) {
+    const Item it = decode_item(P, i);
+    const Side &sd = P.side[it.side];
+    const T *x = static_cast<const T *>(sd.x) + it.b * sd.xb + it.s * sd.xt + col;
+    T *o = static_cast<T *>(sd.out) + it.b * sd.ob + it.s * sd.ot + col;
+    float w[8];
+    load_weight(sd.w, P.wdt, col, w);
+    const Turn t = load_turn<kPairs>(P.cos_t, P.sin_t, it.at, P.R, col, lane, it.turn);
+    for (int hb = it.h0; hb < it.h1; hb += kRows * kAhead) {
+      float y[kAhead][8];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int hh = hb + a * kRows + sub;
+        if (hh < it.h1) {
+          load8(x + (long)hh * D, y[a]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[a][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (hb + a * kRows >= it.h1) break;  // the same for the whole warp
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(y[a][j], y[a][j], ss);
+        const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[a][j] *= r * w[j];
+        turn8<kPairs, false>(y[a], t);
+        const int hh = hb + a * kRows + sub;
+        if (hh < it.h1) store8(o + (long)hh * D, y[a]);
+      }
+    }
+  }
+}
+
+// dx row by row as above; every warp keeps the column sums of dy x r of both sides
+// in registers over all its items, the block joins its warps' sums in a fixed order
+// and writes one row per block, and qk_dw_kernel adds the rows.  Items are dealt out
+// by index alone, so dw is the same from run to run.
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams P) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 2;
+  __shared__ float sums[kWarps][2 * D];
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
+  pdl_launch_dependents();
+  pdl_wait();
+  float acc[2][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[0][j] = acc[1][j] = 0.f;
+  const long stride = (long)gridDim.x * kWarps;
+  for (long i = (long)blockIdx.x * kWarps + warp; i < P.items; i += stride) {
+    const Item it = decode_item(P, i);
+    const Side &sd = P.side[it.side];
+    const T *x = static_cast<const T *>(sd.x) + it.b * sd.xb + it.s * sd.xt + col;
+    const T *dz = static_cast<const T *>(sd.dz) + it.b * sd.zb + it.s * sd.zt + col;
+    T *o = static_cast<T *>(sd.out) + it.b * sd.ob + it.s * sd.ot + col;
+    float w[8], part[8];
+    load_weight(sd.w, P.wdt, col, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[j] = 0.f;
+    const Turn t = load_turn<kPairs>(P.cos_t, P.sin_t, it.at, P.R, col, lane, it.turn);
+    for (int hb = it.h0; hb < it.h1; hb += kRows * kAhead) {
+      float xv[kAhead][8], g[kAhead][8];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int hh = hb + a * kRows + sub;
+        if (hh < it.h1) {
+          load8(x + (long)hh * D, xv[a]);
+          load8(dz + (long)hh * D, g[a]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) xv[a][j] = g[a][j] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (hb + a * kRows >= it.h1) break;  // the same for the whole warp
+        turn8<kPairs, true>(g[a], t);        // dy
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss = fmaf(xv[a][j], xv[a][j], ss);
+          dot = fmaf(g[a][j] * w[j], xv[a][j], dot);
+        }
+        const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
+        const float m = row_sum<kLanes>(dot) * (1.f / D) * r * r;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (hb + a * kRows + sub < it.h1) part[j] = fmaf(g[a][j] * r, xv[a][j], part[j]);
+          g[a][j] = r * fmaf(-xv[a][j], m, g[a][j] * w[j]);
+        }
+        const int hh = hb + a * kRows + sub;
+        if (hh < it.h1) store8(o + (long)hh * D, g[a]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      acc[0][j] += it.side ? 0.f : part[j];
+      acc[1][j] += it.side ? part[j] : 0.f;
+    }
+  }
+  if (!P.partial) return;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v = acc[sd][j];
+#pragma unroll
+      for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0) sums[warp][sd * D + col + j] = v;
+    }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += sums[k][c];
+    P.partial[(size_t)blockIdx.x * 2 * D + c] = v;
+  }
+}
+
+// dw: the blocks' rows added up, 32 columns a block, 32 rows at a time.
+__global__ void __launch_bounds__(1024) qk_dw_kernel(const float *__restrict__ partial, int rows,
+                                                     int D, void *dwq, void *dwk,
+                                                     nabla_dtype wdt) {
+  __shared__ float sums[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r0 = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  float v = 0.f;
+  for (int r = r0; r < rows; r += 32) v += partial[(size_t)r * 2 * D + c];
+  sums[r0][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (r0) return;
+  v = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) v += sums[k][threadIdx.x];
+  void *dw = c < D ? dwq : dwk;
+  if (!dw) return;
+  const int at = c < D ? c : c - D;
+  if (wdt == NABLA_BF16)
+    static_cast<__nv_bfloat16 *>(dw)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float *>(dw)[at] = v;
+}
+
+// Blocks of the backward at most: enough warps to keep HBM busy, few enough rows of
+// partial sums (the workspace holds this many).
+constexpr int kBwdBlocksPerSm = 4, kBwdBlocksMost = 1024;
+
+template <typename T, int D, bool kPairs>
+cudaError_t launch_typed(const QkParams &p, bool bwd, unsigned grid, cudaStream_t st) {
+  if (bwd) return launch_pdl(qk_norm_bwd_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
+  return launch_pdl(qk_norm_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
+}
+
+template <typename T>
+cudaError_t launch_dtype(const QkParams &p, int D, bool pairs, bool bwd, unsigned grid,
+                         cudaStream_t st) {
+  if (D == 64)
+    return pairs ? launch_typed<T, 64, true>(p, bwd, grid, st)
+                 : launch_typed<T, 64, false>(p, bwd, grid, st);
+  return pairs ? launch_typed<T, 128, true>(p, bwd, grid, st)
+               : launch_typed<T, 128, false>(p, bwd, grid, st);
+}
+
+}  // namespace
+
+size_t qk_norm_bwd_workspace(int D) {
+  return (size_t)kBwdBlocksMost * 2 * D * sizeof(float);
+}
+
+cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st) {
+  const bool bwd = a.dz[0] != nullptr;
+  QkParams p{};
+  p.wdt = a.wdt;
+  p.cos_t = a.cos_t;
+  p.sin_t = a.sin_t;
+  p.pos = a.pos;
+  p.tokens = (long)a.B * a.S;
+  p.S = a.S;
+  p.rows = a.rope_rows;
+  p.R = a.R;
+  p.eps = a.eps;
+  p.status = a.status;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // Heads per item: all of a token's heads of one side, or, where that leaves the GPU
+  // short of warps, as few as one pass of the warp takes.
+  const int pass = 32 / (a.D / 8) * (bwd ? 2 : 4);
+  const int most = a.h[0] > a.h[1] ? a.h[0] : a.h[1];
+  int hpi = most;
+  if (p.tokens * 2 < (long)sms * 64) hpi = pass;
+  p.heads_per_item = hpi;
+  p.items = 0;
+  for (int i = 0; i < 2; ++i) {
+    Side &s = p.side[i];
+    s.x = a.x[i];
+    s.dz = a.dz[i];
+    s.out = a.out[i];
+    s.w = a.w[i];
+    s.xb = a.x_st[i].batch;
+    s.xt = a.x_st[i].token;
+    s.ob = a.out_st[i].batch;
+    s.ot = a.out_st[i].token;
+    s.zb = a.dz_st[i].batch;
+    s.zt = a.dz_st[i].token;
+    s.h = a.h[i];
+    s.chunks = (a.h[i] + hpi - 1) / hpi;
+    p.items += p.tokens * s.chunks;
+  }
+  const long need = (p.items + kWarps - 1) / kWarps;
+  long cap = bwd ? (long)sms * kBwdBlocksPerSm : (long)sms * 64;
+  if (bwd && cap > kBwdBlocksMost) cap = kBwdBlocksMost;
+  const unsigned grid = (unsigned)(need < cap ? need : cap);
+  if (bwd && (a.dw[0] || a.dw[1])) p.partial = static_cast<float *>(a.workspace);
+  e = a.dt == NABLA_BF16 ? launch_dtype<__nv_bfloat16>(p, a.D, a.interleaved, bwd, grid, st)
+                         : launch_dtype<float>(p, a.D, a.interleaved, bwd, grid, st);
+  if (e != cudaSuccess || !p.partial) return e;
+  return launch_pdl(qk_dw_kernel, dim3(2 * a.D / 32), dim3(1024), 0, st,
+                    (const float *)p.partial, (int)grid, a.D, a.dw[0], a.dw[1], a.wdt);
+}
+
+}  // namespace nabla

@@ -25,6 +25,11 @@ NABLA_F32, NABLA_BF16 = 0, 1
 _lib = None
 
 
+class _Strides(ctypes.Structure):
+    """nabla_strides of include/nabla.h: batch and token strides in elements."""
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+
+
 class NablaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -72,6 +77,14 @@ def load() -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = i32
         fn.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    st, f32 = ctypes.POINTER(_Strides), ctypes.c_float
+    qk = [vp, st, vp, st, i32, i32, i32, i32, i32, i32, vp, vp, i32, vp, vp, i32, i32, i32, vp, f32]
+    lib.nabla_qk_norm_rope.restype = i32
+    lib.nabla_qk_norm_rope.argtypes = qk + [vp, st, vp, st, vp]
+    lib.nabla_qk_norm_rope_bwd_workspace_bytes.restype = sz
+    lib.nabla_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32]
+    lib.nabla_qk_norm_rope_bwd.restype = i32
+    lib.nabla_qk_norm_rope_bwd.argtypes = qk + [vp, st, vp, st, vp, st, vp, st, vp, vp, vp, sz, vp]
     lib.nabla_selftest_bounded_wait.restype = i32
     lib.nabla_selftest_bounded_wait.argtypes = [vp]
     lib.nabla_get_last_device_status.restype = i32
@@ -138,6 +151,27 @@ def _buf(t: torch.Tensor, name: str, numel: int, dtype: torch.dtype,
     if t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} elements, needs {numel}")
     _on(t, name, device)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype,
+          device: torch.device) -> Optional[_Strides]:
+    """Checks a [B, S, h, D] tensor that may be a view of a larger one (a token's heads
+    lie together) and returns its strides for the C ABI."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    B, S, h, D = t.shape
+    if t.stride(3) != 1 or (h > 1 and t.stride(2) != D):
+        raise ValueError(f"the heads of a token of {name} must lie together")
+    if (S > 1 and t.stride(1) < h * D) or (
+            B > 1 and t.stride(0) < (S - 1) * (t.stride(1) if S > 1 else 0) + h * D):
+        raise ValueError(f"the tokens of {name} must not overlap")
+    return _Strides(t.stride(0), t.stride(1))
 
 
 def _cuda(t: torch.Tensor) -> None:
@@ -377,6 +411,128 @@ def nabla_fractal_unflatten(y: torch.Tensor, T: int, H: int, W: int, P: int = 8,
                P, _ptr(out), _stream(stream, y.device))
     _check(st, "nabla_fractal_unflatten")
     return out
+
+
+def _qk_args(q, k, wq, wk, cos, sin, pos):
+    """Checks what the query/key norm and its backward have in common and returns the
+    C arguments up to pos, the two tensors' shapes and the weights' type."""
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and t.dim() != 4:
+            raise ValueError(f"{name} must be [B, S, h, D]")
+    B, S, hq, D = q.shape
+    dev = q.device
+    hk = 0 if k is None else k.shape[2]
+    shapes = (B, S, hq, D), (B, S, hk, D)
+    strides = (_rows(q, "q", shapes[0], q.dtype, dev), _rows(k, "k", shapes[1], q.dtype, dev))
+    weights = [w for w in (wq, wk) if w is not None]
+    kind = weights[0].dtype if weights else torch.float32
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _buf(w, name, D, kind, dev)
+            if w.numel() != D:
+                raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    R = n = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must be [rows, R / 2], of the same shape")
+        n, R = cos.shape[0], 2 * cos.shape[1]
+        _buf(cos, "cos", n * R // 2, torch.float32, dev)
+        _buf(sin, "sin", n * R // 2, torch.float32, dev)
+    if pos is not None:
+        if cos is None or pos.shape != (B, S):
+            raise ValueError(f"pos must be [{B}, {S}], with cos and sin")
+        _buf(pos, "pos", B * S, torch.int32, dev)
+    wcode = NABLA_F32 if not weights else _dtype_code(weights[0])
+
+    def args(interleaved, eps):
+        return [_ptr(q), strides[0], _ptr(k), strides[1], _dtype_code(q), B, S, hq, hk, D,
+                _ptr(wq), _ptr(wk), wcode, _ptr(cos), _ptr(sin), n, R, int(bool(interleaved)),
+                _ptr(pos), float(eps)]
+
+    return args, shapes, kind
+
+
+def nabla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                       wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+                       cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+                       pos: Optional[torch.Tensor] = None, interleaved: bool = True,
+                       eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                       k_out: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of q [B,S,hq,D] and k [B,S,hk,D] (or q alone) per head with weights
+    wq, wk [D] (None: 1) and, with cos, sin [rows, R/2] fp32, the position rotation of
+    their first R columns; token s takes table row s, or pos[b, s].  interleaved:
+    rotate columns (2i, 2i + 1), else (i, i + R/2).  q, k and the outputs may be views
+    whose tokens are strided.  Returns (q_out, k_out)."""
+    args, shapes, _ = _qk_args(q, k, wq, wk, cos, sin, pos)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(shapes[0], dtype=q.dtype, device=dev)
+    if k_out is None and k is not None:
+        k_out = torch.empty(shapes[1], dtype=q.dtype, device=dev)
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    qo, ko = (_rows(t, n, s, q.dtype, dev) for t, n, s in
+              ((q_out, "q_out", shapes[0]), (k_out, "k_out", shapes[1])))
+    _cuda(q)
+    st = _call(dev, load().nabla_qk_norm_rope, *args(interleaved, eps), _ptr(q_out), qo,
+               _ptr(k_out), ko, _stream(stream, dev))
+    _check(st, "nabla_qk_norm_rope")
+    return q_out, k_out
+
+
+def nabla_qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
+    return load().nabla_qk_norm_rope_bwd_workspace_bytes(D)
+
+
+def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
+                           wq: Optional[torch.Tensor], wk: Optional[torch.Tensor],
+                           dq_out: torch.Tensor, dk_out: Optional[torch.Tensor] = None,
+                           cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None,
+                           pos: Optional[torch.Tensor] = None, interleaved: bool = True,
+                           eps: float = 1e-6, dq: Optional[torch.Tensor] = None,
+                           dk: Optional[torch.Tensor] = None, dwq: Optional[torch.Tensor] = None,
+                           dwk: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of nabla_qk_norm_rope for the upstream gradients dq_out, dk_out of its
+    outputs: returns (dq, dk, dwq, dwk); dwq, dwk [D] in the weights' type, None where
+    the weight is None."""
+    args, shapes, kind = _qk_args(q, k, wq, wk, cos, sin, pos)
+    dev, D = q.device, q.shape[3]
+    if dq_out is None or (k is None) != (dk_out is None):
+        raise ValueError("dq_out and, with k, dk_out are needed")
+    if k is None and (dk is not None or wk is not None):
+        raise ValueError("dk or wk without k")
+    if dq is None:
+        dq = torch.empty(shapes[0], dtype=q.dtype, device=dev)
+    if dk is None and k is not None:
+        dk = torch.empty(shapes[1], dtype=q.dtype, device=dev)
+    for name, d, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
+        if d is not None:
+            if w is None:
+                raise ValueError(f"{name} without its weight")
+            _buf(d, name, D, kind, dev)
+    if dwq is None and wq is not None:
+        dwq = torch.empty(D, dtype=kind, device=dev)
+    if dwk is None and wk is not None:
+        dwk = torch.empty(D, dtype=kind, device=dev)
+    zq, zk, oq, ok = (_rows(t, n, s, q.dtype, dev) for t, n, s in
+                      ((dq_out, "dq_out", shapes[0]), (dk_out, "dk_out", shapes[1]),
+                       (dq, "dq", shapes[0]), (dk, "dk", shapes[1])))
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(max(nabla_qk_norm_rope_bwd_workspace_bytes(D), 1),
+                                dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _on(workspace, "workspace", dev)
+    _cuda(q)
+    st = _call(dev, load().nabla_qk_norm_rope_bwd, *args(interleaved, eps), _ptr(dq_out), zq,
+               _ptr(dk_out), zk, _ptr(dq), oq, _ptr(dk), ok, _ptr(dwq), _ptr(dwk),
+               _ptr(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(),
+               _stream(stream, dev))
+    _check(st, "nabla_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def _stream_device(stream) -> torch.device:

@@ -323,6 +323,86 @@ nabla_status nabla_fractal_unflatten(const void *y, nabla_dtype dt, int B, int T
                                      int h, int D, int P, void *x, nabla_stream_t stream);
 
 /*
+ * Where the rows of a [B, S, h, D] tensor lie: element (b, s, hh, d) is at
+ * b * batch + s * token + hh * D + d, both strides in elements.  A NULL
+ * nabla_strides pointer means dense (token = h * D, batch = S * h * D).  The
+ * entry points below take one for each tensor that may be a view of a larger
+ * one, e.g. q and k lying in the packed projection [B, S, (h + 2 hk) * D].
+ * Both strides must keep 16-byte alignment; token >= h * D, and for B > 1
+ * batch >= (S - 1) * token + h * D (batch is not looked at for B = 1, token
+ * not for S = 1).
+ */
+typedef struct {
+  int64_t batch, token;
+} nabla_strides;
+
+/*
+ * nabla_qk_norm_rope -- what makes the q and k that nabla_build_mask and
+ * nabla_attn_fwd read: RMS norm of every head's row and the position rotation,
+ * in one pass over both tensors.  For a row x of D columns (one head of one
+ * token) with weights w:
+ *   y = w * x / sqrt(mean(x^2) + eps),
+ * then its first R columns are rotated in pairs (a, b) -> (a c - b s, a s + b c),
+ * i = 0 .. R/2 - 1, by c = cos_t[p, i], s = sin_t[p, i] of the token's table row p:
+ *   interleaved != 0: (a, b) = columns (2i, 2i + 1);
+ *   interleaved == 0: (a, b) = columns (i, i + R/2);
+ * columns R .. D - 1 are not rotated.  Computed in fp32 and rounded once.
+ *
+ *   q, k         [B, S, hq, D] and [B, S, hk, D] device, element type dt, strides
+ *                q_st and k_st.  k = NULL with hk = 0: q alone (the queries or the
+ *                keys of a cross attention, whose lengths differ).
+ *   D            64 or 128; S any length >= 1; hq >= 1.
+ *   wq, wk       [D] device, element type wdt; NULL: weights of 1.
+ *   R            columns rotated: a multiple of 16 in [0, D]; R = 0: no rotation
+ *                (cos_t, sin_t and pos are not looked at).
+ *   cos_t, sin_t [rope_rows, R/2] device fp32, shared by every batch and head.
+ *   pos          [B, S] device int32, the tokens' table rows; NULL: token s of every
+ *                batch takes row s (rope_rows >= S).  A row outside [0, rope_rows) is
+ *                reported as NABLA_ERR_BAD_INDEX by nabla_get_last_device_status; that
+ *                token is normed and not rotated.
+ *   eps          finite, >= 0.
+ *   q_out, k_out as q and k, strides qo_st and ko_st, overwritten.  They may be
+ *                views of one larger tensor but must not overlap q, k or each other.
+ * q, k, q_out, k_out, wq, wk, cos_t and sin_t are 16-byte aligned, pos 4-byte.
+ * Errors: NABLA_ERR_INVALID_ARG for anything else.
+ */
+nabla_status nabla_qk_norm_rope(const void *q, const nabla_strides *q_st, const void *k,
+                                const nabla_strides *k_st, nabla_dtype dt, int B, int S, int hq,
+                                int hk, int D, const void *wq, const void *wk, nabla_dtype wdt,
+                                const float *cos_t, const float *sin_t, int rope_rows, int R,
+                                int interleaved, const int32_t *pos, float eps, void *q_out,
+                                const nabla_strides *qo_st, void *k_out,
+                                const nabla_strides *ko_st, nabla_stream_t stream);
+
+/*
+ * nabla_qk_norm_rope_bwd -- gradients of nabla_qk_norm_rope with respect to q, k
+ * and the weights, from its inputs and the upstream gradients dq_out and dk_out
+ * (what nabla_attn_bwd calls dq and dk).  With dy the upstream row rotated back,
+ * r = 1 / sqrt(mean(x^2) + eps) and g = w * dy:
+ *   dx = r (g - x r^2 mean(g x)),   dw = sum over batches, tokens and heads of dy x r.
+ * fp32 throughout, each gradient rounded once.  dw is summed in an order that
+ * depends on the shape and the number of SMs alone: repeated calls give the same
+ * bits.  The tables have no gradient.
+ *
+ *   dq_out, dk_out  as q_out and k_out, strides dqo_st and dko_st.
+ *   dq, dk          as q and k, strides dq_st and dk_st, overwritten; not
+ *                   overlapping any other argument.
+ *   dwq, dwk        [D] device, element type wdt, overwritten; NULL: not wanted.
+ *   workspace       device scratch of ws_bytes >= nabla_qk_norm_rope_bwd_workspace_bytes()
+ *                   (256-byte aligned); not looked at when dwq and dwk are NULL.
+ * Everything else, and the errors, as for nabla_qk_norm_rope.
+ */
+size_t nabla_qk_norm_rope_bwd_workspace_bytes(int D);
+nabla_status nabla_qk_norm_rope_bwd(
+    const void *q, const nabla_strides *q_st, const void *k, const nabla_strides *k_st,
+    nabla_dtype dt, int B, int S, int hq, int hk, int D, const void *wq, const void *wk,
+    nabla_dtype wdt, const float *cos_t, const float *sin_t, int rope_rows, int R,
+    int interleaved, const int32_t *pos, float eps, const void *dq_out,
+    const nabla_strides *dqo_st, const void *dk_out, const nabla_strides *dko_st, void *dq,
+    const nabla_strides *dq_st, void *dk, const nabla_strides *dk_st, void *dwq, void *dwk,
+    void *workspace, size_t ws_bytes, nabla_stream_t stream);
+
+/*
  * Diagnostic of the failure-detection path (no counterpart on the pages):
  * enqueues one CTA that waits on an mbarrier nothing ever arrives on, through
  * the same bounded wait the attention kernel uses, with a 20 ms limit.  The

@@ -370,3 +370,86 @@ def topk_mask(q: np.ndarray, k: np.ndarray, topk_ratio: float):
     kv_nb, kv_inds = csr_from_mask(keep)
     return {"kv_nb": kv_nb, "kv_inds": kv_inds, "mask": keep, "scores": sc, "topk": kk}
 
+
+
+# ---------------------------------------------------------------------------
+# The operators around the path in a transformer block (no counterpart on the
+# pages): the per-head RMS norm with rotation that makes q and k, and the
+# attention to an encoder's states.
+# ---------------------------------------------------------------------------
+def rotate(y: np.ndarray, c: np.ndarray, s: np.ndarray, interleaved: bool) -> np.ndarray:
+    """y [B, S, h, D], c and s [B or 1, S, R/2]: (a, b) -> (a c - b s, a s + b c) for the
+    columns (2i, 2i + 1) or (i, i + R/2), i < R/2; columns from R on unchanged."""
+    n = c.shape[-1]
+    a_at = np.arange(0, 2 * n, 2) if interleaved else np.arange(n)
+    b_at = a_at + (1 if interleaved else n)
+    c, s = c[:, :, None, :].astype(np.float64), s[:, :, None, :].astype(np.float64)
+    out = np.array(y, dtype=np.float64)
+    a, b = out[..., a_at].copy(), out[..., b_at].copy()
+    out[..., a_at] = a * c - b * s
+    out[..., b_at] = a * s + b * c
+    return out
+
+
+def qk_norm_rope(x, w, c, s, interleaved: bool, eps: float) -> np.ndarray:
+    """z = Rot(w x / sqrt(mean x^2 + eps)) of x [B, S, h, D], w [D] or None."""
+    x = np.asarray(x, np.float64)
+    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    if w is not None:
+        y = y * np.asarray(w, np.float64)
+    return rotate(y, c, s, interleaved)
+
+
+def qk_norm_rope_bwd(x, w, dz, c, s, interleaved: bool, eps: float):
+    """Gradients (dx, dw) of qk_norm_rope for the upstream gradient dz."""
+    x = np.asarray(x, np.float64)
+    w = np.ones(x.shape[-1]) if w is None else np.asarray(w, np.float64)
+    dy = rotate(np.asarray(dz, np.float64), c, -np.asarray(s), interleaved)
+    r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    g = dy * w
+    dx = r * (g - x * r * r * (g * x).mean(-1, keepdims=True))
+    return dx, (dy * x * r).sum(axis=(0, 1, 2))
+
+
+def cross_attention(q, k, v, kv_len, scale: float):
+    """o [B, Sq, h, D] and the base-2 log-sum-exp [B, h, Sq] of q [B, Sq, h, D] over the
+    first kv_len[b] of k, v [B, Sk, hk, D]; head i reads key head i // (h / hk)."""
+    B, Sq, h, D = q.shape
+    hk = k.shape[2]
+    o = np.zeros((B, Sq, h, D))
+    lse = np.full((B, h, Sq), -np.inf)
+    for b in range(B):
+        n = int(kv_len[b])
+        for i in range(h if n else 0):
+            j = i // (h // hk)
+            Q, K, V = (t.astype(np.float64) for t in (q[b, :, i], k[b, :n, j], v[b, :n, j]))
+            z = scale * (Q @ K.T)
+            m = z.max(axis=1, keepdims=True)
+            P = np.exp(z - m)
+            o[b, :, i] = (P @ V) / P.sum(axis=1, keepdims=True)
+            lse[b, i] = (m[:, 0] + np.log(P.sum(axis=1))) / math.log(2.0)
+    return o, lse
+
+
+def cross_attention_bwd(q, k, v, dout, kv_len, scale: float, o=None):
+    """(dq, dk, dv) of cross_attention; delta from the o passed in (R17), gradients of a
+    key head summed over the heads that read it, 0 for states past kv_len."""
+    B, Sq, h, D = q.shape
+    hk = k.shape[2]
+    dq, dk = np.zeros(q.shape), np.zeros(k.shape)
+    dv = np.zeros(k.shape)
+    for b in range(B):
+        n = int(kv_len[b])
+        for i in range(h if n else 0):
+            j = i // (h // hk)
+            Q, K, V, dO = (t.astype(np.float64) for t in
+                           (q[b, :, i], k[b, :n, j], v[b, :n, j], dout[b, :, i]))
+            z = scale * (Q @ K.T)
+            P = np.exp(z - z.max(axis=1, keepdims=True))
+            P /= P.sum(axis=1, keepdims=True)
+            out = P @ V if o is None else o[b, :, i].astype(np.float64)
+            dz = P * (dO @ V.T - (dO * out).sum(axis=1, keepdims=True))
+            dq[b, :, i] = scale * (dz @ K)
+            dk[b, :n, j] += scale * (dz.T @ Q)
+            dv[b, :n, j] += P.T @ dO
+    return dq, dk, dv
