@@ -415,6 +415,95 @@ nabla_status nabla_qk_norm_rope_bwd(
                       stream);
 }
 
+namespace nabla {
+namespace {
+
+bool valid_cross_shape(const CrossShape &s) {
+  if (s.B < 1 || s.Sq < 1 || s.Sk < 1 || s.h < 1 || s.hk < 1) return false;
+  if (s.D != 64 && s.D != 128) return false;
+  if (s.h % s.hk != 0 || s.h / s.hk > 64) return false;
+  if (s.Sq > (1 << 30) || s.Sk > (1 << 30)) return false;
+  // element counts and the grids' block counts must fit the kernels' arithmetic
+  if ((double)s.B * s.Sq * s.h * s.D > 4.0e12 || (double)s.B * s.Sk * s.hk * s.D > 4.0e12)
+    return false;
+  return (double)s.B * s.h * s.Sq <= 2.0e9 && (double)s.B * s.h * s.Sk <= 2.0e9;
+}
+
+// Checks of q, k, v (and their strides, filled in) and kv_len; the rows' extents.
+struct CrossRows {
+  Rows q, k, v;
+  uintptr_t qn, kn, vn;
+};
+bool valid_cross_inputs(CrossArgs &a, const nabla_strides *q_st, const nabla_strides *k_st,
+                        const nabla_strides *v_st, size_t esz, CrossRows &r) {
+  const CrossShape &s = a.s;
+  if (!std::isfinite(a.scale) || !aligned(a.kv_len, 4)) return false;
+  r.q = rows_of(a.q, q_st, s.B, s.Sq, s.h, s.D);
+  r.k = rows_of(a.k, k_st, s.B, s.Sk, s.hk, s.D);
+  r.v = rows_of(a.v, v_st, s.B, s.Sk, s.hk, s.D);
+  if (!valid_rows(r.q, s.B, s.Sq, s.D, esz) || !valid_rows(r.k, s.B, s.Sk, s.D, esz) ||
+      !valid_rows(r.v, s.B, s.Sk, s.D, esz))
+    return false;
+  a.q_st = r.q.st;
+  a.k_st = r.k.st;
+  a.v_st = r.v.st;
+  r.qn = extent(r.q, s.B, s.Sq, s.D, esz);
+  r.kn = extent(r.k, s.B, s.Sk, s.D, esz);
+  r.vn = extent(r.v, s.B, s.Sk, s.D, esz);
+  return true;
+}
+// Whether what is written (n bytes at p) meets an input.
+bool meets_inputs(const void *p, uintptr_t n, const CrossArgs &a, const CrossRows &r) {
+  return ranges_meet(p, n, r.q.p, r.qn) || ranges_meet(p, n, r.k.p, r.kn) ||
+         ranges_meet(p, n, r.v.p, r.vn) ||
+         (a.kv_len && ranges_meet(p, n, a.kv_len, (uintptr_t)a.s.B * 4));
+}
+
+}  // namespace
+}  // namespace nabla
+
+size_t nabla_cross_attn_fwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                            int D) {
+  const nabla::CrossShape s{B, Sq, Sk, h, hk, D};
+  if (!nabla::valid_dtype(dt) || !nabla::valid_cross_shape(s)) return 0;
+  return nabla::cross_fwd_workspace(s, dt);
+}
+
+nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, const void *k,
+                                  const nabla_strides *k_st, const void *v,
+                                  const nabla_strides *v_st, nabla_dtype dt, int B, int Sq, int Sk,
+                                  int h, int hk, int D, const int32_t *kv_len, float scale,
+                                  void *o, float *lse, void *workspace, size_t ws_bytes,
+                                  nabla_stream_t stream) {
+  using namespace nabla;
+  CrossArgs a{};
+  a.s = CrossShape{B, Sq, Sk, h, hk, D};
+  if (!valid_dtype(dt) || !valid_cross_shape(a.s)) return NABLA_ERR_INVALID_ARG;
+  const size_t esz = dt == NABLA_BF16 ? 2 : 4;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.kv_len = kv_len;
+  a.scale = scale;
+  CrossRows r;
+  if (!valid_cross_inputs(a, q_st, k_st, v_st, esz, r)) return NABLA_ERR_INVALID_ARG;
+  const uintptr_t rows = (uintptr_t)B * Sq * h, on = rows * D * esz;
+  if (!o || !aligned(o, 16) || !aligned(lse, 4) || meets_inputs(o, on, a, r) ||
+      (lse && (meets_inputs(lse, rows * 4, a, r) || ranges_meet(o, on, lse, rows * 4))))
+    return NABLA_ERR_INVALID_ARG;
+  const size_t need = cross_fwd_workspace(a.s, dt);
+  if (need && (!workspace || !aligned(workspace, 256) || ws_bytes < need))
+    return NABLA_ERR_INVALID_ARG;
+  a.o = o;
+  a.lse = lse;
+  a.workspace = workspace;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  a.status = device_status_ptr(&e);
+  if (!a.status) return NABLA_ERR_CUDA;
+  return from_cuda(dt == NABLA_BF16 ? launch_cross_attn_tc(a, st) : launch_cross_attn_simt(a, st));
+}
+
 nabla_status nabla_selftest_bounded_wait(nabla_stream_t stream) {
   return nabla::from_cuda(nabla::launch_bounded_wait_probe(reinterpret_cast<cudaStream_t>(stream)));
 }

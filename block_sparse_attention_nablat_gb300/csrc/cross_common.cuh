@@ -1,0 +1,60 @@
+// What the cross-attention kernels share: how query rows are packed into tiles and
+// how a batch's states are cut into tiles.
+//
+// The heads of a group (G = h / hk) read the same keys, so their rows go into one
+// tile: a 64-row subtile holds tq = 64 / G tokens of all G heads of the group, row
+// r = (token) * G + (head in the group); rows from tq * G on (G not dividing 64) stay
+// zero.  One K/V tile then serves all the heads that share it, and a single token of a
+// grouped model fills G rows instead of one.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "internal.h"
+
+namespace nabla {
+namespace cross {
+
+constexpr int kTile = 128;  // states per tile
+
+struct Packing {
+  int G, tq, nsub;  // heads per group, tokens per 64-row subtile, subtiles per (b, key head)
+};
+inline Packing packing(const CrossShape &s) {
+  Packing p;
+  p.G = s.h / s.hk;
+  p.tq = 64 / p.G;
+  p.nsub = (s.Sq + p.tq - 1) / p.tq;
+  return p;
+}
+
+__device__ __forceinline__ int batch_len(const int32_t *kv_len, int b, int Sk) {
+  if (!kv_len) return Sk;
+  const int n = __ldg(kv_len + b);
+  return n < 0 ? 0 : n > Sk ? Sk : n;
+}
+
+// A lane reports a kv_len outside [0, Sk] (it is used clamped).
+__device__ __forceinline__ void check_len(const int32_t *kv_len, int b, int Sk, int *status) {
+  if (kv_len && (kv_len[b] < 0 || kv_len[b] > Sk)) atomicCAS(status, kDevOk, kDevBadIndex);
+}
+
+// ---------------------------------------------------------------- host side
+// [B, S, heads, D] bf16 with strides as a 4-D tensor (D, heads, S, B); box = 64 columns
+// of `bh` heads of `tokens` tokens.
+inline bool cross_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, const void *ptr,
+                      int B, int S, int heads, int D, const nabla_strides &st, int bh,
+                      int tokens) {
+  cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)S, (cuuint64_t)B};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)st.token * 2, (cuuint64_t)st.batch * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)tokens, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+}  // namespace cross
+}  // namespace nabla

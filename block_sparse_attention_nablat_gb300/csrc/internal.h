@@ -109,6 +109,30 @@ struct QkNormArgs {
   void *workspace;  // backward: qk_norm_bwd_workspace(D) bytes of partial sums
   int *status;
 };
+// Cross attention: B batches, Sq queries of h heads, Sk states of hk heads (hk | h).
+struct CrossShape {
+  int B, Sq, Sk, h, hk, D;
+};
+struct CrossArgs {
+  CrossShape s;
+  const void *q, *k, *v;
+  nabla_strides q_st, k_st, v_st;
+  const int32_t *kv_len;  // [B] or null
+  float scale;
+  void *o;     // forward: [B, Sq, h, D]
+  float *lse;  // [B, h, Sq]; forward: or null
+  const void *of, *dout;  // backward: the forward's o, the upstream gradient
+  void *dq, *dk, *dv;
+  void *workspace;
+  int *status;
+};
+// Runs of states the bf16 forward splits its units into, and the scratch they need.
+int cross_fwd_splits(const CrossShape &s);
+size_t cross_fwd_workspace(const CrossShape &s, nabla_dtype dt);
+// K9: bf16, tcgen05.  K9f: fp32, CUDA cores.
+cudaError_t launch_cross_attn_tc(const CrossArgs &a, cudaStream_t st);
+cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st);
+
 size_t qk_norm_bwd_workspace(int D);
 cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);
 

@@ -85,6 +85,11 @@ def load() -> ctypes.CDLL:
     lib.nabla_qk_norm_rope_bwd_workspace_bytes.argtypes = [i32]
     lib.nabla_qk_norm_rope_bwd.restype = i32
     lib.nabla_qk_norm_rope_bwd.argtypes = qk + [vp, st, vp, st, vp, st, vp, st, vp, vp, vp, sz, vp]
+    xs = [i32, i32, i32, i32, i32, i32, i32]  # dtype, B, Sq, Sk, h, hk, D
+    lib.nabla_cross_attn_fwd_workspace_bytes.restype = sz
+    lib.nabla_cross_attn_fwd_workspace_bytes.argtypes = xs
+    lib.nabla_cross_attn_fwd.restype = i32
+    lib.nabla_cross_attn_fwd.argtypes = [vp, st, vp, st, vp, st] + xs + [vp, f32, vp, vp, vp, sz, vp]
     lib.nabla_selftest_bounded_wait.restype = i32
     lib.nabla_selftest_bounded_wait.argtypes = [vp]
     lib.nabla_get_last_device_status.restype = i32
@@ -533,6 +538,81 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
                _stream(stream, dev))
     _check(st, "nabla_qk_norm_rope_bwd")
     return dq, dk, dwq, dwk
+
+
+def _cross_args(q, k, v, kv_len):
+    """Checks q, k, v and kv_len of a cross attention; returns the C ABI's strides and
+    its (dtype, B, Sq, Sk, h, hk, D)."""
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != 4:
+            raise ValueError(f"{name} must be [B, S, h, D]")
+    B, Sq, h, D = q.shape
+    Sk, hk = k.shape[1:3]
+    dev = q.device
+    strides = (_rows(q, "q", (B, Sq, h, D), q.dtype, dev),
+               _rows(k, "k", (B, Sk, hk, D), q.dtype, dev),
+               _rows(v, "v", (B, Sk, hk, D), q.dtype, dev))
+    if kv_len is not None:
+        if kv_len.shape != (B,):
+            raise ValueError(f"kv_len must be [{B}], got {tuple(kv_len.shape)}")
+        _buf(kv_len, "kv_len", B, torch.int32, dev)
+    return strides, (_dtype_code(q), B, Sq, Sk, h, hk, D)
+
+
+def nabla_cross_attn_fwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk: int, h: int,
+                                         hk: int, D: int) -> int:
+    code = NABLA_BF16 if dtype == torch.bfloat16 else NABLA_F32
+    return load().nabla_cross_attn_fwd_workspace_bytes(code, B, Sq, Sk, h, hk, D)
+
+
+def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
+    strides, sizes = _cross_args(q, k, v, kv_len)
+    dev = q.device
+    if scale is None:
+        scale = 1.0 / math.sqrt(sizes[-1])
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _buf(o, "o", q.numel(), q.dtype, dev)
+    if lse is not None:
+        _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
+    lib = load()
+    if workspace is None:
+        need = lib.nabla_cross_attn_fwd_workspace_bytes(*sizes)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _on(workspace, "workspace", dev)
+    _cuda(q)
+    st = _call(dev, lib.nabla_cross_attn_fwd, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
+               strides[2], *sizes, _ptr(kv_len), float(scale), _ptr(o), _ptr(lse),
+               _ptr(workspace),
+               0 if workspace is None else workspace.numel() * workspace.element_size(),
+               _stream(stream, dev))
+    _check(st, "nabla_cross_attn_fwd")
+    return o
+
+
+def nabla_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                         kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         o: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of q [B,Sq,h,D] to the first kv_len[b] (int32 [B]; None: all) of the
+    states k, v [B,Sk,hk,D], hk dividing h; q, k, v may be views whose tokens are
+    strided.  Returns o [B,Sq,h,D]."""
+    return _cross_fwd(q, k, v, kv_len, scale, o, None, workspace, stream)
+
+
+def nabla_cross_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                             kv_len: Optional[torch.Tensor] = None,
+                             scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                             lse: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None, stream=None):
+    """nabla_cross_attn_fwd that also returns the rows' base-2 log-sum-exp:
+    (o, lse [B,h,Sq] fp32)."""
+    if lse is None:
+        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
+                          device=q.device)
+    return _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream), lse
 
 
 def _stream_device(stream) -> torch.device:

@@ -403,6 +403,48 @@ nabla_status nabla_qk_norm_rope_bwd(
     void *workspace, size_t ws_bytes, nabla_stream_t stream);
 
 /*
+ * nabla_cross_attn_fwd -- attention of the (video) tokens to an encoder's states of
+ * another length, the attention of a block that follows the block-sparse one.  For
+ * every batch b, query token s and head i, with key head j = i / (h / hk):
+ *   o[b, s, i, :] = sum_u softmax_u( scale * <q[b,s,i], k[b,u,j]> ) v[b, u, j, :],
+ *   u = 0 .. kv_len[b] - 1;
+ *   lse[(b*h + i)*Sq + s] = log2( sum_u 2^(scale * log2(e) * <q, k_u>) ).
+ * A batch with kv_len[b] = 0 gets o = 0 and lse = -INFINITY.  k and v from kv_len[b]
+ * on are padding: nothing they hold (NaN, infinities) reaches o or lse.
+ * bf16: both products run on the tcgen05 tensor cores with fp32 accumulators (P is
+ * rounded to bf16 before the second); f32: fp32 arithmetic on CUDA cores.  Repeated
+ * calls on the same inputs give the same bits.
+ *
+ *   q          [B, Sq, h, D] device, element type dt, strides q_st (see nabla_strides).
+ *   k, v       [B, Sk, hk, D] device, element type dt, strides k_st and v_st, e.g. two
+ *              views of one projection [B, Sk, 2, hk, D].
+ *   D          64 or 128; Sq and Sk any lengths >= 1 (at most 2^30); hk divides h and
+ *              h / hk <= 64.
+ *   kv_len     [B] device int32, the batches' lengths in [0, Sk]; NULL: all Sk.  One
+ *              outside is used clamped and reported as NABLA_ERR_BAD_INDEX by
+ *              nabla_get_last_device_status.
+ *   scale      softmax scale, finite (normally 1/sqrt(D)).
+ *   o          [B, Sq, h, D] device, dense, element type dt, overwritten.
+ *   lse        [B, h, Sq] device fp32, 4-byte aligned, overwritten; NULL: not wanted.
+ *   workspace  device scratch of ws_bytes >= nabla_cross_attn_fwd_workspace_bytes()
+ *              (256-byte aligned); not looked at where that is 0.  Few query rows
+ *              against many states are split over runs of the states, whose partial
+ *              results lie here; calls that overlap on the GPU (other streams, graphs
+ *              replayed side by side) need a workspace each.
+ * q, k, v and o are 16-byte aligned, kv_len 4-byte; o and lse overlap no other argument.
+ * nabla_cross_attn_fwd_workspace_bytes returns 0 for a shape that is not valid, too.
+ * Errors: NABLA_ERR_INVALID_ARG for anything else.
+ */
+size_t nabla_cross_attn_fwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                            int D);
+nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, const void *k,
+                                  const nabla_strides *k_st, const void *v,
+                                  const nabla_strides *v_st, nabla_dtype dt, int B, int Sq, int Sk,
+                                  int h, int hk, int D, const int32_t *kv_len, float scale,
+                                  void *o, float *lse, void *workspace, size_t ws_bytes,
+                                  nabla_stream_t stream);
+
+/*
  * Diagnostic of the failure-detection path (no counterpart on the pages):
  * enqueues one CTA that waits on an mbarrier nothing ever arrives on, through
  * the same bounded wait the attention kernel uses, with a 20 ms limit.  The
