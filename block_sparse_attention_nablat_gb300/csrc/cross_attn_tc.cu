@@ -14,16 +14,21 @@
 //  * TMEM: O in columns [0, D), three score buffers of 128 columns, so S of step g + 2
 //    waits only for the PV of step g - 1.  Shared memory: two Q tiles (the next unit's
 //    loads during this one), three K and two V tiles.
-//  * Warp 0 loads Q and K (TMA), warp 3 V; one thread of warp 1 issues the QK^T, one of
-//    warp 2 the PV; warps 4-7 and 8-11 take 64 columns each of every step's softmax and
-//    half of O's columns in the epilogue.
+//  * Encoder states are few (a prompt is four tiles), so a unit is short and every role
+//    runs ahead into the next unit: warp 0 loads Q and K (TMA), warp 3 V; one thread of
+//    warp 1 issues the QK^T, one of warp 2 the PV; eight softmax warps (two threads per
+//    row, 64 columns each) do nothing but softmax; four warps take O out of TMEM, scale
+//    and store it.
 //  * Softmax in base 2 with the scale folded in.  The running maximum is only the
-//    exponent's bias: it is the row maximum of a unit's first step, and is raised again
-//    only when a step's P sum exceeds 2^60 (then O and l are rescaled and the step
-//    redone).  P is rounded to bf16 for the tensor cores, l sums the fp32 P.
+//    exponent's bias: it is the row maximum of a unit's first step, and is raised (O and
+//    l rescaled) only for a step whose maximum exceeds it by more than 8, so P stays
+//    below 2^8.  The two threads of a row tell each other the maximum of their halves
+//    through shared memory.  P is rounded to bf16 for the tensor cores, l sums the fp32 P.
 //  * States past kv_len never enter: their columns get P = 0 whatever K holds there, and
 //    the rows of V that share the last 16-row MMA step with them are zeroed in shared
 //    memory before it runs, so a NaN behind the length stays there.
+//  * The output warps write a unit's rows as bf16 into its own Q tile (no MMA reads it
+//    any more) and from there by TMA.
 // Every mbarrier wait is bounded (1 s); on expiry the kernel records
 // NABLA_ERR_TIMEOUT, the roles stop waiting, copies and MMAs in flight are drained and
 // TMEM is released.
@@ -41,41 +46,38 @@ namespace nabla {
 namespace {
 
 using namespace tc;
+using cross::kTile;
 using tcattn::add2;
 using tcattn::f2;
 using tcattn::fma2;
 using tcattn::max3;
-using tcattn::min3;
 using tcattn::Ring;
 using tcattn::unf2;
-using cross::kTile;
 
 template <int D>
 struct XCfg {
-  static constexpr int kBoxes = D / 64;           // 64-column (128-byte) swizzle boxes
-  static constexpr int kBox = 128 * 128;          // one box of a 128-row tile
+  static constexpr int kBoxes = D / 64;   // 64-column (128-byte) swizzle boxes
+  static constexpr int kBox = 128 * 128;  // one box of a 128-row tile
   static constexpr int kTileBytes = kBoxes * kBox;
   static constexpr int kQBufs = 2, kKBufs = 3, kVBufs = 2, kSBufs = 3;
   static_assert(kKBufs == kSBufs, "a K tile is freed by its step's s_full");
   static_assert(kVBufs < kSBufs, "pv_done of step g - kVBufs cannot have moved on");
-  static constexpr uint32_t kSCol = 128;          // score buffer b at 128 + 128 b
+  static constexpr uint32_t kSCol = 128;  // score buffer b at 128 + 128 b
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr int kThreads = 384;
+  static constexpr int kThreads = 512;
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQBufs * kTileBytes;
   static constexpr int kOffV = kOffK + kKBufs * kTileBytes;
-  // what the two softmax groups tell each other: [2 groups][128 rows] maxima and sums,
-  // and [2 parities][2 groups][128 rows] flags
-  static constexpr int kOffXmax = kOffV + kVBufs * kTileBytes;
-  static constexpr int kOffXl = kOffXmax + 2 * 128 * 4;
-  static constexpr int kOffXflag = kOffXl + 2 * 128 * 4;
-  static constexpr int kOffSync = kOffXflag + 2 * 2 * 128;
+  static constexpr int kOffL = kOffV + kVBufs * kTileBytes;  // the halves' l: [2][128]
+  static constexpr int kOffX = kOffL + 2 * 128 * 4;          // the halves' maxima: [2][128]
+  static constexpr int kOffM = kOffX + 2 * 128 * 4;          // the rows' bias: [128]
+  static constexpr int kOffSync = kOffM + 128 * 4;
 };
 
 struct XSync {
   uint64_t q_full[2], q_empty[2], k_full[3], v_full[2], v_raw;
   uint64_t s_full[3], p_full[3], pv_done[3];
-  uint64_t o_free, drain;
+  uint64_t o_free, l_full, l_empty, drain;
   uint32_t tmem_slot;
   int abort;
 };
@@ -94,28 +96,36 @@ struct XParams {
   float *po, *plse;   // runs (nsplit > 1): [nsplit, B, h, Sq, D] and [nsplit, B, h, Sq]
   const int32_t *kv_len;
   int B, Sq, Sk, h, hk, G, tq, nqt, nsplit;
-  float scale_log2;
+  uint32_t units;  // B hk nqt nsplit
+  float scale_log2;  // of |scale|, never 0
+  uint32_t neg;      // kIdescNegA for a negative scale: the scores come negated
   int *status;
 };
 
 struct XUnit {
-  int b, j, qt, sp, len, t0, n;  // n tiles from t0
+  int b, j, qt, sp, len, t0, n;  // n state tiles from t0
 };
-__device__ __forceinline__ long x_units(const XParams &P) {
-  return (long)P.B * P.hk * P.nqt * P.nsplit;
-}
-__device__ __forceinline__ XUnit x_unit(const XParams &P, long u) {
+// Unit u: runs of one tile of queries first, then query tiles, key heads, batches.
+__device__ __noinline__ XUnit x_unit(const XParams &P, uint32_t u) {
   XUnit r;
-  const long v = u / P.nsplit;
-  r.sp = (int)(u - v * P.nsplit);
-  const long bj = v / P.nqt;
-  r.qt = (int)(v - bj * P.nqt);
-  r.b = (int)(bj / P.hk);
-  r.j = (int)(bj - (long)r.b * P.hk);
+  uint32_t v = u;
+  r.sp = 0;
+  if (P.nsplit > 1) {
+    v = u / (uint32_t)P.nsplit;
+    r.sp = (int)(u - v * (uint32_t)P.nsplit);
+  }
+  const uint32_t bj = v / (uint32_t)P.nqt;
+  r.qt = (int)(v - bj * (uint32_t)P.nqt);
+  r.b = (int)(bj / (uint32_t)P.hk);
+  r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
   r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
   const int nt = (r.len + kTile - 1) / kTile;
-  r.t0 = (int)((long)nt * r.sp / P.nsplit);
-  r.n = (int)((long)nt * (r.sp + 1) / P.nsplit) - r.t0;
+  r.t0 = 0;
+  r.n = nt;
+  if (P.nsplit > 1) {
+    r.t0 = (int)((long)nt * r.sp / P.nsplit);
+    r.n = (int)((long)nt * (r.sp + 1) / P.nsplit) - r.t0;
+  }
   return r;
 }
 // 16-state MMA steps of tile t (8, or fewer in the last tile).
@@ -132,13 +142,12 @@ __device__ void x_load_qk(const XParams &P, const CUtensorMap *mq, const CUtenso
   uint32_t g = 0, kq = 0;
   bool go = true;
   const uint32_t qbytes = (uint32_t)(P.G * P.tq) * 128 * 2 * C::kBoxes;
-  const long units = x_units(P);
-  for (long i = blockIdx.x; i < units && go && !*abort; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && go && !*abort; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     if (u.n == 0) continue;
     const uint32_t qb = kq & 1u;
-    go = mbar_wait(&sy->q_empty[qb], ((kq >> 1) & 1u) ^ 1u, abort, P.status, kDevTimeout);
+    go = mbar_wait_small(&sy->q_empty[qb], ((kq >> 1) & 1u) ^ 1u, abort, P.status, kDevTimeout);
     if (!go) break;
     mbar_expect_tx(&sy->q_full[qb], qbytes);
 #pragma unroll
@@ -151,7 +160,7 @@ __device__ void x_load_qk(const XParams &P, const CUtensorMap *mq, const CUtenso
     for (int s = 0; s < u.n && go; ++s, ++g) {
       // slot g % 3 is free once the QK^T of step g - 3 is done: s_full[g % 3]
       const uint32_t ks = g % C::kKBufs;
-      go = mbar_wait(&sy->s_full[ks], ((g / C::kKBufs) & 1u) ^ 1u, abort, P.status, kDevTimeout);
+      go = mbar_wait_small(&sy->s_full[ks], ((g / C::kKBufs) & 1u) ^ 1u, abort, P.status, kDevTimeout);
       if (!go) break;
       mbar_expect_tx(&sy->k_full[ks], C::kTileBytes);
 #pragma unroll
@@ -162,9 +171,9 @@ __device__ void x_load_qk(const XParams &P, const CUtensorMap *mq, const CUtenso
   }
   if (!go || *abort) {  // let copies in flight land before the CTA exits
     for (uint32_t e = g > (uint32_t)C::kKBufs ? g - C::kKBufs : 0u; e < g; ++e)
-      mbar_wait(&sy->k_full[e % C::kKBufs], (e / C::kKBufs) & 1u, nullptr, P.status, kDevTimeout);
+      mbar_wait_small(&sy->k_full[e % C::kKBufs], (e / C::kKBufs) & 1u, nullptr, P.status, kDevTimeout);
     for (uint32_t e = kq > 2 ? kq - 2 : 0u; e < kq; ++e)
-      mbar_wait(&sy->q_full[e & 1u], (e >> 1) & 1u, nullptr, P.status, kDevTimeout);
+      mbar_wait_small(&sy->q_full[e & 1u], (e >> 1) & 1u, nullptr, P.status, kDevTimeout);
   }
 }
 
@@ -178,8 +187,7 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
   const int lane = threadIdx.x & 31;
   uint32_t g = 0, raw = 0;
   bool go = true;
-  const long units = x_units(P);
-  for (long i = blockIdx.x; i < units && go; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && go; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     for (int s = 0; s < u.n && go; ++s, ++g) {
       const uint32_t vs = g % C::kVBufs;
@@ -192,7 +200,7 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
         ok = !*abort;
         if (ok && g >= (uint32_t)C::kVBufs) {
           const uint32_t gp = g - C::kVBufs;
-          ok = mbar_wait(&sy->pv_done[gp % C::kSBufs], (gp / C::kSBufs) & 1u, abort, P.status,
+          ok = mbar_wait_small(&sy->pv_done[gp % C::kSBufs], (gp / C::kSBufs) & 1u, abort, P.status,
                          kDevTimeout);
         }
         if (ok) {
@@ -201,7 +209,7 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
 #pragma unroll
           for (int c = 0; c < C::kBoxes; ++c)
             tma_load_4d(tile + c * C::kBox, mv, bar, c * 64, u.j, t * kTile, u.b);
-          if (mend) ok = mbar_wait(&sy->v_raw, raw & 1u, nullptr, P.status, kDevTimeout);
+          if (mend) ok = mbar_wait_small(&sy->v_raw, raw & 1u, nullptr, P.status, kDevTimeout);
         }
       }
       go = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -213,7 +221,7 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
           for (int e = lane; e < n16; e += 32)
             *reinterpret_cast<uint4 *>(tile + c * C::kBox + rows * 128 + e * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sy->v_full[vs]);
       }
@@ -221,7 +229,7 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
   }
   if (lane == 0 && (!go || *abort))
     for (uint32_t e = g > (uint32_t)C::kVBufs ? g - C::kVBufs : 0u; e < g; ++e)
-      mbar_wait(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status, kDevTimeout);
+      mbar_wait_small(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status, kDevTimeout);
 }
 
 // Warp 1, lane 0: S of step g into score buffer g % 3, once the PV of step g - 3 (its
@@ -235,21 +243,20 @@ __device__ void x_qk(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
   Ring<C::kSBufs> sb;
   uint32_t kq = 0;
   bool ok = true;
-  const long units = x_units(P);
-  for (long i = blockIdx.x; i < units && ok && !*abort; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && ok && !*abort; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
     const uint32_t qb = kq & 1u;
-    ok = mbar_wait(&sy->q_full[qb], (kq >> 1) & 1u, abort, P.status, kDevTimeout);
+    ok = mbar_wait_small(&sy->q_full[qb], (kq >> 1) & 1u, abort, P.status, kDevTimeout);
     const uint64_t qd = q_desc + (uint64_t)((qb * C::kTileBytes) >> 4);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = mbar_wait(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status, kDevTimeout) &&
-           mbar_wait(&sy->k_full[sb.slot], sb.phase, abort, P.status, kDevTimeout);
+      ok = mbar_wait_small(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status, kDevTimeout) &&
+           mbar_wait_small(&sy->k_full[sb.slot], sb.phase, abort, P.status, kDevTimeout);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + C::kSCol + sb.slot * 128;
       const uint64_t kd = k_desc + (uint64_t)((sb.slot * C::kTileBytes) >> 4);
-      const uint32_t id = idesc_bf16(128, x_k16(u, u.t0 + s) * 16, 0, 0);
+      const uint32_t id = idesc_bf16(128, x_k16(u, u.t0 + s) * 16, 0, 0) | P.neg;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         // 16 columns: 32 bytes inside a 128-byte swizzle row, every 4 the next box
@@ -257,16 +264,15 @@ __device__ void x_qk(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
         mma_ss(d, qd + at, kd + at, id, kk > 0 ? 1u : 0u);
       }
       mma_commit(&sy->s_full[sb.slot]);  // also frees the K slot
-      if (s + 1 == u.n) mma_commit(&sy->q_empty[qb]);
       sb.next();
     }
     ++kq;
   }
   mma_commit(&sy->drain);  // never exit with MMAs in flight
-  mbar_wait(&sy->drain, 0, nullptr, P.status, kDevTimeout);
+  mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
-// Warp 2, lane 0: O += P V once both softmax groups have written the step's P.
+// Warp 2, lane 0: O += P V once the softmax warps have written the step's P.
 template <int D>
 __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
                      volatile int *abort) {
@@ -277,22 +283,21 @@ __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
   Ring<C::kVBufs> vs;
   uint32_t kq = 0;
   bool ok = true;
-  const long units = x_units(P);
-  for (long i = blockIdx.x; i < units && ok && !*abort; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && ok && !*abort; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
     // the previous unit's O must have been read before the first PV overwrites it
-    if (kq > 0) ok = mbar_wait(&sy->o_free, (kq - 1) & 1u, abort, P.status, kDevTimeout);
+    if (kq > 0) ok = mbar_wait_small(&sy->o_free, (kq - 1) & 1u, abort, P.status, kDevTimeout);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = mbar_wait(&sy->p_full[sb.slot], sb.phase, abort, P.status, kDevTimeout) &&
-           mbar_wait(&sy->v_full[vs.slot], vs.phase, abort, P.status, kDevTimeout);
+      ok = mbar_wait_small(&sy->p_full[sb.slot], sb.phase, abort, P.status, kDevTimeout) &&
+           mbar_wait_small(&sy->v_full[vs.slot], vs.phase, abort, P.status, kDevTimeout);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = v_desc + (uint64_t)((vs.slot * C::kTileBytes) >> 4);
       const uint32_t a = tmem + C::kSCol + sb.slot * 128;
       const int k16 = x_k16(u, u.t0 + s);
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 16 states: 8 columns of P; group 1's from column 64
+      for (int kk = 0; kk < 8; ++kk)  // 16 states: 8 columns of P; the right half's from column 64
         if (kk < k16)
           mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
                  id, (s > 0 || kk > 0) ? 1u : 0u);
@@ -303,21 +308,13 @@ __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
     ++kq;
   }
   mma_commit(&sy->drain);
-  mbar_wait(&sy->drain, 0, nullptr, P.status, kDevTimeout);
+  mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
-constexpr int kXArrivals = 8;  // softmax warps
 __device__ __forceinline__ void x_arrive(uint64_t *bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
-// The two warps that hold the same 32 rows.
-__device__ __forceinline__ void x_pair_sync(int q4) {
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
-}
-
-// A step's P is kept as computed unless its sum exceeds this.
-constexpr float kXBig = 1.152921504606846976e18f;  // 2^60
 
 // 32 scores -> P = 2^(s * sl2 - m) in bf16 pairs (16 words); sums in acc0, acc1.
 __device__ __forceinline__ void x_exp(const uint32_t (&r)[32], uint64_t sc2, uint64_t nm2,
@@ -339,238 +336,247 @@ __device__ __forceinline__ void x_exp(const uint32_t (&r)[32], uint64_t sc2, uin
   }
 }
 
-// The same with P = 0 from column `valid` on (a batch's last tile).
-__device__ __forceinline__ float x_exp_masked(const uint32_t (&r)[32], float sl2, float m,
-                                              int valid, uint32_t (&pk)[16]) {
-  float sum = 0.f;
+// 32 scores from TMEM; those from column `valid` on (past the batch's states) as -inf,
+// whatever was computed there.
+__device__ __forceinline__ void x_scores(uint32_t ta, int valid, uint32_t (&r)[32]) {
+  tmem_ld32(ta, r);
+  tmem_wait_ld();
+  reg_fence(r);
+  if (valid < 32) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float p0 = 2 * i < valid ? ex2(fmaf(__uint_as_float(r[2 * i]), sl2, -m)) : 0.f;
-    const float p1 = 2 * i + 1 < valid ? ex2(fmaf(__uint_as_float(r[2 * i + 1]), sl2, -m)) : 0.f;
-    sum += p0 + p1;
-    pk[i] = pack_bf16x2(p0, p1);
+    for (int i = 0; i < 32; ++i) r[i] = i < valid ? r[i] : 0xff800000u;
   }
-  return sum;
 }
 
-// Row maximum of the first `valid` of 64 scores times sl2 (-inf for none).
-__device__ __forceinline__ float x_row_max(const uint32_t (&r0)[32], const uint32_t (&r1)[32],
-                                           float sl2, int valid) {
-  float a0 = -INFINITY, a1 = -INFINITY, b0 = INFINITY, b1 = INFINITY;
-  if (valid >= 64) {
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      a0 = max3(a0, __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
-      a1 = max3(a1, __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
-    }
-    if (sl2 < 0.f) {
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        b0 = min3(b0, __uint_as_float(r0[i]), __uint_as_float(r0[i + 1]));
-        b1 = min3(b1, __uint_as_float(r1[i]), __uint_as_float(r1[i + 1]));
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i < valid) {
-        a0 = fmaxf(a0, __uint_as_float(r0[i]));
-        b0 = fminf(b0, __uint_as_float(r0[i]));
-      }
-      if (i + 32 < valid) {
-        a1 = fmaxf(a1, __uint_as_float(r1[i]));
-        b1 = fminf(b1, __uint_as_float(r1[i]));
-      }
-    }
-    if (valid <= 0) return -INFINITY;
-  }
-  return sl2 >= 0.f ? fmaxf(a0, a1) * sl2 : fminf(b0, b1) * sl2;
+// The two softmax warps that hold the same rows (q4) meet on barrier 1 + q4; a warp that
+// has read its partner's maxima says so on the partner's barrier, and a warp waits on
+// its own before it writes new ones.
+__device__ __forceinline__ void x_pair_sync(int q4) {
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + q4) : "memory");
+}
+__device__ __forceinline__ void x_read_arrive(int q4, int of) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(5 + of * 4 + q4) : "memory");
+}
+__device__ __forceinline__ void x_read_wait(int q4, int of) {
+  asm volatile("bar.sync %0, 64;" ::"r"(5 + of * 4 + q4) : "memory");
 }
 
-// Warps 4-11: P of every step (group grp: columns 64 grp ..), then the unit's rows.
+// A step's maximum may exceed the bias by this much (base 2) before O is rescaled.
+constexpr float kXSlack = 8.f;
+
+// Warps 4-11: P of every step; thread = row, group grp takes columns 64 grp .. + 63.
 template <int D>
 __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
                           volatile int *abort) {
   using C = XCfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int grp = (warp - 4) >> 2, q4 = warp & 3;
-  const int row = q4 * 32 + lane, r64 = row & 63;
-  const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
-  float *xmax = reinterpret_cast<float *>(smem + C::kOffXmax);
-  float *xl = reinterpret_cast<float *>(smem + C::kOffXl);
-  const int other = (grp ^ 1) * 128 + row, mine = grp * 128 + row;
-  const int tok = r64 / P.G, head = r64 - tok * P.G;  // of this row, in its subtile
-  const bool row_used = tok < P.tq;
+  const int grp = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+  const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16);
+  float *xl = reinterpret_cast<float *>(smem + C::kOffL) + grp * 128;
+  float *xm = reinterpret_cast<float *>(smem + C::kOffM);
+  float *xx = reinterpret_cast<float *>(smem + C::kOffX);
   const float sl2 = P.scale_log2;
-  uint32_t gs = 0;
-  bool live = true;  // false after a wait gave up: keep meeting the pair barriers, do no work
-  const long units = x_units(P);
-  for (long i = blockIdx.x; i < units; i += gridDim.x) {
+  Ring<C::kSBufs> sb;
+  uint32_t g = 0, kq = 0;
+  bool live = true;  // false after a wait gave up: keep meeting the barriers, do no work
+  for (uint32_t i = blockIdx.x; i < P.units; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
+    if (u.n == 0) continue;
     float m_run = -INFINITY, l_run = 0.f;
-    for (int s = 0; s < u.n; ++s) {
-      const uint32_t g = gs + s, b = g % C::kSBufs, use = g / C::kSBufs;
-      const int valid = u.len - (u.t0 + s) * kTile - grp * 64;
-      live = __all_sync(0xffffffffu, live && mbar_wait(&sy->s_full[b], use & 1u, abort, P.status,
-                                                        kDevTimeout));
+    for (int s = 0; s < u.n; ++s, ++g, sb.next()) {
+      const int left = u.len - (u.t0 + s) * kTile;  // states of this step, from its first column
+      const int mine = left - grp * 64;
+      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->s_full[sb.slot], sb.phase, abort,
+                                                        P.status, kDevTimeout));
       tc_fence_after();
-      const uint32_t sbase = tmem + lane_base + C::kSCol + b * 128 + grp * 64;
-      const bool act = live && valid > 0;
-      uint32_t r0[32], r1[32], pk0[16], pk1[16];
-      if (act) {
-        tmem_ld32(sbase, r0);
-        tmem_ld32(sbase + 32, r1);
-        tmem_wait_ld();
-        reg_fence(r0);
-        reg_fence(r1);
-      }
-      float sum = 0.f;
-      auto step_p = [&]() {
-        if (valid >= 64) {
-          const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-m_run, -m_run);
-          uint64_t acc0 = f2(0.f, 0.f), acc1 = acc0;
-          x_exp(r0, sc2, nm2, acc0, acc1, pk0);
-          x_exp(r1, sc2, nm2, acc0, acc1, pk1);
-          float s0, s1, s2, s3;
-          unf2(acc0, s0, s1);
-          unf2(acc1, s2, s3);
-          sum = (s0 + s1) + (s2 + s3);
-        } else {
-          sum = x_exp_masked(r0, sl2, m_run, valid, pk0) +
-                x_exp_masked(r1, sl2, m_run, valid - 32, pk1);
-        }
-      };
-      if (s == 0) {  // the bias of the unit's first step: the row maximum of both halves
-        const float mx = act ? x_row_max(r0, r1, sl2, valid) : -INFINITY;
-        xmax[mine] = mx;
-        x_pair_sync(q4);
-        m_run = fmaxf(mx, xmax[other]);
-        if (act) step_p();
-      } else {
-        if (act) step_p();
-        const bool big = !(sum <= kXBig);  // also for an infinite or NaN sum
-        // two sets of flags in turn: the partner may still be reading the last step's
-        uint8_t *xflag = smem + C::kOffXflag + (g & 1u) * 2 * 128;
-        xflag[mine] = big ? 1 : 0;
-        x_pair_sync(q4);
-        const bool need = big || xflag[other] != 0;
-        if (__any_sync(0xffffffffu, need)) {  // the partner warp sees the same flags
-          const float mx = (need && act) ? x_row_max(r0, r1, sl2, valid) : -INFINITY;
-          xmax[mine] = mx;
-          x_pair_sync(q4);
-          const float m_new = need ? fmaxf(m_run, fmaxf(mx, xmax[other])) : m_run;
-          const bool resc = need && m_new > m_run;
-          if (__any_sync(0xffffffffu, resc)) {
-            // O must hold every PV up to the previous step before it is rescaled; each
-            // group rescales its half of the D columns
-            const uint32_t gp = g - 1;
-            const float alpha = resc ? ex2(m_run - m_new) : 1.0f;
-            live = __all_sync(0xffffffffu,
-                              live && mbar_wait(&sy->pv_done[gp % C::kSBufs],
-                                                (gp / C::kSBufs) & 1u, abort, P.status,
-                                                kDevTimeout));
-            if (live) {
-              tc_fence_after();
+      const uint32_t own = at + C::kSCol + sb.slot * 128 + grp * 64;
+      uint32_t r[32];
+      float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll 1
-              for (int c = 0; c < D / 32; ++c) {
-                const uint32_t ta = tmem + lane_base + grp * (D / 2) + c * 16;
-                uint32_t t[16];
-                tmem_ld16(ta, t);
-                tmem_wait_ld();
-                reg_fence16(t);
+      for (int x = 0; x < 64 && x < mine; x += 32) {
+        x_scores(own + x, mine - x, r);
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
-                tmem_st16(ta, t);
-              }
-              tmem_wait_st();
-            }
-            if (resc) l_run *= alpha;
-          }
-          if (need) m_run = m_new;
-          if (need && act) step_p();
+        for (int e = 0; e < 32; e += 4) {
+          a0 = max3(a0, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+          a1 = max3(a1, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
         }
       }
-      if (act) {
-        l_run += sum;
-        tmem_st16(sbase, pk0);
-        tmem_st16(sbase + 16, pk1);
+      const float mm = fmaxf(a0, a1) * sl2;
+      if (g > 0) x_read_wait(q4, grp);
+      xx[grp * 128 + row] = mm;
+      x_pair_sync(q4);
+      const float mx = fmaxf(mm, xx[(grp ^ 1) * 128 + row]);
+      x_read_arrive(q4, grp ^ 1);
+      const bool raise = s > 0 && mx > m_run + kXSlack;
+      if (s == 0) m_run = mx;
+      if (__any_sync(0xffffffffu, raise)) {
+        // O must hold every PV up to the previous step before it is rescaled; each
+        // group takes half of its columns (both decide alike, from the same scores)
+        const uint32_t gp = g - 1;
+        const float alpha = raise ? ex2(m_run - mx) : 1.0f;
+        live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->pv_done[gp % C::kSBufs],
+                                                         (gp / C::kSBufs) & 1u, abort, P.status,
+                                                         kDevTimeout));
+        tc_fence_after();
+#pragma unroll 1
+        for (int x = 0; x < D / 32; ++x) {
+          const uint32_t ta = at + grp * (D / 2) + x * 16;
+          uint32_t t[16];
+          tmem_ld16(ta, t);
+          tmem_wait_ld();
+          reg_fence16(t);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
+          tmem_st16(ta, t);
+        }
         tmem_wait_st();
+        if (raise) {
+          l_run *= alpha;
+          m_run = mx;
+        }
       }
+      const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-m_run, -m_run);
+      uint64_t acc0 = f2(0.f, 0.f), acc1 = acc0;
+      // P of columns 0 .. 31 lies over scores 0 .. 15, of 32 .. 63 over 16 .. 31: read before
+#pragma unroll 1
+      for (int x = 0; x < 64 && x < mine; x += 32) {
+        uint32_t pk[16];
+        x_scores(own + x, mine - x, r);
+        x_exp(r, sc2, nm2, acc0, acc1, pk);
+        tmem_st16(own + (x >> 1), pk);
+      }
+      float s0, s1, s2, s3;
+      unf2(acc0, s0, s1);
+      unf2(acc1, s2, s3);
+      l_run += (s0 + s1) + (s2 + s3);
+      tmem_wait_st();
       tc_fence_before();
-      x_arrive(&sy->p_full[b], lane);
+      x_arrive(&sy->p_full[sb.slot], lane);
     }
-    // ---- O / l of the row: half of the columns each
-    float lt = 0.f;
+    // the output warps have read the last unit's l and bias
+    live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->l_empty, (kq & 1u) ^ 1u, abort,
+                                                      P.status, kDevTimeout));
+    xl[row] = l_run;
+    if (grp == 0) xm[row] = m_run;
+    x_arrive(&sy->l_full, lane);
+    ++kq;
+  }
+  if (g > 0) x_read_wait(q4, grp);  // meets the partner's last arrival
+}
+
+// The four output warps.
+__device__ __forceinline__ void x_out_sync() { asm volatile("bar.sync 13, 128;" ::: "memory"); }
+
+// Warps 12-15: the units' rows; thread = row.
+template <int D>
+__device__ void x_output(const XParams &P, const CUtensorMap *mo, uint8_t *smem, XSync *sy,
+                         uint32_t tmem, volatile int *abort) {
+  using C = XCfg<D>;
+  const int lane = threadIdx.x & 31, q4 = (threadIdx.x >> 5) & 3;
+  const int row = q4 * 32 + lane, r64 = row & 63;
+  const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16);
+  const float *xl = reinterpret_cast<const float *>(smem + C::kOffL);
+  const float *xm = reinterpret_cast<const float *>(smem + C::kOffM);
+  const int tok = r64 / P.G, head = r64 - tok * P.G;  // of this row, in its subtile
+  uint32_t gs = 0, kq = 0;  // steps and units (with states) so far
+  bool live = true;         // false after a wait gave up: keep meeting the barrier, do no work
+  for (uint32_t i = blockIdx.x; i < P.units; i += gridDim.x) {
+    const XUnit u = x_unit(P, i);
+    const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok, hh = u.j * P.G + head;
+    const bool row_ok = tok < P.tq && token < P.Sq;
+    const size_t lrow = ((size_t)u.b * P.h + hh) * P.Sq + token;
+    float l = 0.f, m = 0.f;
     if (u.n > 0) {
       const uint32_t gl = gs + u.n - 1;
       live = __all_sync(0xffffffffu,
-                        live && mbar_wait(&sy->pv_done[gl % C::kSBufs], (gl / C::kSBufs) & 1u,
+                        live && mbar_wait_small(&sy->l_full, kq & 1u, abort, P.status, kDevTimeout));
+      l = xl[row] + xl[128 + row];
+      m = xm[row];
+      x_arrive(&sy->l_empty, lane);
+      live = __all_sync(0xffffffffu,
+                        live && mbar_wait_small(&sy->pv_done[gl % C::kSBufs], (gl / C::kSBufs) & 1u,
                                           abort, P.status, kDevTimeout));
       tc_fence_after();
-      xl[mine] = l_run;  // read before the next unit's first barrier, written again after it
-      x_pair_sync(q4);
-      lt = l_run + xl[other];
     }
-    const float inv = lt > 0.f ? 1.0f / lt : lt;  // 0 for no states; NaN stays
-    const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok;
-    const bool row_ok = live && row_used && token < P.Sq;
-    const int hh = u.j * P.G + head;
-    const size_t lrow = ((size_t)u.b * P.h + hh) * P.Sq + token;
-    const float lse = lt > 0.f ? m_run + log2f(lt) : lt == 0.f ? -INFINITY : lt;
-    if (row_ok && grp == 0) {
+    const float inv = l > 0.f ? 1.0f / l : l;  // 0 for no states; NaN stays
+    uint8_t *tile = smem + C::kOffQ + (kq & 1u) * C::kTileBytes;
+    float *run = P.po + ((size_t)u.sp * P.B * P.h * P.Sq + lrow) * D;
+    if (u.n > 0) {
+#pragma unroll 1
+      for (int x = 0; x < D / 32; ++x) {
+        uint32_t t[32];
+        tmem_ld32(at + x * 32, t);
+        tmem_wait_ld();
+        reg_fence(t);
+        if (x + 1 == D / 32) {
+          tc_fence_before();
+          x_arrive(&sy->o_free, lane);
+        }
+        if (P.nsplit > 1) {
+          if (row_ok && live)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4 *>(run + x * 32 + e) = make_float4(
+                  __uint_as_float(t[e]) * inv, __uint_as_float(t[e + 1]) * inv,
+                  __uint_as_float(t[e + 2]) * inv, __uint_as_float(t[e + 3]) * inv);
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = pack_bf16x2(__uint_as_float(t[8 * e + 2 * y]) * inv,
+                               __uint_as_float(t[8 * e + 2 * y + 1]) * inv);
+          // 16-byte piece of the row's 128 bytes in box x / 2, swizzled by the row
+          const int piece = (x & 1) * 4 + e;
+          *reinterpret_cast<uint4 *>(tile + (x >> 1) * C::kBox + row * 128 +
+                                     ((piece ^ (row & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_async_smem();
+      x_out_sync();
+      if (q4 == 0 && lane == 0) {
+        if (live && P.nsplit == 1) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const int t0 = (u.qt * 2 + side) * P.tq;
+            if (t0 >= P.Sq) break;
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+              tma_store_4d(mo, tile + x * C::kBox + side * 64 * 128, x * 64, u.j * P.G, t0, u.b);
+          }
+          bulk_commit();
+          bulk_wait_read();
+        }
+        mbar_arrive(&sy->q_empty[kq & 1u]);  // the loader may have the tile back
+      }
+      gs += u.n;
+      ++kq;
+    } else if (P.nsplit == 1 && row_ok) {  // o = 0 (joining runs leaves one without states out)
+      uint4 *dst = reinterpret_cast<uint4 *>(P.o + (((size_t)u.b * P.Sq + token) * P.h + hh) * D);
+#pragma unroll
+      for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (row_ok && live) {
+      const float lse = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
       if (P.nsplit > 1)
         P.plse[(size_t)u.sp * P.B * P.h * P.Sq + lrow] = lse;
       else if (P.lse)
         P.lse[lrow] = lse;
     }
-    if (P.nsplit == 1 || u.n > 0) {
-#pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        const int c = grp * (D / 32) + cc;  // this group's 16-column pieces
-        uint32_t t[16];
-        if (u.n > 0) {
-          tmem_ld16(tmem + lane_base + c * 16, t);
-          tmem_wait_ld();
-          reg_fence16(t);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) t[e] = 0u;
-        }
-        if (!row_ok) continue;
-        if (P.nsplit > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(
-              P.po + ((size_t)u.sp * P.B * P.h * P.Sq + lrow) * D + c * 16);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            dst[e] = make_float4(__uint_as_float(t[4 * e]) * inv,
-                                 __uint_as_float(t[4 * e + 1]) * inv,
-                                 __uint_as_float(t[4 * e + 2]) * inv,
-                                 __uint_as_float(t[4 * e + 3]) * inv);
-        } else {
-          uint32_t w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = pack_bf16x2(__uint_as_float(t[2 * e]) * inv,
-                               __uint_as_float(t[2 * e + 1]) * inv);
-          uint4 *dst = reinterpret_cast<uint4 *>(
-              P.o + (((size_t)u.b * P.Sq + token) * P.h + hh) * D + c * 16);
-          __stcs(dst, make_uint4(w[0], w[1], w[2], w[3]));
-          __stcs(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
-        }
-      }
-    }
-    tc_fence_before();
-    if (u.n > 0) x_arrive(&sy->o_free, lane);
-    gs += u.n;
   }
+  if (q4 == 0 && lane == 0) bulk_wait_all();
 }
 
 template <int D>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(512, 1)
     cross_attn_tc_kernel(const __grid_constant__ CUtensorMap mq,
                          const __grid_constant__ CUtensorMap mk,
-                         const __grid_constant__ CUtensorMap mv, const __grid_constant__ XParams P) {
+                         const __grid_constant__ CUtensorMap mv,
+                         const __grid_constant__ CUtensorMap mo,
+                         const __grid_constant__ XParams P) {
   using C = XCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   XSync *sy = reinterpret_cast<XSync *>(smem + C::kOffSync);
@@ -591,25 +597,28 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 3; ++i) {
       mbar_init(&sy->k_full[i], 1);
       mbar_init(&sy->s_full[i], 1);
-      mbar_init(&sy->p_full[i], kXArrivals);
+      mbar_init(&sy->p_full[i], 8);  // softmax warps
       mbar_init(&sy->pv_done[i], 1);
     }
-    mbar_init(&sy->o_free, kXArrivals);
+    mbar_init(&sy->o_free, 4);  // output warps
+    mbar_init(&sy->l_full, 8);
+    mbar_init(&sy->l_empty, 4);
     mbar_init(&sy->drain, 2);  // one commit per MMA-issuing thread
     sy->abort = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
+    tma_prefetch_desc(&mo);
     fence_barrier_init();
   }
   // rows of the Q tiles that no box fills (G not dividing 64)
   const int used = P.G * P.tq;
   for (int e = threadIdx.x; e < (64 - used) * 8 * 2 * C::kBoxes * C::kQBufs; e += C::kThreads) {
-    const int per = (64 - used) * 8, sub = e / per, at = e - sub * per;
-    *reinterpret_cast<uint4 *>(smem + C::kOffQ + sub * 64 * 128 + used * 128 + at * 16) =
+    const int per = (64 - used) * 8, sub = e / per, to = e - sub * per;
+    *reinterpret_cast<uint4 *>(smem + C::kOffQ + sub * 64 * 128 + used * 128 + to * 16) =
         make_uint4(0u, 0u, 0u, 0u);
   }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  fence_async_smem();
   if (warp == 1) tmem_alloc(&sy->tmem_slot, C::kTmemCols);
   tc_fence_before();
   __syncthreads();
@@ -617,20 +626,21 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t tmem = sy->tmem_slot;
   pdl_wait();  // the inputs are written; no earlier kernel still reads o
 
-  if (warp == 0) {
-    if (lane == 0) x_load_qk<D>(P, &mq, &mk, smem, sy, abort);
+  if (warp < 4) {
+    if (warp == 0) {
+      if (lane == 0) x_load_qk<D>(P, &mq, &mk, smem, sy, abort);
+    } else if (warp == 1) {
+      if (lane == 0) x_qk<D>(P, smem, sy, tmem, abort);
+    } else if (warp == 2) {
+      if (lane == 0) x_pv<D>(P, smem, sy, tmem, abort);
+    } else {
+      x_load_v<D>(P, &mv, smem, sy, abort);
+    }
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) x_qk<D>(P, smem, sy, tmem, abort);
-    __syncwarp();
-  } else if (warp == 2) {
-    if (lane == 0) x_pv<D>(P, smem, sy, tmem, abort);
-    __syncwarp();
-  } else if (warp == 3) {
-    x_load_v<D>(P, &mv, smem, sy, abort);
-    __syncwarp();
-  } else {
+  } else if (warp < 12) {
     x_softmax<D>(P, smem, sy, tmem, abort);
+  } else {
+    x_output<D>(P, &mo, smem, sy, tmem, abort);
   }
   tc_fence_before();
   __syncthreads();
@@ -676,6 +686,28 @@ __global__ void __launch_bounds__(256) cross_combine_kernel(const XParams P) {
   if (P.lse && lane == 0) P.lse[row] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
 }
 
+// How the rows and states are cut into units.  Runs: 1 where the units fill the GPU,
+// else enough for about four units per SM (batches differ in length), at least two state
+// tiles each.  Sized for GB300's 152 SMs, so that the workspace depends on the shape
+// alone.
+struct FwdPlan {
+  int nqt, nsplit;
+};
+FwdPlan fwd_plan(const CrossShape &s) {
+  constexpr long kSms = 152;
+  const cross::Packing pk = cross::packing(s);
+  FwdPlan f;
+  f.nqt = (pk.nsub + 1) / 2;
+  f.nsplit = 1;
+  const long units = (long)s.B * s.hk * f.nqt;
+  const int nt = (s.Sk + kTile - 1) / kTile;
+  if (units < kSms && nt >= 4) {
+    const long want = (4 * kSms + units - 1) / units;
+    f.nsplit = (int)(want < nt / 2 ? want : nt / 2);
+  }
+  return f;
+}
+
 template <int D>
 cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   using C = XCfg<D>;
@@ -684,10 +716,12 @@ cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   auto enc = tensor_map_encoder(&err);
   if (!enc) return err;
   const cross::Packing pk = cross::packing(s);
-  CUtensorMap mq, mk, mv;
+  const nabla_strides o_st{(int64_t)s.Sq * s.h * D, (int64_t)s.h * D};
+  CUtensorMap mq, mk, mv, mo;
   if (!cross::cross_map(enc, &mq, a.q, s.B, s.Sq, s.h, D, a.q_st, pk.G, pk.tq) ||
       !cross::cross_map(enc, &mk, a.k, s.B, s.Sk, s.hk, D, a.k_st, 1, kTile) ||
-      !cross::cross_map(enc, &mv, a.v, s.B, s.Sk, s.hk, D, a.v_st, 1, kTile))
+      !cross::cross_map(enc, &mv, a.v, s.B, s.Sk, s.hk, D, a.v_st, 1, kTile) ||
+      !cross::cross_map(enc, &mo, a.o, s.B, s.Sq, s.h, D, o_st, pk.G, pk.tq))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
@@ -702,18 +736,22 @@ cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   p.lse = a.lse;
   p.kv_len = a.kv_len;
   p.B = s.B, p.Sq = s.Sq, p.Sk = s.Sk, p.h = s.h, p.hk = s.hk;
-  p.G = pk.G, p.tq = pk.tq, p.nqt = (pk.nsub + 1) / 2;
-  p.nsplit = cross_fwd_splits(s);
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.G = pk.G, p.tq = pk.tq;
+  const FwdPlan plan = fwd_plan(s);
+  p.nqt = plan.nqt, p.nsplit = plan.nsplit;
+  // a scale of 0 weighs all states alike, as one too small to tell scores apart does
+  p.scale_log2 = a.scale == 0.f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
+  p.neg = a.scale < 0.f ? kIdescNegA : 0u;
   p.status = a.status;
   const long rows = (long)s.B * s.h * s.Sq;
   if (p.nsplit > 1) {
     p.po = static_cast<float *>(a.workspace);
     p.plse = p.po + (size_t)p.nsplit * rows * D;
   }
-  const long units = (long)s.B * s.hk * p.nqt * p.nsplit;
-  const int grid = (int)(units < sms ? units : sms);
-  err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), x_smem_bytes<D>(), st, mq, mk, mv, p);
+  p.units = (uint32_t)((long)s.B * s.hk * p.nqt * p.nsplit);
+  const unsigned grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
+  err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), x_smem_bytes<D>(), st, mq, mk, mv, mo,
+                   p);
   if (err != cudaSuccess || p.nsplit == 1) return err;
   return launch_pdl(cross_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st,
                     p);
@@ -721,17 +759,7 @@ cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
 
 }  // namespace
 
-// Runs per unit: 1 where the units alone fill the GPU; else enough for about four
-// units per SM (batches differ in length), at least two state tiles each.  Sized for
-// the 152 SMs of GB300, so that the workspace depends on the shape alone.
-int cross_fwd_splits(const CrossShape &s) {
-  const cross::Packing pk = cross::packing(s);
-  const long units = (long)s.B * s.hk * ((pk.nsub + 1) / 2);
-  const int nt = (s.Sk + kTile - 1) / kTile;
-  if (units >= 152 || nt < 4) return 1;
-  const long want = (4 * 152 + units - 1) / units;
-  return (int)(want < nt / 2 ? want : nt / 2);
-}
+int cross_fwd_splits(const CrossShape &s) { return fwd_plan(s).nsplit; }
 
 size_t cross_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
   const int n = dt == NABLA_BF16 ? cross_fwd_splits(s) : 1;
