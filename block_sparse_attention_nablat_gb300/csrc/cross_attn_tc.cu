@@ -12,8 +12,8 @@
 //    O += P V a TS MMA with P (bf16) in TMEM over the scores it came from.  The last
 //    tile of a batch runs at N = its states rounded up to 16.
 //  * TMEM: O in columns [0, D), three score buffers of 128 columns, so S of step g + 2
-//    waits only for the PV of step g - 1.  Shared memory: two Q tiles (the next unit's
-//    loads during this one), three K and two V tiles.
+//    waits only for the PV of step g - 1.  Shared memory: two Q, two K and two V tiles
+//    and one for the rows on their way out.
 //  * Encoder states are few (a prompt is four tiles), so a unit is short and every role
 //    runs ahead into the next unit: warp 0 loads Q and K (TMA), warp 3 V; one thread of
 //    warp 1 issues the QK^T, one of warp 2 the PV; eight softmax warps (two threads per
@@ -27,8 +27,7 @@
 //  * States past kv_len never enter: their columns get P = 0 whatever K holds there, and
 //    the rows of V that share the last 16-row MMA step with them are zeroed in shared
 //    memory before it runs, so a NaN behind the length stays there.
-//  * The output warps write a unit's rows as bf16 into its own Q tile (no MMA reads it
-//    any more) and from there by TMA.
+//  * The output warps stage a unit's rows as bf16 in shared memory and store them by TMA.
 // Every mbarrier wait is bounded (1 s); on expiry the kernel records
 // NABLA_ERR_TIMEOUT, the roles stop waiting, copies and MMAs in flight are drained and
 // TMEM is released.
@@ -59,8 +58,8 @@ struct XCfg {
   static constexpr int kBoxes = D / 64;   // 64-column (128-byte) swizzle boxes
   static constexpr int kBox = 128 * 128;  // one box of a 128-row tile
   static constexpr int kTileBytes = kBoxes * kBox;
-  static constexpr int kQBufs = 2, kKBufs = 3, kVBufs = 2, kSBufs = 3;
-  static_assert(kKBufs == kSBufs, "a K tile is freed by its step's s_full");
+  static constexpr int kQBufs = 2, kKBufs = 2, kVBufs = 2, kSBufs = 3;
+  static_assert(kKBufs < kSBufs, "s_full of step g - kKBufs cannot have moved on");
   static_assert(kVBufs < kSBufs, "pv_done of step g - kVBufs cannot have moved on");
   static constexpr uint32_t kSCol = 128;  // score buffer b at 128 + 128 b
   static constexpr uint32_t kTmemCols = 512;
@@ -68,14 +67,15 @@ struct XCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kQBufs * kTileBytes;
   static constexpr int kOffV = kOffK + kKBufs * kTileBytes;
-  static constexpr int kOffL = kOffV + kVBufs * kTileBytes;  // the halves' l: [2][128]
+  static constexpr int kOffO = kOffV + kVBufs * kTileBytes;  // rows on their way out
+  static constexpr int kOffL = kOffO + kTileBytes;  // the halves' l: [2][128]
   static constexpr int kOffX = kOffL + 2 * 128 * 4;          // the halves' maxima: [2][128]
   static constexpr int kOffM = kOffX + 2 * 128 * 4;          // the rows' bias: [128]
   static constexpr int kOffSync = kOffM + 128 * 4;
 };
 
 struct XSync {
-  uint64_t q_full[2], q_empty[2], k_full[3], v_full[2], v_raw;
+  uint64_t q_full[2], q_empty[2], k_full[2], v_full[2], v_raw;
   uint64_t s_full[3], p_full[3], pv_done[3];
   uint64_t o_free, l_full, l_empty, drain;
   uint32_t tmem_slot;
@@ -140,28 +140,32 @@ __device__ void x_load_qk(const XParams &P, const CUtensorMap *mq, const CUtenso
                           uint8_t *smem, XSync *sy, volatile int *abort) {
   using C = XCfg<D>;
   uint32_t g = 0, kq = 0;
+  Ring<C::kQBufs> q;
   bool go = true;
   const uint32_t qbytes = (uint32_t)(P.G * P.tq) * 128 * 2 * C::kBoxes;
   for (uint32_t i = blockIdx.x; i < P.units && go && !*abort; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     if (u.n == 0) continue;
-    const uint32_t qb = kq & 1u;
-    go = mbar_wait_small(&sy->q_empty[qb], ((kq >> 1) & 1u) ^ 1u, abort, P.status, kDevTimeout);
+    go = mbar_wait_small(&sy->q_empty[q.slot], q.phase ^ 1u, abort, P.status, kDevTimeout);
     if (!go) break;
-    mbar_expect_tx(&sy->q_full[qb], qbytes);
+    mbar_expect_tx(&sy->q_full[q.slot], qbytes);
 #pragma unroll
     for (int side = 0; side < 2; ++side)
 #pragma unroll
       for (int c = 0; c < C::kBoxes; ++c)  // tokens past Sq are zero-filled
-        tma_load_4d(smem + C::kOffQ + qb * C::kTileBytes + c * C::kBox + side * 64 * 128, mq,
-                    &sy->q_full[qb], c * 64, u.j * P.G, (u.qt * 2 + side) * P.tq, u.b);
+        tma_load_4d(smem + C::kOffQ + q.slot * C::kTileBytes + c * C::kBox + side * 64 * 128, mq,
+                    &sy->q_full[q.slot], c * 64, u.j * P.G, (u.qt * 2 + side) * P.tq, u.b);
     ++kq;
+    q.next();
     for (int s = 0; s < u.n && go; ++s, ++g) {
-      // slot g % 3 is free once the QK^T of step g - 3 is done: s_full[g % 3]
       const uint32_t ks = g % C::kKBufs;
-      go = mbar_wait_small(&sy->s_full[ks], ((g / C::kKBufs) & 1u) ^ 1u, abort, P.status, kDevTimeout);
-      if (!go) break;
+      if (g >= (uint32_t)C::kKBufs) {  // free once the QK^T of step g - 2 is done
+        const uint32_t gp = g - C::kKBufs;
+        go = mbar_wait_small(&sy->s_full[gp % C::kSBufs], (gp / C::kSBufs) & 1u, abort, P.status,
+                             kDevTimeout);
+        if (!go) break;
+      }
       mbar_expect_tx(&sy->k_full[ks], C::kTileBytes);
 #pragma unroll
       for (int c = 0; c < C::kBoxes; ++c)
@@ -171,9 +175,11 @@ __device__ void x_load_qk(const XParams &P, const CUtensorMap *mq, const CUtenso
   }
   if (!go || *abort) {  // let copies in flight land before the CTA exits
     for (uint32_t e = g > (uint32_t)C::kKBufs ? g - C::kKBufs : 0u; e < g; ++e)
-      mbar_wait_small(&sy->k_full[e % C::kKBufs], (e / C::kKBufs) & 1u, nullptr, P.status, kDevTimeout);
-    for (uint32_t e = kq > 2 ? kq - 2 : 0u; e < kq; ++e)
-      mbar_wait_small(&sy->q_full[e & 1u], (e >> 1) & 1u, nullptr, P.status, kDevTimeout);
+      mbar_wait_small(&sy->k_full[e % C::kKBufs], (e / C::kKBufs) & 1u, nullptr, P.status,
+                      kDevTimeout);
+    for (uint32_t e = kq > (uint32_t)C::kQBufs ? kq - C::kQBufs : 0u; e < kq; ++e)
+      mbar_wait_small(&sy->q_full[e % C::kQBufs], (e / C::kQBufs) & 1u, nullptr, P.status,
+                      kDevTimeout);
   }
 }
 
@@ -232,8 +238,14 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
       mbar_wait_small(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status, kDevTimeout);
 }
 
-// Warp 1, lane 0: S of step g into score buffer g % 3, once the PV of step g - 3 (its
-// last reader) is done.
+// A wait of a whole warp that goes on in step.
+__device__ __forceinline__ bool x_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       int *status) {
+  return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort, status, kDevTimeout));
+}
+
+// Warp 1: S of step g into score buffer g % 3, once the PV of step g - 3 (its last
+// reader) is done.
 template <int D>
 __device__ void x_qk(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
                      volatile int *abort) {
@@ -241,38 +253,44 @@ __device__ void x_qk(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
   const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
   const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
   Ring<C::kSBufs> sb;
-  uint32_t kq = 0;
+  Ring<C::kKBufs> ks;
+  Ring<C::kQBufs> q;
   bool ok = true;
-  for (uint32_t i = blockIdx.x; i < P.units && ok && !*abort; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && ok; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
-    const uint32_t qb = kq & 1u;
-    ok = mbar_wait_small(&sy->q_full[qb], (kq >> 1) & 1u, abort, P.status, kDevTimeout);
-    const uint64_t qd = q_desc + (uint64_t)((qb * C::kTileBytes) >> 4);
+    ok = x_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
+    const uint64_t qd = q_desc + (uint64_t)((q.slot * C::kTileBytes) >> 4);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = mbar_wait_small(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status, kDevTimeout) &&
-           mbar_wait_small(&sy->k_full[sb.slot], sb.phase, abort, P.status, kDevTimeout);
+      ok = x_wait(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status) &&
+           x_wait(&sy->k_full[ks.slot], ks.phase, abort, P.status);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + C::kSCol + sb.slot * 128;
-      const uint64_t kd = k_desc + (uint64_t)((sb.slot * C::kTileBytes) >> 4);
+      const uint64_t kd = k_desc + (uint64_t)((ks.slot * C::kTileBytes) >> 4);
       const uint32_t id = idesc_bf16(128, x_k16(u, u.t0 + s) * 16, 0, 0) | P.neg;
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        // 16 columns: 32 bytes inside a 128-byte swizzle row, every 4 the next box
-        const uint64_t at = (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4);
-        mma_ss(d, qd + at, kd + at, id, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          // 16 columns: 32 bytes inside a 128-byte swizzle row, every 4 the next box
+          const uint64_t at = (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4);
+          mma_ss(d, qd + at, kd + at, id, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&sy->s_full[sb.slot]);  // also frees the K slot
+        if (s + 1 == u.n) mma_commit(&sy->q_empty[q.slot]);
       }
-      mma_commit(&sy->s_full[sb.slot]);  // also frees the K slot
+      __syncwarp();
       sb.next();
+      ks.next();
     }
-    ++kq;
+    q.next();
   }
-  mma_commit(&sy->drain);  // never exit with MMAs in flight
+  if (elect_one()) mma_commit(&sy->drain);
+  __syncwarp();  // never exit with MMAs in flight
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
-// Warp 2, lane 0: O += P V once the softmax warps have written the step's P.
+// Warp 2: O += P V once the softmax warps have written the step's P.
 template <int D>
 __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
                      volatile int *abort) {
@@ -283,31 +301,43 @@ __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
   Ring<C::kVBufs> vs;
   uint32_t kq = 0;
   bool ok = true;
-  for (uint32_t i = blockIdx.x; i < P.units && ok && !*abort; i += gridDim.x) {
+  for (uint32_t i = blockIdx.x; i < P.units && ok; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
     // the previous unit's O must have been read before the first PV overwrites it
-    if (kq > 0) ok = mbar_wait_small(&sy->o_free, (kq - 1) & 1u, abort, P.status, kDevTimeout);
+    if (kq > 0) ok = x_wait(&sy->o_free, (kq - 1) & 1u, abort, P.status);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = mbar_wait_small(&sy->p_full[sb.slot], sb.phase, abort, P.status, kDevTimeout) &&
-           mbar_wait_small(&sy->v_full[vs.slot], vs.phase, abort, P.status, kDevTimeout);
+      ok = x_wait(&sy->v_full[vs.slot], vs.phase, abort, P.status) &&
+           x_wait(&sy->p_full[sb.slot], sb.phase, abort, P.status);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = v_desc + (uint64_t)((vs.slot * C::kTileBytes) >> 4);
       const uint32_t a = tmem + C::kSCol + sb.slot * 128;
       const int k16 = x_k16(u, u.t0 + s);
+      if (elect_one()) {
+        // 16 states a MMA: 8 columns of P, the right half's from 64; all eight without a
+        // branch between them but in a batch's last tile
+        if (k16 == 8) {
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // 16 states: 8 columns of P; the right half's from column 64
-        if (kk < k16)
-          mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8, vd + (uint64_t)((kk * 16 * 128) >> 4),
-                 id, (s > 0 || kk > 0) ? 1u : 0u);
-      mma_commit(&sy->pv_done[sb.slot]);  // frees the score buffer and the V slot
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
+                   vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
+        } else {
+#pragma unroll 1
+          for (int kk = 0; kk < k16; ++kk)
+            mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
+                   vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
+        }
+        mma_commit(&sy->pv_done[sb.slot]);  // frees the score buffer and the V slot
+      }
+      __syncwarp();
       sb.next();
       vs.next();
     }
     ++kq;
   }
-  mma_commit(&sy->drain);
+  if (elect_one()) mma_commit(&sy->drain);
+  __syncwarp();
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
@@ -336,15 +366,18 @@ __device__ __forceinline__ void x_exp(const uint32_t (&r)[32], uint64_t sc2, uin
   }
 }
 
-// 32 scores from TMEM; those from column `valid` on (past the batch's states) as -inf,
-// whatever was computed there.
-__device__ __forceinline__ void x_scores(uint32_t ta, int valid, uint32_t (&r)[32]) {
-  tmem_ld32(ta, r);
-  tmem_wait_ld();
-  reg_fence(r);
-  if (valid < 32) {
+// Scores from column `valid` on (past the batch's states) as -inf, whatever was computed
+// there.
+__device__ __forceinline__ void x_mask(int valid, uint32_t (&r)[32]) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) r[i] = i < valid ? r[i] : 0xff800000u;
+  for (int i = 0; i < 32; ++i) r[i] = i < valid ? r[i] : 0xff800000u;
+}
+
+__device__ __forceinline__ void x_max(const uint32_t (&r)[32], float &a0, float &a1) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    a0 = max3(a0, __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+    a1 = max3(a1, __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
   }
 }
 
@@ -390,17 +423,19 @@ __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t t
                                                         P.status, kDevTimeout));
       tc_fence_after();
       const uint32_t own = at + C::kSCol + sb.slot * 128 + grp * 64;
-      uint32_t r[32];
-      float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll 1
-      for (int x = 0; x < 64 && x < mine; x += 32) {
-        x_scores(own + x, mine - x, r);
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          a0 = max3(a0, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-          a1 = max3(a1, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
-        }
+      uint32_t r0[32], r1[32];
+      tmem_ld32(own, r0);
+      tmem_ld32(own + 32, r1);
+      tmem_wait_ld();
+      reg_fence(r0);
+      reg_fence(r1);
+      if (mine < 64) {
+        x_mask(mine, r0);
+        x_mask(mine - 32, r1);
       }
+      float a0 = -INFINITY, a1 = -INFINITY;
+      x_max(r0, a0, a1);
+      x_max(r1, a0, a1);
       const float mm = fmaxf(a0, a1) * sl2;
       if (g > 0) x_read_wait(q4, grp);
       xx[grp * 128 + row] = mm;
@@ -437,14 +472,11 @@ __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t t
       }
       const uint64_t sc2 = f2(sl2, sl2), nm2 = f2(-m_run, -m_run);
       uint64_t acc0 = f2(0.f, 0.f), acc1 = acc0;
-      // P of columns 0 .. 31 lies over scores 0 .. 15, of 32 .. 63 over 16 .. 31: read before
-#pragma unroll 1
-      for (int x = 0; x < 64 && x < mine; x += 32) {
-        uint32_t pk[16];
-        x_scores(own + x, mine - x, r);
-        x_exp(r, sc2, nm2, acc0, acc1, pk);
-        tmem_st16(own + (x >> 1), pk);
-      }
+      uint32_t pk[16];
+      x_exp(r0, sc2, nm2, acc0, acc1, pk);
+      tmem_st16(own, pk);
+      x_exp(r1, sc2, nm2, acc0, acc1, pk);
+      tmem_st16(own + 16, pk);
       float s0, s1, s2, s3;
       unf2(acc0, s0, s1);
       unf2(acc1, s2, s3);
@@ -477,6 +509,7 @@ __device__ void x_output(const XParams &P, const CUtensorMap *mo, uint8_t *smem,
   const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16);
   const float *xl = reinterpret_cast<const float *>(smem + C::kOffL);
   const float *xm = reinterpret_cast<const float *>(smem + C::kOffM);
+  uint8_t *tile = smem + C::kOffO;
   const int tok = r64 / P.G, head = r64 - tok * P.G;  // of this row, in its subtile
   uint32_t gs = 0, kq = 0;  // steps and units (with states) so far
   bool live = true;         // false after a wait gave up: keep meeting the barrier, do no work
@@ -488,18 +521,22 @@ __device__ void x_output(const XParams &P, const CUtensorMap *mo, uint8_t *smem,
     float l = 0.f, m = 0.f;
     if (u.n > 0) {
       const uint32_t gl = gs + u.n - 1;
-      live = __all_sync(0xffffffffu,
-                        live && mbar_wait_small(&sy->l_full, kq & 1u, abort, P.status, kDevTimeout));
+      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->l_full, kq & 1u, abort,
+                                                              P.status, kDevTimeout));
       l = xl[row] + xl[128 + row];
       m = xm[row];
       x_arrive(&sy->l_empty, lane);
-      live = __all_sync(0xffffffffu,
-                        live && mbar_wait_small(&sy->pv_done[gl % C::kSBufs], (gl / C::kSBufs) & 1u,
-                                          abort, P.status, kDevTimeout));
+      // the last unit's store has read the tile (long ago)
+      if (q4 == 0 && lane == 0) bulk_wait_read();
+      x_out_sync();
+      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->pv_done[gl % C::kSBufs],
+                                                              (gl / C::kSBufs) & 1u, abort,
+                                                              P.status, kDevTimeout));
       tc_fence_after();
+      gs += u.n;
+      ++kq;
     }
     const float inv = l > 0.f ? 1.0f / l : l;  // 0 for no states; NaN stays
-    uint8_t *tile = smem + C::kOffQ + (kq & 1u) * C::kTileBytes;
     float *run = P.po + ((size_t)u.sp * P.B * P.h * P.Sq + lrow) * D;
     if (u.n > 0) {
 #pragma unroll 1
@@ -537,26 +574,20 @@ __device__ void x_output(const XParams &P, const CUtensorMap *mo, uint8_t *smem,
       }
       fence_async_smem();
       x_out_sync();
-      if (q4 == 0 && lane == 0) {
-        if (live && P.nsplit == 1) {
+      if (q4 == 0 && lane == 0 && live && P.nsplit == 1) {
 #pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            const int t0 = (u.qt * 2 + side) * P.tq;
-            if (t0 >= P.Sq) break;
+        for (int side = 0; side < 2; ++side) {
+          const int t0 = (u.qt * 2 + side) * P.tq;
+          if (t0 >= P.Sq) break;
 #pragma unroll
-            for (int x = 0; x < C::kBoxes; ++x)
-              tma_store_4d(mo, tile + x * C::kBox + side * 64 * 128, x * 64, u.j * P.G, t0, u.b);
-          }
-          bulk_commit();
-          bulk_wait_read();
+          for (int x = 0; x < C::kBoxes; ++x)
+            tma_store_4d(mo, tile + x * C::kBox + side * 64 * 128, x * 64, u.j * P.G, t0, u.b);
         }
-        mbar_arrive(&sy->q_empty[kq & 1u]);  // the loader may have the tile back
+        bulk_commit();
       }
-      gs += u.n;
-      ++kq;
     } else if (P.nsplit == 1 && row_ok) {  // o = 0 (joining runs leaves one without states out)
       uint4 *dst = reinterpret_cast<uint4 *>(P.o + (((size_t)u.b * P.Sq + token) * P.h + hh) * D);
-#pragma unroll
+#pragma unroll 1
       for (int e = 0; e < D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
     }
     if (row_ok && live) {
@@ -591,11 +622,11 @@ __global__ void __launch_bounds__(512, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sy->q_full[i], 1);
       mbar_init(&sy->q_empty[i], 1);
+      mbar_init(&sy->k_full[i], 1);
       mbar_init(&sy->v_full[i], 1);
     }
     mbar_init(&sy->v_raw, 1);
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&sy->k_full[i], 1);
       mbar_init(&sy->s_full[i], 1);
       mbar_init(&sy->p_full[i], 8);  // softmax warps
       mbar_init(&sy->pv_done[i], 1);
@@ -630,9 +661,9 @@ __global__ void __launch_bounds__(512, 1)
     if (warp == 0) {
       if (lane == 0) x_load_qk<D>(P, &mq, &mk, smem, sy, abort);
     } else if (warp == 1) {
-      if (lane == 0) x_qk<D>(P, smem, sy, tmem, abort);
+      x_qk<D>(P, smem, sy, tmem, abort);
     } else if (warp == 2) {
-      if (lane == 0) x_pv<D>(P, smem, sy, tmem, abort);
+      x_pv<D>(P, smem, sy, tmem, abort);
     } else {
       x_load_v<D>(P, &mv, smem, sy, abort);
     }
