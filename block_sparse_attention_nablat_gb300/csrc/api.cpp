@@ -504,6 +504,61 @@ nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, cons
   return from_cuda(dt == NABLA_BF16 ? launch_cross_attn_tc(a, st) : launch_cross_attn_simt(a, st));
 }
 
+size_t nabla_cross_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                            int D) {
+  const nabla::CrossShape s{B, Sq, Sk, h, hk, D};
+  if (!nabla::valid_dtype(dt) || !nabla::valid_cross_shape(s)) return 0;
+  return nabla::cross_bwd_workspace(s);
+}
+
+nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
+                                  const nabla_strides *k_st, const void *v,
+                                  const nabla_strides *v_st, const void *o, const float *lse,
+                                  const void *dout, nabla_dtype dt, int B, int Sq, int Sk, int h,
+                                  int hk, int D, const int32_t *kv_len, float scale, void *dq,
+                                  void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                  nabla_stream_t stream) {
+  using namespace nabla;
+  CrossArgs a{};
+  a.s = CrossShape{B, Sq, Sk, h, hk, D};
+  if (!valid_dtype(dt) || !valid_cross_shape(a.s)) return NABLA_ERR_INVALID_ARG;
+  const size_t esz = dt == NABLA_BF16 ? 2 : 4;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.kv_len = kv_len;
+  a.scale = scale;
+  CrossRows r;
+  if (!valid_cross_inputs(a, q_st, k_st, v_st, esz, r)) return NABLA_ERR_INVALID_ARG;
+  if (!o || !lse || !dout || !dq || !dk || !dv || !workspace) return NABLA_ERR_INVALID_ARG;
+  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(dout, 16) || !aligned(workspace, 256))
+    return NABLA_ERR_INVALID_ARG;
+  const uintptr_t rows = (uintptr_t)B * Sq * h, qn = rows * D * esz;
+  const uintptr_t kn = (uintptr_t)B * Sk * hk * D * esz;
+  void *const out[3] = {dq, dk, dv};
+  const uintptr_t on[3] = {qn, kn, kn};
+  for (int i = 0; i < 3; ++i) {
+    if (!aligned(out[i], 16) || meets_inputs(out[i], on[i], a, r) ||
+        ranges_meet(out[i], on[i], o, qn) || ranges_meet(out[i], on[i], dout, qn) ||
+        ranges_meet(out[i], on[i], lse, rows * 4))
+      return NABLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (ranges_meet(out[i], on[i], out[j], on[j])) return NABLA_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < cross_bwd_workspace(a.s)) return NABLA_ERR_INVALID_ARG;
+  a.of = o;
+  a.lse = const_cast<float *>(lse);
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.workspace = workspace;
+  cudaError_t e;
+  a.status = device_status_ptr(&e);
+  if (!a.status) return NABLA_ERR_CUDA;
+  return from_cuda(launch_cross_bwd(a, dt, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 nabla_status nabla_selftest_bounded_wait(nabla_stream_t stream) {
   return nabla::from_cuda(nabla::launch_bounded_wait_probe(reinterpret_cast<cudaStream_t>(stream)));
 }

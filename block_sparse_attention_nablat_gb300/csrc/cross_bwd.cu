@@ -1,0 +1,188 @@
+// The parts of the cross attention backward around its products: the rows' lse and delta
+// in packed order (before), and the sum of the dK / dV runs (after).
+#include <cuda_bf16.h>
+
+#include "cross_common.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+
+namespace nabla {
+namespace {
+
+__device__ __forceinline__ float dot8(const float *a, const float *b) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 4) {
+    const float4 x = *reinterpret_cast<const float4 *>(a + i);
+    const float4 y = *reinterpret_cast<const float4 *>(b + i);
+    s = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, s))));
+  }
+  return s;
+}
+__device__ __forceinline__ float dot8(const __nv_bfloat16 *a, const __nv_bfloat16 *b) {
+  const uint4 x = *reinterpret_cast<const uint4 *>(a), y = *reinterpret_cast<const uint4 *>(b);
+  const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), s);
+    s = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), s);
+  }
+  return s;
+}
+
+// -lse and -delta = -<dout, o> of the packed rows [B, hk, nsub, 64]: -inf and 0 where a
+// row is none or has no states, so that its P is 0.  D / 8 lanes a row, 16 bytes a lane;
+// HBM-bound (o and dout read once).
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+    cross_prep_kernel(const T *__restrict__ o, const T *__restrict__ dout,
+                      const float *__restrict__ lse, int Sq, int h, int hk, int G, int tq,
+                      int nsub, long rows, float *__restrict__ nlse, float *__restrict__ ndelta) {
+  constexpr int kLanes = D / 8;
+  const int lane = threadIdx.x % kLanes;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long row = ((long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  if (row >= rows) return;  // a whole group of kLanes lanes
+  const int r = (int)(row & 63);
+  const long sb = row >> 6;
+  const long bj = sb / nsub;
+  const int sub = (int)(sb - bj * nsub);
+  const int b = (int)(bj / hk), j = (int)(bj - (long)b * hk);
+  const int t = r / G, token = sub * tq + t, hh = j * G + r - t * G;
+  const bool ok = t < tq && token < Sq;
+  float s = 0.f, l = -INFINITY;
+  if (ok) {
+    const size_t at = (((size_t)b * Sq + token) * h + hh) * D + lane * 8;
+    s = dot8(dout + at, o + at);
+    l = lse[((size_t)b * h + hh) * Sq + token];
+  }
+  const unsigned mask = kLanes == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+#pragma unroll
+  for (int x = kLanes / 2; x; x >>= 1) s += __shfl_xor_sync(mask, s, x);
+  if (lane == 0) {
+    nlse[row] = l == -INFINITY ? -INFINITY : -l;
+    ndelta[row] = -s;
+  }
+}
+
+// dK and dV: the runs' fp32 sums added up in order and rounded; 0 past the length (where
+// no run wrote anything).
+template <typename T>
+__global__ void __launch_bounds__(256)
+    cross_dkv_join_kernel(const float *__restrict__ part, int nsplit, int Sk, int row, long n4,
+                          const int32_t *kv_len, T *dk, T *dv) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;  // four columns of dK, then of dV
+  if (i >= 2 * n4) return;
+  const bool v = i >= n4;
+  const long e = (v ? i - n4 : i) * 4, state = e / row;
+  const long b = state / Sk;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (state - b * Sk < cross::batch_len(kv_len, (int)b, Sk)) {
+    for (int k = 0; k < nsplit; ++k) {
+      const float4 p =
+          *reinterpret_cast<const float4 *>(part + ((size_t)k * 2 + v) * (size_t)n4 * 4 + e);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+  }
+  T *o = (v ? dv : dk) + e;
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+    *reinterpret_cast<uint2 *>(o) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                                               *reinterpret_cast<const uint32_t *>(&hi));
+  } else {
+    *reinterpret_cast<float4 *>(o) = s;
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_prep(const CrossArgs &a, const cross::Packing &pk, int nsub, float *nlse,
+                        float *ndelta, cudaStream_t st) {
+  const long rows = (long)a.s.B * a.s.hk * nsub * 64;
+  const long blocks = (rows * (D / 8) + 255) / 256;
+  return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)blocks), dim3(256), 0, st,
+                    static_cast<const T *>(a.of), static_cast<const T *>(a.dout),
+                    (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub, rows, nlse,
+                    ndelta);
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct BwdLayout {
+  int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
+  size_t nlse, ndelta, part, total;
+};
+BwdLayout bwd_layout(const CrossShape &s) {
+  BwdLayout w;
+  w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
+  const size_t rows = round_up((size_t)s.B * s.hk * w.nsub * 64 * sizeof(float));
+  const int n = cross_dkv_splits(s);
+  w.nlse = 0;
+  w.ndelta = rows;
+  w.part = 2 * rows;
+  w.total = w.part + (n > 1 ? round_up((size_t)n * 2 * s.B * s.Sk * s.hk * s.D * sizeof(float))
+                            : 0);
+  return w;
+}
+
+}  // namespace
+
+cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const float *part,
+                                  int nsplit, cudaStream_t st) {
+  const long n4 = (long)a.s.B * a.s.Sk * a.s.hk * a.s.D / 4;
+  const dim3 grid((unsigned)((2 * n4 + 255) / 256));
+  if (dt == NABLA_BF16)
+    return launch_pdl(cross_dkv_join_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, part, nsplit,
+                      a.s.Sk, a.s.hk * a.s.D, n4, a.kv_len, static_cast<__nv_bfloat16 *>(a.dk),
+                      static_cast<__nv_bfloat16 *>(a.dv));
+  return launch_pdl(cross_dkv_join_kernel<float>, grid, dim3(256), 0, st, part, nsplit, a.s.Sk,
+                    a.s.hk * a.s.D, n4, a.kv_len, static_cast<float *>(a.dk),
+                    static_cast<float *>(a.dv));
+}
+
+// Runs of query tiles the dK / dV units are split into.  Cost in steps (a 128 x 128 tile,
+// about a microsecond): the waves of units over GB300's 152 SMs times a unit's steps (two
+// more to start and end it), and the runs' sums written and read back (a step's time moves
+// about 6 MB).
+int cross_dkv_splits(const CrossShape &s) {
+  const long units = (long)s.B * s.hk * ((s.Sk + cross::kTile - 1) / cross::kTile);
+  const int nq = (cross::packing(s).nsub + 1) / 2;
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= nq && n <= 64; ++n) {
+    const double waves = (double)((units * n + 151) / 152);
+    double cost = waves * ((nq + n - 1) / n + 2);
+    if (n > 1) cost += 2.0 + (double)units * n * cross::kTile * s.D * 2 * 4 * 2 / 6.0e6;
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+size_t cross_bwd_workspace(const CrossShape &s) { return bwd_layout(s).total; }
+
+cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st) {
+  const BwdLayout w = bwd_layout(a.s);
+  char *ws = static_cast<char *>(a.workspace);
+  float *nlse = reinterpret_cast<float *>(ws + w.nlse);
+  float *ndelta = reinterpret_cast<float *>(ws + w.ndelta);
+  float *part = reinterpret_cast<float *>(ws + w.part);
+  const cross::Packing pk = cross::packing(a.s);
+  cudaError_t e;
+  if (dt == NABLA_BF16)
+    e = a.s.D == 64 ? launch_prep<__nv_bfloat16, 64>(a, pk, w.nsub, nlse, ndelta, st)
+                    : launch_prep<__nv_bfloat16, 128>(a, pk, w.nsub, nlse, ndelta, st);
+  else
+    e = a.s.D == 64 ? launch_prep<float, 64>(a, pk, w.nsub, nlse, ndelta, st)
+                    : launch_prep<float, 128>(a, pk, w.nsub, nlse, ndelta, st);
+  if (e != cudaSuccess) return e;
+  return dt == NABLA_BF16 ? launch_cross_bwd_tc(a, nlse, ndelta, part, st)
+                          : launch_cross_bwd_simt(a, nlse, ndelta, part, w.nsub, st);
+}
+
+}  // namespace nabla

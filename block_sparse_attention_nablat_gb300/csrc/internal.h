@@ -120,7 +120,7 @@ struct CrossArgs {
   const int32_t *kv_len;  // [B] or null
   float scale;
   void *o;     // forward: [B, Sq, h, D]
-  float *lse;  // [B, h, Sq]; forward: or null
+  float *lse;  // [B, h, Sq]; written by the forward (or null), read by the backward
   const void *of, *dout;  // backward: the forward's o, the upstream gradient
   void *dq, *dk, *dv;
   void *workspace;
@@ -132,6 +132,18 @@ size_t cross_fwd_workspace(const CrossShape &s, nabla_dtype dt);
 // K9: bf16, tcgen05.  K9f: fp32, CUDA cores.
 cudaError_t launch_cross_attn_tc(const CrossArgs &a, cudaStream_t st);
 cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st);
+// K10: the backward (prep, products, join).  Workspace: -lse and -delta of the packed
+// rows, then the runs' sums of dK and dV where these are split (cross_dkv_splits).
+int cross_dkv_splits(const CrossShape &s);
+size_t cross_bwd_workspace(const CrossShape &s);
+cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st);
+// Its parts: the products in bf16 (tcgen05) and fp32 (CUDA cores), each with the join.
+cudaError_t launch_cross_bwd_tc(const CrossArgs &a, const float *nlse, const float *ndelta,
+                                float *part, cudaStream_t st);
+cudaError_t launch_cross_bwd_simt(const CrossArgs &a, const float *nlse, const float *ndelta,
+                                  float *part, int nsub, cudaStream_t st);
+cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const float *part,
+                                  int nsplit, cudaStream_t st);
 
 size_t qk_norm_bwd_workspace(int D);
 cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);

@@ -90,6 +90,11 @@ def load() -> ctypes.CDLL:
     lib.nabla_cross_attn_fwd_workspace_bytes.argtypes = xs
     lib.nabla_cross_attn_fwd.restype = i32
     lib.nabla_cross_attn_fwd.argtypes = [vp, st, vp, st, vp, st] + xs + [vp, f32, vp, vp, vp, sz, vp]
+    lib.nabla_cross_attn_bwd_workspace_bytes.restype = sz
+    lib.nabla_cross_attn_bwd_workspace_bytes.argtypes = xs
+    lib.nabla_cross_attn_bwd.restype = i32
+    lib.nabla_cross_attn_bwd.argtypes = ([vp, st, vp, st, vp, st, vp, vp, vp] + xs +
+                                         [vp, f32, vp, vp, vp, vp, sz, vp])
     lib.nabla_selftest_bounded_wait.restype = i32
     lib.nabla_selftest_bounded_wait.argtypes = [vp]
     lib.nabla_get_last_device_status.restype = i32
@@ -613,6 +618,52 @@ def nabla_cross_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
                           device=q.device)
     return _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream), lse
+
+
+def nabla_cross_attn_bwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk: int, h: int,
+                                         hk: int, D: int) -> int:
+    code = NABLA_BF16 if dtype == torch.bfloat16 else NABLA_F32
+    return load().nabla_cross_attn_bwd_workspace_bytes(code, B, Sq, Sk, h, hk, D)
+
+
+def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                         lse: torch.Tensor, dout: torch.Tensor,
+                         kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                         dv: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of nabla_cross_attn_fwd, from its inputs, the o and lse of
+    nabla_cross_attn_fwd_lse and the upstream gradient dout of o: returns dq [B,Sq,h,D] and
+    dk, dv [B,Sk,hk,D] (0 for states past kv_len)."""
+    strides, sizes = _cross_args(q, k, v, kv_len)
+    dev = q.device
+    for name, t in (("o", o), ("dout", dout)):
+        if t.shape != q.shape:
+            raise ValueError(f"{name} must be {tuple(q.shape)}, got {tuple(t.shape)}")
+        _buf(t, name, q.numel(), q.dtype, dev)
+    _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(sizes[-1])
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    if dv is None:
+        dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    for name, t, n in (("dq", dq, q.numel()), ("dk", dk, k.numel()), ("dv", dv, k.numel())):
+        _buf(t, name, n, q.dtype, dev)
+    lib = load()
+    if workspace is None:
+        need = lib.nabla_cross_attn_bwd_workspace_bytes(*sizes)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _on(workspace, "workspace", dev)
+    _cuda(q)
+    st = _call(dev, lib.nabla_cross_attn_bwd, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
+               strides[2], _ptr(o), _ptr(lse), _ptr(dout), *sizes, _ptr(kv_len), float(scale),
+               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+               workspace.numel() * workspace.element_size(), _stream(stream, dev))
+    _check(st, "nabla_cross_attn_bwd")
+    return dq, dk, dv
 
 
 def _stream_device(stream) -> torch.device:

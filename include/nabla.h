@@ -445,6 +445,37 @@ nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, cons
                                   nabla_stream_t stream);
 
 /*
+ * nabla_cross_attn_bwd -- gradients of nabla_cross_attn_fwd with respect to q, k and v.
+ * With P the softmax weights (rebuilt from lse), and the upstream gradient dout:
+ *   delta_s = <dout_s, o_s>,   dz_su = P_su (<dout_s, v_u> - delta_s),
+ *   dq_s = scale sum_u dz_su k_u,   dk_u = scale sum_s dz_su q_s,   dv_u = sum_s P_su dout_s,
+ * the sums over s running over the tokens of all the heads that share the key head.  A
+ * batch without states gets dq = 0; states from kv_len[b] on get dk = dv = 0, whatever k
+ * and v hold there.  delta is formed from the o passed in, which must be the forward's.
+ * bf16: the products run on tcgen05 with fp32 accumulators, P and dz enter them as bf16;
+ * f32: fp32 arithmetic on CUDA cores.  No atomics: repeated calls give the same bits.
+ *
+ *   q, k, v, kv_len, scale  as given to nabla_cross_attn_fwd.
+ *   o, dout     [B, Sq, h, D] device, dense, element type dt.
+ *   lse         [B, h, Sq] device fp32, 4-byte aligned, from nabla_cross_attn_fwd.
+ *   dq          [B, Sq, h, D], dk and dv [B, Sk, hk, D] device, dense, element type dt,
+ *               overwritten; they overlap no other argument.
+ *   workspace   device scratch of ws_bytes >= nabla_cross_attn_bwd_workspace_bytes()
+ *               (256-byte aligned).
+ * o, dout, dq, dk and dv are 16-byte aligned.  Everything else, and the errors, as for
+ * nabla_cross_attn_fwd.
+ */
+size_t nabla_cross_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                            int D);
+nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
+                                  const nabla_strides *k_st, const void *v,
+                                  const nabla_strides *v_st, const void *o, const float *lse,
+                                  const void *dout, nabla_dtype dt, int B, int Sq, int Sk, int h,
+                                  int hk, int D, const int32_t *kv_len, float scale, void *dq,
+                                  void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                  nabla_stream_t stream);
+
+/*
  * Diagnostic of the failure-detection path (no counterpart on the pages):
  * enqueues one CTA that waits on an mbarrier nothing ever arrives on, through
  * the same bounded wait the attention kernel uses, with a 20 ms limit.  The
