@@ -2,6 +2,7 @@
 // The operations and their sources are documented in include/nabla.h.
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "internal.h"
 
@@ -40,25 +41,37 @@ struct Rows {
 };
 
 Rows rows_of(const void *p, const nabla_strides *st, int B, int S, int h, int D) {
-  Rows r{p, {(int64_t)S * h * D, (int64_t)h * D}, h};
+  Rows r{p, {(int64_t)S * h * D, (int64_t)h * D, D}, h};
   if (st) {
     if (B > 1) r.st.batch = st->batch;
     if (S > 1) r.st.token = st->token;
+    if (h > 1) r.st.head = st->head;
   }
   return r;
 }
 
 bool valid_rows(const Rows &r, int B, int S, int D, size_t esz) {
   if (!r.p || !aligned(r.p, 16)) return false;
-  const int64_t row = (int64_t)r.h * D, most = (int64_t)1 << 40;
-  if (r.st.token < row || r.st.token > most || r.st.batch > most) return false;
-  if (B > 1 && r.st.batch < (S - 1) * r.st.token + row) return false;
-  return r.st.token * esz % 16 == 0 && r.st.batch * esz % 16 == 0;
+  int64_t st[3] = {r.st.head, r.st.token, r.st.batch}, n[3] = {r.h, S, B};
+  for (int i = 0; i < 2; ++i)  // the smallest stride first
+    for (int j = 0; j < 2 - i; ++j)
+      if (st[j] > st[j + 1]) {
+        std::swap(st[j], st[j + 1]);
+        std::swap(n[j], n[j + 1]);
+      }
+  int64_t span = D;  // elements from the first to behind the last, dimension by dimension
+  for (int i = 0; i < 3; ++i) {
+    if (n[i] == 1) continue;
+    if (st[i] < span || st[i] > (int64_t)1 << 38 || st[i] * esz % 16 != 0) return false;
+    span += st[i] * (n[i] - 1);
+  }
+  return true;
 }
 
 // Bytes from the tensor's first element to behind its last.
 uintptr_t extent(const Rows &r, int B, int S, int D, size_t esz) {
-  return (uintptr_t)((B - 1) * r.st.batch + (S - 1) * r.st.token + (int64_t)r.h * D) * esz;
+  return (uintptr_t)((B - 1) * r.st.batch + (S - 1) * r.st.token + (r.h - 1) * r.st.head + D) *
+         esz;
 }
 
 bool ranges_meet(const void *a, uintptr_t an, const void *b, uintptr_t bn) {
@@ -67,10 +80,11 @@ bool ranges_meet(const void *a, uintptr_t an, const void *b, uintptr_t bn) {
 }
 
 // Whether two written tensors share elements: they do not if their ranges are apart,
-// or if they are columns of one larger tensor (the same strides, batches a whole number
-// of tokens apart) that stay apart within the token.
+// or if they are columns of one larger tensor (heads together, the same strides, batches
+// a whole number of tokens apart) that stay apart within the token.
 bool rows_collide(const Rows &a, const Rows &b, int B, int S, int D, size_t esz) {
   if (!ranges_meet(a.p, extent(a, B, S, D, esz), b.p, extent(b, B, S, D, esz))) return false;
+  if ((a.h > 1 && a.st.head != D) || (b.h > 1 && b.st.head != D)) return true;
   if (S > 1 && a.st.token != b.st.token) return true;
   if (B > 1 && a.st.batch != b.st.batch) return true;
   const int64_t pitch = S > 1 ? a.st.token : a.st.batch;
@@ -513,10 +527,11 @@ size_t nabla_cross_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int S
 
 nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
                                   const nabla_strides *k_st, const void *v,
-                                  const nabla_strides *v_st, const void *o, const float *lse,
-                                  const void *dout, nabla_dtype dt, int B, int Sq, int Sk, int h,
-                                  int hk, int D, const int32_t *kv_len, float scale, void *dq,
-                                  void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                  const nabla_strides *v_st, const void *o,
+                                  const nabla_strides *o_st, const float *lse, const void *dout,
+                                  const nabla_strides *dout_st, nabla_dtype dt, int B, int Sq,
+                                  int Sk, int h, int hk, int D, const int32_t *kv_len, float scale,
+                                  void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes,
                                   nabla_stream_t stream) {
   using namespace nabla;
   CrossArgs a{};
@@ -530,16 +545,21 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
   a.scale = scale;
   CrossRows r;
   if (!valid_cross_inputs(a, q_st, k_st, v_st, esz, r)) return NABLA_ERR_INVALID_ARG;
-  if (!o || !lse || !dout || !dq || !dk || !dv || !workspace) return NABLA_ERR_INVALID_ARG;
-  if (!aligned(o, 16) || !aligned(lse, 4) || !aligned(dout, 16) || !aligned(workspace, 256))
+  if (!lse || !dq || !dk || !dv || !workspace) return NABLA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(workspace, 256)) return NABLA_ERR_INVALID_ARG;
+  const Rows ro = rows_of(o, o_st, B, Sq, h, D), rg = rows_of(dout, dout_st, B, Sq, h, D);
+  if (!valid_rows(ro, B, Sq, D, esz) || !valid_rows(rg, B, Sq, D, esz))
     return NABLA_ERR_INVALID_ARG;
+  a.o_st = ro.st;
+  a.dout_st = rg.st;
   const uintptr_t rows = (uintptr_t)B * Sq * h, qn = rows * D * esz;
   const uintptr_t kn = (uintptr_t)B * Sk * hk * D * esz;
   void *const out[3] = {dq, dk, dv};
   const uintptr_t on[3] = {qn, kn, kn};
   for (int i = 0; i < 3; ++i) {
     if (!aligned(out[i], 16) || meets_inputs(out[i], on[i], a, r) ||
-        ranges_meet(out[i], on[i], o, qn) || ranges_meet(out[i], on[i], dout, qn) ||
+        ranges_meet(out[i], on[i], o, extent(ro, B, Sq, D, esz)) ||
+        ranges_meet(out[i], on[i], dout, extent(rg, B, Sq, D, esz)) ||
         ranges_meet(out[i], on[i], lse, rows * 4))
       return NABLA_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)

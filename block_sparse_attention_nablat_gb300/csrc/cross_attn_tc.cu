@@ -756,7 +756,7 @@ cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   auto enc = tensor_map_encoder(&err);
   if (!enc) return err;
   const cross::Packing pk = cross::packing(s);
-  const nabla_strides o_st{(int64_t)s.Sq * s.h * D, (int64_t)s.h * D};
+  const nabla_strides o_st{(int64_t)s.Sq * s.h * D, (int64_t)s.h * D, D};
   CUtensorMap mq, mk, mv, mo;
   if (!cross::cross_map(enc, &mq, a.q, s.B, s.Sq, s.h, D, a.q_st, pk.G, pk.tq) ||
       !cross::cross_map(enc, &mk, a.k, s.B, s.Sk, s.hk, D, a.k_st, 1, kTile) ||

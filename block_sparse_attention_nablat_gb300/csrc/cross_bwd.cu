@@ -36,7 +36,8 @@ __device__ __forceinline__ float dot8(const __nv_bfloat16 *a, const __nv_bfloat1
 // HBM-bound (o and dout read once).
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-    cross_prep_kernel(const T *__restrict__ o, const T *__restrict__ dout,
+    cross_prep_kernel(const T *__restrict__ o, const nabla_strides o_st,
+                      const T *__restrict__ dout, const nabla_strides g_st,
                       const float *__restrict__ lse, int Sq, int h, int hk, int G, int tq,
                       int nsub, long rows, float *__restrict__ nlse, float *__restrict__ ndelta) {
   constexpr int kLanes = D / 8;
@@ -54,8 +55,8 @@ __global__ void __launch_bounds__(256)
   const bool ok = t < tq && token < Sq;
   float s = 0.f, l = -INFINITY;
   if (ok) {
-    const size_t at = (((size_t)b * Sq + token) * h + hh) * D + lane * 8;
-    s = dot8(dout + at, o + at);
+    s = dot8(dout + b * g_st.batch + token * g_st.token + hh * g_st.head + lane * 8,
+             o + b * o_st.batch + token * o_st.token + hh * o_st.head + lane * 8);
     l = lse[((size_t)b * h + hh) * Sq + token];
   }
   const unsigned mask = kLanes == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
@@ -104,7 +105,7 @@ cudaError_t launch_prep(const CrossArgs &a, const cross::Packing &pk, int nsub, 
   const long rows = (long)a.s.B * a.s.hk * nsub * 64;
   const long blocks = (rows * (D / 8) + 255) / 256;
   return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)blocks), dim3(256), 0, st,
-                    static_cast<const T *>(a.of), static_cast<const T *>(a.dout),
+                    static_cast<const T *>(a.of), a.o_st, static_cast<const T *>(a.dout), a.dout_st,
                     (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub, rows, nlse,
                     ndelta);
 }

@@ -44,9 +44,8 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   if (tid == 0) check_len(P.kv_len, b, P.Sk, P.status);
   const int len = batch_len(P.kv_len, b, P.Sk);
-  const nabla_strides g_st{(int64_t)P.Sq * P.h * D, (int64_t)P.h * D};
   load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, part * M);
-  load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), g_st}, P, b, j, sub, part * M);
+  load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, part * M);
   float nl[A], nd[A];
 #pragma unroll
   for (int a = 0; a < A; ++a) {
@@ -117,7 +116,6 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   const int len = batch_len(P.kv_len, b, P.Sk), k0 = kt * kCols;
   if (P.nsplit > 1 && k0 >= len) return;  // the join writes the zeros
-  const nabla_strides g_st{(int64_t)P.Sq * P.h * D, (int64_t)P.h * D};
   load_states<D>(Ks, static_cast<const float *>(P.k), P.k_st, b, j, k0, len);
   load_states<D>(Vs, static_cast<const float *>(P.v), P.v_st, b, j, k0, len);
   uint64_t dk[4][E][2], dv[4][E][2];
@@ -130,7 +128,7 @@ __global__ void __launch_bounds__(256)
   for (int sub = s0; sub < s1 && k0 < len; ++sub) {
     __syncthreads();
     load_rows<D, 64>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, 0);
-    load_rows<D, 64>(Gs, Side{static_cast<const float *>(P.dout), g_st}, P, b, j, sub, 0);
+    load_rows<D, 64>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, 0);
     if (tid < 128) ls[tid] = (tid < 64 ? P.lse : P.delta)[(bj * P.nsub + sub) * 64 + (tid & 63)];
     __syncthreads();
     float s[4][4], dp[4][4];  // rows: states ty + 16 a; columns: query rows tx + 16 c

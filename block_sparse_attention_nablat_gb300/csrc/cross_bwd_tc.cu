@@ -964,13 +964,13 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
   auto enc = tensor_map_encoder(&err);
   if (!enc) return err;
   const cross::Packing pk = cross::packing(s);
-  const nabla_strides o_st{(int64_t)s.Sq * s.h * D, (int64_t)s.h * D};
+  const nabla_strides dq_st{(int64_t)s.Sq * s.h * D, (int64_t)s.h * D, D};
   CUtensorMap mq, mk, mv, mg, mo;
   if (!cross::cross_map(enc, &mq, a.q, s.B, s.Sq, s.h, D, a.q_st, pk.G, pk.tq) ||
       !cross::cross_map(enc, &mk, a.k, s.B, s.Sk, s.hk, D, a.k_st, 1, kTile) ||
       !cross::cross_map(enc, &mv, a.v, s.B, s.Sk, s.hk, D, a.v_st, 1, kTile) ||
-      !cross::cross_map(enc, &mg, a.dout, s.B, s.Sq, s.h, D, o_st, pk.G, pk.tq) ||
-      !cross::cross_map(enc, &mo, a.dq, s.B, s.Sq, s.h, D, o_st, pk.G, pk.tq))
+      !cross::cross_map(enc, &mg, a.dout, s.B, s.Sq, s.h, D, a.dout_st, pk.G, pk.tq) ||
+      !cross::cross_map(enc, &mo, a.dq, s.B, s.Sq, s.h, D, dq_st, pk.G, pk.tq))
     return cudaErrorInvalidValue;
   int dev = 0, sms = 0;
   if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;

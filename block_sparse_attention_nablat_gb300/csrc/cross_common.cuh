@@ -47,7 +47,8 @@ inline bool cross_map(PFN_cuTensorMapEncodeTiled_v12000 enc, CUtensorMap *m, con
                       int B, int S, int heads, int D, const nabla_strides &st, int bh,
                       int tokens) {
   cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)S, (cuuint64_t)B};
-  cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)st.token * 2, (cuuint64_t)st.batch * 2};
+  cuuint64_t strides[3] = {(cuuint64_t)st.head * 2, (cuuint64_t)st.token * 2,
+                           (cuuint64_t)st.batch * 2};
   cuuint32_t box[4] = {64, (cuuint32_t)bh, (cuuint32_t)tokens, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dims, strides,

@@ -17,7 +17,7 @@ constexpr int kCols = 64;  // states per tile
 
 struct SimtParams {
   const void *q, *k, *v, *dout;
-  nabla_strides q_st, k_st, v_st;
+  nabla_strides q_st, k_st, v_st, dout_st;
   const float *lse, *delta;  // backward, packed rows [B, hk, nsub, 64]
   float *out, *out2;         // o; dq; dk and dv (or their parts)
   float *lse_out;
@@ -31,7 +31,7 @@ inline SimtParams simt_params(const CrossArgs &a) {
   SimtParams p{};
   const Packing pk = packing(a.s);
   p.q = a.q, p.k = a.k, p.v = a.v, p.dout = a.dout;
-  p.q_st = a.q_st, p.k_st = a.k_st, p.v_st = a.v_st;
+  p.q_st = a.q_st, p.k_st = a.k_st, p.v_st = a.v_st, p.dout_st = a.dout_st;
   p.kv_len = a.kv_len;
   p.B = a.s.B, p.Sq = a.s.Sq, p.Sk = a.s.Sk, p.h = a.s.h, p.hk = a.s.hk;
   p.G = pk.G, p.tq = pk.tq, p.nsub = pk.nsub, p.nsplit = 1;
@@ -70,7 +70,7 @@ __device__ __forceinline__ void load_rows(float *dst, const Side &x, const SimtP
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (w.ok)
       v = *reinterpret_cast<const float4 *>(x.p + b * x.st.batch + w.token * x.st.token +
-                                            (int64_t)w.head * D + c);
+                                            w.head * x.st.head + c);
     *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = v;
   }
 }
@@ -85,7 +85,7 @@ __device__ __forceinline__ void load_states(float *dst, const float *x, const na
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (k0 + r < len)
       v = *reinterpret_cast<const float4 *>(x + b * st.batch + (int64_t)(k0 + r) * st.token +
-                                            (int64_t)j * D + c);
+                                            j * st.head + c);
     *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = v;
   }
 }

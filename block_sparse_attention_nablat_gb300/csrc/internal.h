@@ -116,7 +116,7 @@ struct CrossShape {
 struct CrossArgs {
   CrossShape s;
   const void *q, *k, *v;
-  nabla_strides q_st, k_st, v_st;
+  nabla_strides q_st, k_st, v_st, o_st, dout_st;  // o_st, dout_st: backward
   const int32_t *kv_len;  // [B] or null
   float scale;
   void *o;     // forward: [B, Sq, h, D]

@@ -52,6 +52,36 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight columns as they lie in memory: rows on their way in take half the registers that
+// way in bf16, so more of them are under way.
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T *p, bool on) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    r.v[i] = on ? reinterpret_cast<const uint4 *>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw<float> &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.v[i].x), v[4 * i + 1] = __uint_as_float(r.v[i].y);
+    v[4 * i + 2] = __uint_as_float(r.v[i].z), v[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw<__nv_bfloat16> &r, float (&v)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
 // Weights of this lane's columns (1 where the caller gave none).
 __device__ __forceinline__ void load_weight(const void *w, nabla_dtype wdt, int col,
                                             float (&v)[8]) {
@@ -135,7 +165,7 @@ struct Side {  // q or k
   const void *x, *dz;
   void *out;  // z, or dx
   const void *w;
-  int64_t xb, xt, ob, ot, zb, zt;  // batch and token strides of x, out and dz (elements)
+  nabla_strides x_st, z_st, o_st;  // of x, dz and out
   int h, chunks;                   // heads, items per token
 };
 
@@ -178,8 +208,11 @@ __device__ __forceinline__ Item decode_item(const QkParams &P, long i) {
   return it;
 }
 
-template <typename T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) qk_norm_kernel(QkParams P) {
+// kDense: every tensor's heads lie D apart, so a row's place is an immediate offset from
+// the item's first (with strides in registers instead the backward took 336 us where it
+// takes 237, 480p).
+template <typename T, int D, bool kPairs, bool kDense>
+__global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant__ QkParams P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 4;
   const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
   pdl_launch_dependents();
@@ -188,36 +221,34 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(QkParams P) {
   for (long i = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < P.items; i += stride) {
     const Item it = decode_item(P, i);
     const Side &sd = P.side[it.side];
-    const T *x = static_cast<const T *>(sd.x) + it.b * sd.xb + it.s * sd.xt + col;
-    T *o = static_cast<T *>(sd.out) + it.b * sd.ob + it.s * sd.ot + col;
+    const int64_t xh = kDense ? D : sd.x_st.head, oh = kDense ? D : sd.o_st.head;
+    const T *x = static_cast<const T *>(sd.x) + it.b * sd.x_st.batch + it.s * sd.x_st.token +
+                 (it.h0 + sub) * xh + col;
+    T *o = static_cast<T *>(sd.out) + it.b * sd.o_st.batch + it.s * sd.o_st.token +
+           (it.h0 + sub) * oh + col;
     float w[8];
     load_weight(sd.w, P.wdt, col, w);
     const Turn t = load_turn<kPairs>(P.cos_t, P.sin_t, it.at, P.R, col, lane, it.turn);
     for (int hb = it.h0; hb < it.h1; hb += kRows * kAhead) {
-      float y[kAhead][8];
+      Raw<T> in[kAhead];
 #pragma unroll
-      for (int a = 0; a < kAhead; ++a) {
-        const int hh = hb + a * kRows + sub;
-        if (hh < it.h1) {
-          load8(x + (long)hh * D, y[a]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[a][j] = 0.f;
-        }
-      }
+      for (int a = 0; a < kAhead; ++a)
+        in[a] = load_raw(x + a * kRows * xh, hb + a * kRows + sub < it.h1);
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         if (hb + a * kRows >= it.h1) break;  // the same for the whole warp
-        float ss = 0.f;
+        float y[8], ss = 0.f;
+        unpack8(in[a], y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(y[a][j], y[a][j], ss);
+        for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
         const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[a][j] *= r * w[j];
-        turn8<kPairs, false>(y[a], t);
-        const int hh = hb + a * kRows + sub;
-        if (hh < it.h1) store8(o + (long)hh * D, y[a]);
+        for (int j = 0; j < 8; ++j) y[j] *= r * w[j];
+        turn8<kPairs, false>(y, t);
+        if (hb + a * kRows + sub < it.h1) store8(o + a * kRows * oh, y);
       }
+      x += kRows * kAhead * xh;
+      o += kRows * kAhead * oh;
     }
   }
 }
@@ -226,9 +257,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(QkParams P) {
 // in registers over all its items, the block joins its warps' sums in a fixed order
 // and writes one row per block, and qk_dw_kernel adds the rows.  Items are dealt out
 // by index alone, so dw is the same from run to run.
-template <typename T, int D, bool kPairs>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams P) {
-  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 2;
+template <typename T, int D, bool kPairs, bool kDense>
+__global__ void __launch_bounds__(kThreads)
+    qk_norm_bwd_kernel(const __grid_constant__ QkParams P) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = sizeof(T) == 2 ? 4 : 2;
   __shared__ float sums[kWarps][2 * D];
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
@@ -241,47 +273,52 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(QkParams P) {
   for (long i = (long)blockIdx.x * kWarps + warp; i < P.items; i += stride) {
     const Item it = decode_item(P, i);
     const Side &sd = P.side[it.side];
-    const T *x = static_cast<const T *>(sd.x) + it.b * sd.xb + it.s * sd.xt + col;
-    const T *dz = static_cast<const T *>(sd.dz) + it.b * sd.zb + it.s * sd.zt + col;
-    T *o = static_cast<T *>(sd.out) + it.b * sd.ob + it.s * sd.ot + col;
+    const int64_t xh = kDense ? D : sd.x_st.head, zh = kDense ? D : sd.z_st.head,
+                  oh = kDense ? D : sd.o_st.head;
+    const T *x = static_cast<const T *>(sd.x) + it.b * sd.x_st.batch + it.s * sd.x_st.token +
+                 (it.h0 + sub) * xh + col;
+    const T *dz = static_cast<const T *>(sd.dz) + it.b * sd.z_st.batch + it.s * sd.z_st.token +
+                  (it.h0 + sub) * zh + col;
+    T *o = static_cast<T *>(sd.out) + it.b * sd.o_st.batch + it.s * sd.o_st.token +
+           (it.h0 + sub) * oh + col;
     float w[8], part[8];
     load_weight(sd.w, P.wdt, col, w);
 #pragma unroll
     for (int j = 0; j < 8; ++j) part[j] = 0.f;
     const Turn t = load_turn<kPairs>(P.cos_t, P.sin_t, it.at, P.R, col, lane, it.turn);
     for (int hb = it.h0; hb < it.h1; hb += kRows * kAhead) {
-      float xv[kAhead][8], g[kAhead][8];
+      Raw<T> xin[kAhead], zin[kAhead];
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
-        const int hh = hb + a * kRows + sub;
-        if (hh < it.h1) {
-          load8(x + (long)hh * D, xv[a]);
-          load8(dz + (long)hh * D, g[a]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) xv[a][j] = g[a][j] = 0.f;
-        }
+        const bool on = hb + a * kRows + sub < it.h1;
+        xin[a] = load_raw(x + a * kRows * xh, on);
+        zin[a] = load_raw(dz + a * kRows * zh, on);
       }
 #pragma unroll
       for (int a = 0; a < kAhead; ++a) {
         if (hb + a * kRows >= it.h1) break;  // the same for the whole warp
-        turn8<kPairs, true>(g[a], t);        // dy
-        float ss = 0.f, dot = 0.f;
+        float xv[8], g[8], ss = 0.f, dot = 0.f;
+        unpack8(xin[a], xv);
+        unpack8(zin[a], g);
+        turn8<kPairs, true>(g, t);  // dy
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          ss = fmaf(xv[a][j], xv[a][j], ss);
-          dot = fmaf(g[a][j] * w[j], xv[a][j], dot);
+          ss = fmaf(xv[j], xv[j], ss);
+          dot = fmaf(g[j] * w[j], xv[j], dot);
         }
         const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
         const float m = row_sum<kLanes>(dot) * (1.f / D) * r * r;
+        const bool on = hb + a * kRows + sub < it.h1;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (hb + a * kRows + sub < it.h1) part[j] = fmaf(g[a][j] * r, xv[a][j], part[j]);
-          g[a][j] = r * fmaf(-xv[a][j], m, g[a][j] * w[j]);
+          if (on) part[j] = fmaf(g[j] * r, xv[j], part[j]);
+          g[j] = r * fmaf(-xv[j], m, g[j] * w[j]);
         }
-        const int hh = hb + a * kRows + sub;
-        if (hh < it.h1) store8(o + (long)hh * D, g[a]);
+        if (on) store8(o + a * kRows * oh, g);
       }
+      x += kRows * kAhead * xh;
+      dz += kRows * kAhead * zh;
+      o += kRows * kAhead * oh;
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -337,20 +374,27 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float *__restrict__ p
 // partial sums (the workspace holds this many).
 constexpr int kBwdBlocksPerSm = 4, kBwdBlocksMost = 1024;
 
-template <typename T, int D, bool kPairs>
+template <typename T, int D, bool kPairs, bool kDense>
 cudaError_t launch_typed(const QkParams &p, bool bwd, unsigned grid, cudaStream_t st) {
-  if (bwd) return launch_pdl(qk_norm_bwd_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
-  return launch_pdl(qk_norm_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
+  if (bwd) return launch_pdl(qk_norm_bwd_kernel<T, D, kPairs, kDense>, grid, kThreads, 0, st, p);
+  return launch_pdl(qk_norm_kernel<T, D, kPairs, kDense>, grid, kThreads, 0, st, p);
+}
+
+template <typename T, int D>
+cudaError_t launch_dim(const QkParams &p, bool pairs, bool bwd, bool dense, unsigned grid,
+                       cudaStream_t st) {
+  if (dense)
+    return pairs ? launch_typed<T, D, true, true>(p, bwd, grid, st)
+                 : launch_typed<T, D, false, true>(p, bwd, grid, st);
+  return pairs ? launch_typed<T, D, true, false>(p, bwd, grid, st)
+               : launch_typed<T, D, false, false>(p, bwd, grid, st);
 }
 
 template <typename T>
-cudaError_t launch_dtype(const QkParams &p, int D, bool pairs, bool bwd, unsigned grid,
+cudaError_t launch_dtype(const QkParams &p, int D, bool pairs, bool bwd, bool dense, unsigned grid,
                          cudaStream_t st) {
-  if (D == 64)
-    return pairs ? launch_typed<T, 64, true>(p, bwd, grid, st)
-                 : launch_typed<T, 64, false>(p, bwd, grid, st);
-  return pairs ? launch_typed<T, 128, true>(p, bwd, grid, st)
-               : launch_typed<T, 128, false>(p, bwd, grid, st);
+  return D == 64 ? launch_dim<T, 64>(p, pairs, bwd, dense, grid, st)
+                 : launch_dim<T, 128>(p, pairs, bwd, dense, grid, st);
 }
 
 }  // namespace
@@ -378,24 +422,24 @@ cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // Heads per item: all of a token's heads of one side, or, where that leaves the GPU
   // short of warps, as few as one pass of the warp takes.
-  const int pass = 32 / (a.D / 8) * (bwd ? 2 : 4);
+  const int pass = 32 / (a.D / 8) * (bwd && a.dt == NABLA_F32 ? 2 : 4);
   const int most = a.h[0] > a.h[1] ? a.h[0] : a.h[1];
   int hpi = most;
   if (p.tokens * 2 < (long)sms * 64) hpi = pass;
   p.heads_per_item = hpi;
   p.items = 0;
+  bool dense = true;
   for (int i = 0; i < 2; ++i) {
     Side &s = p.side[i];
     s.x = a.x[i];
     s.dz = a.dz[i];
     s.out = a.out[i];
     s.w = a.w[i];
-    s.xb = a.x_st[i].batch;
-    s.xt = a.x_st[i].token;
-    s.ob = a.out_st[i].batch;
-    s.ot = a.out_st[i].token;
-    s.zb = a.dz_st[i].batch;
-    s.zt = a.dz_st[i].token;
+    s.x_st = a.x_st[i];
+    s.z_st = a.dz_st[i];
+    s.o_st = a.out_st[i];
+    if (a.h[i] > 1 && (s.x_st.head != a.D || s.o_st.head != a.D || (bwd && s.z_st.head != a.D)))
+      dense = false;
     s.h = a.h[i];
     s.chunks = (a.h[i] + hpi - 1) / hpi;
     p.items += p.tokens * s.chunks;
@@ -405,8 +449,8 @@ cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st) {
   if (bwd && cap > kBwdBlocksMost) cap = kBwdBlocksMost;
   const unsigned grid = (unsigned)(need < cap ? need : cap);
   if (bwd && (a.dw[0] || a.dw[1])) p.partial = static_cast<float *>(a.workspace);
-  e = a.dt == NABLA_BF16 ? launch_dtype<__nv_bfloat16>(p, a.D, a.interleaved, bwd, grid, st)
-                         : launch_dtype<float>(p, a.D, a.interleaved, bwd, grid, st);
+  e = a.dt == NABLA_BF16 ? launch_dtype<__nv_bfloat16>(p, a.D, a.interleaved, bwd, dense, grid, st)
+                         : launch_dtype<float>(p, a.D, a.interleaved, bwd, dense, grid, st);
   if (e != cudaSuccess || !p.partial) return e;
   return launch_pdl(qk_dw_kernel, dim3(2 * a.D / 32), dim3(1024), 0, st,
                     (const float *)p.partial, (int)grid, a.D, a.dw[0], a.dw[1], a.wdt);

@@ -26,8 +26,8 @@ _lib = None
 
 
 class _Strides(ctypes.Structure):
-    """nabla_strides of include/nabla.h: batch and token strides in elements."""
-    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64)]
+    """nabla_strides of include/nabla.h, in elements."""
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class NablaError(RuntimeError):
@@ -93,7 +93,7 @@ def load() -> ctypes.CDLL:
     lib.nabla_cross_attn_bwd_workspace_bytes.restype = sz
     lib.nabla_cross_attn_bwd_workspace_bytes.argtypes = xs
     lib.nabla_cross_attn_bwd.restype = i32
-    lib.nabla_cross_attn_bwd.argtypes = ([vp, st, vp, st, vp, st, vp, vp, vp] + xs +
+    lib.nabla_cross_attn_bwd.argtypes = ([vp, st, vp, st, vp, st, vp, st, vp, vp, st] + xs +
                                          [vp, f32, vp, vp, vp, vp, sz, vp])
     lib.nabla_selftest_bounded_wait.restype = i32
     lib.nabla_selftest_bounded_wait.argtypes = [vp]
@@ -120,6 +120,24 @@ def _call(device: torch.device, fn, *args) -> int:
     and takes its per-device state from, the current device."""
     with torch.cuda.device(device):
         return fn(*args)
+
+
+def _run(device: torch.device, stream, fn, where: str, *args) -> None:
+    """One C-ABI call whose last argument is the stream, on the tensors' device, raising
+    what it returns.  The device is switched only where another one is current, and the
+    default stream is asked for by number: a small call is a few microseconds of GPU work,
+    and both would cost it as much again."""
+    index = device.index
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = _stream(stream, device)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
+    else:
+        st = _call(device, fn, *args, stream)
+    if st != NABLA_OK:
+        raise NablaError(st, where)
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -165,23 +183,27 @@ def _buf(t: torch.Tensor, name: str, numel: int, dtype: torch.dtype,
 
 def _rows(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype,
           device: torch.device) -> Optional[_Strides]:
-    """Checks a [B, S, h, D] tensor that may be a view of a larger one (a token's heads
-    lie together) and returns its strides for the C ABI."""
+    """Checks a [B, S, h, D] tensor that may be a view of a larger one, or lie in another
+    order, and returns its strides for the C ABI."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    B, S, h, D = t.shape
-    if t.stride(3) != 1 or (h > 1 and t.stride(2) != D):
-        raise ValueError(f"the heads of a token of {name} must lie together")
-    if (S > 1 and t.stride(1) < h * D) or (
-            B > 1 and t.stride(0) < (S - 1) * (t.stride(1) if S > 1 else 0) + h * D):
-        raise ValueError(f"the tokens of {name} must not overlap")
-    return _Strides(t.stride(0), t.stride(1))
+    if t.is_contiguous():
+        return None  # dense
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the columns of {name} must lie together")
+    span = t.shape[3]
+    for s, n in sorted((s, n) for s, n in zip(st[:3], t.shape) if n > 1):
+        if s < span:
+            raise ValueError(f"the rows of {name} must not overlap")
+        span += s * (n - 1)
+    return _Strides(*st[:3])
 
 
 def _cuda(t: torch.Tensor) -> None:
@@ -423,45 +445,48 @@ def nabla_fractal_unflatten(y: torch.Tensor, T: int, H: int, W: int, P: int = 8,
     return out
 
 
-def _qk_args(q, k, wq, wk, cos, sin, pos):
+def _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps):
     """Checks what the query/key norm and its backward have in common and returns the
-    C arguments up to pos, the two tensors' shapes and the weights' type."""
-    for name, t in (("q", q), ("k", k)):
-        if t is not None and t.dim() != 4:
-            raise ValueError(f"{name} must be [B, S, h, D]")
-    B, S, hq, D = q.shape
-    dev = q.device
-    hk = 0 if k is None else k.shape[2]
-    shapes = (B, S, hq, D), (B, S, hk, D)
-    strides = (_rows(q, "q", shapes[0], q.dtype, dev), _rows(k, "k", shapes[1], q.dtype, dev))
-    weights = [w for w in (wq, wk) if w is not None]
-    kind = weights[0].dtype if weights else torch.float32
-    for name, w in (("wq", wq), ("wk", wk)):
-        if w is not None:
-            _buf(w, name, D, kind, dev)
-            if w.numel() != D:
-                raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
+    C arguments up to eps, the two tensors' shapes and the weights' type."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, S, h, D]")
+    B, S, hq, D = q_shape = q.shape
+    dev, dtype = q.device, q.dtype
+    hk, k_shape, k_ptr, k_st = 0, None, None, None
+    q_st = _rows(q, "q", q_shape, dtype, dev)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("k must be [B, S, h, D]")
+        k_shape = k.shape
+        hk = k_shape[2]
+        k_st = _rows(k, "k", (B, S, hk, D), dtype, dev)
+        k_ptr = k.data_ptr()
+    kind, wcode = torch.float32, NABLA_F32
+    w = wq if wq is not None else wk
+    if w is not None:
+        kind, wcode = w.dtype, _dtype_code(w)
+        for name, w in (("wq", wq), ("wk", wk)):
+            if w is not None:
+                _buf(w, name, D, kind, dev)
+                if w.numel() != D:
+                    raise ValueError(f"{name} must be [{D}], got {tuple(w.shape)}")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
     R = n = 0
     if cos is not None:
         if cos.dim() != 2 or cos.shape != sin.shape:
             raise ValueError("cos and sin must be [rows, R / 2], of the same shape")
-        n, R = cos.shape[0], 2 * cos.shape[1]
-        _buf(cos, "cos", n * R // 2, torch.float32, dev)
-        _buf(sin, "sin", n * R // 2, torch.float32, dev)
+        n, half = cos.shape
+        R = 2 * half
+        _buf(cos, "cos", n * half, torch.float32, dev)
+        _buf(sin, "sin", n * half, torch.float32, dev)
     if pos is not None:
         if cos is None or pos.shape != (B, S):
             raise ValueError(f"pos must be [{B}, {S}], with cos and sin")
         _buf(pos, "pos", B * S, torch.int32, dev)
-    wcode = NABLA_F32 if not weights else _dtype_code(weights[0])
-
-    def args(interleaved, eps):
-        return [_ptr(q), strides[0], _ptr(k), strides[1], _dtype_code(q), B, S, hq, hk, D,
-                _ptr(wq), _ptr(wk), wcode, _ptr(cos), _ptr(sin), n, R, int(bool(interleaved)),
-                _ptr(pos), float(eps)]
-
-    return args, shapes, kind
+    return (q.data_ptr(), q_st, k_ptr, k_st, _dtype_code(q), B, S, hq, hk, D, _ptr(wq), _ptr(wk),
+            wcode, _ptr(cos), _ptr(sin), n, R, 1 if interleaved else 0, _ptr(pos),
+            eps), q_shape, k_shape, kind
 
 
 def nabla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -475,20 +500,23 @@ def nabla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     their first R columns; token s takes table row s, or pos[b, s].  interleaved:
     rotate columns (2i, 2i + 1), else (i, i + R/2).  q, k and the outputs may be views
     whose tokens are strided.  Returns (q_out, k_out)."""
-    args, shapes, _ = _qk_args(q, k, wq, wk, cos, sin, pos)
+    args, q_shape, k_shape, _ = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps)
     dev = q.device
+    qo = ko = None
     if q_out is None:
-        q_out = torch.empty(shapes[0], dtype=q.dtype, device=dev)
-    if k_out is None and k is not None:
-        k_out = torch.empty(shapes[1], dtype=q.dtype, device=dev)
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    qo, ko = (_rows(t, n, s, q.dtype, dev) for t, n, s in
-              ((q_out, "q_out", shapes[0]), (k_out, "k_out", shapes[1])))
+        q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
+    else:
+        qo = _rows(q_out, "q_out", q_shape, q.dtype, dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+    elif k_out is None:
+        k_out = torch.empty(k_shape, dtype=q.dtype, device=dev)
+    else:
+        ko = _rows(k_out, "k_out", k_shape, q.dtype, dev)
     _cuda(q)
-    st = _call(dev, load().nabla_qk_norm_rope, *args(interleaved, eps), _ptr(q_out), qo,
-               _ptr(k_out), ko, _stream(stream, dev))
-    _check(st, "nabla_qk_norm_rope")
+    _run(dev, stream, load().nabla_qk_norm_rope, "nabla_qk_norm_rope", *args, q_out.data_ptr(), qo,
+         _ptr(k_out), ko)
     return q_out, k_out
 
 
@@ -508,16 +536,24 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
     """Gradients of nabla_qk_norm_rope for the upstream gradients dq_out, dk_out of its
     outputs: returns (dq, dk, dwq, dwk); dwq, dwk [D] in the weights' type, None where
     the weight is None."""
-    args, shapes, kind = _qk_args(q, k, wq, wk, cos, sin, pos)
-    dev, D = q.device, q.shape[3]
+    args, q_shape, k_shape, kind = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps)
+    dev, dtype, D = q.device, q.dtype, q.shape[3]
     if dq_out is None or (k is None) != (dk_out is None):
         raise ValueError("dq_out and, with k, dk_out are needed")
     if k is None and (dk is not None or wk is not None):
         raise ValueError("dk or wk without k")
+    zq, zk = _rows(dq_out, "dq_out", q_shape, dtype, dev), _rows(dk_out, "dk_out", k_shape, dtype,
+                                                                 dev)
+    oq = ok = None
     if dq is None:
-        dq = torch.empty(shapes[0], dtype=q.dtype, device=dev)
-    if dk is None and k is not None:
-        dk = torch.empty(shapes[1], dtype=q.dtype, device=dev)
+        dq = torch.empty(q_shape, dtype=dtype, device=dev)
+    else:
+        oq = _rows(dq, "dq", q_shape, dtype, dev)
+    if k is not None:
+        if dk is None:
+            dk = torch.empty(k_shape, dtype=dtype, device=dev)
+        else:
+            ok = _rows(dk, "dk", k_shape, dtype, dev)
     for name, d, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
         if d is not None:
             if w is None:
@@ -527,36 +563,32 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
         dwq = torch.empty(D, dtype=kind, device=dev)
     if dwk is None and wk is not None:
         dwk = torch.empty(D, dtype=kind, device=dev)
-    zq, zk, oq, ok = (_rows(t, n, s, q.dtype, dev) for t, n, s in
-                      ((dq_out, "dq_out", shapes[0]), (dk_out, "dk_out", shapes[1]),
-                       (dq, "dq", shapes[0]), (dk, "dk", shapes[1])))
+    lib = load()
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(max(nabla_qk_norm_rope_bwd_workspace_bytes(D), 1),
-                                dtype=torch.uint8, device=dev)
+        workspace = torch.empty(lib.nabla_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
+                                device=dev)
     if workspace is not None:
         _on(workspace, "workspace", dev)
     _cuda(q)
-    st = _call(dev, load().nabla_qk_norm_rope_bwd, *args(interleaved, eps), _ptr(dq_out), zq,
-               _ptr(dk_out), zk, _ptr(dq), oq, _ptr(dk), ok, _ptr(dwq), _ptr(dwk),
-               _ptr(workspace),
-               0 if workspace is None else workspace.numel() * workspace.element_size(),
-               _stream(stream, dev))
-    _check(st, "nabla_qk_norm_rope_bwd")
+    _run(dev, stream, lib.nabla_qk_norm_rope_bwd, "nabla_qk_norm_rope_bwd", *args,
+         dq_out.data_ptr(), zq, _ptr(dk_out), zk, dq.data_ptr(), oq, _ptr(dk), ok, _ptr(dwq),
+         _ptr(dwk), _ptr(workspace),
+         0 if workspace is None else workspace.numel() * workspace.element_size())
     return dq, dk, dwq, dwk
 
 
 def _cross_args(q, k, v, kv_len):
     """Checks q, k, v and kv_len of a cross attention; returns the C ABI's strides and
     its (dtype, B, Sq, Sk, h, hk, D)."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != 4:
-            raise ValueError(f"{name} must be [B, S, h, D]")
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        name = "q" if q.dim() != 4 else "k" if k.dim() != 4 else "v"
+        raise ValueError(f"{name} must be [B, S, h, D]")
     B, Sq, h, D = q.shape
     Sk, hk = k.shape[1:3]
-    dev = q.device
-    strides = (_rows(q, "q", (B, Sq, h, D), q.dtype, dev),
-               _rows(k, "k", (B, Sk, hk, D), q.dtype, dev),
-               _rows(v, "v", (B, Sk, hk, D), q.dtype, dev))
+    dev, dtype = q.device, q.dtype
+    kv = (B, Sk, hk, D)
+    strides = (_rows(q, "q", q.shape, dtype, dev), _rows(k, "k", kv, dtype, dev),
+               _rows(v, "v", kv, dtype, dev))
     if kv_len is not None:
         if kv_len.shape != (B,):
             raise ValueError(f"kv_len must be [{B}], got {tuple(kv_len.shape)}")
@@ -577,7 +609,8 @@ def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
         scale = 1.0 / math.sqrt(sizes[-1])
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _buf(o, "o", q.numel(), q.dtype, dev)
+    else:
+        _buf(o, "o", q.numel(), q.dtype, dev)
     if lse is not None:
         _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
     lib = load()
@@ -588,12 +621,10 @@ def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
     if workspace is not None:
         _on(workspace, "workspace", dev)
     _cuda(q)
-    st = _call(dev, lib.nabla_cross_attn_fwd, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
-               strides[2], *sizes, _ptr(kv_len), float(scale), _ptr(o), _ptr(lse),
-               _ptr(workspace),
-               0 if workspace is None else workspace.numel() * workspace.element_size(),
-               _stream(stream, dev))
-    _check(st, "nabla_cross_attn_fwd")
+    _run(dev, stream, lib.nabla_cross_attn_fwd, "nabla_cross_attn_fwd", q.data_ptr(), strides[0],
+         k.data_ptr(), strides[1], v.data_ptr(), strides[2], *sizes, _ptr(kv_len), scale,
+         o.data_ptr(), _ptr(lse), _ptr(workspace),
+         0 if workspace is None else workspace.numel() * workspace.element_size())
     return o
 
 
@@ -637,32 +668,28 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
     dk, dv [B,Sk,hk,D] (0 for states past kv_len)."""
     strides, sizes = _cross_args(q, k, v, kv_len)
     dev = q.device
-    for name, t in (("o", o), ("dout", dout)):
-        if t.shape != q.shape:
-            raise ValueError(f"{name} must be {tuple(q.shape)}, got {tuple(t.shape)}")
-        _buf(t, name, q.numel(), q.dtype, dev)
+    so, sg = _rows(o, "o", q.shape, q.dtype, dev), _rows(dout, "dout", q.shape, q.dtype, dev)
     _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(sizes[-1])
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    if dv is None:
-        dv = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    for name, t, n in (("dq", dq, q.numel()), ("dk", dk, k.numel()), ("dv", dv, k.numel())):
-        _buf(t, name, n, q.dtype, dev)
+    outs = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+        if t is None:
+            t = torch.empty(like.shape, dtype=q.dtype, device=dev)
+        else:
+            _buf(t, name, like.numel(), q.dtype, dev)
+        outs.append(t)
+    dq, dk, dv = outs
     lib = load()
     if workspace is None:
         need = lib.nabla_cross_attn_bwd_workspace_bytes(*sizes)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     _on(workspace, "workspace", dev)
     _cuda(q)
-    st = _call(dev, lib.nabla_cross_attn_bwd, _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
-               strides[2], _ptr(o), _ptr(lse), _ptr(dout), *sizes, _ptr(kv_len), float(scale),
-               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-               workspace.numel() * workspace.element_size(), _stream(stream, dev))
-    _check(st, "nabla_cross_attn_bwd")
+    _run(dev, stream, lib.nabla_cross_attn_bwd, "nabla_cross_attn_bwd", q.data_ptr(), strides[0],
+         k.data_ptr(), strides[1], v.data_ptr(), strides[2], o.data_ptr(), so, lse.data_ptr(),
+         dout.data_ptr(), sg, *sizes, _ptr(kv_len), scale, dq.data_ptr(), dk.data_ptr(),
+         dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv
 
 

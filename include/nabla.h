@@ -324,16 +324,17 @@ nabla_status nabla_fractal_unflatten(const void *y, nabla_dtype dt, int B, int T
 
 /*
  * Where the rows of a [B, S, h, D] tensor lie: element (b, s, hh, d) is at
- * b * batch + s * token + hh * D + d, both strides in elements.  A NULL
- * nabla_strides pointer means dense (token = h * D, batch = S * h * D).  The
- * entry points below take one for each tensor that may be a view of a larger
- * one, e.g. q and k lying in the packed projection [B, S, (h + 2 hk) * D].
- * Both strides must keep 16-byte alignment; token >= h * D, and for B > 1
- * batch >= (S - 1) * token + h * D (batch is not looked at for B = 1, token
- * not for S = 1).
+ * b * batch + s * token + hh * head + d, the strides in elements.  A NULL
+ * nabla_strides pointer means dense (head = D, token = h * D, batch = S * h * D).
+ * The entry points below take one for each tensor that may be a view of a larger
+ * one, e.g. q and k lying in the packed projection [B, S, (h + 2 hk) * D], or may
+ * lie in another order, e.g. heads before tokens.  The strides are positive, keep
+ * 16-byte alignment, and no two rows overlap: in the order of their size, each is at
+ * least what the ones before it span.  The stride of a dimension of size 1 is not
+ * looked at.
  */
 typedef struct {
-  int64_t batch, token;
+  int64_t batch, token, head;
 } nabla_strides;
 
 /*
@@ -456,7 +457,7 @@ nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, cons
  * f32: fp32 arithmetic on CUDA cores.  No atomics: repeated calls give the same bits.
  *
  *   q, k, v, kv_len, scale  as given to nabla_cross_attn_fwd.
- *   o, dout     [B, Sq, h, D] device, dense, element type dt.
+ *   o, dout     [B, Sq, h, D] device, element type dt, strides o_st and dout_st.
  *   lse         [B, h, Sq] device fp32, 4-byte aligned, from nabla_cross_attn_fwd.
  *   dq          [B, Sq, h, D], dk and dv [B, Sk, hk, D] device, dense, element type dt,
  *               overwritten; they overlap no other argument.
@@ -469,10 +470,11 @@ size_t nabla_cross_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int S
                                             int D);
 nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
                                   const nabla_strides *k_st, const void *v,
-                                  const nabla_strides *v_st, const void *o, const float *lse,
-                                  const void *dout, nabla_dtype dt, int B, int Sq, int Sk, int h,
-                                  int hk, int D, const int32_t *kv_len, float scale, void *dq,
-                                  void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                  const nabla_strides *v_st, const void *o,
+                                  const nabla_strides *o_st, const float *lse, const void *dout,
+                                  const nabla_strides *dout_st, nabla_dtype dt, int B, int Sq,
+                                  int Sk, int h, int hk, int D, const int32_t *kv_len, float scale,
+                                  void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes,
                                   nabla_stream_t stream);
 
 /*

@@ -54,6 +54,9 @@ def inputs(B, Sq, Sk, h, hk, D, dtype, seed=0, packed=False, spread=1.0):
     def draw(*shape):
         return (torch.randn(*shape, generator=g) * spread).to(dt).to(DEV)
 
+    if packed == "heads":  # heads before tokens
+        return [draw(*s).transpose(1, 2) for s in
+                ((B, h, Sq, D), (B, hk, Sk, D), (B, hk, Sk, D))]
     if packed:  # q between other columns, k and v in one projection
         q = draw(B, Sq, (h + 1) * D)[..., D:].unflatten(-1, (h, D))
         kv = draw(B, Sk, 2, hk, D)
@@ -113,6 +116,7 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (1, 5, 700, 64, 1, 64, [641], False),          # 64 heads on one key head
     (2, 1, 900, 14, 2, 128, [900, 385], True),     # seven heads a group, runs
     (1, 1537, 513, 2, 1, 128, None, True),
+    (2, 333, 150, 4, 2, 128, [150, 90], "heads"),
 ]
 
 

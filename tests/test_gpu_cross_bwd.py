@@ -55,6 +55,10 @@ def inputs(B, Sq, Sk, h, hk, D, dtype, seed=0, packed=False, spread=1.2):
     def draw(*shape, s=spread):
         return (torch.randn(*shape, generator=g) * s).to(dt).to(DEV)
 
+    if packed == "heads":  # everything heads before tokens
+        q, k, v, g_ = [draw(*s).transpose(1, 2) for s in
+                       ((B, h, Sq, D), (B, hk, Sk, D), (B, hk, Sk, D), (B, h, Sq, D))]
+        return q, k, v, g_ * 0.5
     if packed:
         q = draw(B, Sq, (h + 1) * D)[..., D:].unflatten(-1, (h, D))
         kv = draw(B, Sk, 2, hk, D)
@@ -120,6 +124,7 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (1, 5, 700, 64, 1, 64, [641], False),           # 64 heads on one key head
     (2, 900, 64, 14, 2, 128, [64, 50], False),      # seven heads a group
     (1, 2000, 200, 4, 4, 64, [199], False),
+    (2, 333, 150, 4, 2, 128, [150, 90], "heads"),
 ]
 
 
@@ -133,6 +138,8 @@ def test_backward(nabla, B, Sq, Sk, h, hk, D, lens, packed, dtype):
             k[b, m:] = float("nan")
             v[b, m:] = float("inf") if b % 2 else float("nan")
     o, lse = nabla.nabla_cross_attn_fwd_lse(q, k, v, kv_len=n)
+    if packed == "heads":
+        o = o.transpose(1, 2).contiguous().transpose(1, 2)
     got = nabla.nabla_cross_attn_bwd(q, k, v, o, lse, dout, kv_len=n)
     assert nabla.nabla_get_last_device_status() == 0
     check(got, q, k, v, o, dout, lens or [Sk] * B, 1 / math.sqrt(D))

@@ -59,7 +59,10 @@ def table(rows, R, seed=0):
 def inputs(B, S, hq, hk, D, dtype, seed=0, packed=False, spread=1.5):
     g = torch.Generator().manual_seed(seed)
     dt = TYPES[dtype]
-    if packed:  # views of one projection
+    if packed == "heads":  # heads before tokens
+        q = (torch.randn(B, hq, S, D, generator=g) * spread).to(dt).to(DEV).transpose(1, 2)
+        k = (torch.randn(B, hk, S, D, generator=g) * spread).to(dt).to(DEV).transpose(1, 2)
+    elif packed:  # views of one projection
         x = (torch.randn(B, S, (hq + 2 * hk) * D, generator=g) * spread).to(dt).to(DEV)
         q = x[..., :hq * D].view(B, S, hq, D)
         k = x[..., hq * D:(hq + hk) * D].view(B, S, hk, D) if hk else None
@@ -126,6 +129,7 @@ CASES = [  # B, S, hq, hk, D, R, dtype, pairs, packed, positions
     (2, 9, 4, 4, 128, 0, "bf16", True, False, False),      # norm alone
     (1, 257, 6, 0, 64, 32, "bf16", False, False, False),   # q alone
     (2, 300, 24, 24, 128, 128, "f32", True, False, False),
+    (2, 50, 6, 3, 64, 64, "bf16", True, "heads", False),
 ]
 
 

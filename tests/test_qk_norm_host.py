@@ -23,8 +23,8 @@ def lib():
         return N.load()
 
 
-def st(batch, token):
-    return ctypes.byref(N._Strides(batch, token))
+def st(batch, token, head=64):
+    return ctypes.byref(N._Strides(batch, token, head))
 
 
 def fwd(lib, **kw):
@@ -53,6 +53,8 @@ BAD = [dict(q=None), dict(q=M + 8), dict(k=2 * M + 2), dict(dt=2), dict(wdt=5), 
        dict(eps=float("nan")), dict(eps=float("inf")), dict(wq=3 * M + 8),
        dict(q_st=st(8 * 256, 255)), dict(q_st=st(8 * 256, 260 * 1)), dict(q_st=st(2047, 256)),
        dict(q_st=st(7 * 256, 256)), dict(k_st=st(-8 * 128, 128)),
+       dict(q_st=st(8 * 256, 256, 60)), dict(q_st=st(8 * 256, 256, 72)),
+       dict(q_st=st(8 * 256, 64, 7 * 64)), dict(q_st=st(8 * 256, 256, 0)),
        dict(B=2 ** 31 - 1, S=2 ** 31 - 1)]
 
 
@@ -98,6 +100,7 @@ def test_binding_passes_good_tensors_up_to_the_device_check():
     for call in (lambda: N.nabla_qk_norm_rope(q, k, w, w, c, s),
                  lambda: N.nabla_qk_norm_rope(pq, pk, w, None, c, s, interleaved=False),
                  lambda: N.nabla_qk_norm_rope(q),
+                 lambda: N.nabla_qk_norm_rope(q.transpose(1, 2).contiguous().transpose(1, 2)),
                  lambda: N.nabla_qk_norm_rope(q, k, w, w, c, s, q_out=pq, k_out=pk),
                  lambda: N.nabla_qk_norm_rope(
                      q, k, w, w, c, s, pos=torch.zeros(2, 8, dtype=torch.int32)),
@@ -114,8 +117,8 @@ def test_binding_refuses():
         ("k must be", lambda: N.nabla_qk_norm_rope(q, k[:, :4], w, w, c, s)),
         ("k must be torch.bfloat16", lambda: N.nabla_qk_norm_rope(q, k.float(), w, w, c, s)),
         ("k is on meta", lambda: N.nabla_qk_norm_rope(q, k.to("meta"), w, w, c, s)),
-        ("lie together", lambda: N.nabla_qk_norm_rope(q.transpose(1, 2).contiguous()
-                                                      .transpose(1, 2))),
+        ("lie together", lambda: N.nabla_qk_norm_rope(q.transpose(2, 3).contiguous()
+                                                      .transpose(2, 3))),
         ("must not overlap", lambda: N.nabla_qk_norm_rope(q[:1].expand(2, 8, 4, 64))),
         ("wk must be torch.bfloat16", lambda: N.nabla_qk_norm_rope(q, k, w, w.float(), c, s)),
         ("wq holds", lambda: N.nabla_qk_norm_rope(q, k, w[:32], w)),
