@@ -241,12 +241,6 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
       mbar_wait_small(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status, kDevTimeout);
 }
 
-// A wait of a whole warp that goes on in step.
-__device__ __forceinline__ bool x_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       int *status) {
-  return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort, status, kDevTimeout));
-}
-
 // Warp 1: S of step g into score buffer g % 3, once the PV of step g - 3 (its last
 // reader) is done.
 template <int D>
@@ -262,34 +256,30 @@ __device__ void x_qk(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
   for (uint32_t i = blockIdx.x; i < P.units && ok; i += gridDim.x) {
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
-    ok = x_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
+    ok = cross::thread_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
     const uint64_t qd = q_desc + (uint64_t)((q.slot * C::kTileBytes) >> 4);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = x_wait(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status) &&
-           x_wait(&sy->k_full[ks.slot], ks.phase, abort, P.status);
+      ok = cross::thread_wait(&sy->pv_done[sb.slot], sb.phase ^ 1u, abort, P.status) &&
+           cross::thread_wait(&sy->k_full[ks.slot], ks.phase, abort, P.status);
       if (!ok) break;
       tc_fence_after();
       const uint32_t d = tmem + C::kSCol + sb.slot * 128;
       const uint64_t kd = k_desc + (uint64_t)((ks.slot * C::kTileBytes) >> 4);
       const uint32_t id = idesc_bf16(128, x_k16(u, u.t0 + s) * 16, 0, 0) | P.neg;
-      if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          // 16 columns: 32 bytes inside a 128-byte swizzle row, every 4 the next box
-          const uint64_t at = (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4);
-          mma_ss(d, qd + at, kd + at, id, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&sy->s_full[sb.slot]);  // also frees the K slot
-        if (s + 1 == u.n) mma_commit(&sy->q_empty[q.slot]);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        // 16 columns: 32 bytes inside a 128-byte swizzle row, every 4 the next box
+        const uint64_t at = (uint64_t)(((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4);
+        mma_ss(d, qd + at, kd + at, id, kk > 0 ? 1u : 0u);
       }
-      __syncwarp();
+      mma_commit(&sy->s_full[sb.slot]);  // also frees the K slot
+      if (s + 1 == u.n) mma_commit(&sy->q_empty[q.slot]);
       sb.next();
       ks.next();
     }
     q.next();
   }
-  if (elect_one()) mma_commit(&sy->drain);
-  __syncwarp();  // never exit with MMAs in flight
+  mma_commit(&sy->drain);  // never exit with MMAs in flight
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
@@ -308,39 +298,35 @@ __device__ void x_pv(const XParams &P, uint8_t *smem, XSync *sy, uint32_t tmem,
     const XUnit u = x_unit(P, i);
     if (u.n == 0) continue;
     // the previous unit's O must have been read before the first PV overwrites it
-    if (kq > 0) ok = x_wait(&sy->o_free, (kq - 1) & 1u, abort, P.status);
+    if (kq > 0) ok = cross::thread_wait(&sy->o_free, (kq - 1) & 1u, abort, P.status);
     for (int s = 0; s < u.n && ok; ++s) {
-      ok = x_wait(&sy->v_full[vs.slot], vs.phase, abort, P.status) &&
-           x_wait(&sy->p_full[sb.slot], sb.phase, abort, P.status);
+      ok = cross::thread_wait(&sy->v_full[vs.slot], vs.phase, abort, P.status) &&
+           cross::thread_wait(&sy->p_full[sb.slot], sb.phase, abort, P.status);
       if (!ok) break;
       tc_fence_after();
       const uint64_t vd = v_desc + (uint64_t)((vs.slot * C::kTileBytes) >> 4);
       const uint32_t a = tmem + C::kSCol + sb.slot * 128;
       const int k16 = x_k16(u, u.t0 + s);
-      if (elect_one()) {
-        // 16 states a MMA: 8 columns of P, the right half's from 64; all eight without a
-        // branch between them but in a batch's last tile
-        if (k16 == 8) {
+      // 16 states a MMA: 8 columns of P, the right half's from 64; all eight without a
+      // branch between them but in a batch's last tile
+      if (k16 == 8) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
-                   vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
-        } else {
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
+                 vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
+      } else {
 #pragma unroll 1
-          for (int kk = 0; kk < k16; ++kk)
-            mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
-                   vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
-        }
-        mma_commit(&sy->pv_done[sb.slot]);  // frees the score buffer and the V slot
+        for (int kk = 0; kk < k16; ++kk)
+          mma_ts(tmem, a + (kk >> 2) * 64 + (kk & 3) * 8,
+                 vd + (uint64_t)((kk * 16 * 128) >> 4), id, (s > 0 || kk > 0) ? 1u : 0u);
       }
-      __syncwarp();
+      mma_commit(&sy->pv_done[sb.slot]);  // frees the score buffer and the V slot
       sb.next();
       vs.next();
     }
     ++kq;
   }
-  if (elect_one()) mma_commit(&sy->drain);
-  __syncwarp();
+  mma_commit(&sy->drain);
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
@@ -417,8 +403,7 @@ __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t t
     float m_run = 0.f, l_run = 0.f;
     for (int s = 0; s < u.n; ++s, ++g, sb.next()) {
       const int mine = u.len - (u.t0 + s) * kTile - grp * 64;  // own columns that are states
-      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->s_full[sb.slot], sb.phase,
-                                                              abort, P.status, kDevTimeout));
+      cross::warp_wait(live, &sy->s_full[sb.slot], sb.phase, abort, P.status);
       tc_fence_after();
       const uint32_t own = at + C::kSCol + sb.slot * 128 + grp * 64;
       uint32_t r0[32], r1[32];
@@ -461,9 +446,8 @@ __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t t
         // takes half of its columns
         const uint32_t gp = g - 1;
         const float alpha = ex2(m_run - m_new);
-        live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->pv_done[gp % C::kSBufs],
-                                                               (gp / C::kSBufs) & 1u, abort,
-                                                               P.status, kDevTimeout));
+        cross::warp_wait(live, &sy->pv_done[gp % C::kSBufs], (gp / C::kSBufs) & 1u, abort,
+                         P.status);
         tc_fence_after();
 #pragma unroll 1
         for (int x = 0; x < D / 32; ++x) {
@@ -495,8 +479,7 @@ __device__ void x_softmax(const XParams &P, uint8_t *smem, XSync *sy, uint32_t t
     x_pair_sync(q4);
     if (grp == 0) {
       // the output warps have read the last unit's l and bias
-      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->l_empty, (kq & 1u) ^ 1u, abort,
-                                                              P.status, kDevTimeout));
+      cross::warp_wait(live, &sy->l_empty, (kq & 1u) ^ 1u, abort, P.status);
       *xl = l_run + xx[0];
       *xm = m_run;
       x_arrive(&sy->l_full, lane);
@@ -530,17 +513,14 @@ __device__ void x_output(const XParams &P, const CUtensorMap *mo, uint8_t *smem,
     float l = 0.f, m = 0.f;
     if (u.n > 0) {
       const uint32_t gl = gs + u.n - 1;
-      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->l_full, kq & 1u, abort,
-                                                              P.status, kDevTimeout));
+      cross::warp_wait(live, &sy->l_full, kq & 1u, abort, P.status);
       l = xl[row];
       m = xm[row];
       x_arrive(&sy->l_empty, lane);
       // the last unit's store has read the tile (long ago)
       if (q4 == 0 && lane == 0) bulk_wait_read();
       x_out_sync();
-      live = __all_sync(0xffffffffu, live && mbar_wait_small(&sy->pv_done[gl % C::kSBufs],
-                                                              (gl / C::kSBufs) & 1u, abort,
-                                                              P.status, kDevTimeout));
+      cross::warp_wait(live, &sy->pv_done[gl % C::kSBufs], (gl / C::kSBufs) & 1u, abort, P.status);
       tc_fence_after();
       gs += u.n;
       ++kq;
@@ -670,9 +650,9 @@ __global__ void __launch_bounds__(512, 1)
     if (warp == 0) {
       if (lane == 0) x_load_qk<D>(P, &mq, &mk, smem, sy, abort);
     } else if (warp == 1) {
-      x_qk<D>(P, smem, sy, tmem, abort);
+      if (elect_one()) x_qk<D>(P, smem, sy, tmem, abort);
     } else if (warp == 2) {
-      x_pv<D>(P, smem, sy, tmem, abort);
+      if (elect_one()) x_pv<D>(P, smem, sy, tmem, abort);
     } else {
       x_load_v<D>(P, &mv, smem, sy, abort);
     }

@@ -14,9 +14,11 @@
 //    tile of 128 packed query rows: X = K Q^T, Y = V dO^T (SS MMAs, M = N = 128),
 //    P^T = 2^(X - lse), dz^T = P^T (Y - delta) as bf16 over X and Y in TMEM, then
 //    dV += P^T dO, dK += dz^T Q (TS MMAs).  TMEM holds dK, dV, X and Y: 4 x 128 columns.
-//    One warp issues dV and X (which reuses P's columns), another dK and Y: two chains
-//    that fill each other's gaps.  Where there are few state tiles the query tiles are
-//    split over several units whose fp32 sums cross_dkv_join adds up in a fixed order.
+//    One warp issues dV and X (which goes over P), another dK and Y: two chains that fill
+//    each other's gaps.  (One warp for all four, in the best order, leaves the tensor pipe
+//    to drain at every wait: 3500 cycles a step where two take 3100, of 2048 in the pipe.)
+//    Where there are few state tiles the query tiles are split over several units whose
+//    fp32 sums cross_dkv_join adds up in a fixed order.
 //  * dQ: unit = a tile of 128 packed query rows over the batch's state tiles.  X = Q K^T,
 //    Y = dO V^T, dz as bf16 in one of two buffers, dQ += dz K.  X and Y are free for the
 //    next step as soon as the softmax warps have them in registers.
@@ -74,13 +76,13 @@ struct YCfg {
 
 struct KSync {
   uint64_t kv_full, kv_empty, q_full[3], q_empty[3], g_full[2], g_empty[2];
-  uint64_t x_full, y_full, p_full, z_full, dv_done, dk_done, acc_full, acc_free, drain;
+  uint64_t x_full, y_full, p_full[2], z_full[2], dv_done, dk_done, acc_full, acc_free, drain;
   uint32_t tmem_slot;
   int abort;
 };
 struct QSync {
   uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw, v_full, v_empty;
-  uint64_t x_full, y_full, x_free, y_free, z_full[2], dq_done[2], acc_full, acc_free, drain;
+  uint64_t x_full, y_full, x_free, y_free, z_full[2], acc_full, drain;
   uint32_t tmem_slot;
   int abort;
 };
@@ -98,15 +100,12 @@ struct YParams {
   const int32_t *kv_len;
   int B, Sq, Sk, h, hk, G, tq, nq, nkt, nsplit;  // nq: tiles of 128 packed rows
   uint32_t units;
+  cross::WalkStep walk;
   float scale, scale_log2;  // scale_log2 of |scale|, never 0
   uint32_t neg;             // kIdescNegA for a negative scale
   int *status;
 };
 
-__device__ __forceinline__ bool y_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
-                                       int *status) {
-  return __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort, status, kDevTimeout));
-}
 __device__ __forceinline__ void y_arrive(uint64_t *bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
@@ -126,6 +125,18 @@ __device__ __forceinline__ void issue_ss(uint32_t d, uint64_t a, uint64_t b, uin
     mma_ss(d, a + at, b + at, id, kk > 0 ? 1u : 0u);
   }
 }
+// The half of such a product: 16-row steps 2 half, 2 half + 1 of each side (the first 32
+// of every 64 columns of A, or the others).
+template <int D>
+__device__ __forceinline__ void issue_ts_half(uint32_t d, uint32_t a, uint32_t right, uint64_t b,
+                                              int half, bool first) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int kk = (x >> 1) * 4 + half * 2 + (x & 1);
+    mma_ts(d, a + (kk >> 2) * right + (kk & 3) * 8, b + (uint64_t)((kk * 16 * 128) >> 4),
+           YCfg<D>::kIdTS, x > 0 || half > 0 || !first ? 1u : 0u);
+  }
+}
 // D += A B, A 128 columns of bf16 in TMEM from `a` on (columns 64.. at `a` + right),
 // B an MN-major 128-row tile.
 template <int D>
@@ -142,17 +153,11 @@ __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t right,
 struct KUnit {
   int b, j, kt, sp, len, i0, n;  // n query tiles from i0
 };
-__device__ __noinline__ KUnit k_unit(const YParams &P, uint32_t u) {
-  KUnit r;
-  uint32_t v = u / (uint32_t)P.nsplit;
-  r.sp = (int)(u - v * (uint32_t)P.nsplit);
-  const uint32_t bj = v / (uint32_t)P.nkt;
-  r.kt = (int)(v - bj * (uint32_t)P.nkt);
-  r.b = (int)(bj / (uint32_t)P.hk);
-  r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
-  r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
+__device__ __forceinline__ KUnit k_unit(const YParams &P, const cross::Walk &w) {
+  KUnit r{w.b, w.j, w.t, w.sp, cross::batch_len(P.kv_len, w.b, P.Sk), 0, 0};
+  if (r.kt * kTile >= r.len) return r;  // no states: nothing to walk
   r.i0 = (int)((long)P.nq * r.sp / P.nsplit);
-  r.n = r.kt * kTile < r.len ? (int)((long)P.nq * (r.sp + 1) / P.nsplit) - r.i0 : 0;
+  r.n = (int)((long)P.nq * (r.sp + 1) / P.nsplit) - r.i0;
   return r;
 }
 
@@ -167,7 +172,9 @@ __device__ void k_load(const YParams &P, const CUtensorMap *mq, const CUtensorMa
   uint32_t g = 0, ku = 0;
   bool go = true;
   const uint32_t rows = (uint32_t)(P.G * P.tq) * 128 * 2 * C::kBoxes;
-  for (uint32_t w = blockIdx.x; w < P.units && go && !*abort; w += gridDim.x) {
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units && go && !*abort;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const KUnit u = k_unit(P, w);
     cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     if (u.n == 0) continue;
@@ -221,90 +228,78 @@ __device__ void k_load(const YParams &P, const CUtensorMap *mq, const CUtensorMa
 
 // Warp 1 (kV): dV += P^T dO and X = K Q^T.  Warp 2: dK += dz^T Q and Y = V dO^T.  Each
 // chain's SS product of a step goes over the columns its TS product of the step before
-// has read.
+// has read; the TS product starts on the first half of P or dz.
 template <int D, bool kV>
 __device__ void k_mma(const YParams &P, uint8_t *smem, KSync *sy, uint32_t tmem,
                       volatile int *abort) {
   using C = YCfg<D>;
   const uint64_t a_desc = smem_desc_sw128(smem_u32(smem + (kV ? C::kOffK : C::kOffV)), 16, 1024);
-  const uint64_t q_kmaj = smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-  const uint64_t g_kmaj = smem_desc_sw128(smem_u32(smem + C::kOffG), 16, 1024);
-  const uint64_t q_mn = smem_desc_sw128(smem_u32(smem + C::kOffQ), C::kBox, 1024);
-  const uint64_t g_mn = smem_desc_sw128(smem_u32(smem + C::kOffG), C::kBox, 1024);
+  const uint64_t b_desc = smem_desc_sw128(smem_u32(smem + (kV ? C::kOffQ : C::kOffG)), 16, 1024);
+  const uint64_t t_desc =
+      smem_desc_sw128(smem_u32(smem + (kV ? C::kOffG : C::kOffQ)), C::kBox, 1024);
   const uint32_t xy = tmem + (kV ? C::kX1 : C::kY1), acc = tmem + (kV ? C::kDV : C::kDK);
-  uint64_t *ss_full = kV ? &sy->x_full : &sy->y_full;    // X or Y of a step is there
-  uint64_t *a_full = kV ? &sy->p_full : &sy->z_full;     // P or dz of a step is there
-  uint64_t *ts_done = kV ? &sy->dv_done : &sy->dk_done;  // and has been read
-  Ring<C::kQ> q, q2;   // of the SS and the TS product's step
-  Ring<C::kG> gr, gr2;
+  uint64_t *b_full = kV ? sy->q_full : sy->g_full, *t_full = kV ? sy->g_full : sy->q_full;
+  uint64_t *ss_full = kV ? &sy->x_full : &sy->y_full;  // X or Y of a step is there
+  uint64_t *a_full = kV ? sy->p_full : sy->z_full;     // the halves of its P or dz are there
+  uint64_t *ts_done = kV ? &sy->dv_done : &sy->dk_done;
+  Ring<kV ? C::kQ : C::kG> br;  // of the SS product's tile, and of the TS product's
+  Ring<kV ? C::kG : C::kQ> tr;
   uint32_t g = 0, ku = 0;
   bool ok = true;
-  auto ss = [&](bool last) {  // the SS product of the next step
-    if (kV) {
-      ok = y_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
-    } else {
-      ok = y_wait(&sy->g_full[gr.slot], gr.phase, abort, P.status);
-    }
-    if (!ok) return;
+  auto issue = [&](bool last) {  // the SS product of the next step
     tc_fence_after();
-    if (elect_one()) {
-      if (kV) {
-        issue_ss<D>(xy, a_desc, q_kmaj + (uint64_t)((q.slot * C::kTileBytes) >> 4),
-                    C::kIdSS | P.neg);
-      } else {
-        issue_ss<D>(xy, a_desc, g_kmaj + (uint64_t)((gr.slot * C::kTileBytes) >> 4), C::kIdSS);
-        mma_commit(&sy->g_empty[gr.slot]);
-      }
-      mma_commit(ss_full);
-      if (last) mma_commit(&sy->kv_empty);
-    }
-    __syncwarp();
-    q.next();
-    gr.next();
+    issue_ss<D>(xy, a_desc, b_desc + (uint64_t)((br.slot * C::kTileBytes) >> 4),
+                kV ? C::kIdSS | P.neg : C::kIdSS);
+    mma_commit(ss_full);
+    if (!kV) mma_commit(&sy->g_empty[br.slot]);
+    if (last) mma_commit(&sy->kv_empty);
+    br.next();
   };
-  for (uint32_t w = blockIdx.x; w < P.units && ok; w += gridDim.x) {
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units && ok;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const KUnit u = k_unit(P, w);
     if (u.n == 0) continue;
-    ok = y_wait(&sy->kv_full, ku & 1u, abort, P.status);
-    if (ok && g > 0) ok = y_wait(ts_done, (g - 1) & 1u, abort, P.status);
-    if (ok) ss(u.n == 1);
+    ok = cross::thread_wait(&sy->kv_full, ku & 1u, abort, P.status) &&
+         cross::thread_wait(&b_full[br.slot], br.phase, abort, P.status) &&
+         (g == 0 || cross::thread_wait(ts_done, (g - 1) & 1u, abort, P.status));
+    if (!ok) break;
+    issue(u.n == 1);
+    // the last unit's rows of dK and dV have been read
+    if (ku > 0) ok = cross::thread_wait(&sy->acc_free, (ku - 1) & 1u, abort, P.status);
     for (int i = 0; i < u.n && ok; ++i, ++g) {
-      // the tile of the TS product: Q was waited for by the other chain only
-      ok = kV ? y_wait(&sy->g_full[gr2.slot], gr2.phase, abort, P.status)
-              : y_wait(&sy->q_full[q2.slot], q2.phase, abort, P.status);
-      if (ok && i == 0 && ku > 0)
-        ok = y_wait(&sy->acc_free, (ku - 1) & 1u, abort, P.status);
-      if (ok) ok = y_wait(a_full, g & 1u, abort, P.status);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
-        if (kV) {
-          issue_ts<D>(acc, xy, 64, g_mn + (uint64_t)((gr2.slot * C::kTileBytes) >> 4), i == 0);
-          mma_commit(&sy->g_empty[gr2.slot]);
-        } else {
-          issue_ts<D>(acc, xy, 64, q_mn + (uint64_t)((q2.slot * C::kTileBytes) >> 4), i == 0);
-          mma_commit(&sy->q_empty[q2.slot]);
+      const bool more = i + 1 < u.n;
+      ok = cross::thread_wait(&t_full[tr.slot], tr.phase, abort, P.status);
+      const uint64_t b = t_desc + (uint64_t)((tr.slot * C::kTileBytes) >> 4);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (ok) ok = cross::thread_wait(&a_full[half], g & 1u, abort, P.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_ts_half<D>(acc, xy, 64, b, half, i == 0);
+        if (half) {
+          mma_commit(ts_done);
+          mma_commit(kV ? &sy->g_empty[tr.slot] : &sy->q_empty[tr.slot]);
+          if (!more) mma_commit(&sy->acc_full);
         }
-        mma_commit(ts_done);
-        if (i + 1 == u.n) mma_commit(&sy->acc_full);
       }
-      __syncwarp();
-      q2.next();
-      gr2.next();
-      if (i + 1 < u.n) {
-        ok = y_wait(ts_done, g & 1u, abort, P.status);
-        if (ok) ss(i + 2 == u.n);
+      if (!ok) break;
+      tr.next();
+      if (more) {
+        ok = cross::thread_wait(&b_full[br.slot], br.phase, abort, P.status) &&
+             cross::thread_wait(ts_done, g & 1u, abort, P.status);
+        if (ok) issue(i + 2 == u.n);
       }
     }
     ++ku;
   }
-  if (elect_one()) mma_commit(&sy->drain);  // never exit with MMAs in flight
-  __syncwarp();
+  mma_commit(&sy->drain);  // never exit with MMAs in flight
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
 // Warps 4-11: P^T and dz^T of every step, then the unit's rows of dK and dV.  Thread =
-// state, columns = query rows, whose lse and delta come with dO.
+// state, columns = query rows, whose lse and delta come with dO.  Each half (32 of a
+// group's 64 columns) is handed on as it is written.
 template <int D>
 __device__ void k_softmax(const YParams &P, uint8_t *smem, KSync *sy, uint32_t tmem,
                           volatile int *abort) {
@@ -317,83 +312,79 @@ __device__ void k_softmax(const YParams &P, uint8_t *smem, KSync *sy, uint32_t t
   Ring<C::kG> gr;
   uint32_t g = 0, ku = 0;
   bool live = true;
-  for (uint32_t w = blockIdx.x; w < P.units && live; w += gridDim.x) {
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const KUnit u = k_unit(P, w);
     const int state = u.kt * kTile + row;
     const bool act = state < u.len;
     for (int i = 0; i < u.n; ++i, ++g, gr.next()) {
-      live = y_wait(&sy->g_full[gr.slot], gr.phase, abort, P.status) &&
-             y_wait(&sy->x_full, g & 1u, abort, P.status);
-      if (!live) break;
+      cross::warp_wait(live, &sy->g_full[gr.slot], gr.phase, abort, P.status);
+      cross::warp_wait(live, &sy->x_full, g & 1u, abort, P.status);
       tc_fence_after();
       const float *ld = reinterpret_cast<const float *>(smem + C::kOffL + gr.slot * 1024) +
                         grp * 64;
       float p[64];
+      uint32_t r[2][32], pk[16];
+      tmem_ld32(xa, r[0]);
+      tmem_ld32(xa + 32, r[1]);
+      tmem_wait_ld();
+      reg_fence(r[0]);
+      reg_fence(r[1]);
 #pragma unroll
-      for (int x = 0; x < 64; x += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(xa + x, r);
-        tmem_wait_ld();
-        reg_fence(r);
+      for (int half = 0; half < 2; ++half) {
+        float *ph = p + half * 32;
+        const uint32_t *rh = r[half];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(ld + x + e);
-          unf2(fma2(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), sc2, nl.x), p[x + e],
-               p[x + e + 1]);
-          unf2(fma2(f2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), sc2, nl.y),
-               p[x + e + 2], p[x + e + 3]);
+          const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(ld + half * 32 + e);
+          unf2(fma2(f2(__uint_as_float(rh[e]), __uint_as_float(rh[e + 1])), sc2, nl.x), ph[e],
+               ph[e + 1]);
+          unf2(fma2(f2(__uint_as_float(rh[e + 2]), __uint_as_float(rh[e + 3])), sc2, nl.y),
+               ph[e + 2], ph[e + 3]);
 #pragma unroll
-          for (int y = 0; y < 4; ++y) p[x + e + y] = ex2(p[x + e + y]);
-          pk[e >> 1] = pack_bf16x2(p[x + e], p[x + e + 1]);
-          pk[(e >> 1) + 1] = pack_bf16x2(p[x + e + 2], p[x + e + 3]);
+          for (int y = 0; y < 4; ++y) ph[e + y] = ex2(ph[e + y]);
+          pk[e >> 1] = act ? pack_bf16x2(ph[e], ph[e + 1]) : 0u;
+          pk[(e >> 1) + 1] = act ? pack_bf16x2(ph[e + 2], ph[e + 3]) : 0u;
         }
-        if (!act) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        }
-        tmem_st16(xa + (x >> 1), pk);
+        tmem_st16(xa + half * 16, pk);  // over scores this thread has read
+        tmem_wait_st();
+        tc_fence_before();
+        y_arrive(&sy->p_full[half], lane);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      y_arrive(&sy->p_full, lane);
-      live = y_wait(&sy->y_full, g & 1u, abort, P.status);
-      if (!live) break;
+      cross::warp_wait(live, &sy->y_full, g & 1u, abort, P.status);
       tc_fence_after();
+      tmem_ld32(ya, r[0]);
+      tmem_ld32(ya + 32, r[1]);
+      tmem_wait_ld();
+      reg_fence(r[0]);
+      reg_fence(r[1]);
 #pragma unroll
-      for (int x = 0; x < 64; x += 32) {
-        uint32_t r[32], pk[16];
-        tmem_ld32(ya + x, r);
-        tmem_wait_ld();
-        reg_fence(r);
+      for (int half = 0; half < 2; ++half) {
+        const float *ph = p + half * 32;
+        const uint32_t *rh = r[half];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const ulonglong2 nd = *reinterpret_cast<const ulonglong2 *>(ld + 128 + x + e);
+          const ulonglong2 nd = *reinterpret_cast<const ulonglong2 *>(ld + 128 + half * 32 + e);
           float a, b, c, d;
-          unf2(mul2(f2(p[x + e], p[x + e + 1]),
-                    add2(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), nd.x)),
-               a, b);
-          unf2(mul2(f2(p[x + e + 2], p[x + e + 3]),
-                    add2(f2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), nd.y)),
-               c, d);
-          pk[e >> 1] = pack_bf16x2(a, b);
-          pk[(e >> 1) + 1] = pack_bf16x2(c, d);
+          unf2(mul2(f2(ph[e], ph[e + 1]),
+                    add2(f2(__uint_as_float(rh[e]), __uint_as_float(rh[e + 1])), nd.x)), a, b);
+          unf2(mul2(f2(ph[e + 2], ph[e + 3]),
+                    add2(f2(__uint_as_float(rh[e + 2]), __uint_as_float(rh[e + 3])), nd.y)), c,
+               d);
+          pk[e >> 1] = act ? pack_bf16x2(a, b) : 0u;
+          pk[(e >> 1) + 1] = act ? pack_bf16x2(c, d) : 0u;
         }
-        if (!act) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        }
-        tmem_st16(ya + (x >> 1), pk);
+        tmem_st16(ya + half * 16, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        y_arrive(&sy->z_full[half], lane);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      y_arrive(&sy->z_full, lane);
       if (lane == 0) mbar_arrive(&sy->g_empty[gr.slot]);  // lse and delta have been read
     }
-    if (!live) break;
     // ---- the unit's rows: dV, dK (scaled), or their sums over this run; 0 past the length
     if (u.n > 0) {
-      live = y_wait(&sy->acc_full, ku & 1u, abort, P.status);
-      if (!live) break;
+      cross::warp_wait(live, &sy->acc_full, ku & 1u, abort, P.status);
       tc_fence_after();
     }
     if (u.n > 0 || P.nsplit == 1) {
@@ -480,8 +471,10 @@ __global__ void __launch_bounds__(384, 1)
     }
     mbar_init(&sy->x_full, 1);
     mbar_init(&sy->y_full, 1);
-    mbar_init(&sy->p_full, 8);
-    mbar_init(&sy->z_full, 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sy->p_full[i], 8);
+      mbar_init(&sy->z_full[i], 8);
+    }
     mbar_init(&sy->dv_done, 1);
     mbar_init(&sy->dk_done, 1);
     mbar_init(&sy->acc_full, 2);
@@ -506,9 +499,11 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) k_load<D>(P, &mq, &mk, &mv, &mg, smem, sy, abort);
     __syncwarp();
   } else if (warp == 1) {
-    k_mma<D, true>(P, smem, sy, tmem, abort);
+    if (elect_one()) k_mma<D, true>(P, smem, sy, tmem, abort);
+    __syncwarp();
   } else if (warp == 2) {
-    k_mma<D, false>(P, smem, sy, tmem, abort);
+    if (elect_one()) k_mma<D, false>(P, smem, sy, tmem, abort);
+    __syncwarp();
   } else if (warp >= 4) {
     k_softmax<D>(P, smem, sy, tmem, abort);
   }
@@ -526,13 +521,8 @@ __global__ void __launch_bounds__(384, 1)
 struct QUnit {
   int b, j, qt, len, n;  // n state tiles
 };
-__device__ __noinline__ QUnit q_unit(const YParams &P, uint32_t u) {
-  QUnit r;
-  const uint32_t bj = u / (uint32_t)P.nq;
-  r.qt = (int)(u - bj * (uint32_t)P.nq);
-  r.b = (int)(bj / (uint32_t)P.hk);
-  r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
-  r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
+__device__ __forceinline__ QUnit q_unit(const YParams &P, const cross::Walk &w) {
+  QUnit r{w.b, w.j, w.t, cross::batch_len(P.kv_len, w.b, P.Sk), 0};
   r.n = (r.len + kTile - 1) / kTile;
   return r;
 }
@@ -546,7 +536,9 @@ __device__ void q_load(const YParams &P, const CUtensorMap *mq, const CUtensorMa
   uint32_t ku = 0;
   bool go = true;
   const uint32_t rows = (uint32_t)(P.G * P.tq) * 128 * 2 * C::kBoxes;
-  for (uint32_t w = blockIdx.x; w < P.units && go && !*abort; w += gridDim.x) {
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units && go && !*abort;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const QUnit u = q_unit(P, w);
     if (u.n == 0) continue;
 #pragma unroll 1
@@ -587,7 +579,9 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
   Ring<C::kK> kr;
   uint32_t g = 0, raw = 0;
   bool go = true;
-  for (uint32_t w = blockIdx.x; w < P.units && go; w += gridDim.x) {
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units && go;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const QUnit u = q_unit(P, w);
     if (lane == 0) cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     for (int t = 0; t < u.n && go; ++t, ++g, kr.next()) {
@@ -641,103 +635,89 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
   }
 }
 
-// Warp 1: X = Q K^T and Y = dO V^T of every step, each over the last step's once the
-// softmax warps hold that.
+// Warp 1: all products: X = Q K^T, Y = dO V^T of every step, each over the last step's
+// once the softmax warps hold that, and dQ += dz K of the step before.  A step's X is
+// committed after the dQ of two steps before, so x_full also says that the dz buffer is
+// free; and dz of a unit's first step comes after the last unit's rows were read, so it
+// says that dQ may be written over.  Y of a unit's first step comes after that dQ, since
+// it may still wait for dO.
 template <int D>
-__device__ void q_ss(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
-                     volatile int *abort) {
+__device__ void q_mma(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
+                      volatile int *abort) {
   using C = YCfg<D>;
   const uint64_t q_desc = smem_desc_sw128(smem_u32(smem), 16, 1024);
   const uint64_t g_desc = smem_desc_sw128(smem_u32(smem + C::kOffG2), 16, 1024);
   const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + C::kOffK2), 16, 1024);
+  const uint64_t k_mn = smem_desc_sw128(smem_u32(smem + C::kOffK2), C::kBox, 1024);
   const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffV2), 16, 1024);
   Ring<2> q;
-  Ring<C::kK> kr;
-  uint32_t g = 0, ku = 0;
-  bool ok = true;
-  for (uint32_t w = blockIdx.x; w < P.units && ok; w += gridDim.x) {
+  Ring<C::kK> kr, kd;           // of X's step, and of dQ's
+  uint32_t g = 0, ku = 0;       // steps of X so far
+  int left = 0;                 // states from the first of dQ's next tile on
+  bool first = true, ok = true;  // dQ's next step begins a unit
+  auto issue_dq = [&](bool last) {  // of step g - 1
+    ok = cross::thread_wait(&sy->z_full[(g - 1) & 1u], ((g - 1) >> 1) & 1u, abort, P.status);
+    if (!ok) return;
+    tc_fence_after();
+    const uint32_t a = tmem + C::kZ + ((g - 1) & 1u) * 64;
+    const uint64_t b = k_mn + (uint64_t)((kd.slot * C::kTileBytes) >> 4);
+    if (left > kTile - 16) {
+      issue_ts<D>(tmem + C::kDQ, a, 32, b, first);
+    } else {  // the batch's last tile: its 16-state steps only
+#pragma unroll 1
+      for (int kk = 0; kk * 16 < left; ++kk)
+        mma_ts(tmem + C::kDQ, a + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), C::kIdTS,
+               kk > 0 || !first ? 1u : 0u);
+    }
+    mma_commit(&sy->k_empty[kd.slot]);
+    if (last) mma_commit(&sy->acc_full);
+    kd.next();
+    first = last;
+  };
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units && ok;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const QUnit u = q_unit(P, w);
     if (u.n == 0) continue;
-    ok = y_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
-    for (int t = 0; t < u.n && ok; ++t, ++g, kr.next()) {
-      ok = y_wait(&sy->k_full[kr.slot], kr.phase, abort, P.status) &&
-           y_wait(&sy->x_free, (g & 1u) ^ 1u, abort, P.status);
+    ok = cross::thread_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
+    for (int t = 0; t < u.n && ok; ++t, ++g) {
+      ok = cross::thread_wait(&sy->k_full[kr.slot], kr.phase, abort, P.status) &&
+           cross::thread_wait(&sy->x_free, (g & 1u) ^ 1u, abort, P.status);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        issue_ss<D>(tmem + C::kX2, q_desc + (uint64_t)((q.slot * C::kTileBytes) >> 4),
-                    k_desc + (uint64_t)((kr.slot * C::kTileBytes) >> 4), C::kIdSS | P.neg);
-        mma_commit(&sy->x_full);
+      issue_ss<D>(tmem + C::kX2, q_desc + (uint64_t)((q.slot * C::kTileBytes) >> 4),
+                  k_desc + (uint64_t)((kr.slot * C::kTileBytes) >> 4), C::kIdSS | P.neg);
+      mma_commit(&sy->x_full);
+      kr.next();
+      if (t == 0) {
+        if (g > 0) issue_dq(true);  // the last unit's last step
+        ok = ok && cross::thread_wait(&sy->g_full, ku & 1u, abort, P.status);
       }
-      __syncwarp();
-      if (t == 0) ok = y_wait(&sy->g_full, ku & 1u, abort, P.status);
-      ok = ok && y_wait(&sy->v_full, g & 1u, abort, P.status) &&
-           y_wait(&sy->y_free, (g & 1u) ^ 1u, abort, P.status);
+      ok = ok && cross::thread_wait(&sy->v_full, g & 1u, abort, P.status) &&
+           cross::thread_wait(&sy->y_free, (g & 1u) ^ 1u, abort, P.status);
       if (!ok) break;
       tc_fence_after();
-      if (elect_one()) {
-        issue_ss<D>(tmem + C::kY2, g_desc, v_desc, C::kIdSS);
-        mma_commit(&sy->y_full);
-        mma_commit(&sy->v_empty);
-        if (t + 1 == u.n) mma_commit(&sy->g_empty);
-      }
-      __syncwarp();
+      issue_ss<D>(tmem + C::kY2, g_desc, v_desc, C::kIdSS);
+      mma_commit(&sy->y_full);
+      mma_commit(&sy->v_empty);
+      if (t + 1 == u.n) mma_commit(&sy->g_empty);
+      if (t > 0) issue_dq(false);
+      left = u.len - t * kTile;
     }
     q.next();
     ++ku;
   }
-  if (elect_one()) mma_commit(&sy->drain);
-  __syncwarp();
-  mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
-}
-
-// Warp 2: dQ += dz K.
-template <int D>
-__device__ void q_ts(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
-                     volatile int *abort) {
-  using C = YCfg<D>;
-  const uint64_t k_mn = smem_desc_sw128(smem_u32(smem + C::kOffK2), C::kBox, 1024);
-  Ring<C::kK> kr;
-  uint32_t g = 0, ku = 0;
-  bool ok = true;
-  for (uint32_t w = blockIdx.x; w < P.units && ok; w += gridDim.x) {
-    const QUnit u = q_unit(P, w);
-    if (u.n == 0) continue;
-    for (int t = 0; t < u.n && ok; ++t, ++g, kr.next()) {
-      ok = y_wait(&sy->k_full[kr.slot], kr.phase, abort, P.status);
-      if (ok && t == 0 && ku > 0) ok = y_wait(&sy->acc_free, (ku - 1) & 1u, abort, P.status);
-      if (ok) ok = y_wait(&sy->z_full[g & 1u], (g >> 1) & 1u, abort, P.status);
-      if (!ok) break;
-      tc_fence_after();
-      const int left = u.len - t * kTile;
-      if (elect_one()) {
-        const uint32_t a = tmem + C::kZ + (g & 1u) * 64;
-        const uint64_t b = k_mn + (uint64_t)((kr.slot * C::kTileBytes) >> 4);
-        if (left > kTile - 16) {
-          issue_ts<D>(tmem + C::kDQ, a, 32, b, t == 0);
-        } else {  // the batch's last tile: its 16-state steps only
-#pragma unroll 1
-          for (int kk = 0; kk * 16 < left; ++kk)
-            mma_ts(tmem + C::kDQ, a + kk * 8, b + (uint64_t)((kk * 16 * 128) >> 4), C::kIdTS,
-                   kk > 0 || t > 0 ? 1u : 0u);
-        }
-        mma_commit(&sy->dq_done[g & 1u]);
-        mma_commit(&sy->k_empty[kr.slot]);
-        if (t + 1 == u.n) mma_commit(&sy->acc_full);
-      }
-      __syncwarp();
-    }
-    ++ku;
-  }
-  if (elect_one()) mma_commit(&sy->drain);
-  __syncwarp();
+  if (ok && g > 0) issue_dq(true);
+  mma_commit(&sy->drain);
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
 __device__ __forceinline__ void q_group_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Warps 4-11: dz of every step, then the unit's rows of dQ (through the unit's Q tile,
-// which no MMA reads any more, and out by TMA).  Thread = query row, columns = states.
+// Warps 4-11: dz of every step, and the units' rows of dQ (through the unit's Q tile,
+// which no MMA reads any more, and out by TMA).  Thread = query row, columns = states.  A
+// unit's rows are written in the first step of the next unit, after its exponentials, so
+// that the last dQ product runs meanwhile.
 template <int D>
 __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem, QSync *sy,
                           uint32_t tmem, volatile int *abort) {
@@ -748,26 +728,80 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
   const uint64_t sc2 = f2(P.scale_log2, P.scale_log2);
   const int tok = r64 / P.G, head = r64 - tok * P.G;
   uint32_t g = 0, ku = 0;
-  bool live = true;     // false after a wait gave up: keep meeting the barrier, do no work
+  bool live = true;
   bool stored = false;  // the last unit's tile is still to be handed back to the loader
-  for (uint32_t w = blockIdx.x; w < P.units; w += gridDim.x) {
-    const QUnit u = q_unit(P, w);
-    const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok, hh = u.j * P.G + head;
-    if (u.n == 0) {
+  int last_qt = 0, last_j = 0, last_b = 0;  // the unit whose rows are to be written (ku > 0)
+  auto write_rows = [&]() {                 // of unit ku - 1
+    cross::warp_wait(live, &sy->acc_full, (ku - 1) & 1u, abort, P.status);
+    tc_fence_after();
+    uint8_t *base = smem + ((ku - 1) & 1u) * C::kTileBytes, *tile = base + row * 128;
+#pragma unroll 1
+    for (int x = 0; x < D / 32; ++x) {  // 16 columns of this group's D / 2
+      const int c = grp * (D / 2) + x * 16;
+      uint32_t t[16];
+      tmem_ld16(at + C::kDQ + c, t);
+      tmem_wait_ld();
+      reg_fence16(t);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t v[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+          v[y] = pack_bf16x2(__uint_as_float(t[8 * e + 2 * y]) * P.scale,
+                             __uint_as_float(t[8 * e + 2 * y + 1]) * P.scale);
+        const int piece = (c >> 3) + e;  // 16-byte piece of the row, swizzled in its box
+        *reinterpret_cast<uint4 *>(tile + (piece >> 3) * C::kBox +
+                                   (((piece & 7) ^ (row & 7)) << 4)) =
+            make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+    fence_async_smem();
+    q_group_sync();
+    if (threadIdx.x == 128 && live) {
+#pragma unroll 1
+      for (int x = 0; x < 2 * C::kBoxes; ++x) {
+        const int t0 = (last_qt * 2 + (x & 1)) * P.tq;
+        if (t0 < P.Sq)
+          tma_store_4d(mo, base + (x >> 1) * C::kBox + (x & 1) * 64 * 128, (x >> 1) * 64,
+                       last_j * P.G, t0, last_b);
+      }
+      bulk_commit();
+    }
+    stored = true;
+  };
+  auto rows_at = [&](const cross::Walk &w) {
+    return ((size_t)((uint32_t)w.b * P.hk + w.j) * P.nq + w.t) * 128 + row;
+  };
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  float nl_next = 0.f, nd_next = 0.f;
+  if (blockIdx.x < P.units) {
+    const size_t r = rows_at(w);
+    nl_next = __ldg(P.nlse + r);
+    nd_next = __ldg(P.ndelta + r);
+  }
+  for (uint32_t i0 = blockIdx.x; i0 < P.units; i0 += gridDim.x) {
+    const QUnit c = q_unit(P, w);
+    const float nl = nl_next, nd = nd_next;
+    cross::walk_next(P.walk, w);
+    if (i0 + gridDim.x < P.units) {  // the next unit's rows, long before they are needed
+      const size_t r = rows_at(w);
+      nl_next = __ldg(P.nlse + r);
+      nd_next = __ldg(P.ndelta + r);
+    }
+    if (c.n == 0) {
+      const int token = (c.qt * 2 + (row >> 6)) * P.tq + tok, hh = c.j * P.G + head;
       if (tok < P.tq && token < P.Sq) {
         uint4 *o = reinterpret_cast<uint4 *>(
-            P.dq + (((size_t)u.b * P.Sq + token) * P.h + hh) * D + grp * (D / 2));
+            P.dq + (((size_t)c.b * P.Sq + token) * P.h + hh) * D + grp * (D / 2));
 #pragma unroll 1
         for (int e = 0; e < D / 16; ++e) o[e] = make_uint4(0u, 0u, 0u, 0u);
       }
       continue;
     }
-    const size_t lrow = ((size_t)((uint32_t)u.b * P.hk + u.j) * P.nq + u.qt) * 128 + row;
-    const float nl = __ldg(P.nlse + lrow), nd = __ldg(P.ndelta + lrow);
     const uint64_t nl2 = f2(nl, nl), nd2 = f2(nd, nd);
-    for (int t = 0; t < u.n; ++t, ++g) {
-      const int mine = u.len - t * kTile - grp * 64;  // own columns that are states
-      live = live && y_wait(&sy->x_full, g & 1u, abort, P.status);
+    for (int t = 0; t < c.n; ++t, ++g) {
+      const int mine = c.len - t * kTile - grp * 64;  // own columns that are states
+      cross::warp_wait(live, &sy->x_full, g & 1u, abort, P.status);
       tc_fence_after();
       uint32_t x0[32], x1[32];
       tmem_ld32(at + C::kX2 + grp * 64, x0);
@@ -789,7 +823,8 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
         p[32 + e] = ex2(p[32 + e]);
         p[33 + e] = ex2(p[33 + e]);
       }
-      live = live && y_wait(&sy->y_full, g & 1u, abort, P.status);
+      if (t == 0 && ku > 0) write_rows();
+      cross::warp_wait(live, &sy->y_full, g & 1u, abort, P.status);
       tc_fence_after();
       tmem_ld32(at + C::kY2 + grp * 64, x0);
       tmem_ld32(at + C::kY2 + grp * 64 + 32, x1);
@@ -798,9 +833,6 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
       reg_fence(x1);
       tc_fence_before();
       y_arrive(&sy->y_free, lane);
-      if (g >= 2)  // the dz buffer was read by step g - 2
-        live = live && y_wait(&sy->dq_done[g & 1u], ((g - 2) >> 1) & 1u, abort, P.status);
-      tc_fence_after();
       uint32_t pk[16];
       const uint32_t za = at + C::kZ + (g & 1u) * 64 + grp * 32;
 #pragma unroll
@@ -826,56 +858,18 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
       tmem_wait_st();
       tc_fence_before();
       y_arrive(&sy->z_full[g & 1u], lane);
-      if (stored && threadIdx.x == 128) {  // the store has long read the tile
-        bulk_wait_read();
-        mbar_arrive(&sy->q_empty[(ku & 1u) ^ 1u]);
-      }
-      stored = false;
-    }
-    // ---- the unit's rows
-    live = live && y_wait(&sy->acc_full, ku & 1u, abort, P.status);
-    tc_fence_after();
-    uint8_t *tile = smem + (ku & 1u) * C::kTileBytes + row * 128;
-#pragma unroll 1
-    for (int x = 0; x < D / 32; ++x) {  // 16 columns of this group's D / 2
-      const int c = grp * (D / 2) + x * 16;
-      uint32_t t[16];
-      tmem_ld16(at + C::kDQ + c, t);
-      tmem_wait_ld();
-      reg_fence16(t);
-      if (x + 1 == D / 32) {
-        tc_fence_before();
-        y_arrive(&sy->acc_free, lane);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t v[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-          v[y] = pack_bf16x2(__uint_as_float(t[8 * e + 2 * y]) * P.scale,
-                             __uint_as_float(t[8 * e + 2 * y + 1]) * P.scale);
-        const int piece = (c >> 3) + e;  // 16-byte piece of the row, swizzled in its box
-        *reinterpret_cast<uint4 *>(tile + (piece >> 3) * C::kBox +
-                                   (((piece & 7) ^ (row & 7)) << 4)) =
-            make_uint4(v[0], v[1], v[2], v[3]);
+      if (stored && (t == 1 || t + 1 == c.n)) {  // the store has read the tile by now
+        if (threadIdx.x == 128) {
+          bulk_wait_read();
+          mbar_arrive(&sy->q_empty[(ku & 1u) ^ 1u]);
+        }
+        stored = false;
       }
     }
-    fence_async_smem();
-    q_group_sync();
-    if (threadIdx.x == 128 && live) {
-#pragma unroll 1
-      for (int x = 0; x < 2 * C::kBoxes; ++x) {
-        const int t0 = (u.qt * 2 + (x & 1)) * P.tq;
-        if (t0 < P.Sq)
-          tma_store_4d(mo, smem + (ku & 1u) * C::kTileBytes + (x >> 1) * C::kBox +
-                               (x & 1) * 64 * 128,
-                       (x >> 1) * 64, u.j * P.G, t0, u.b);
-      }
-      bulk_commit();
-    }
-    stored = true;
+    last_qt = c.qt, last_j = c.j, last_b = c.b;
     ++ku;
   }
+  if (ku > 0) write_rows();
   if (threadIdx.x == 128) bulk_wait_all();
 }
 
@@ -899,7 +893,6 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&sy->q_full[i], 1);
       mbar_init(&sy->q_empty[i], 1);
       mbar_init(&sy->z_full[i], 8);
-      mbar_init(&sy->dq_done[i], 1);
     }
     for (int i = 0; i < C::kK; ++i) {
       mbar_init(&sy->k_full[i], 1);
@@ -915,8 +908,7 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(&sy->x_free, 8);
     mbar_init(&sy->y_free, 8);
     mbar_init(&sy->acc_full, 1);
-    mbar_init(&sy->acc_free, 8);
-    mbar_init(&sy->drain, 2);
+    mbar_init(&sy->drain, 1);
     sy->abort = 0;
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
@@ -937,13 +929,12 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) q_load<D>(P, &mq, &mg, smem, sy, abort);
     __syncwarp();
   } else if (warp == 1) {
-    q_ss<D>(P, smem, sy, tmem, abort);
-  } else if (warp == 2) {
-    q_ts<D>(P, smem, sy, tmem, abort);
+    if (elect_one()) q_mma<D>(P, smem, sy, tmem, abort);
+    __syncwarp();
   } else if (warp == 3) {
     q_load_kv<D>(P, &mk, &mv, smem, sy, abort);
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     q_softmax<D>(P, &mo, smem, sy, tmem, abort);
   }
   tc_fence_before();
@@ -997,6 +988,7 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
                                   y_smem_bytes<D, false>())) != cudaSuccess)
     return err;
   unsigned grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
+  p.walk = cross::walk_step(grid, p.nsplit, p.nkt, s.hk);
   err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), y_smem_bytes<D, false>(), st, mq, mk, mv,
                    mg, p);
   if (err != cudaSuccess) return err;
@@ -1009,6 +1001,7 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
                                   y_smem_bytes<D, true>())) != cudaSuccess)
     return err;
   grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
+  p.walk = cross::walk_step(grid, 1, p.nq, s.hk);
   return launch_pdl(kern2, dim3(grid), dim3(C::kThreads), y_smem_bytes<D, true>(), st, mq, mk, mv,
                     mg, mo, p);
 }

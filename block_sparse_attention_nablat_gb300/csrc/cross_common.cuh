@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "internal.h"
+#include "tc_ptx.cuh"
 
 namespace nabla {
 namespace cross {
@@ -27,6 +28,61 @@ inline Packing packing(const CrossShape &s) {
   p.tq = 64 / p.G;
   p.nsub = (s.Sq + p.tq - 1) / p.tq;
   return p;
+}
+
+// One thread's wait, and a whole warp's.  A lane whose wait gave up waits no more but goes
+// on through its loops, over whatever the buffers hold: later waits return at once, the
+// role meets its barriers, and the status word says that the results are void.  So the
+// lanes need no vote on each wait, which cost the softmax warps 100 cycles and more.
+__device__ __forceinline__ bool thread_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                            int *status) {
+  return tc::mbar_wait_small(bar, parity, abort, status, kDevTimeout);
+}
+__device__ __forceinline__ void warp_wait(bool &live, uint64_t *bar, uint32_t parity,
+                                          volatile int *abort, int *status) {
+  if (live) live = tc::mbar_wait_small(bar, parity, abort, status, kDevTimeout);
+  __syncwarp();
+}
+
+// The work units of a kernel, numbered with the run of the split axis first, then the
+// tile, the key head and the batch; a CTA takes every gridDim.x-th.  The divisions are
+// done once, for the CTA's first unit (and on the host, for the step): a unit of a few
+// tiles is short enough for them to show.
+struct Walk {
+  int sp, t, j, b;
+};
+struct WalkStep {
+  int nsplit, nt, hk;  // radices
+  int sp, t, j, b;     // digits of gridDim.x
+};
+inline WalkStep walk_step(unsigned grid, int nsplit, int nt, int hk) {
+  WalkStep s{nsplit, nt, hk, 0, 0, 0, 0};
+  s.sp = (int)(grid % nsplit);
+  grid /= nsplit;
+  s.t = (int)(grid % nt);
+  grid /= nt;
+  s.j = (int)(grid % hk);
+  s.b = (int)(grid / hk);
+  return s;
+}
+__device__ __forceinline__ Walk walk_start(const WalkStep &s, uint32_t u) {
+  Walk w;
+  w.sp = (int)(u % (uint32_t)s.nsplit);
+  u /= (uint32_t)s.nsplit;
+  w.t = (int)(u % (uint32_t)s.nt);
+  u /= (uint32_t)s.nt;
+  w.j = (int)(u % (uint32_t)s.hk);
+  w.b = (int)(u / (uint32_t)s.hk);
+  return w;
+}
+__device__ __forceinline__ void walk_next(const WalkStep &s, Walk &w) {
+  w.sp += s.sp;
+  w.t += s.t;
+  w.j += s.j;
+  w.b += s.b;
+  if (w.sp >= s.nsplit) w.sp -= s.nsplit, ++w.t;
+  if (w.t >= s.nt) w.t -= s.nt, ++w.j;
+  if (w.j >= s.hk) w.j -= s.hk, ++w.b;
 }
 
 __device__ __forceinline__ int batch_len(const int32_t *kv_len, int b, int Sk) {
