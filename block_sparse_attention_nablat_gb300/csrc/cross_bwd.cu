@@ -32,39 +32,46 @@ __device__ __forceinline__ float dot8(const __nv_bfloat16 *a, const __nv_bfloat1
 }
 
 // -lse and -delta = -<dout, o> of the packed rows [B, hk, nsub, 64]: -inf and 0 where a
-// row is none or has no states, so that its P is 0.  D / 8 lanes a row, 16 bytes a lane;
-// HBM-bound (o and dout read once).
+// row is none or has no states, so that its P is 0.  A block takes a 64-row subtile,
+// D / 8 lanes a row, 16 bytes of bf16 a lane; HBM-bound (o and dout read once), so a
+// thread's rows are all in flight at once.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
     cross_prep_kernel(const T *__restrict__ o, const nabla_strides o_st,
                       const T *__restrict__ dout, const nabla_strides g_st,
                       const float *__restrict__ lse, int Sq, int h, int hk, int G, int tq,
-                      int nsub, long rows, float *__restrict__ nlse, float *__restrict__ ndelta) {
-  constexpr int kLanes = D / 8;
-  const int lane = threadIdx.x % kLanes;
+                      int nsub, float *__restrict__ nlse, float *__restrict__ ndelta) {
+  constexpr int kLanes = D / 8, kPass = 256 / kLanes, kRows = 64 / kPass;
+  const int lane = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
   pdl_launch_dependents();
+  const uint32_t bj = blockIdx.x / (uint32_t)nsub, sub = blockIdx.x - bj * nsub;
+  const uint32_t b = bj / (uint32_t)hk, j = bj - b * hk;
+  o += b * o_st.batch + lane * 8;
+  dout += b * g_st.batch + lane * 8;
+  lse += (size_t)b * h * Sq;
   pdl_wait();
-  const long row = ((long)blockIdx.x * 256 + threadIdx.x) / kLanes;
-  if (row >= rows) return;  // a whole group of kLanes lanes
-  const int r = (int)(row & 63);
-  const long sb = row >> 6;
-  const long bj = sb / nsub;
-  const int sub = (int)(sb - bj * nsub);
-  const int b = (int)(bj / hk), j = (int)(bj - (long)b * hk);
-  const int t = r / G, token = sub * tq + t, hh = j * G + r - t * G;
-  const bool ok = t < tq && token < Sq;
-  float s = 0.f, l = -INFINITY;
-  if (ok) {
-    s = dot8(dout + b * g_st.batch + token * g_st.token + hh * g_st.head + lane * 8,
-             o + b * o_st.batch + token * o_st.token + hh * o_st.head + lane * 8);
-    l = lse[((size_t)b * h + hh) * Sq + token];
-  }
-  const unsigned mask = kLanes == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+  float s[kRows], l[kRows];
 #pragma unroll
-  for (int x = kLanes / 2; x; x >>= 1) s += __shfl_xor_sync(mask, s, x);
-  if (lane == 0) {
-    nlse[row] = l == -INFINITY ? -INFINITY : -l;
-    ndelta[row] = -s;
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t r = r0 + i * kPass, t = r / (uint32_t)G;
+    const int token = (int)(sub * tq + t), hh = (int)(j * G + r - t * G);
+    s[i] = 0.f;
+    l[i] = -INFINITY;
+    if (t < (uint32_t)tq && token < Sq) {
+      s[i] = dot8(dout + token * g_st.token + hh * g_st.head,
+                  o + token * o_st.token + hh * o_st.head);
+      if (lane == 0) l[i] = lse[(size_t)hh * Sq + token];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+    for (int x = kLanes / 2; x; x >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], x);
+    if (lane == 0) {
+      const size_t row = (size_t)blockIdx.x * 64 + r0 + i * kPass;
+      nlse[row] = l[i] == -INFINITY ? -INFINITY : -l[i];
+      ndelta[row] = -s[i];
+    }
   }
 }
 
@@ -102,12 +109,10 @@ __global__ void __launch_bounds__(256)
 template <typename T, int D>
 cudaError_t launch_prep(const CrossArgs &a, const cross::Packing &pk, int nsub, float *nlse,
                         float *ndelta, cudaStream_t st) {
-  const long rows = (long)a.s.B * a.s.hk * nsub * 64;
-  const long blocks = (rows * (D / 8) + 255) / 256;
-  return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)blocks), dim3(256), 0, st,
-                    static_cast<const T *>(a.of), a.o_st, static_cast<const T *>(a.dout), a.dout_st,
-                    (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub, rows, nlse,
-                    ndelta);
+  return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)(a.s.B * a.s.hk * nsub)), dim3(256),
+                    0, st, static_cast<const T *>(a.of), a.o_st, static_cast<const T *>(a.dout),
+                    a.dout_st, (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub,
+                    nlse, ndelta);
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }

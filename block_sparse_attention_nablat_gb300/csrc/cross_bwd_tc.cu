@@ -82,7 +82,7 @@ struct KSync {
 };
 struct QSync {
   uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw, v_full, v_empty;
-  uint64_t x_full, y_full, x_free, y_free, z_full[2], acc_full, drain;
+  uint64_t x_full, y_full, x_free, y_free, z_full[2], acc_full, out_full, drain;
   uint32_t tmem_slot;
   int abort;
 };
@@ -226,9 +226,17 @@ __device__ void k_load(const YParams &P, const CUtensorMap *mq, const CUtensorMa
   }
 }
 
+// A wait of a whole warp that goes on in step.
+__device__ __forceinline__ bool k_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                       int *status) {
+  return __all_sync(0xffffffffu, cross::thread_wait(bar, parity, abort, status));
+}
+
 // Warp 1 (kV): dV += P^T dO and X = K Q^T.  Warp 2: dK += dz^T Q and Y = V dO^T.  Each
 // chain's SS product of a step goes over the columns its TS product of the step before
-// has read; the TS product starts on the first half of P or dz.
+// has read; the TS product starts on the first half of P or dz.  (As single threads, the form of
+// the other kernels, the two chains are 4% slower: 288 against 280 us at 32768 x 512,
+// 2286 against 2203 at 32768 x 4096, 24 heads, D 128.)
 template <int D, bool kV>
 __device__ void k_mma(const YParams &P, uint8_t *smem, KSync *sy, uint32_t tmem,
                       volatile int *abort) {
@@ -248,11 +256,14 @@ __device__ void k_mma(const YParams &P, uint8_t *smem, KSync *sy, uint32_t tmem,
   bool ok = true;
   auto issue = [&](bool last) {  // the SS product of the next step
     tc_fence_after();
-    issue_ss<D>(xy, a_desc, b_desc + (uint64_t)((br.slot * C::kTileBytes) >> 4),
-                kV ? C::kIdSS | P.neg : C::kIdSS);
-    mma_commit(ss_full);
-    if (!kV) mma_commit(&sy->g_empty[br.slot]);
-    if (last) mma_commit(&sy->kv_empty);
+    if (elect_one()) {
+      issue_ss<D>(xy, a_desc, b_desc + (uint64_t)((br.slot * C::kTileBytes) >> 4),
+                  kV ? C::kIdSS | P.neg : C::kIdSS);
+      mma_commit(ss_full);
+      if (!kV) mma_commit(&sy->g_empty[br.slot]);
+      if (last) mma_commit(&sy->kv_empty);
+    }
+    __syncwarp();
     br.next();
   };
   cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
@@ -260,40 +271,44 @@ __device__ void k_mma(const YParams &P, uint8_t *smem, KSync *sy, uint32_t tmem,
        i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const KUnit u = k_unit(P, w);
     if (u.n == 0) continue;
-    ok = cross::thread_wait(&sy->kv_full, ku & 1u, abort, P.status) &&
-         cross::thread_wait(&b_full[br.slot], br.phase, abort, P.status) &&
-         (g == 0 || cross::thread_wait(ts_done, (g - 1) & 1u, abort, P.status));
+    ok = k_wait(&sy->kv_full, ku & 1u, abort, P.status) &&
+         k_wait(&b_full[br.slot], br.phase, abort, P.status) &&
+         (g == 0 || k_wait(ts_done, (g - 1) & 1u, abort, P.status));
     if (!ok) break;
     issue(u.n == 1);
     // the last unit's rows of dK and dV have been read
-    if (ku > 0) ok = cross::thread_wait(&sy->acc_free, (ku - 1) & 1u, abort, P.status);
+    if (ku > 0) ok = k_wait(&sy->acc_free, (ku - 1) & 1u, abort, P.status);
     for (int i = 0; i < u.n && ok; ++i, ++g) {
       const bool more = i + 1 < u.n;
-      ok = cross::thread_wait(&t_full[tr.slot], tr.phase, abort, P.status);
+      ok = k_wait(&t_full[tr.slot], tr.phase, abort, P.status);
       const uint64_t b = t_desc + (uint64_t)((tr.slot * C::kTileBytes) >> 4);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        if (ok) ok = cross::thread_wait(&a_full[half], g & 1u, abort, P.status);
+        if (ok) ok = k_wait(&a_full[half], g & 1u, abort, P.status);
         if (!ok) break;
         tc_fence_after();
-        issue_ts_half<D>(acc, xy, 64, b, half, i == 0);
-        if (half) {
-          mma_commit(ts_done);
-          mma_commit(kV ? &sy->g_empty[tr.slot] : &sy->q_empty[tr.slot]);
-          if (!more) mma_commit(&sy->acc_full);
+        if (elect_one()) {
+          issue_ts_half<D>(acc, xy, 64, b, half, i == 0);
+          if (half) {
+            mma_commit(ts_done);
+            mma_commit(kV ? &sy->g_empty[tr.slot] : &sy->q_empty[tr.slot]);
+            if (!more) mma_commit(&sy->acc_full);
+          }
         }
+        __syncwarp();
       }
       if (!ok) break;
       tr.next();
       if (more) {
-        ok = cross::thread_wait(&b_full[br.slot], br.phase, abort, P.status) &&
-             cross::thread_wait(ts_done, g & 1u, abort, P.status);
+        ok = k_wait(&b_full[br.slot], br.phase, abort, P.status) &&
+             k_wait(ts_done, g & 1u, abort, P.status);
         if (ok) issue(i + 2 == u.n);
       }
     }
     ++ku;
   }
-  mma_commit(&sy->drain);  // never exit with MMAs in flight
+  if (elect_one()) mma_commit(&sy->drain);  // never exit with MMAs in flight
+  __syncwarp();
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
@@ -499,11 +514,9 @@ __global__ void __launch_bounds__(384, 1)
     if (lane == 0) k_load<D>(P, &mq, &mk, &mv, &mg, smem, sy, abort);
     __syncwarp();
   } else if (warp == 1) {
-    if (elect_one()) k_mma<D, true>(P, smem, sy, tmem, abort);
-    __syncwarp();
+    k_mma<D, true>(P, smem, sy, tmem, abort);
   } else if (warp == 2) {
-    if (elect_one()) k_mma<D, false>(P, smem, sy, tmem, abort);
-    __syncwarp();
+    k_mma<D, false>(P, smem, sy, tmem, abort);
   } else if (warp >= 4) {
     k_softmax<D>(P, smem, sy, tmem, abort);
   }
@@ -712,15 +725,42 @@ __device__ void q_mma(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
   mbar_wait_small(&sy->drain, 0, nullptr, P.status, kDevTimeout);
 }
 
-__device__ __forceinline__ void q_group_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+// Warp 2: hands the units' rows from their Q tiles to the TMA, and the tiles back to the
+// loader once they have been read.
+template <int D>
+__device__ void q_store(const YParams &P, const CUtensorMap *mo, const uint8_t *smem, QSync *sy,
+                        volatile int *abort) {
+  using C = YCfg<D>;
+  uint32_t ku = 0;
+  cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
+  for (uint32_t i0 = blockIdx.x; i0 < P.units;
+       i0 += gridDim.x, cross::walk_next(P.walk, w)) {
+    const QUnit u = q_unit(P, w);
+    if (u.n == 0) continue;
+    if (!cross::thread_wait(&sy->out_full, ku & 1u, abort, P.status)) break;
+    const uint8_t *tile = smem + (ku & 1u) * C::kTileBytes;
+#pragma unroll 1
+    for (int x = 0; x < 2 * C::kBoxes; ++x) {
+      const int t0 = (u.qt * 2 + (x & 1)) * P.tq;
+      if (t0 < P.Sq)
+        tma_store_4d(mo, tile + (x >> 1) * C::kBox + (x & 1) * 64 * 128, (x >> 1) * 64,
+                     u.j * P.G, t0, u.b);
+    }
+    bulk_commit();
+    bulk_wait_read();
+    mbar_arrive(&sy->q_empty[ku & 1u]);
+    ++ku;
+  }
+  bulk_wait_all();
+}
 
 // Warps 4-11: dz of every step, and the units' rows of dQ (through the unit's Q tile,
-// which no MMA reads any more, and out by TMA).  Thread = query row, columns = states.  A
+// which no MMA reads any more).  Thread = query row, columns = states.  A
 // unit's rows are written in the first step of the next unit, after its exponentials, so
 // that the last dQ product runs meanwhile.
 template <int D>
-__device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem, QSync *sy,
-                          uint32_t tmem, volatile int *abort) {
+__device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
+                          volatile int *abort) {
   using C = YCfg<D>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = (warp - 4) >> 2, q4 = warp & 3, row = q4 * 32 + lane, r64 = row & 63;
@@ -729,12 +769,10 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
   const int tok = r64 / P.G, head = r64 - tok * P.G;
   uint32_t g = 0, ku = 0;
   bool live = true;
-  bool stored = false;  // the last unit's tile is still to be handed back to the loader
-  int last_qt = 0, last_j = 0, last_b = 0;  // the unit whose rows are to be written (ku > 0)
-  auto write_rows = [&]() {                 // of unit ku - 1
+  auto write_rows = [&]() {  // of unit ku - 1, over its Q
     cross::warp_wait(live, &sy->acc_full, (ku - 1) & 1u, abort, P.status);
     tc_fence_after();
-    uint8_t *base = smem + ((ku - 1) & 1u) * C::kTileBytes, *tile = base + row * 128;
+    uint8_t *tile = smem + ((ku - 1) & 1u) * C::kTileBytes + row * 128;
 #pragma unroll 1
     for (int x = 0; x < D / 32; ++x) {  // 16 columns of this group's D / 2
       const int c = grp * (D / 2) + x * 16;
@@ -756,18 +794,7 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
       }
     }
     fence_async_smem();
-    q_group_sync();
-    if (threadIdx.x == 128 && live) {
-#pragma unroll 1
-      for (int x = 0; x < 2 * C::kBoxes; ++x) {
-        const int t0 = (last_qt * 2 + (x & 1)) * P.tq;
-        if (t0 < P.Sq)
-          tma_store_4d(mo, base + (x >> 1) * C::kBox + (x & 1) * 64 * 128, (x >> 1) * 64,
-                       last_j * P.G, t0, last_b);
-      }
-      bulk_commit();
-    }
-    stored = true;
+    y_arrive(&sy->out_full, lane);
   };
   auto rows_at = [&](const cross::Walk &w) {
     return ((size_t)((uint32_t)w.b * P.hk + w.j) * P.nq + w.t) * 128 + row;
@@ -858,19 +885,10 @@ __device__ void q_softmax(const YParams &P, const CUtensorMap *mo, uint8_t *smem
       tmem_wait_st();
       tc_fence_before();
       y_arrive(&sy->z_full[g & 1u], lane);
-      if (stored && (t == 1 || t + 1 == c.n)) {  // the store has read the tile by now
-        if (threadIdx.x == 128) {
-          bulk_wait_read();
-          mbar_arrive(&sy->q_empty[(ku & 1u) ^ 1u]);
-        }
-        stored = false;
-      }
     }
-    last_qt = c.qt, last_j = c.j, last_b = c.b;
     ++ku;
   }
   if (ku > 0) write_rows();
-  if (threadIdx.x == 128) bulk_wait_all();
 }
 
 template <int D>
@@ -908,6 +926,7 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(&sy->x_free, 8);
     mbar_init(&sy->y_free, 8);
     mbar_init(&sy->acc_full, 1);
+    mbar_init(&sy->out_full, 8);
     mbar_init(&sy->drain, 1);
     sy->abort = 0;
     tma_prefetch_desc(&mq);
@@ -931,11 +950,14 @@ __global__ void __launch_bounds__(384, 1)
   } else if (warp == 1) {
     if (elect_one()) q_mma<D>(P, smem, sy, tmem, abort);
     __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) q_store<D>(P, &mo, smem, sy, abort);
+    __syncwarp();
   } else if (warp == 3) {
     q_load_kv<D>(P, &mk, &mv, smem, sy, abort);
     __syncwarp();
   } else if (warp >= 4) {
-    q_softmax<D>(P, &mo, smem, sy, tmem, abort);
+    q_softmax<D>(P, smem, sy, tmem, abort);
   }
   tc_fence_before();
   __syncthreads();
