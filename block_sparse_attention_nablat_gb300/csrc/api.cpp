@@ -522,7 +522,7 @@ size_t nabla_cross_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int S
                                             int D) {
   const nabla::CrossShape s{B, Sq, Sk, h, hk, D};
   if (!nabla::valid_dtype(dt) || !nabla::valid_cross_shape(s)) return 0;
-  return nabla::cross_bwd_workspace(s);
+  return nabla::cross_bwd_workspace(s, dt);
 }
 
 nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
@@ -565,7 +565,7 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
     for (int j = 0; j < i; ++j)
       if (ranges_meet(out[i], on[i], out[j], on[j])) return NABLA_ERR_INVALID_ARG;
   }
-  if (ws_bytes < cross_bwd_workspace(a.s)) return NABLA_ERR_INVALID_ARG;
+  if (ws_bytes < cross_bwd_workspace(a.s, dt)) return NABLA_ERR_INVALID_ARG;
   a.of = o;
   a.lse = const_cast<float *>(lse);
   a.dout = dout;

@@ -121,11 +121,11 @@ struct BwdLayout {
   int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
   size_t nlse, ndelta, part, total;
 };
-BwdLayout bwd_layout(const CrossShape &s) {
+BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
   w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
   const size_t rows = round_up((size_t)s.B * s.hk * w.nsub * 64 * sizeof(float));
-  const int n = cross_dkv_splits(s);
+  const int n = cross_dkv_splits(s, dt);
   w.nlse = 0;
   w.ndelta = rows;
   w.part = 2 * rows;
@@ -149,19 +149,22 @@ cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const floa
                     static_cast<float *>(a.dv));
 }
 
-// Runs of query tiles the dK / dV units are split into.  Cost in steps (a 128 x 128 tile,
-// about a microsecond): the waves of units over GB300's 152 SMs times a unit's steps (two
-// more to start and end it), and the runs' sums written and read back (a step's time moves
-// about 6 MB).
-int cross_dkv_splits(const CrossShape &s) {
-  const long units = (long)s.B * s.hk * ((s.Sk + cross::kTile - 1) / cross::kTile);
-  const int nq = (cross::packing(s).nsub + 1) / 2;
+// Runs of query tiles the dK / dV units are split into.  Cost in steps: the waves of units
+// over GB300's 152 SMs times a unit's steps (and what it takes to start and end one), and
+// the runs' sums written and read back.  A step is a 128 x 128 tile in bf16, about a
+// microsecond, in which 6 MB move; in fp32 64 x 64 on CUDA cores, about 15.
+int cross_dkv_splits(const CrossShape &s, nabla_dtype dt) {
+  const bool tc = dt == NABLA_BF16;
+  const int tile = tc ? cross::kTile : 64, nsub = cross::packing(s).nsub;
+  const long units = (long)s.B * s.hk * ((s.Sk + tile - 1) / tile);
+  const int nq = tc ? (nsub + 1) / 2 : nsub;
+  const double start = tc ? 2.0 : 0.2, moved = tc ? 6.0e6 : 90.0e6;
   int best = 1;
   double least = 0.0;
   for (int n = 1; n <= nq && n <= 64; ++n) {
     const double waves = (double)((units * n + 151) / 152);
-    double cost = waves * ((nq + n - 1) / n + 2);
-    if (n > 1) cost += 2.0 + (double)units * n * cross::kTile * s.D * 2 * 4 * 2 / 6.0e6;
+    double cost = waves * ((nq + n - 1) / n + start);
+    if (n > 1) cost += start + (double)units * n * tile * s.D * 2 * 4 * 2 / moved;
     if (n == 1 || cost < least) {
       best = n;
       least = cost;
@@ -170,10 +173,10 @@ int cross_dkv_splits(const CrossShape &s) {
   return best;
 }
 
-size_t cross_bwd_workspace(const CrossShape &s) { return bwd_layout(s).total; }
+size_t cross_bwd_workspace(const CrossShape &s, nabla_dtype dt) { return bwd_layout(s, dt).total; }
 
 cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st) {
-  const BwdLayout w = bwd_layout(a.s);
+  const BwdLayout w = bwd_layout(a.s, dt);
   char *ws = static_cast<char *>(a.workspace);
   float *nlse = reinterpret_cast<float *>(ws + w.nlse);
   float *ndelta = reinterpret_cast<float *>(ws + w.ndelta);

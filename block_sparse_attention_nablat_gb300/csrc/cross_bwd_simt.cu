@@ -40,8 +40,7 @@ __global__ void __launch_bounds__(256)
   const int sub = (int)(su % P.nsub);
   const long bj = su / P.nsub;
   const int b = (int)(bj / P.hk), j = (int)(bj - (long)b * P.hk);
-  pdl_launch_dependents();
-  pdl_wait();
+  pdl_launch_dependents();  // no wait: dkv's blocks launched this one after theirs
   if (tid == 0) check_len(P.kv_len, b, P.Sk, P.status);
   const int len = batch_len(P.kv_len, b, P.Sk);
   load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, part * M);
@@ -90,6 +89,7 @@ __global__ void __launch_bounds__(256)
           make_float4(w.x * P.scale, w.y * P.scale, w.z * P.scale, w.w * P.scale);
     }
   }
+  pdl_wait();  // whoever waits for this kernel waits for dK and dV
 }
 
 template <int D>
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(256)
   const int kt = (int)(ku % nkt);
   const long bj = ku / nkt;
   const int b = (int)(bj / P.hk), j = (int)(bj - (long)b * P.hk);
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // dQ, which needs no more than this kernel
   const int len = batch_len(P.kv_len, b, P.Sk), k0 = kt * kCols;
   if (P.nsplit > 1 && k0 >= len) return;  // the join writes the zeros
   load_states<D>(Ks, static_cast<const float *>(P.k), P.k_st, b, j, k0, len);
@@ -191,11 +191,12 @@ cudaError_t launch_d(const CrossArgs &a, SimtParams p, float *part, int nsplit, 
   p.out2 = static_cast<float *>(a.dv);
   const long units = (long)p.B * p.hk * ((p.Sk + kCols - 1) / kCols) * nsplit;
   e = launch_pdl(kern, dim3((unsigned)units), dim3(256), dkv_smem<D>(), st, p);
-  if (e == cudaSuccess && nsplit > 1) e = launch_cross_dkv_join(a, NABLA_F32, part, nsplit, st);
   if (e != cudaSuccess) return e;
   p.out = static_cast<float *>(a.dq);
   const bool few = (long)p.B * p.hk * p.nsub < 152;  // one CTA on each of GB300's SMs
-  return few ? launch_dq<D, 1>(p, st) : launch_dq<D, 4>(p, st);
+  e = few ? launch_dq<D, 1>(p, st) : launch_dq<D, 4>(p, st);
+  if (e != cudaSuccess || nsplit == 1) return e;
+  return launch_cross_dkv_join(a, NABLA_F32, part, nsplit, st);
 }
 
 }  // namespace
@@ -206,7 +207,7 @@ cudaError_t launch_cross_bwd_simt(const CrossArgs &a, const float *nlse, const f
   p.lse = nlse;
   p.delta = ndelta;
   p.nsub = nsub;  // the packed rows' own, a whole number of pairs
-  const int nsplit = cross_dkv_splits(a.s);
+  const int nsplit = cross_dkv_splits(a.s, NABLA_F32);
   return a.s.D == 64 ? launch_d<64>(a, p, part, nsplit, st)
                      : launch_d<128>(a, p, part, nsplit, st);
 }

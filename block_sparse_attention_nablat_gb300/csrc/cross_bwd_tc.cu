@@ -999,7 +999,7 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
   p.kv_len = a.kv_len;
   p.B = s.B, p.Sq = s.Sq, p.Sk = s.Sk, p.h = s.h, p.hk = s.hk;
   p.G = pk.G, p.tq = pk.tq, p.nq = (pk.nsub + 1) / 2, p.nkt = (s.Sk + kTile - 1) / kTile;
-  p.nsplit = cross_dkv_splits(s);
+  p.nsplit = cross_dkv_splits(s, NABLA_BF16);
   p.scale = a.scale;
   p.scale_log2 = a.scale == 0.f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
   p.neg = a.scale < 0.f ? kIdescNegA : 0u;
@@ -1013,10 +1013,9 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
   p.walk = cross::walk_step(grid, p.nsplit, p.nkt, s.hk);
   err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), y_smem_bytes<D, false>(), st, mq, mk, mv,
                    mg, p);
+  if (err == cudaSuccess && p.nsplit > 1)
+    err = launch_cross_dkv_join(a, NABLA_BF16, part, p.nsplit, st);
   if (err != cudaSuccess) return err;
-  if (p.nsplit > 1 && (err = launch_cross_dkv_join(a, NABLA_BF16, part, p.nsplit, st)) !=
-                          cudaSuccess)
-    return err;
   p.units = (uint32_t)((long)s.B * s.hk * p.nq);
   auto kern2 = cross_dq_kernel<D>;
   if ((err = cudaFuncSetAttribute(kern2, cudaFuncAttributeMaxDynamicSharedMemorySize,
