@@ -9,7 +9,8 @@
 // scores along D, P V along the states) and multiply pairs (fma.rn.f32x2), so a warp
 // issues 32 pair-FMAs for 12 wavefronts of shared memory and the FMA pipe bounds the
 // kernel.  P takes over K's tile, which leaves room for two CTAs per SM at D = 128.
-// 64 rows a CTA, or 16 where 64 would leave SMs without work (short queries).
+// 64 rows a CTA, or 32 or 16 where 64 would leave SMs without work (short queries); where
+// those are still few the states are split into runs (cross_combine joins them).
 #include <cfloat>
 
 #include "attn_common.cuh"
@@ -36,7 +37,8 @@ __global__ void __launch_bounds__(256, 2)
   float *Qs = sm, *Ks = Qs + M * LD, *Vs = Ks + kCols * LD, *Ps = Ks;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int parts = 64 / M;
-  const long blk = blockIdx.x;
+  const int sp = (int)(blockIdx.x % P.nsplit);
+  const long blk = blockIdx.x / P.nsplit;
   const int part = (int)(blk % parts);
   const long su = blk / parts;
   const int sub = (int)(su % P.nsub);
@@ -45,9 +47,12 @@ __global__ void __launch_bounds__(256, 2)
   pdl_launch_dependents();
   pdl_wait();
   if (tid == 0) check_len(P.kv_len, b, P.Sk, P.status);
-  const int len = batch_len(P.kv_len, b, P.Sk);
+  if (!packed_row(P, j, sub, part * M).ok) return;  // nor is any later row of the tile
+  const int len = batch_len(P.kv_len, b, P.Sk), tiles = (len + kCols - 1) / kCols;
+  const int t0 = (int)((long)tiles * sp / P.nsplit), t1 = (int)((long)tiles * (sp + 1) / P.nsplit);
   const Side q{static_cast<const float *>(P.q), P.q_st};
   load_rows<D, M>(Qs, q, P, b, j, sub, part * M);
+  copy_commit();
 
   float m_run[A], l_run[A];
   uint64_t acc[A][E][2];
@@ -58,14 +63,18 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[a][e][0] = acc[a][e][1] = 0ull;
   }
-  for (int k0 = 0; k0 < len; k0 += kCols) {
+  for (int k0 = t0 * kCols; k0 < t1 * kCols; k0 += kCols) {
     __syncthreads();  // the last tile's P and V are no longer read
     load_states<D>(Ks, static_cast<const float *>(P.k), P.k_st, b, j, k0, len);
+    copy_commit();
     load_states<D>(Vs, static_cast<const float *>(P.v), P.v_st, b, j, k0, len);
+    copy_commit();
+    copy_wait<1>();  // Q, K
     __syncthreads();
     float s[A][4];
     dot_rows<D, A>(Qs, Ks, ty, tx, s);
-    __syncthreads();  // K is no longer read: P takes its place
+    copy_wait<0>();
+    __syncthreads();  // V is there; K is no longer read: P takes its place
 #pragma unroll
     for (int a = 0; a < A; ++a) {
       float mx = -FLT_MAX;
@@ -104,10 +113,14 @@ __global__ void __launch_bounds__(256, 2)
     const PackedRow r = packed_row(P, j, sub, part * M + ty + 16 * a);
     if (!r.ok) continue;
     const float l = l_run[a], inv = l > 0.f ? 1.0f / l : l;
-    if (P.lse_out && tx == 0)
-      P.lse_out[((size_t)b * P.h + r.head) * P.Sq + r.token] =
-          l > 0.f ? m_run[a] + log2f(l) : l == 0.f ? -INFINITY : l;
-    float *o = P.out + (((size_t)b * P.Sq + r.token) * P.h + r.head) * D + 4 * tx;
+    const size_t row = ((size_t)b * P.h + r.head) * P.Sq + r.token;
+    const size_t run = (size_t)sp * P.B * P.h * P.Sq + row;  // of a run's sums
+    float *lse = P.nsplit > 1 ? P.plse + run : P.lse_out ? P.lse_out + row : nullptr;
+    if (lse && tx == 0) *lse = l > 0.f ? m_run[a] + log2f(l) : l == 0.f ? -INFINITY : l;
+    if (P.nsplit > 1 && t0 == t1) continue;  // not read
+    float *o = (P.nsplit > 1 ? P.po + run * D
+                             : P.out + (((size_t)b * P.Sq + r.token) * P.h + r.head) * D) +
+               4 * tx;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float4 w;
@@ -125,7 +138,14 @@ cudaError_t launch_f(const SimtParams &p, long subs, cudaStream_t st) {
   const int smem = fwd_smem<D, A>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)(subs * (4 / A))), dim3(256), smem, st, p);
+  return launch_pdl(kern, dim3((unsigned)(subs * (4 / A) * p.nsplit)), dim3(256), smem, st, p);
+}
+
+template <int D>
+cudaError_t launch_a(const SimtParams &p, int A, long subs, cudaStream_t st) {
+  return A == 1   ? launch_f<D, 1>(p, subs, st)
+         : A == 2 ? launch_f<D, 2>(p, subs, st)
+                  : launch_f<D, 4>(p, subs, st);
 }
 
 }  // namespace
@@ -134,10 +154,15 @@ cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st) {
   SimtParams p = simt_params(a);
   p.out = static_cast<float *>(a.o);
   p.lse_out = a.lse;
+  const CrossSimtPlan plan = cross_simt_plan(a.s);
+  p.nsplit = plan.nsplit;
+  const CrossRuns runs = cross_runs(a, p.nsplit);
+  p.po = runs.po, p.plse = runs.plse;
   const long subs = (long)a.s.B * a.s.hk * p.nsub;
-  const bool few = subs < 2 * 152;  // two CTAs on each of GB300's SMs
-  if (a.s.D == 64) return few ? launch_f<64, 1>(p, subs, st) : launch_f<64, 4>(p, subs, st);
-  return few ? launch_f<128, 1>(p, subs, st) : launch_f<128, 4>(p, subs, st);
+  const cudaError_t e = a.s.D == 64 ? launch_a<64>(p, plan.A, subs, st)
+                                    : launch_a<128>(p, plan.A, subs, st);
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  return launch_cross_combine(a, NABLA_F32, p.nsplit, st);
 }
 
 }  // namespace nabla

@@ -238,7 +238,8 @@ __device__ void x_load_v(const XParams &P, const CUtensorMap *mv, uint8_t *smem,
   }
   if (lane == 0 && (!go || *abort))
     for (uint32_t e = g > (uint32_t)C::kVBufs ? g - C::kVBufs : 0u; e < g; ++e)
-      mbar_wait_small(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status, kDevTimeout);
+      mbar_wait_small(&sy->v_full[e % C::kVBufs], (e / C::kVBufs) & 1u, nullptr, P.status,
+                      kDevTimeout);
 }
 
 // Warp 1: S of step g into score buffer g % 3, once the PV of step g - 3 (its last
@@ -671,63 +672,6 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-// Joins the runs of a row: o = sum_i 2^(lse_i - lse) o_i.  A warp per row.
-template <int D>
-__global__ void __launch_bounds__(256) cross_combine_kernel(const XParams P) {
-  const int lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  pdl_wait();
-  const long rows = (long)P.B * P.h * P.Sq;
-  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  float m = -INFINITY;
-  for (int i = lane; i < P.nsplit; i += 32) m = fmaxf(m, P.plse[(size_t)i * rows + row]);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  constexpr int kV = D / 32;
-  float acc[kV], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-  for (int i = 0; i < P.nsplit; ++i) {
-    const float li = P.plse[(size_t)i * rows + row];
-    if (li == -INFINITY) continue;  // no states in this run: nothing was written
-    const float w = ex2(li - m);
-    l += w;
-    const float *src = P.po + ((size_t)i * rows + row) * D + lane * kV;
-#pragma unroll
-    for (int e = 0; e < kV; ++e) acc[e] = fmaf(w, src[e], acc[e]);
-  }
-  const float inv = l > 0.f ? 1.0f / l : l;
-  const long bh = row / P.Sq, token = row - bh * P.Sq, b = bh / P.h, hh = bh - b * P.h;
-  __nv_bfloat16 *dst = P.o + ((b * P.Sq + token) * P.h + hh) * D + lane * kV;
-#pragma unroll
-  for (int e = 0; e < kV; e += 2)
-    *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (P.lse && lane == 0) P.lse[row] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-}
-
-// How the rows and states are cut into units.  Runs: 1 where the units fill the GPU,
-// else enough for about four units per SM (batches differ in length), at least two state
-// tiles each.  Sized for GB300's 152 SMs, so that the workspace depends on the shape
-// alone.
-struct FwdPlan {
-  int nqt, nsplit;
-};
-FwdPlan fwd_plan(const CrossShape &s) {
-  constexpr long kSms = 152;
-  const cross::Packing pk = cross::packing(s);
-  FwdPlan f;
-  f.nqt = (pk.nsub + 1) / 2;
-  f.nsplit = 1;
-  const long units = (long)s.B * s.hk * f.nqt;
-  const int nt = (s.Sk + kTile - 1) / kTile;
-  if (units < kSms && nt >= 4) {
-    const long want = (4 * kSms + units - 1) / units;
-    f.nsplit = (int)(want < nt / 2 ? want : nt / 2);
-  }
-  return f;
-}
-
 template <int D>
 cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   using C = XCfg<D>;
@@ -757,34 +701,22 @@ cudaError_t launch_x(const CrossArgs &a, cudaStream_t st) {
   p.kv_len = a.kv_len;
   p.B = s.B, p.Sq = s.Sq, p.Sk = s.Sk, p.h = s.h, p.hk = s.hk;
   p.G = pk.G, p.tq = pk.tq;
-  const FwdPlan plan = fwd_plan(s);
-  p.nqt = plan.nqt, p.nsplit = plan.nsplit;
+  p.nqt = (pk.nsub + 1) / 2, p.nsplit = cross_fwd_splits(s, NABLA_BF16);
   // a scale of 0 weighs all states alike, as one too small to tell scores apart does
   p.scale_log2 = a.scale == 0.f ? 1e-30f : fabsf(a.scale) * 1.4426950408889634f;
   p.neg = a.scale < 0.f ? kIdescNegA : 0u;
   p.status = a.status;
-  const long rows = (long)s.B * s.h * s.Sq;
-  if (p.nsplit > 1) {
-    p.po = static_cast<float *>(a.workspace);
-    p.plse = p.po + (size_t)p.nsplit * rows * D;
-  }
+  const CrossRuns runs = cross_runs(a, p.nsplit);
+  p.po = runs.po, p.plse = runs.plse;
   p.units = (uint32_t)((long)s.B * s.hk * p.nqt * p.nsplit);
   const unsigned grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
   err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), x_smem_bytes<D>(), st, mq, mk, mv, mo,
                    p);
   if (err != cudaSuccess || p.nsplit == 1) return err;
-  return launch_pdl(cross_combine_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st,
-                    p);
+  return launch_cross_combine(a, NABLA_BF16, p.nsplit, st);
 }
 
 }  // namespace
-
-int cross_fwd_splits(const CrossShape &s) { return fwd_plan(s).nsplit; }
-
-size_t cross_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
-  const int n = dt == NABLA_BF16 ? cross_fwd_splits(s) : 1;
-  return n > 1 ? (size_t)n * s.B * s.h * s.Sq * (s.D + 1) * sizeof(float) : 0;
-}
 
 cudaError_t launch_cross_attn_tc(const CrossArgs &a, cudaStream_t st) {
   return a.s.D == 64 ? launch_x<64>(a, st) : launch_x<128>(a, st);

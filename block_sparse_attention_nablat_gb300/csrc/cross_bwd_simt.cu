@@ -42,6 +42,10 @@ __global__ void __launch_bounds__(256)
   const int b = (int)(bj / P.hk), j = (int)(bj - (long)b * P.hk);
   pdl_launch_dependents();  // no wait: dkv's blocks launched this one after theirs
   if (tid == 0) check_len(P.kv_len, b, P.Sk, P.status);
+  if (!packed_row(P, j, sub, part * M).ok) {  // nor is any later row of the tile
+    pdl_wait();
+    return;
+  }
   const int len = batch_len(P.kv_len, b, P.Sk);
   load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, part * M);
   load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, part * M);
@@ -60,10 +64,15 @@ __global__ void __launch_bounds__(256)
   for (int k0 = 0; k0 < len; k0 += kCols) {
     __syncthreads();
     load_states<D>(Ks, static_cast<const float *>(P.k), P.k_st, b, j, k0, len);
+    copy_commit();  // with q and dout
     load_states<D>(Vs, static_cast<const float *>(P.v), P.v_st, b, j, k0, len);
+    copy_commit();
+    copy_wait<1>();
     __syncthreads();
     float s[A][4], dp[A][4];
     dot_rows<D, A>(Qs, Ks, ty, tx, s);
+    copy_wait<0>();
+    __syncthreads();
     dot_rows<D, A>(Gs, Vs, ty, tx, dp);
 #pragma unroll
     for (int a = 0; a < A; ++a)
@@ -124,12 +133,15 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int e = 0; e < E; ++e)
       dk[a][e][0] = dk[a][e][1] = dv[a][e][0] = dv[a][e][1] = 0ull;
-  const int s0 = (int)((long)P.nsub * sp / P.nsplit), s1 = (int)((long)P.nsub * (sp + 1) / P.nsplit);
+  const int s0 = (int)((long)P.nsub * sp / P.nsplit);
+  const int s1 = (int)((long)P.nsub * (sp + 1) / P.nsplit);
   for (int sub = s0; sub < s1 && k0 < len; ++sub) {
     __syncthreads();
     load_rows<D, 64>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, 0);
     load_rows<D, 64>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, 0);
+    copy_commit();
     if (tid < 128) ls[tid] = (tid < 64 ? P.lse : P.delta)[(bj * P.nsub + sub) * 64 + (tid & 63)];
+    copy_wait<0>();
     __syncthreads();
     float s[4][4], dp[4][4];  // rows: states ty + 16 a; columns: query rows tx + 16 c
     dot_rows<D, 4>(Ks, Qs, ty, tx, s);
@@ -193,7 +205,10 @@ cudaError_t launch_d(const CrossArgs &a, SimtParams p, float *part, int nsplit, 
   e = launch_pdl(kern, dim3((unsigned)units), dim3(256), dkv_smem<D>(), st, p);
   if (e != cudaSuccess) return e;
   p.out = static_cast<float *>(a.dq);
-  const bool few = (long)p.B * p.hk * p.nsub < 152;  // one CTA on each of GB300's SMs
+  // 16 rows a CTA only where 64 would leave most SMs idle: beside dK and dV, whose blocks
+  // fill SMs too, 96 CTAs of 64 rows do better than 384 of 16 (66 against 75 us in all at
+  // 2 x 500 x 77 tokens, 6 heads on 2)
+  const bool few = (long)p.B * p.hk * p.nsub < 64;
   e = few ? launch_dq<D, 1>(p, st) : launch_dq<D, 4>(p, st);
   if (e != cudaSuccess || nsplit == 1) return e;
   return launch_cross_dkv_join(a, NABLA_F32, part, nsplit, st);

@@ -21,6 +21,7 @@ struct SimtParams {
   const float *lse, *delta;  // backward, packed rows [B, hk, nsub, 64]
   float *out, *out2;         // o; dq; dk and dv (or their parts)
   float *lse_out;
+  float *po, *plse;  // forward, nsplit > 1
   const int32_t *kv_len;
   int B, Sq, Sk, h, hk, G, tq, nsub, nsplit;
   float scale, scale_log2;
@@ -59,6 +60,22 @@ __device__ __forceinline__ PackedRow packed_row(const SimtParams &P, int j, int 
   return w;
 }
 
+// 16 bytes to shared memory, asynchronously (a tile's copies are all in flight together:
+// as loads and stores they went one latency after the other, 11 us a tile); zeros if !ok.
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>  // all but the last N groups committed
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // M packed query rows from row r0 of subtile `sub` (rows that are none: zeros).
 template <int D, int M>
 __device__ __forceinline__ void load_rows(float *dst, const Side &x, const SimtParams &P, int b,
@@ -67,11 +84,8 @@ __device__ __forceinline__ void load_rows(float *dst, const Side &x, const SimtP
   for (int e = threadIdx.x; e < M * kVec; e += 256) {
     const int r = e / kVec, c = (e - r * kVec) * 4;
     const PackedRow w = packed_row(P, j, sub, r0 + r);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (w.ok)
-      v = *reinterpret_cast<const float4 *>(x.p + b * x.st.batch + w.token * x.st.token +
-                                            w.head * x.st.head + c);
-    *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = v;
+    copy16(dst + r * (D + 4) + c,
+           w.ok ? x.p + b * x.st.batch + w.token * x.st.token + w.head * x.st.head + c : x.p, w.ok);
   }
 }
 
@@ -82,11 +96,9 @@ __device__ __forceinline__ void load_states(float *dst, const float *x, const na
   constexpr int kVec = D / 4;
   for (int e = threadIdx.x; e < kCols * kVec; e += 256) {
     const int r = e / kVec, c = (e - r * kVec) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (k0 + r < len)
-      v = *reinterpret_cast<const float4 *>(x + b * st.batch + (int64_t)(k0 + r) * st.token +
-                                            j * st.head + c);
-    *reinterpret_cast<float4 *>(dst + r * (D + 4) + c) = v;
+    const bool ok = k0 + r < len;
+    copy16(dst + r * (D + 4) + c,
+           ok ? x + b * st.batch + (int64_t)(k0 + r) * st.token + j * st.head + c : x, ok);
   }
 }
 

@@ -127,8 +127,17 @@ struct CrossArgs {
   int *status;
 };
 // Runs of states the bf16 forward splits its units into, and the scratch they need.
-int cross_fwd_splits(const CrossShape &s);
+int cross_fwd_splits(const CrossShape &s, nabla_dtype dt);
+struct CrossSimtPlan {
+  int A, nsplit;
+};
+CrossSimtPlan cross_simt_plan(const CrossShape &s);
 size_t cross_fwd_workspace(const CrossShape &s, nabla_dtype dt);
+struct CrossRuns {
+  float *po, *plse;  // [nsplit, B, h, Sq, D] and [nsplit, B, h, Sq]; none for one run
+};
+CrossRuns cross_runs(const CrossArgs &a, int nsplit);
+cudaError_t launch_cross_combine(const CrossArgs &a, nabla_dtype dt, int nsplit, cudaStream_t st);
 // K9: bf16, tcgen05.  K9f: fp32, CUDA cores.
 cudaError_t launch_cross_attn_tc(const CrossArgs &a, cudaStream_t st);
 cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st);

@@ -83,7 +83,8 @@ def test_workspace_bytes(lib):
     f, b = lib.nabla_cross_attn_fwd_workspace_bytes, lib.nabla_cross_attn_bwd_workspace_bytes
     assert f(1, 1, 32768, 512, 24, 24, 128) == 0      # enough rows: nothing is split
     assert f(1, 2, 1, 4096, 8, 2, 128) > 0            # one token against long states
-    assert f(0, 2, 1, 4096, 8, 2, 128) == 0           # fp32 is not split
+    assert f(0, 2, 1, 4096, 8, 2, 128) > 0            # in fp32 too
+    assert f(0, 1, 32768, 512, 24, 24, 128) == 0
     assert b(1, 1, 32768, 512, 24, 24, 128) >= 2 * 24 * 32768 * 4
     for bad in [(2, 1, 8, 8, 2, 2, 64), (1, 0, 8, 8, 2, 2, 64), (1, 1, 8, 8, 3, 2, 64),
                 (1, 1, 8, 8, 2, 2, 80)]:
