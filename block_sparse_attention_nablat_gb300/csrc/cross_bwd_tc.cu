@@ -66,11 +66,12 @@ struct YCfg {
   static constexpr int kOffL = kOffG + kG * kTileBytes;
   static constexpr int kOffSync1 = kOffL + kG * 1024;
   static constexpr uint32_t kDK = 0, kDV = 128, kX1 = 256, kY1 = 384;
-  // dQ: two Q tiles, dO, three K tiles, V
-  static constexpr int kK = 3;
+  // dQ: two Q tiles, dO, three K tiles, V (two tiles where there is room: with one, its
+  // loads bound a step)
+  static constexpr int kK = 3, kV = D == 64 ? 2 : 1;
   static constexpr int kOffG2 = 2 * kTileBytes, kOffK2 = 3 * kTileBytes;
   static constexpr int kOffV2 = kOffK2 + kK * kTileBytes;
-  static constexpr int kOffSync2 = kOffV2 + kTileBytes;
+  static constexpr int kOffSync2 = kOffV2 + kV * kTileBytes;
   static constexpr uint32_t kDQ = 0, kX2 = 128, kY2 = 256, kZ = 384;  // dz buffer b: + 64 b
 };
 
@@ -81,7 +82,7 @@ struct KSync {
   int abort;
 };
 struct QSync {
-  uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw, v_full, v_empty;
+  uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw, v_full[2], v_empty[2];
   uint64_t x_full, y_full, x_free, y_free, z_full[2], acc_full, out_full, drain;
   uint32_t tmem_slot;
   int abort;
@@ -590,6 +591,7 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
   using C = YCfg<D>;
   const int lane = threadIdx.x & 31;
   Ring<C::kK> kr;
+  Ring<C::kV> vr;
   uint32_t g = 0, raw = 0;
   bool go = true;
   cross::Walk w = cross::walk_start(P.walk, blockIdx.x);
@@ -597,7 +599,7 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
        i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const QUnit u = q_unit(P, w);
     if (lane == 0) cross::check_len(P.kv_len, u.b, P.Sk, P.status);
-    for (int t = 0; t < u.n && go; ++t, ++g, kr.next()) {
+    for (int t = 0; t < u.n && go; ++t, ++g, kr.next(), vr.next()) {
       const int rows = u.len - t * kTile, end = rows >= kTile ? kTile : (rows + 15) & ~15;
       const bool mend = rows < end && u.len < P.Sk;  // zero K's rows [rows, end)
       uint8_t *tile = smem + C::kOffK2 + kr.slot * C::kTileBytes;
@@ -627,12 +629,12 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
         if (lane == 0) mbar_arrive(&sy->k_full[kr.slot]);
       }
       if (lane == 0) {
-        ok = mbar_wait_small(&sy->v_empty, (g & 1u) ^ 1u, abort, P.status, kDevTimeout);
+        ok = cross::thread_wait(&sy->v_empty[vr.slot], vr.phase ^ 1u, abort, P.status);
         if (ok) {
-          mbar_expect_tx(&sy->v_full, C::kTileBytes);
+          mbar_expect_tx(&sy->v_full[vr.slot], C::kTileBytes);
           for (int c = 0; c < C::kBoxes; ++c)
-            tma_load_4d(smem + C::kOffV2 + c * C::kBox, mv, &sy->v_full, c * 64, u.j, t * kTile,
-                        u.b);
+            tma_load_4d(smem + C::kOffV2 + vr.slot * C::kTileBytes + c * C::kBox, mv,
+                        &sy->v_full[vr.slot], c * 64, u.j, t * kTile, u.b);
         } else {  // the K tile of this step is in flight
           mbar_wait_small(&sy->k_full[kr.slot], kr.phase, nullptr, P.status, kDevTimeout);
         }
@@ -644,7 +646,8 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
   if (lane == 0 && (!go || *abort)) {
     for (uint32_t e = g > (uint32_t)C::kK ? g - C::kK : 0u; e < g; ++e)
       mbar_wait_small(&sy->k_full[e % C::kK], (e / C::kK) & 1u, nullptr, P.status, kDevTimeout);
-    if (g > 0) mbar_wait_small(&sy->v_full, (g - 1) & 1u, nullptr, P.status, kDevTimeout);
+    for (uint32_t e = g > (uint32_t)C::kV ? g - C::kV : 0u; e < g; ++e)
+      mbar_wait_small(&sy->v_full[e % C::kV], (e / C::kV) & 1u, nullptr, P.status, kDevTimeout);
   }
 }
 
@@ -665,6 +668,7 @@ __device__ void q_mma(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
   const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + C::kOffV2), 16, 1024);
   Ring<2> q;
   Ring<C::kK> kr, kd;           // of X's step, and of dQ's
+  Ring<C::kV> vr;
   uint32_t g = 0, ku = 0;       // steps of X so far
   int left = 0;                 // states from the first of dQ's next tile on
   bool first = true, ok = true;  // dQ's next step begins a unit
@@ -706,13 +710,15 @@ __device__ void q_mma(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
         if (g > 0) issue_dq(true);  // the last unit's last step
         ok = ok && cross::thread_wait(&sy->g_full, ku & 1u, abort, P.status);
       }
-      ok = ok && cross::thread_wait(&sy->v_full, g & 1u, abort, P.status) &&
+      ok = ok && cross::thread_wait(&sy->v_full[vr.slot], vr.phase, abort, P.status) &&
            cross::thread_wait(&sy->y_free, (g & 1u) ^ 1u, abort, P.status);
       if (!ok) break;
       tc_fence_after();
-      issue_ss<D>(tmem + C::kY2, g_desc, v_desc, C::kIdSS);
+      issue_ss<D>(tmem + C::kY2, g_desc, v_desc + (uint64_t)((vr.slot * C::kTileBytes) >> 4),
+                  C::kIdSS);
       mma_commit(&sy->y_full);
-      mma_commit(&sy->v_empty);
+      mma_commit(&sy->v_empty[vr.slot]);
+      vr.next();
       if (t + 1 == u.n) mma_commit(&sy->g_empty);
       if (t > 0) issue_dq(false);
       left = u.len - t * kTile;
@@ -774,14 +780,14 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
     tc_fence_after();
     uint8_t *tile = smem + ((ku - 1) & 1u) * C::kTileBytes + row * 128;
 #pragma unroll 1
-    for (int x = 0; x < D / 32; ++x) {  // 16 columns of this group's D / 2
-      const int c = grp * (D / 2) + x * 16;
-      uint32_t t[16];
-      tmem_ld16(at + C::kDQ + c, t);
+    for (int x = 0; x < D / 64; ++x) {  // 32 columns of this group's D / 2
+      const int c = grp * (D / 2) + x * 32;
+      uint32_t t[32];
+      tmem_ld32(at + C::kDQ + c, t);
       tmem_wait_ld();
-      reg_fence16(t);
+      reg_fence(t);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 4; ++e) {
         uint32_t v[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y)
@@ -919,8 +925,10 @@ __global__ void __launch_bounds__(384, 1)
     mbar_init(&sy->g_full, 1);
     mbar_init(&sy->g_empty, 1);
     mbar_init(&sy->k_raw, 1);
-    mbar_init(&sy->v_full, 1);
-    mbar_init(&sy->v_empty, 1);
+    for (int i = 0; i < C::kV; ++i) {
+      mbar_init(&sy->v_full[i], 1);
+      mbar_init(&sy->v_empty[i], 1);
+    }
     mbar_init(&sy->x_full, 1);
     mbar_init(&sy->y_full, 1);
     mbar_init(&sy->x_free, 8);
