@@ -30,6 +30,15 @@
 //    the rows of V that share the last 16-row MMA step with them are zeroed in shared
 //    memory before it runs, so a NaN behind the length stays there.
 //  * The output warps stage a unit's rows as bf16 in shared memory and store them by TMA.
+//
+// 32768 tokens, 24 heads, D 128: 512 states 161 us, 1280 TFLOP/s; 4096 states 984 us, 1680
+// (0.87 of a large library product's rate); 128 states 79 us, 5.1 TB/s of rows in and out.
+// A unit costs about 1,500 cycles a step and 1,900 more: at few steps its start and end,
+// and the instruction fetches of code that runs once a unit, bound it, so the waits' slow
+// paths are out of line and no role's code exists twice.
+// Measured and not kept at 512 states: two chains of four softmax warps each 256 us,
+// output by the softmax warps 248, two or three sets of softmax warps on alternating steps
+// 168 to 200, the units walked without divisions (more code) 165.
 // Every mbarrier wait is bounded (1 s); on expiry the kernel records
 // NABLA_ERR_TIMEOUT, the roles stop waiting, copies and MMAs in flight are drained and
 // TMEM is released.

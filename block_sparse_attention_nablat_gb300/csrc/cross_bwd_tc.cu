@@ -16,7 +16,7 @@
 //    dV += P^T dO, dK += dz^T Q (TS MMAs).  TMEM holds dK, dV, X and Y: 4 x 128 columns.
 //    One warp issues dV and X (which goes over P), another dK and Y: two chains that fill
 //    each other's gaps.  (One warp for all four, in the best order, leaves the tensor pipe
-//    to drain at every wait: 3500 cycles a step where two take 3100, of 2048 in the pipe.)
+//    to drain at every wait: 3500 cycles a step where two take 2900, of 2048 in the pipe.)
 //    Where there are few state tiles the query tiles are split over several units whose
 //    fp32 sums cross_dkv_join adds up in a fixed order.
 //  * dQ: unit = a tile of 128 packed query rows over the batch's state tiles.  X = Q K^T,
@@ -28,6 +28,15 @@
 // are 0 there; in dQ their columns are 0 and the rows of K that share the last 16-row MMA
 // step with them are zeroed in shared memory.  Query rows that are none (a tile's end)
 // have lse = +inf, so P = 0.
+//
+// 32768 tokens, 24 heads, D 128, 512 states: 589 us in all, 875 TFLOP/s of the five
+// products (0.45 of a large library product's rate): rows' lse and delta 72, dK and dV 281
+// (tensor pipe 63% active), their sum 11, dQ 218 (59%).  4096 states: 3.96 ms, 1040.  A step of
+// dK / dV is bound by the chain X, P, dV, next X (X goes over P: TMEM is full); one of dQ
+// by V's tile, which is loaded when the last Y is done, and the products' own chain.
+// Measured and not kept: dO as dQ's TMEM operand, which makes room for a second V tile,
+// but starts a unit later: 4096 states 3.80 ms, 512 584 us, 256 416 against 399; dQ started
+// on the SMs that dK / dV leave: 600 against 595 at 512 states, 313 against 321 at 128.
 // Every mbarrier wait is bounded (1 s), as in the forward.
 #include <cuda.h>
 #include <cudaTypedefs.h>

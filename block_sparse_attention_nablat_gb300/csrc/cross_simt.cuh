@@ -60,8 +60,9 @@ __device__ __forceinline__ PackedRow packed_row(const SimtParams &P, int j, int 
   return w;
 }
 
-// 16 bytes to shared memory, asynchronously (a tile's copies are all in flight together:
-// as loads and stores they went one latency after the other, 11 us a tile); zeros if !ok.
+// 16 bytes to shared memory, asynchronously, so that a tile's copies are all in flight
+// together (as loads and stores: 731 us against 633 for one token each against 16 x 4096
+// states in one run, 24 heads on 8, D 128); zeros if !ok.
 __device__ __forceinline__ void copy16(float *dst, const float *src, bool ok) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                    (uint32_t)__cvta_generic_to_shared(dst)),

@@ -12,7 +12,9 @@
 // lanes hold a row and a warp 32 / (D / 8) rows at a time, so the norm's sum is
 // log2(D / 8) shuffles and no shared memory is touched.  A warp's item is a run of
 // one token's heads, so the token's angles and the weights are read once per item
-// and stay in registers.
+// and stay in registers.  At 32768 tokens, 24 + 24 heads, D 128, bf16: 123 us, 6.6 TB/s
+// of rows read and written (97% of a plain copy's rate); backward 208 us, 5.8 TB/s (86%:
+// its 128 registers a thread leave fewer loads in flight).
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -209,8 +211,8 @@ __device__ __forceinline__ Item decode_item(const QkParams &P, long i) {
 }
 
 // kDense: every tensor's heads lie D apart, so a row's place is an immediate offset from
-// the item's first (with strides in registers instead the backward took 336 us where it
-// takes 237, 480p).
+// the item's first (with strides in registers instead the backward took 336 us where this
+// one took 237 then, 32768 tokens, 24 + 24 heads, D 128).
 template <typename T, int D, bool kPairs, bool kDense>
 __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant__ QkParams P) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 4;
