@@ -109,10 +109,10 @@ __global__ void __launch_bounds__(256)
 template <typename T, int D>
 cudaError_t launch_prep(const CrossArgs &a, const cross::Packing &pk, int nsub, float *nlse,
                         float *ndelta, cudaStream_t st) {
-  return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)(a.s.B * a.s.hk * nsub)), dim3(256),
-                    0, st, static_cast<const T *>(a.of), a.o_st, static_cast<const T *>(a.dout),
-                    a.dout_st, (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub,
-                    nlse, ndelta);
+  const long blocks = (long)a.s.B * a.s.hk * nsub;
+  return launch_pdl(cross_prep_kernel<T, D>, dim3((unsigned)blocks), dim3(256), 0, st,
+                    static_cast<const T *>(a.of), a.o_st, static_cast<const T *>(a.dout), a.dout_st,
+                    (const float *)a.lse, a.s.Sq, a.s.h, a.s.hk, pk.G, pk.tq, nsub, nlse, ndelta);
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -125,16 +125,22 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
   w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
   const size_t rows = round_up((size_t)s.B * s.hk * w.nsub * 64 * sizeof(float));
-  const int n = cross_dkv_splits(s, dt);
+  const int n = cross_few_rows(s, dt) ? 1 : cross_dkv_splits(s, dt);
   w.nlse = 0;
   w.ndelta = rows;
   w.part = 2 * rows;
   w.total = w.part + (n > 1 ? round_up((size_t)n * 2 * s.B * s.Sk * s.hk * s.D * sizeof(float))
                             : 0);
+  if (cross_few_rows(s, dt))
+    w.total += round_up((size_t)((s.Sk + 63) / 64) * s.B * s.h * s.Sq * s.D * sizeof(float));
   return w;
 }
 
 }  // namespace
+
+bool cross_few_rows(const CrossShape &s, nabla_dtype dt) {
+  return dt == NABLA_F32 && (long)s.Sq * (s.h / s.hk) <= 16;
+}
 
 cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const float *part,
                                   int nsplit, cudaStream_t st) {

@@ -21,7 +21,7 @@ struct SimtParams {
   const float *lse, *delta;  // backward, packed rows [B, hk, nsub, 64]
   float *out, *out2;         // o; dq; dk and dv (or their parts)
   float *lse_out;
-  float *po, *plse;  // forward, nsplit > 1
+  float *po, *plse;  // runs (forward) or tiles (dq of few rows): their parts
   const int32_t *kv_len;
   int B, Sq, Sk, h, hk, G, tq, nsub, nsplit;
   float scale, scale_log2;
@@ -168,6 +168,25 @@ __device__ __forceinline__ void mul_rows(const float *W, const float *Y, int ty,
       }
     }
   }
+}
+
+// The same, summed apart first.
+template <int D, int A>
+__device__ __forceinline__ void add_rows(const float *W, const float *Y, int ty, int tx,
+                                         uint64_t (&acc)[A][D / 64][2]) {
+  uint64_t t[A][D / 64][2];
+#pragma unroll
+  for (int a = 0; a < A; ++a)
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) t[a][e][0] = t[a][e][1] = 0ull;
+  mul_rows<D, A>(W, Y, ty, tx, t);
+#pragma unroll
+  for (int a = 0; a < A; ++a)
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) {
+      acc[a][e][0] = tcattn::add2(acc[a][e][0], t[a][e][0]);
+      acc[a][e][1] = tcattn::add2(acc[a][e][1], t[a][e][1]);
+    }
 }
 
 }  // namespace cross

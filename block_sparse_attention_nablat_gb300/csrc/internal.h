@@ -144,6 +144,8 @@ cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st);
 // K10: the backward (prep, products, join).  Workspace: -lse and -delta of the packed
 // rows, then the runs' sums of dK and dV where these are split (cross_dkv_splits).
 int cross_dkv_splits(const CrossShape &s, nabla_dtype dt);
+// Whether the fp32 backward takes its form for few rows (the tiles' dq follow the rows).
+bool cross_few_rows(const CrossShape &s, nabla_dtype dt);
 size_t cross_bwd_workspace(const CrossShape &s, nabla_dtype dt);
 cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st);
 // Its parts: the products in bf16 (tcgen05) and fp32 (CUDA cores), each with the join.

@@ -150,3 +150,40 @@ def test_order(nabla, dtype, D):
         for a, b in zip(ref, outs):
             assert torch.equal(a, b)
     assert nabla.nabla_get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_offsets_past_32_bits(nabla, dtype):
+    """Rows more than 2^31 elements apart give the bits of the dense call."""
+    n, h, D = 260, 2, 64
+    pitch = 2 ** 31 // (n - 1) // 8 * 8 + 64  # of a token, elements
+    assert (n - 2) * pitch <= 2 ** 31 < (n - 1) * pitch
+    g = torch.Generator().manual_seed(5)
+    dense = [torch.randn(1, n, h, D, generator=g).to(TYPES[dtype]).to(DEV) for _ in range(4)]
+
+    def far(t=None):
+        room = torch.empty((n - 1) * pitch + h * D, dtype=TYPES[dtype], device=DEV)
+        view = room.as_strided((1, n, h, D), (room.numel(), pitch, D, 1))
+        if t is not None:
+            view.copy_(t)
+        return view
+
+    q, k, v, go = dense
+    fq, fk, fv, fg = [far(t) for t in dense]
+    w = torch.rand(D, generator=g).to(TYPES[dtype]).to(DEV)
+    zq, zk = nabla.nabla_qk_norm_rope(q, k, w, w)
+    yq, yk = nabla.nabla_qk_norm_rope(fq, fk, w, w, q_out=far(), k_out=far())
+    assert torch.equal(zq, yq) and torch.equal(zk, yk)
+    want = nabla.nabla_qk_norm_rope_bwd(q, k, w, w, go, v)
+    got = nabla.nabla_qk_norm_rope_bwd(fq, fk, w, w, fg, fv, dq=yq, dk=yk)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    o, lse = nabla.nabla_cross_attn_fwd_lse(q, k, v)
+    p, pse = nabla.nabla_cross_attn_fwd_lse(fq, fk, fv)
+    assert torch.equal(o, p) and torch.equal(lse, pse)
+    yq.copy_(o)
+    want = nabla.nabla_cross_attn_bwd(q, k, v, o, lse, go)
+    got = nabla.nabla_cross_attn_bwd(fq, fk, fv, yq, lse, fg)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    assert nabla.nabla_get_last_device_status() == 0

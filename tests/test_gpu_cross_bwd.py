@@ -125,6 +125,10 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (2, 900, 64, 14, 2, 128, [64, 50], False),      # seven heads a group
     (1, 2000, 200, 4, 4, 64, [199], False),
     (2, 333, 150, 4, 2, 128, [150, 90], "heads"),
+    (4, 1, 2000, 24, 8, 128, [2000, 1999, 130, 0], False),  # one token each
+    (3, 5, 300, 6, 2, 64, [300, 0, 65], True),      # fifteen rows a key head
+    (2, 16, 129, 2, 2, 128, [129, 1], "heads"),     # sixteen
+    (1, 17, 129, 2, 2, 64, None, False),            # one more
 ]
 
 
