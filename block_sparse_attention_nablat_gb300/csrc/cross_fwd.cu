@@ -92,9 +92,12 @@ cudaError_t launch_join(const CrossArgs &a, int nsplit, cudaStream_t st) {
 //
 // fp32: cross_simt_plan.
 int cross_fwd_splits(const CrossShape &s, nabla_dtype dt) {
-  if (dt == NABLA_F32) return cross_simt_plan(s).nsplit;
-  const long units = (long)s.B * s.hk * ((cross::packing(s).nsub + 1) / 2);
-  const long runs = 152 / units, tiles = (s.Sk + cross::kTile - 1) / cross::kTile;
+  const bool few = cross_few_rows(s, dt);
+  if (dt == NABLA_F32 && !few) return cross_simt_plan(s).nsplit;
+  // fp32, few rows: 64-state tiles, a unit per key head, two CTAs on an SM
+  const long units = (long)s.B * s.hk * (few ? 1 : (cross::packing(s).nsub + 1) / 2);
+  const long runs = (few ? 304 : 152) / units;
+  const long tiles = few ? (s.Sk + 63) / 64 : (s.Sk + cross::kTile - 1) / cross::kTile;
   const long n = runs < tiles / 4 ? runs : tiles / 4;
   return n < 2 ? 1 : (int)n;
 }

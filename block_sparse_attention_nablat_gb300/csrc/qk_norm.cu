@@ -168,7 +168,7 @@ struct Side {  // q or k
   void *out;  // z, or dx
   const void *w;
   nabla_strides x_st, z_st, o_st;  // of x, dz and out
-  int h, chunks;                   // heads, items per token
+  int h, chunks;                   // heads, items per token (few heads: tokens per item)
 };
 
 struct QkParams {
@@ -177,6 +177,7 @@ struct QkParams {
   const float *cos_t, *sin_t;
   const int32_t *pos;
   long tokens, items;  // B * S; tokens * (chunks of both sides)
+  long first;          // few heads: items of q, the first ones
   int S, rows, R, heads_per_item;
   float eps;
   float *partial;  // backward: [grid][2][D] column sums
@@ -255,6 +256,32 @@ __global__ void __launch_bounds__(kThreads) qk_norm_kernel(const __grid_constant
   }
 }
 
+// A block's sums of dy x r, its warps' added in order, to its row of `partial`.
+template <int D>
+__device__ __forceinline__ void put_sums(const float (&acc)[2][8], float (*sums)[2 * D],
+                                         float *partial) {
+  constexpr int kLanes = D / 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = (lane % kLanes) * 8, sub = lane / kLanes;
+  if (!partial) return;
+#pragma unroll
+  for (int sd = 0; sd < 2; ++sd)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float v = acc[sd][j];
+#pragma unroll
+      for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0) sums[warp][sd * D + col + j] = v;
+    }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += sums[k][c];
+    partial[(size_t)blockIdx.x * 2 * D + c] = v;
+  }
+}
+
 // dx row by row as above; every warp keeps the column sums of dy x r of both sides
 // in registers over all its items, the block joins its warps' sums in a fixed order
 // and writes one row per block, and qk_dw_kernel adds the rows.  Items are dealt out
@@ -328,23 +355,149 @@ __global__ void __launch_bounds__(kThreads)
       acc[1][j] += it.side ? part[j] : 0.f;
     }
   }
-  if (!P.partial) return;
+  put_sums<D>(acc, sums, P.partial);
+}
+
+// The same for few heads, where one token's rows would leave most of a warp's loads unused:
+// an item is a run of tokens whose rows one pass of the warp takes, each with its own
+// angles.
+struct FewItem {
+  int side, rows;   // rows of the run
+  long t0, b0, s0;  // its first token
+};
+__device__ __forceinline__ FewItem few_item(const QkParams &P, long i) {
+  FewItem it;
+  it.side = i >= P.first;
+  const Side &sd = P.side[it.side];
+  it.t0 = (it.side ? i - P.first : i) * sd.chunks;
+  it.rows = (int)min((long)sd.chunks, P.tokens - it.t0) * sd.h;
+  it.b0 = it.t0 / P.S;
+  it.s0 = it.t0 - it.b0 * P.S;
+  return it;
+}
+struct FewRow {
+  long b, s, at;
+  int head;
+  bool on, turn;
+};
+__device__ __forceinline__ FewRow few_row(const QkParams &P, const FewItem &it, int r, bool lead) {
+  const uint32_t h = (uint32_t)P.side[it.side].h, dt = (uint32_t)r / h;
+  FewRow w;
+  w.on = r < it.rows;
+  w.head = r - (int)(dt * h);
+  const uint32_t st = (uint32_t)it.s0 + dt, db = st / (uint32_t)P.S;
+  w.b = it.b0 + db;
+  w.s = st - db * (uint32_t)P.S;
+  w.at = w.s;
+  w.turn = w.on && P.R > 0;
+  if (w.turn && P.pos) {
+    w.at = P.pos[it.t0 + dt];
+    if (w.at < 0 || w.at >= P.rows) {  // normed, not rotated, and reported
+      if (lead) atomicCAS(P.status, kDevOk, kDevBadIndex);
+      w.turn = false;
+    }
+  }
+  return w;
+}
+__device__ __forceinline__ int64_t row_at(const nabla_strides &st, const FewRow &w) {
+  return w.b * st.batch + w.s * st.token + w.head * st.head;
+}
+
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads) qk_few_kernel(const __grid_constant__ QkParams P) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = 4;
+  const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long stride = (long)gridDim.x * kWarps;
+  for (long i = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < P.items; i += stride) {
+    const FewItem it = few_item(P, i);
+    const Side &sd = P.side[it.side];
+    Raw<T> in[kAhead];
+    Turn t[kAhead];
+    T *o[kAhead];
 #pragma unroll
-  for (int sd = 0; sd < 2; ++sd)
+    for (int a = 0; a < kAhead; ++a) {
+      const FewRow w = few_row(P, it, a * kRows + sub, col == 0);
+      in[a] = load_raw(static_cast<const T *>(sd.x) + row_at(sd.x_st, w) + col, w.on);
+      t[a] = load_turn<kPairs>(P.cos_t, P.sin_t, w.at, P.R, col, lane, w.turn);
+      o[a] = w.on ? static_cast<T *>(sd.out) + row_at(sd.o_st, w) + col : nullptr;
+    }
+    float w[8];
+    load_weight(sd.w, P.wdt, col, w);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (a * kRows >= it.rows) break;  // the same for the whole warp
+      float y[8], ss = 0.f;
+      unpack8(in[a], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+      const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= r * w[j];
+      turn8<kPairs, false>(y, t[a]);
+      if (o[a]) store8(o[a], y);
+    }
+  }
+}
+
+template <typename T, int D, bool kPairs>
+__global__ void __launch_bounds__(kThreads) qk_few_bwd_kernel(const __grid_constant__ QkParams P) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = sizeof(T) == 2 ? 4 : 2;
+  __shared__ float sums[kWarps][2 * D];
+  const int lane = threadIdx.x & 31, col = (lane % kLanes) * 8, sub = lane / kLanes;
+  pdl_launch_dependents();
+  pdl_wait();
+  float acc[2][8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[0][j] = acc[1][j] = 0.f;
+  const long stride = (long)gridDim.x * kWarps;
+  for (long i = (long)blockIdx.x * kWarps + (threadIdx.x >> 5); i < P.items; i += stride) {
+    const FewItem it = few_item(P, i);
+    const Side &sd = P.side[it.side];
+    Raw<T> xin[kAhead], zin[kAhead];
+    Turn t[kAhead];
+    T *o[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const FewRow w = few_row(P, it, a * kRows + sub, col == 0);
+      xin[a] = load_raw(static_cast<const T *>(sd.x) + row_at(sd.x_st, w) + col, w.on);
+      zin[a] = load_raw(static_cast<const T *>(sd.dz) + row_at(sd.z_st, w) + col, w.on);
+      t[a] = load_turn<kPairs>(P.cos_t, P.sin_t, w.at, P.R, col, lane, w.turn);
+      o[a] = w.on ? static_cast<T *>(sd.out) + row_at(sd.o_st, w) + col : nullptr;
+    }
+    float w[8], part[8];
+    load_weight(sd.w, P.wdt, col, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[j] = 0.f;
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      if (a * kRows >= it.rows) break;  // the same for the whole warp
+      float xv[8], g[8], ss = 0.f, dot = 0.f;
+      unpack8(xin[a], xv);
+      unpack8(zin[a], g);
+      turn8<kPairs, true>(g, t[a]);  // dy
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        ss = fmaf(xv[j], xv[j], ss);
+        dot = fmaf(g[j] * w[j], xv[j], dot);
+      }
+      const float r = rsqrtf(fmaf(row_sum<kLanes>(ss), 1.f / D, P.eps));
+      const float m = row_sum<kLanes>(dot) * (1.f / D) * r * r;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (o[a]) part[j] = fmaf(g[j] * r, xv[j], part[j]);
+        g[j] = r * fmaf(-xv[j], m, g[j] * w[j]);
+      }
+      if (o[a]) store8(o[a], g);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float v = acc[sd][j];
-#pragma unroll
-      for (int o = 16; o >= kLanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (sub == 0) sums[warp][sd * D + col + j] = v;
+      acc[0][j] += it.side ? 0.f : part[j];
+      acc[1][j] += it.side ? part[j] : 0.f;
     }
-  __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += sums[k][c];
-    P.partial[(size_t)blockIdx.x * 2 * D + c] = v;
   }
+  put_sums<D>(acc, sums, P.partial);
 }
 
 // dw: the blocks' rows added up, 32 columns a block, 32 rows at a time.
@@ -376,6 +529,14 @@ __global__ void __launch_bounds__(1024) qk_dw_kernel(const float *__restrict__ p
 // partial sums (the workspace holds this many).
 constexpr int kBwdBlocksPerSm = 4, kBwdBlocksMost = 1024;
 
+enum Kind { kDenseHeads, kStrided, kFewHeads };
+
+template <typename T, int D, bool kPairs>
+cudaError_t launch_few(const QkParams &p, bool bwd, unsigned grid, cudaStream_t st) {
+  if (bwd) return launch_pdl(qk_few_bwd_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
+  return launch_pdl(qk_few_kernel<T, D, kPairs>, grid, kThreads, 0, st, p);
+}
+
 template <typename T, int D, bool kPairs, bool kDense>
 cudaError_t launch_typed(const QkParams &p, bool bwd, unsigned grid, cudaStream_t st) {
   if (bwd) return launch_pdl(qk_norm_bwd_kernel<T, D, kPairs, kDense>, grid, kThreads, 0, st, p);
@@ -383,9 +544,12 @@ cudaError_t launch_typed(const QkParams &p, bool bwd, unsigned grid, cudaStream_
 }
 
 template <typename T, int D>
-cudaError_t launch_dim(const QkParams &p, bool pairs, bool bwd, bool dense, unsigned grid,
+cudaError_t launch_dim(const QkParams &p, bool pairs, bool bwd, Kind kind, unsigned grid,
                        cudaStream_t st) {
-  if (dense)
+  if (kind == kFewHeads)
+    return pairs ? launch_few<T, D, true>(p, bwd, grid, st)
+                 : launch_few<T, D, false>(p, bwd, grid, st);
+  if (kind == kDenseHeads)
     return pairs ? launch_typed<T, D, true, true>(p, bwd, grid, st)
                  : launch_typed<T, D, false, true>(p, bwd, grid, st);
   return pairs ? launch_typed<T, D, true, false>(p, bwd, grid, st)
@@ -393,10 +557,10 @@ cudaError_t launch_dim(const QkParams &p, bool pairs, bool bwd, bool dense, unsi
 }
 
 template <typename T>
-cudaError_t launch_dtype(const QkParams &p, int D, bool pairs, bool bwd, bool dense, unsigned grid,
+cudaError_t launch_dtype(const QkParams &p, int D, bool pairs, bool bwd, Kind kind, unsigned grid,
                          cudaStream_t st) {
-  return D == 64 ? launch_dim<T, 64>(p, pairs, bwd, dense, grid, st)
-                 : launch_dim<T, 128>(p, pairs, bwd, dense, grid, st);
+  return D == 64 ? launch_dim<T, 64>(p, pairs, bwd, kind, grid, st)
+                 : launch_dim<T, 128>(p, pairs, bwd, kind, grid, st);
 }
 
 }  // namespace
@@ -430,6 +594,12 @@ cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st) {
   if (p.tokens * 2 < (long)sms * 64) hpi = pass;
   p.heads_per_item = hpi;
   p.items = 0;
+  // Few heads: runs of tokens, where several tokens' rows go into a pass: four, two where
+  // there is more work to a row's angles, eight where the angles take more registers.  (D 128, forward / backward, us, as runs of
+  // tokens against a token an item: 9 x 13717 tokens, 1 + 1 heads, pairs 41 / 51 against
+  // 90 / 172, halves 62 / 113 against 102 / 189; 98304 tokens, 4 + 4 heads, pairs 121 / 149
+  // against 101 / 189, halves 168 / 304 against 115 / 206.)
+  const bool few = most * (a.interleaved ? (bwd ? 2 : 4) : 8) <= pass;
   bool dense = true;
   for (int i = 0; i < 2; ++i) {
     Side &s = p.side[i];
@@ -443,16 +613,23 @@ cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st) {
     if (a.h[i] > 1 && (s.x_st.head != a.D || s.o_st.head != a.D || (bwd && s.z_st.head != a.D)))
       dense = false;
     s.h = a.h[i];
-    s.chunks = (a.h[i] + hpi - 1) / hpi;
-    p.items += p.tokens * s.chunks;
+    if (few) {
+      s.chunks = a.h[i] ? pass / a.h[i] : 1;
+      if (a.h[i]) p.items += (p.tokens + s.chunks - 1) / s.chunks;
+      if (i == 0) p.first = p.items;
+    } else {
+      s.chunks = (a.h[i] + hpi - 1) / hpi;
+      p.items += p.tokens * s.chunks;
+    }
   }
   const long need = (p.items + kWarps - 1) / kWarps;
   long cap = bwd ? (long)sms * kBwdBlocksPerSm : (long)sms * 64;
   if (bwd && cap > kBwdBlocksMost) cap = kBwdBlocksMost;
   const unsigned grid = (unsigned)(need < cap ? need : cap);
   if (bwd && (a.dw[0] || a.dw[1])) p.partial = static_cast<float *>(a.workspace);
-  e = a.dt == NABLA_BF16 ? launch_dtype<__nv_bfloat16>(p, a.D, a.interleaved, bwd, dense, grid, st)
-                         : launch_dtype<float>(p, a.D, a.interleaved, bwd, dense, grid, st);
+  const Kind kind = few ? kFewHeads : dense ? kDenseHeads : kStrided;
+  e = a.dt == NABLA_BF16 ? launch_dtype<__nv_bfloat16>(p, a.D, a.interleaved, bwd, kind, grid, st)
+                         : launch_dtype<float>(p, a.D, a.interleaved, bwd, kind, grid, st);
   if (e != cudaSuccess || !p.partial) return e;
   return launch_pdl(qk_dw_kernel, dim3(2 * a.D / 32), dim3(1024), 0, st,
                     (const float *)p.partial, (int)grid, a.D, a.dw[0], a.dw[1], a.wdt);

@@ -117,6 +117,10 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (2, 1, 900, 14, 2, 128, [900, 385], True),     # seven heads a group, runs
     (1, 1537, 513, 2, 1, 128, None, True),
     (2, 333, 150, 4, 2, 128, [150, 90], "heads"),
+    (3, 5, 300, 6, 2, 64, [300, 0, 65], True),      # fifteen rows a key head
+    (2, 16, 129, 2, 2, 128, [129, 1], "heads"),     # sixteen
+    (1, 17, 129, 2, 2, 64, None, False),            # one more
+    (160, 2, 70, 2, 1, 64, None, False),            # four rows a key head, more than fill the GPU
 ]
 
 

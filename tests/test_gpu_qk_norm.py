@@ -130,6 +130,10 @@ CASES = [  # B, S, hq, hk, D, R, dtype, pairs, packed, positions
     (1, 257, 6, 0, 64, 32, "bf16", False, False, False),   # q alone
     (2, 300, 24, 24, 128, 128, "f32", True, False, False),
     (2, 50, 6, 3, 64, 64, "bf16", True, "heads", False),
+    (5, 1, 3, 1, 64, 64, "bf16", False, False, True),      # few heads: runs of tokens
+    (3, 37, 2, 1, 128, 96, "bf16", True, True, True),
+    (1, 130, 1, 1, 64, 16, "f32", False, True, True),
+    (2, 61, 4, 1, 128, 128, "f32", True, "heads", False),
 ]
 
 
