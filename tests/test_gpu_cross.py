@@ -121,6 +121,7 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (2, 16, 129, 2, 2, 128, [129, 1], "heads"),     # sixteen
     (1, 17, 129, 2, 2, 64, None, False),            # one more
     (160, 2, 70, 2, 1, 64, None, False),            # four rows a key head, more than fill the GPU
+    (3, 650, 1200, 9, 9, 64, [1200, 1100, 64], False),  # many tiles in one run
 ]
 
 
