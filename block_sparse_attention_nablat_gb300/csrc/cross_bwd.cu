@@ -119,7 +119,7 @@ size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 struct BwdLayout {
   int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
-  size_t nlse, ndelta, part, total;
+  size_t nlse, ndelta, part, qpart, total;
 };
 BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
@@ -131,6 +131,9 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   w.part = 2 * rows;
   w.total = w.part + (n > 1 ? round_up((size_t)n * 2 * s.B * s.Sk * s.hk * s.D * sizeof(float))
                             : 0);
+  w.qpart = w.total;
+  if (dt == NABLA_BF16 && cross_dq_splits(s) > 1)
+    w.total += round_up((size_t)cross_dq_splits(s) * s.B * s.Sq * s.h * s.D * sizeof(float));
   if (cross_few_rows(s, dt))
     w.total += round_up((size_t)((s.Sk + 63) / 64) * s.B * s.h * s.Sq * s.D * sizeof(float));
   return w;
@@ -179,6 +182,17 @@ int cross_dkv_splits(const CrossShape &s, nabla_dtype dt) {
   return best;
 }
 
+// Runs of state tiles the bf16 dQ units are split into: as in the forward, only where they
+// still go on the SMs in one wave, four tiles at least.  (Whole backward, D 128, us, in runs
+// and whole: 2 x 6 tokens, 4553 states, 24 heads: 115, 141; 1 x 8192, 1 head: 25, 77;
+// 300 x 4096, 8 heads: 45, 60.)
+int cross_dq_splits(const CrossShape &s) {
+  const long units = (long)s.B * s.hk * ((cross::packing(s).nsub + 1) / 2);
+  const long runs = 152 / units, tiles = (s.Sk + cross::kTile - 1) / cross::kTile;
+  const long n = runs < tiles / 4 ? runs : tiles / 4;
+  return n < 2 ? 1 : (int)n;
+}
+
 size_t cross_bwd_workspace(const CrossShape &s, nabla_dtype dt) { return bwd_layout(s, dt).total; }
 
 cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st) {
@@ -196,7 +210,8 @@ cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st
     e = a.s.D == 64 ? launch_prep<float, 64>(a, pk, w.nsub, nlse, ndelta, st)
                     : launch_prep<float, 128>(a, pk, w.nsub, nlse, ndelta, st);
   if (e != cudaSuccess) return e;
-  return dt == NABLA_BF16 ? launch_cross_bwd_tc(a, nlse, ndelta, part, st)
+  float *qpart = reinterpret_cast<float *>(ws + w.qpart);
+  return dt == NABLA_BF16 ? launch_cross_bwd_tc(a, nlse, ndelta, part, qpart, st)
                           : launch_cross_bwd_simt(a, nlse, ndelta, part, w.nsub, st);
 }
 

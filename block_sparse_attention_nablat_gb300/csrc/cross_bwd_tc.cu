@@ -22,6 +22,8 @@
 //  * dQ: unit = a tile of 128 packed query rows over the batch's state tiles.  X = Q K^T,
 //    Y = dO V^T, dz as bf16 in one of two buffers, dQ += dz K.  X and Y are free for the
 //    next step as soon as the softmax warps have them in registers.
+//    Few units are split over runs of the states (cross_dq_splits), whose fp32 sums
+//    cross_dq_sum adds up in order.
 //
 // Eight softmax warps: thread = TMEM lane, group grp takes columns 64 grp .. + 63; P stays
 // in fp32 registers between the two phases.  States past kv_len: dK/dV rows of P and dz
@@ -91,7 +93,8 @@ struct KSync {
   int abort;
 };
 struct QSync {
-  uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw, v_full[2], v_empty[2];
+  uint64_t q_full[2], q_empty[2], g_full, g_empty, k_full[3], k_empty[3], k_raw;
+  uint64_t v_full[2], v_empty[2];
   uint64_t x_full, y_full, x_free, y_free, z_full[2], acc_full, out_full, drain;
   uint32_t tmem_slot;
   int abort;
@@ -542,11 +545,15 @@ __global__ void __launch_bounds__(384, 1)
 // ---------------------------------------------------------------- dQ
 
 struct QUnit {
-  int b, j, qt, len, n;  // n state tiles
+  int b, j, qt, sp, len, t0, n;  // n state tiles from t0
 };
 __device__ __forceinline__ QUnit q_unit(const YParams &P, const cross::Walk &w) {
-  QUnit r{w.b, w.j, w.t, cross::batch_len(P.kv_len, w.b, P.Sk), 0};
+  QUnit r{w.b, w.j, w.t, w.sp, cross::batch_len(P.kv_len, w.b, P.Sk), 0, 0};
   r.n = (r.len + kTile - 1) / kTile;
+  if (P.nsplit > 1) {  // a run of them
+    r.t0 = (int)((long)r.n * r.sp / P.nsplit);
+    r.n = (int)((long)r.n * (r.sp + 1) / P.nsplit) - r.t0;
+  }
   return r;
 }
 
@@ -609,7 +616,7 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
     const QUnit u = q_unit(P, w);
     if (lane == 0) cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     for (int t = 0; t < u.n && go; ++t, ++g, kr.next(), vr.next()) {
-      const int rows = u.len - t * kTile, end = rows >= kTile ? kTile : (rows + 15) & ~15;
+      const int rows = u.len - (u.t0 + t) * kTile, end = rows >= kTile ? kTile : (rows + 15) & ~15;
       const bool mend = rows < end && u.len < P.Sk;  // zero K's rows [rows, end)
       uint8_t *tile = smem + C::kOffK2 + kr.slot * C::kTileBytes;
       bool ok = true;
@@ -620,7 +627,7 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
           uint64_t *bar = mend ? &sy->k_raw : &sy->k_full[kr.slot];
           mbar_expect_tx(bar, C::kTileBytes);
           for (int c = 0; c < C::kBoxes; ++c)
-            tma_load_4d(tile + c * C::kBox, mk, bar, c * 64, u.j, t * kTile, u.b);
+            tma_load_4d(tile + c * C::kBox, mk, bar, c * 64, u.j, (u.t0 + t) * kTile, u.b);
           if (mend) ok = mbar_wait_small(&sy->k_raw, raw & 1u, nullptr, P.status, kDevTimeout);
         }
       }
@@ -643,7 +650,7 @@ __device__ void q_load_kv(const YParams &P, const CUtensorMap *mk, const CUtenso
           mbar_expect_tx(&sy->v_full[vr.slot], C::kTileBytes);
           for (int c = 0; c < C::kBoxes; ++c)
             tma_load_4d(smem + C::kOffV2 + vr.slot * C::kTileBytes + c * C::kBox, mv,
-                        &sy->v_full[vr.slot], c * 64, u.j, t * kTile, u.b);
+                        &sy->v_full[vr.slot], c * 64, u.j, (u.t0 + t) * kTile, u.b);
         } else {  // the K tile of this step is in flight
           mbar_wait_small(&sy->k_full[kr.slot], kr.phase, nullptr, P.status, kDevTimeout);
         }
@@ -730,7 +737,7 @@ __device__ void q_mma(const YParams &P, uint8_t *smem, QSync *sy, uint32_t tmem,
       vr.next();
       if (t + 1 == u.n) mma_commit(&sy->g_empty);
       if (t > 0) issue_dq(false);
-      left = u.len - t * kTile;
+      left = u.len - (u.t0 + t) * kTile;
     }
     q.next();
     ++ku;
@@ -754,15 +761,17 @@ __device__ void q_store(const YParams &P, const CUtensorMap *mo, const uint8_t *
     if (u.n == 0) continue;
     if (!cross::thread_wait(&sy->out_full, ku & 1u, abort, P.status)) break;
     const uint8_t *tile = smem + (ku & 1u) * C::kTileBytes;
+    if (P.nsplit == 1) {  // (a run's sums do not come this way)
 #pragma unroll 1
-    for (int x = 0; x < 2 * C::kBoxes; ++x) {
-      const int t0 = (u.qt * 2 + (x & 1)) * P.tq;
-      if (t0 < P.Sq)
-        tma_store_4d(mo, tile + (x >> 1) * C::kBox + (x & 1) * 64 * 128, (x >> 1) * 64,
-                     u.j * P.G, t0, u.b);
+      for (int x = 0; x < 2 * C::kBoxes; ++x) {
+        const int t0 = (u.qt * 2 + (x & 1)) * P.tq;
+        if (t0 < P.Sq)
+          tma_store_4d(mo, tile + (x >> 1) * C::kBox + (x & 1) * 64 * 128, (x >> 1) * 64,
+                       u.j * P.G, t0, u.b);
+      }
+      bulk_commit();
+      bulk_wait_read();
     }
-    bulk_commit();
-    bulk_wait_read();
     mbar_arrive(&sy->q_empty[ku & 1u]);
     ++ku;
   }
@@ -784,10 +793,15 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
   const int tok = r64 / P.G, head = r64 - tok * P.G;
   uint32_t g = 0, ku = 0;
   bool live = true;
-  auto write_rows = [&]() {  // of unit ku - 1, over its Q
+  QUnit last{};              // unit ku - 1
+  auto write_rows = [&]() {  // of unit ku - 1, over its Q; a run's sums to their part
     cross::warp_wait(live, &sy->acc_full, (ku - 1) & 1u, abort, P.status);
     tc_fence_after();
     uint8_t *tile = smem + ((ku - 1) & 1u) * C::kTileBytes + row * 128;
+    const int token = (last.qt * 2 + (row >> 6)) * P.tq + tok, hh = last.j * P.G + head;
+    float *part = nullptr;
+    if (P.nsplit > 1 && tok < P.tq && token < P.Sq)
+      part = P.part + ((((size_t)last.sp * P.B + last.b) * P.Sq + token) * P.h + hh) * D;
 #pragma unroll 1
     for (int x = 0; x < D / 64; ++x) {  // 32 columns of this group's D / 2
       const int c = grp * (D / 2) + x * 32;
@@ -795,6 +809,14 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
       tmem_ld32(at + C::kDQ + c, t);
       tmem_wait_ld();
       reg_fence(t);
+      if (P.nsplit > 1) {
+        if (part)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4 *>(part + c + e) =
+                make_uint4(t[e], t[e + 1], t[e + 2], t[e + 3]);
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint32_t v[4];
@@ -832,7 +854,7 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
     }
     if (c.n == 0) {
       const int token = (c.qt * 2 + (row >> 6)) * P.tq + tok, hh = c.j * P.G + head;
-      if (tok < P.tq && token < P.Sq) {
+      if (P.nsplit == 1 && tok < P.tq && token < P.Sq) {
         uint4 *o = reinterpret_cast<uint4 *>(
             P.dq + (((size_t)c.b * P.Sq + token) * P.h + hh) * D + grp * (D / 2));
 #pragma unroll 1
@@ -842,7 +864,7 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
     }
     const uint64_t nl2 = f2(nl, nl), nd2 = f2(nd, nd);
     for (int t = 0; t < c.n; ++t, ++g) {
-      const int mine = c.len - t * kTile - grp * 64;  // own columns that are states
+      const int mine = c.len - (c.t0 + t) * kTile - grp * 64;  // own columns that are states
       cross::warp_wait(live, &sy->x_full, g & 1u, abort, P.status);
       tc_fence_after();
       uint32_t x0[32], x1[32];
@@ -901,6 +923,7 @@ __device__ void q_softmax(const YParams &P, uint8_t *smem, QSync *sy, uint32_t t
       tc_fence_before();
       y_arrive(&sy->z_full[g & 1u], lane);
     }
+    last = c;
     ++ku;
   }
   if (ku > 0) write_rows();
@@ -985,9 +1008,30 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
+// dQ of runs: their sums added up in order, scaled and rounded.  A thread per four columns.
+__global__ void __launch_bounds__(256)
+    cross_dq_sum_kernel(const __grid_constant__ YParams P, long n4, int row) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const long e = i * 4;
+  const int b = (int)(e / row / P.Sq);
+  const int tiles = (cross::batch_len(P.kv_len, b, P.Sk) + kTile - 1) / kTile;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int sp = 0; sp < P.nsplit; ++sp) {
+    if ((long)tiles * sp / P.nsplit == (long)tiles * (sp + 1) / P.nsplit) continue;  // no states
+    const float4 x = *reinterpret_cast<const float4 *>(P.part + (size_t)sp * n4 * 4 + e);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+  *reinterpret_cast<uint2 *>(P.dq + e) = make_uint2(pack_bf16x2(s.x * P.scale, s.y * P.scale),
+                                                    pack_bf16x2(s.z * P.scale, s.w * P.scale));
+}
+
 template <int D>
 cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta, float *part,
-                     cudaStream_t st) {
+                     float *qpart, cudaStream_t st) {
   using C = YCfg<D>;
   const CrossShape &s = a.s;
   cudaError_t err;
@@ -1033,23 +1077,29 @@ cudaError_t launch_y(const CrossArgs &a, const float *nlse, const float *ndelta,
   if (err == cudaSuccess && p.nsplit > 1)
     err = launch_cross_dkv_join(a, NABLA_BF16, part, p.nsplit, st);
   if (err != cudaSuccess) return err;
-  p.units = (uint32_t)((long)s.B * s.hk * p.nq);
+  p.nsplit = cross_dq_splits(s);
+  p.part = qpart;
+  p.units = (uint32_t)((long)s.B * s.hk * p.nq * p.nsplit);
   auto kern2 = cross_dq_kernel<D>;
   if ((err = cudaFuncSetAttribute(kern2, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   y_smem_bytes<D, true>())) != cudaSuccess)
     return err;
   grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
-  p.walk = cross::walk_step(grid, 1, p.nq, s.hk);
-  return launch_pdl(kern2, dim3(grid), dim3(C::kThreads), y_smem_bytes<D, true>(), st, mq, mk, mv,
-                    mg, mo, p);
+  p.walk = cross::walk_step(grid, p.nsplit, p.nq, s.hk);
+  err = launch_pdl(kern2, dim3(grid), dim3(C::kThreads), y_smem_bytes<D, true>(), st, mq, mk, mv,
+                   mg, mo, p);
+  if (err != cudaSuccess || p.nsplit == 1) return err;
+  const long n4 = (long)s.B * s.Sq * s.h * (D / 4);
+  return launch_pdl(cross_dq_sum_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, p,
+                    n4, s.h * D);
 }
 
 }  // namespace
 
 cudaError_t launch_cross_bwd_tc(const CrossArgs &a, const float *nlse, const float *ndelta,
-                                float *part, cudaStream_t st) {
-  return a.s.D == 64 ? launch_y<64>(a, nlse, ndelta, part, st)
-                     : launch_y<128>(a, nlse, ndelta, part, st);
+                                float *part, float *qpart, cudaStream_t st) {
+  return a.s.D == 64 ? launch_y<64>(a, nlse, ndelta, part, qpart, st)
+                     : launch_y<128>(a, nlse, ndelta, part, qpart, st);
 }
 
 }  // namespace nabla

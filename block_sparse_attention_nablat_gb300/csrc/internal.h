@@ -126,7 +126,7 @@ struct CrossArgs {
   void *workspace;
   int *status;
 };
-// Runs of states the bf16 forward splits its units into, and the scratch they need.
+// Runs of states the forward splits its units into, and the scratch they need.
 int cross_fwd_splits(const CrossShape &s, nabla_dtype dt);
 struct CrossSimtPlan {
   int A, nsplit;
@@ -142,15 +142,16 @@ cudaError_t launch_cross_combine(const CrossArgs &a, nabla_dtype dt, int nsplit,
 cudaError_t launch_cross_attn_tc(const CrossArgs &a, cudaStream_t st);
 cudaError_t launch_cross_attn_simt(const CrossArgs &a, cudaStream_t st);
 // K10: the backward (prep, products, join).  Workspace: -lse and -delta of the packed
-// rows, then the runs' sums of dK and dV where these are split (cross_dkv_splits).
+// rows, then the runs' sums of dK and dV and of dQ where these are split.
 int cross_dkv_splits(const CrossShape &s, nabla_dtype dt);
+int cross_dq_splits(const CrossShape &s);  // bf16
 // Whether the fp32 backward takes its form for few rows (the tiles' dq follow the rows).
 bool cross_few_rows(const CrossShape &s, nabla_dtype dt);
 size_t cross_bwd_workspace(const CrossShape &s, nabla_dtype dt);
 cudaError_t launch_cross_bwd(const CrossArgs &a, nabla_dtype dt, cudaStream_t st);
 // Its parts: the products in bf16 (tcgen05) and fp32 (CUDA cores), each with the join.
 cudaError_t launch_cross_bwd_tc(const CrossArgs &a, const float *nlse, const float *ndelta,
-                                float *part, cudaStream_t st);
+                                float *part, float *qpart, cudaStream_t st);
 cudaError_t launch_cross_bwd_simt(const CrossArgs &a, const float *nlse, const float *ndelta,
                                   float *part, int nsub, cudaStream_t st);
 cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const float *part,

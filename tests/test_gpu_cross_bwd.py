@@ -129,6 +129,7 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (3, 5, 300, 6, 2, 64, [300, 0, 65], True),      # fifteen rows a key head
     (2, 16, 129, 2, 2, 128, [129, 1], "heads"),     # sixteen
     (1, 17, 129, 2, 2, 64, None, False),            # one more
+    (3, 6, 2300, 4, 4, 128, [2300, 700, 0], True),  # few rows, runs of states
 ]
 
 
