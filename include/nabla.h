@@ -390,7 +390,8 @@ nabla_status nabla_qk_norm_rope(const void *q, const nabla_strides *q_st, const 
  *                   overlapping any other argument.
  *   dwq, dwk        [D] device, element type wdt, overwritten; NULL: not wanted.
  *   workspace       device scratch of ws_bytes >= nabla_qk_norm_rope_bwd_workspace_bytes()
- *                   (256-byte aligned); not looked at when dwq and dwk are NULL.
+ *                   (256-byte aligned); not looked at when dwq and dwk are NULL.  Calls
+ *                   that overlap on the GPU need a workspace each.
  * Everything else, and the errors, as for nabla_qk_norm_rope.
  */
 size_t nabla_qk_norm_rope_bwd_workspace_bytes(int D);
@@ -462,7 +463,7 @@ nabla_status nabla_cross_attn_fwd(const void *q, const nabla_strides *q_st, cons
  *   dq          [B, Sq, h, D], dk and dv [B, Sk, hk, D] device, dense, element type dt,
  *               overwritten; they overlap no other argument.
  *   workspace   device scratch of ws_bytes >= nabla_cross_attn_bwd_workspace_bytes()
- *               (256-byte aligned).
+ *               (256-byte aligned); calls that overlap on the GPU need one each.
  * o, dout, dq, dk and dv are 16-byte aligned.  Everything else, and the errors, as for
  * nabla_cross_attn_fwd.
  */
