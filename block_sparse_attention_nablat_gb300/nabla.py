@@ -3,8 +3,10 @@
 Argument marshalling only: every step of the hot path runs in the library's
 CUDA kernels.  torch supplies device memory (outputs and the mask-builder
 workspace are allocated here with torch when the caller passes none) and the
-current CUDA stream.  If the library is missing, every call raises; there is
-no fallback.
+current CUDA stream.  A call given another `stream` allocates from that stream's
+memory: its scratch is reused only behind its kernels, and its outputs may be read
+on that stream and, once ordered behind it, on the stream that was current.  If the
+library is missing, every call raises; there is no fallback.
 """
 from __future__ import annotations
 
@@ -140,6 +142,38 @@ def _run(device: torch.device, stream, fn, where: str, *args) -> None:
         raise NablaError(st, where)
 
 
+def _allocators(stream, device: torch.device):
+    """torch.empty for the outputs and for the scratch of a call on `stream`.
+
+    The caching allocator hands a freed block out again in the order of the stream it was
+    allocated on.  A block of the current stream would go to the next allocation there,
+    or to a call on a third stream, while this call's kernels on `stream` still use it
+    (its scratch is dropped when the call returns), and might itself still be in use by
+    work of the current stream.  So both come from `stream`, and the outputs, which the
+    caller goes on using, are also kept until the current stream is done with them."""
+    if stream is None or device.type != "cuda":
+        return torch.empty, torch.empty
+    handle = _stream(stream, device)
+    current = torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return torch.empty, torch.empty
+    if handle in (0, 1):  # 1: cudaStreamLegacy, the default stream's other name
+        stream = torch.cuda.default_stream(device)
+    elif not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle, device)
+
+    def scratch(*size, **kw):
+        with torch.cuda.stream(stream):
+            return torch.empty(*size, **kw)
+
+    def outputs(*size, **kw):
+        t = scratch(*size, **kw)
+        t.record_stream(current)
+        return t
+
+    return outputs, scratch
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return NABLA_BF16
@@ -240,16 +274,17 @@ def nabla_build_mask(q: torch.Tensor, k: torch.Tensor, sta: torch.Tensor, thr: f
         raise ValueError("k must match q")
     s1 = S // 64
     dev = q.device
+    empty, scratch = _allocators(stream, dev)
     if kv_nb is None:
-        kv_nb = torch.empty((B, h, s1), dtype=torch.int32, device=dev)
+        kv_nb = empty((B, h, s1), dtype=torch.int32, device=dev)
     if kv_inds is None:
-        kv_inds = torch.empty((B, h, s1, s1), dtype=torch.int32, device=dev)
+        kv_inds = empty((B, h, s1, s1), dtype=torch.int32, device=dev)
     _on(k, "k", dev)
     _buf(sta, "sta", s1 * s1, torch.uint8, dev)
     _csr(kv_nb, kv_inds, B, h, s1, dev)
     need = lib.nabla_build_mask_workspace_bytes(B, S, h, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
     _on(workspace, "workspace", dev)
     _cuda(q)
     st = _call(dev, lib.nabla_build_mask, _ptr(q), _ptr(k), _dtype_code(q), B, S, h, D, _ptr(sta),
@@ -289,15 +324,16 @@ def nabla_build_mask_topk(q: torch.Tensor, k: torch.Tensor, topk_ratio: float,
         raise ValueError("k must match q")
     s1 = S // 64
     dev = q.device
+    empty, scratch = _allocators(stream, dev)
     if kv_nb is None:
-        kv_nb = torch.empty((B, h, s1), dtype=torch.int32, device=dev)
+        kv_nb = empty((B, h, s1), dtype=torch.int32, device=dev)
     if kv_inds is None:
-        kv_inds = torch.empty((B, h, s1, s1), dtype=torch.int32, device=dev)
+        kv_inds = empty((B, h, s1, s1), dtype=torch.int32, device=dev)
     _on(k, "k", dev)
     _csr(kv_nb, kv_inds, B, h, s1, dev)
     need = lib.nabla_build_mask_workspace_bytes(B, S, h, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
     _on(workspace, "workspace", dev)
     _cuda(q)
     st = _call(dev, lib.nabla_build_mask_topk, _ptr(q), _ptr(k), _dtype_code(q), B, S, h, D,
@@ -318,7 +354,7 @@ def nabla_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_nb: tor
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if o is None:
-        o = torch.empty_like(q)
+        o = _allocators(stream, q.device)[0](q.shape, dtype=q.dtype, device=q.device)
     _on(k, "k", q.device)
     _on(v, "v", q.device)
     _csr(kv_nb, kv_inds, B, h, S // 64, q.device)
@@ -345,8 +381,9 @@ def nabla_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_nb:
         raise ValueError("k, v must match q")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, h, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    empty, _ = _allocators(stream, q.device)
+    o = empty(q.shape, dtype=q.dtype, device=q.device) if o is None else o
+    lse = empty((B, h, S), dtype=torch.float32, device=q.device) if lse is None else lse
     _on(k, "k", q.device)
     _on(v, "v", q.device)
     _csr(kv_nb, kv_inds, B, h, S // 64, q.device)
@@ -375,9 +412,9 @@ def nabla_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.T
             raise ValueError("k, v, o, dout must match q")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(q) if dk is None else dk
-    dv = torch.empty_like(q) if dv is None else dv
+    empty, scratch = _allocators(stream, q.device)
+    dq, dk, dv = (empty(q.shape, dtype=q.dtype, device=q.device) if t is None else t
+                  for t in (dq, dk, dv))
     for name, t in (("k", k), ("v", v), ("o", o), ("dout", dout)):
         _on(t, name, q.device)
     _csr(kv_nb, kv_inds, B, h, S // 64, q.device)
@@ -387,7 +424,7 @@ def nabla_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.T
         _buf(lse, "lse", B * h * S, torch.float32, q.device)
     need = lib.nabla_attn_bwd_workspace_bytes(B, S, h, D)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=q.device)
     _on(workspace, "workspace", q.device)
     _cuda(q)
     st = _call(q.device, lib.nabla_attn_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
@@ -404,7 +441,8 @@ def nabla_sta_mask(T: int, H: int, W: int, wt: int, wh: int, ww: int, device=Non
     lib = load()
     s1 = T * H * W
     if out is None:
-        out = torch.empty((s1, s1), dtype=torch.uint8, device=device or "cuda")
+        dev = torch.device(device or "cuda")
+        out = _allocators(stream, dev)[0]((s1, s1), dtype=torch.uint8, device=dev)
     _buf(out, "out", s1 * s1, torch.uint8, out.device)
     _cuda(out)
     st = _call(out.device, lib.nabla_sta_mask, T, H, W, wt, wh, ww, _ptr(out),
@@ -420,7 +458,8 @@ def nabla_fractal_flatten(x: torch.Tensor, P: int = 8, out: Optional[torch.Tenso
         raise ValueError("x must be a contiguous [B, T, H, W, h, D] tensor")
     B, T, H, W, h, D = x.shape
     if out is None:
-        out = torch.empty((B, T * H * W, h, D), dtype=x.dtype, device=x.device)
+        out = _allocators(stream, x.device)[0]((B, T * H * W, h, D), dtype=x.dtype,
+                                               device=x.device)
     _buf(out, "out", x.numel(), x.dtype, x.device)
     _cuda(x)
     st = _call(x.device, load().nabla_fractal_flatten, _ptr(x), _dtype_code(x), B, T, H, W, h, D,
@@ -436,7 +475,8 @@ def nabla_fractal_unflatten(y: torch.Tensor, T: int, H: int, W: int, P: int = 8,
         raise ValueError("y must be a contiguous [B, T*H*W, h, D] tensor")
     B, _, h, D = y.shape
     if out is None:
-        out = torch.empty((B, T, H, W, h, D), dtype=y.dtype, device=y.device)
+        out = _allocators(stream, y.device)[0]((B, T, H, W, h, D), dtype=y.dtype,
+                                               device=y.device)
     _buf(out, "out", y.numel(), y.dtype, y.device)
     _cuda(y)
     st = _call(y.device, load().nabla_fractal_unflatten, _ptr(y), _dtype_code(y), B, T, H, W, h, D,
@@ -502,16 +542,17 @@ def nabla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     whose tokens are strided.  Returns (q_out, k_out)."""
     args, q_shape, k_shape, _ = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps)
     dev = q.device
+    empty, _ = _allocators(stream, dev)
     qo = ko = None
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=q.dtype, device=dev)
+        q_out = empty(q_shape, dtype=q.dtype, device=dev)
     else:
         qo = _rows(q_out, "q_out", q_shape, q.dtype, dev)
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
     elif k_out is None:
-        k_out = torch.empty(k_shape, dtype=q.dtype, device=dev)
+        k_out = empty(k_shape, dtype=q.dtype, device=dev)
     else:
         ko = _rows(k_out, "k_out", k_shape, q.dtype, dev)
     _cuda(q)
@@ -544,14 +585,15 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
         raise ValueError("dk or wk without k")
     zq, zk = _rows(dq_out, "dq_out", q_shape, dtype, dev), _rows(dk_out, "dk_out", k_shape, dtype,
                                                                  dev)
+    empty, scratch = _allocators(stream, dev)
     oq = ok = None
     if dq is None:
-        dq = torch.empty(q_shape, dtype=dtype, device=dev)
+        dq = empty(q_shape, dtype=dtype, device=dev)
     else:
         oq = _rows(dq, "dq", q_shape, dtype, dev)
     if k is not None:
         if dk is None:
-            dk = torch.empty(k_shape, dtype=dtype, device=dev)
+            dk = empty(k_shape, dtype=dtype, device=dev)
         else:
             ok = _rows(dk, "dk", k_shape, dtype, dev)
     for name, d, w in (("dwq", dwq, wq), ("dwk", dwk, wk)):
@@ -560,13 +602,13 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
                 raise ValueError(f"{name} without its weight")
             _buf(d, name, D, kind, dev)
     if dwq is None and wq is not None:
-        dwq = torch.empty(D, dtype=kind, device=dev)
+        dwq = empty(D, dtype=kind, device=dev)
     if dwk is None and wk is not None:
-        dwk = torch.empty(D, dtype=kind, device=dev)
+        dwk = empty(D, dtype=kind, device=dev)
     lib = load()
     if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(lib.nabla_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
-                                device=dev)
+        workspace = scratch(lib.nabla_qk_norm_rope_bwd_workspace_bytes(D), dtype=torch.uint8,
+                            device=dev)
     if workspace is not None:
         _on(workspace, "workspace", dev)
     _cuda(q)
@@ -605,10 +647,11 @@ def nabla_cross_attn_fwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk
 def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
     strides, sizes = _cross_args(q, k, v, kv_len)
     dev = q.device
+    empty, scratch = _allocators(stream, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(sizes[-1])
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        o = empty(q.shape, dtype=q.dtype, device=dev)
     else:
         _buf(o, "o", q.numel(), q.dtype, dev)
     if lse is not None:
@@ -617,7 +660,7 @@ def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
     if workspace is None:
         need = lib.nabla_cross_attn_fwd_workspace_bytes(*sizes)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = scratch(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
         _on(workspace, "workspace", dev)
     _cuda(q)
@@ -646,8 +689,8 @@ def nabla_cross_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """nabla_cross_attn_fwd that also returns the rows' base-2 log-sum-exp:
     (o, lse [B,h,Sq] fp32)."""
     if lse is None:
-        lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
-                          device=q.device)
+        lse = _allocators(stream, q.device)[0]((q.shape[0], q.shape[2], q.shape[1]),
+                                               dtype=torch.float32, device=q.device)
     return _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream), lse
 
 
@@ -672,10 +715,11 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
     _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(sizes[-1])
+    empty, scratch = _allocators(stream, dev)
     outs = []
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
         if t is None:
-            t = torch.empty(like.shape, dtype=q.dtype, device=dev)
+            t = empty(like.shape, dtype=q.dtype, device=dev)
         else:
             _buf(t, name, like.numel(), q.dtype, dev)
         outs.append(t)
@@ -683,7 +727,7 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
     lib = load()
     if workspace is None:
         need = lib.nabla_cross_attn_bwd_workspace_bytes(*sizes)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
     _on(workspace, "workspace", dev)
     _cuda(q)
     _run(dev, stream, lib.nabla_cross_attn_bwd, "nabla_cross_attn_bwd", q.data_ptr(), strides[0],
