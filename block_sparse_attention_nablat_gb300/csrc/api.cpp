@@ -79,19 +79,62 @@ bool ranges_meet(const void *a, uintptr_t an, const void *b, uintptr_t bn) {
   return a0 < b0 + bn && b0 < a0 + an;
 }
 
-// Whether two written tensors share elements: they do not if their ranges are apart,
-// or if they are columns of one larger tensor (heads together, the same strides, batches
-// a whole number of tokens apart) that stay apart within the token.
-bool rows_collide(const Rows &a, const Rows &b, int B, int S, int D, size_t esz) {
-  if (!ranges_meet(a.p, extent(a, B, S, D, esz), b.p, extent(b, B, S, D, esz))) return false;
-  if ((a.h > 1 && a.st.head != D) || (b.h > 1 && b.st.head != D)) return true;
-  if (S > 1 && a.st.token != b.st.token) return true;
-  if (B > 1 && a.st.batch != b.st.batch) return true;
-  const int64_t pitch = S > 1 ? a.st.token : a.st.batch;
-  if (S > 1 && B > 1 && a.st.batch % a.st.token != 0) return true;
-  const int64_t off = ((const char *)b.p - (const char *)a.p) / (int64_t)esz;
-  const int64_t d = ((off % pitch) + pitch) % pitch;
-  return d < (int64_t)a.h * D || d + (int64_t)b.h * D > pitch;
+// A tensor's dimensions larger than 1, the largest stride first; each stride is at least
+// what the dimensions after it span (valid_rows).
+struct Dim {
+  int64_t st, n;
+};
+struct Nest {
+  Dim d[3];
+  int k;
+};
+
+Nest nest_of(const Rows &r, int B, int S) {
+  const Dim all[3] = {{r.st.batch, B}, {r.st.token, S}, {r.st.head, r.h}};
+  Nest v{};
+  for (const Dim &d : all) {
+    if (d.n == 1) continue;
+    int at = v.k++;
+    for (; at > 0 && v.d[at - 1].st < d.st; --at) v.d[at] = v.d[at - 1];
+    v.d[at] = d;
+  }
+  return v;
+}
+
+int64_t nest_span(const Dim *d, int k, int D) {
+  int64_t n = D;
+  for (int i = 0; i < k; ++i) n += d[i].st * (d[i].n - 1);
+  return n;
+}
+
+// Whether two tensors of rows of D elements share one, b's first element lying `off` behind
+// a's.  The larger stride st is peeled off: step i of a and j of b lie off + (j - i) st
+// apart, and what is inside a step spans at most st, so at most two values of j - i bring
+// the insides together.  Exact where both have the same strides; where the inside of one
+// spans more than the other's stride, they count as sharing.
+bool nests_meet(const Dim *a, int ka, const Dim *b, int kb, int64_t off, int D) {
+  if (off >= nest_span(a, ka, D) || -off >= nest_span(b, kb, D)) return false;
+  if (ka == 0 && kb == 0) return true;
+  const bool of_a = ka > 0 && (kb == 0 || a[0].st >= b[0].st);
+  const bool of_b = kb > 0 && (ka == 0 || b[0].st >= a[0].st);
+  const int64_t st = of_a ? a[0].st : b[0].st, na = of_a ? a[0].n : 1, nb = of_b ? b[0].n : 1;
+  if (of_a) ++a, --ka;
+  if (of_b) ++b, --kb;
+  if (nest_span(a, ka, D) > st || nest_span(b, kb, D) > st) return true;
+  const int64_t d = (off % st + st) % st;
+  for (int64_t x : {d, d - st}) {
+    const int64_t m = (x - off) / st;  // j - i
+    if (m > -na && m < nb && nests_meet(a, ka, b, kb, x, D)) return true;
+  }
+  return false;
+}
+
+// Whether two [B, S, heads, D] tensors share elements.
+bool rows_meet(const Rows &a, const Rows &b, int B, int S, int D, size_t esz) {
+  const Nest x = nest_of(a, B, S), y = nest_of(b, B, S);
+  const int64_t off = (int64_t)(reinterpret_cast<intptr_t>(b.p) - reinterpret_cast<intptr_t>(a.p)) /
+                      (int64_t)esz;
+  return nests_meet(x.d, x.k, y.d, y.k, off, D);
 }
 
 }  // namespace
@@ -358,8 +401,7 @@ static nabla_status qk_norm_call(const void *const (&x)[2], const nabla_strides 
   for (int i = 0; i < sides; ++i) {  // what is written overlaps nothing else
     const uintptr_t n = extent(ro[i], B, S, D, esz);
     for (int j = 0; j < sides; ++j) {
-      if (ranges_meet(ro[i].p, n, rx[j].p, extent(rx[j], B, S, D, esz)) ||
-          (bwd && ranges_meet(ro[i].p, n, rz[j].p, extent(rz[j], B, S, D, esz))))
+      if (rows_meet(ro[i], rx[j], B, S, D, esz) || (bwd && rows_meet(ro[i], rz[j], B, S, D, esz)))
         return NABLA_ERR_INVALID_ARG;
       const size_t row = (size_t)D * wsz;
       if (w[j] && (ranges_meet(ro[i].p, n, w[j], row) ||
@@ -368,7 +410,7 @@ static nabla_status qk_norm_call(const void *const (&x)[2], const nabla_strides 
       if (dw[j] && ranges_meet(ro[i].p, n, dw[j], row)) return NABLA_ERR_INVALID_ARG;
     }
   }
-  if (sides == 2 && rows_collide(ro[0], ro[1], B, S, D, esz)) return NABLA_ERR_INVALID_ARG;
+  if (sides == 2 && rows_meet(ro[0], ro[1], B, S, D, esz)) return NABLA_ERR_INVALID_ARG;
   if (bwd && (dw[0] || dw[1])) {
     if (dw[0] && dw[1] && ranges_meet(dw[0], (size_t)D * wsz, dw[1], (size_t)D * wsz))
       return NABLA_ERR_INVALID_ARG;

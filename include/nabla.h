@@ -363,7 +363,10 @@ typedef struct {
  *                token is normed and not rotated.
  *   eps          finite, >= 0.
  *   q_out, k_out as q and k, strides qo_st and ko_st, overwritten.  They may be
- *                views of one larger tensor but must not overlap q, k or each other.
+ *                views of one larger tensor, of which q and k may be views too, but
+ *                share no element with q, k or each other.  Views that lie between
+ *                each other are told apart where their strides are the same; with
+ *                other strides they may be refused.
  * q, k, q_out, k_out, wq, wk, cos_t and sin_t are 16-byte aligned, pos 4-byte.
  * Errors: NABLA_ERR_INVALID_ARG for anything else.
  */
@@ -386,8 +389,9 @@ nabla_status nabla_qk_norm_rope(const void *q, const nabla_strides *q_st, const 
  * bits.  The tables have no gradient.
  *
  *   dq_out, dk_out  as q_out and k_out, strides dqo_st and dko_st.
- *   dq, dk          as q and k, strides dq_st and dk_st, overwritten; not
- *                   overlapping any other argument.
+ *   dq, dk          as q and k, strides dq_st and dk_st, overwritten; they share no
+ *                   element with any other argument (views of one larger tensor as
+ *                   above).
  *   dwq, dwk        [D] device, element type wdt, overwritten; NULL: not wanted.
  *   workspace       device scratch of ws_bytes >= nabla_qk_norm_rope_bwd_workspace_bytes()
  *                   (256-byte aligned); not looked at when dwq and dwk are NULL.  Calls

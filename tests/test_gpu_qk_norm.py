@@ -286,3 +286,63 @@ def test_gradient_against_differences(nabla):
         e[j] = step
         got = (loss(q, wq + e) - loss(q, wq - e)) / (2 * step)
         assert abs(got - float(dw[j])) <= size + 1e-4
+
+
+def same_as_dense(nabla, q, k, wq, wk, qo, ko, room, marked):
+    """Forward and backward into the views qo, ko of `room` give the dense calls' bits and
+    write nothing else of it."""
+    B, S, _, D = q.shape
+    cos, sin = table(S, D)
+    wanted = list(nabla.nabla_qk_norm_rope(q, k, wq, wk, cos, sin))
+    dzq, dzk = (torch.randn(t.shape, generator=torch.Generator().manual_seed(1)).to(t.dtype)
+                .to(DEV) for t in (q, k))
+    wanted += nabla.nabla_qk_norm_rope_bwd(q, k, wq, wk, dzq, dzk, cos, sin)
+    before = room.clone()
+    got = list(nabla.nabla_qk_norm_rope(q, k, wq, wk, cos, sin, q_out=qo, k_out=ko))
+    got = [t.clone() for t in got]
+    got += nabla.nabla_qk_norm_rope_bwd(q, k, wq, wk, dzq, dzk, cos, sin, dq=qo, dk=ko)
+    assert len(got) == len(wanted) == 6
+    assert all(torch.equal(a, b) for a, b in zip(got, wanted))
+    assert torch.equal(room[~marked], before[~marked])
+    assert nabla.nabla_get_last_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_outputs_between_each_other(nabla, dtype):
+    """q's and k's heads in one tensor, heads before tokens, batch after batch."""
+    B, S, h, hk, D = 3, 21, 4, 2, 64
+    q, k, wq, wk = inputs(B, S, h, hk, D, dtype)
+    room = torch.full((B, h + hk + 1, S, D), 3.0, dtype=q.dtype, device=DEV)
+    marked = torch.zeros_like(room, dtype=torch.bool)
+    marked[:, 1:] = True
+    same_as_dense(nabla, q, k, wq, wk, room[:, 1:1 + h].transpose(1, 2),
+                  room[:, 1 + h:].transpose(1, 2), room, marked)
+
+
+def test_outputs_in_tokens_of_an_odd_batch_pitch(nabla):
+    """Batches apart by no whole number of tokens."""
+    B, S, h, D = 2, 9, 2, 64
+    q, k, wq, wk = inputs(B, S, h, h, D, "bf16")
+    pitch = (2 * h + 1) * D
+    room = torch.full((B * (S * pitch + 72),), 3.0, dtype=q.dtype, device=DEV)
+    marked = torch.zeros_like(room, dtype=torch.bool)
+
+    def views(x):
+        st = (S * pitch + 72, pitch, D, 1)
+        return x.as_strided((B, S, h, D), st), x[h * D:].as_strided((B, S, h, D), st)
+
+    for x in views(marked):
+        x.fill_(True)
+    same_as_dense(nabla, q, k, wq, wk, *views(room), room, marked)
+
+
+def test_outputs_beside_the_inputs(nabla):
+    """q, k, v and the outputs side by side in one tensor of five."""
+    B, S, h, D = 2, 37, 3, 128
+    q, k, wq, wk = inputs(B, S, h, h, D, "bf16")
+    room = torch.full((B, S, 5, h, D), 3.0, dtype=q.dtype, device=DEV)
+    room[:, :, 0], room[:, :, 1] = q, k
+    marked = torch.zeros_like(room, dtype=torch.bool)
+    marked[:, :, 3:] = True
+    same_as_dense(nabla, room[:, :, 0], room[:, :, 1], wq, wk, room[:, :, 3], room[:, :, 4], room,
+                  marked)

@@ -145,3 +145,24 @@ def test_binding_refuses():
     ]:
         with pytest.raises((ValueError, TypeError), match=match):
             call()
+
+
+HM = 8 * 64  # a head of eight tokens, heads before tokens: [2, 6, 8, 64]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(qo=6 * M, qo_st=st(6 * HM, 64, HM), ko=6 * M + 2 * 3 * HM, ko_st=st(6 * HM, 64, HM)),
+    dict(qo=6 * M + 2 * 3 * HM, qo_st=st(6 * HM, 64, HM), ko=6 * M, ko_st=st(6 * HM, 64, HM)),
+    dict(qo=6 * M, qo_st=st(6 * HM, 64, HM), ko=6 * M + 2 * 4 * HM - 16,
+         ko_st=st(6 * HM, 64, HM)),
+    dict(qo=6 * M, qo_st=st(9 * 384, 384), ko=6 * M + 2 * 9 * 384 + 2 * 192,
+         ko_st=st(9 * 384, 384)),
+    dict(q=M, q_st=st(8 * 640, 640), qo=M + 2 * 192, qo_st=st(8 * 640, 640)),
+    dict(q=M, q_st=st(8 * 640, 640), qo=M + 2 * 7 * 640, qo_st=st(8 * 640, 640)),
+], ids=["last head", "first head", "a piece", "the next batch's head", "beside q", "q's last token"])
+def test_views_that_share_elements(lib, kw):
+    """Two outputs, or an output and q, as views of one tensor whose strides agree and which
+    meet in some rows only."""
+    assert fwd(lib, **kw) == INVALID
+    names = dict(qo="dq", ko="dk", qo_st="dq_st", ko_st="dk_st")
+    assert bwd(lib, **{names.get(a, a): v for a, v in kw.items()}) == INVALID
