@@ -94,12 +94,22 @@ cudaError_t launch_join(const CrossArgs &a, int nsplit, cudaStream_t st) {
 int cross_fwd_splits(const CrossShape &s, nabla_dtype dt) {
   const bool few = cross_few_rows(s, dt);
   if (dt == NABLA_F32 && !few) return cross_simt_plan(s).nsplit;
-  // fp32, few rows: 64-state tiles, a unit per key head, two CTAs on an SM
+  // fp32, few rows: 64-state tiles, a unit per key head
   const long units = (long)s.B * s.hk * (few ? 1 : (cross::packing(s).nsub + 1) / 2);
-  const long runs = (few ? 304 : 152) / units;
   const long tiles = few ? (s.Sk + 63) / 64 : (s.Sk + cross::kTile - 1) / cross::kTile;
-  const long n = runs < tiles / 4 ? runs : tiles / 4;
-  return n < 2 ? 1 : (int)n;
+  auto runs = [&](long room) {
+    const long n = room / units < tiles / 4 ? room / units : tiles / 4;
+    return n < 2 ? 1 : (int)n;
+  };
+  if (!few) return runs(152);
+  const int two = runs(304);
+  if (s.Sq * (s.h / s.hk) <= 8) return two;  // two CTAs on an SM
+  // More than 8 rows are held in registers, which leaves one CTA an SM: one wave of longer
+  // runs, or two of shorter ones where those fill the SMs better.  (D 128, us in one wave
+  // and in two: 9 rows x 8192 states, 8 heads: 42, 52; 16 x 2048, 24 heads: 44, 56; D 64:
+  // 10 x 8192, 100 heads: 316 whole, 222 in 3 runs; 16 x 8192, 60 heads: 216, 183.)
+  const int one = runs(152);
+  return 2 * ((tiles + two - 1) / two) < (tiles + one - 1) / one ? two : one;
 }
 
 // Rows per CTA (16 A) and runs of the fp32 kernel's walk over the states, by the time they

@@ -140,3 +140,17 @@ def test_binding_refuses():
     ]:
         with pytest.raises((ValueError, TypeError), match=match):
             call()
+
+
+@pytest.mark.parametrize("Sq,Sk,heads,D,runs", [
+    (8, 8192, 8, 128, 32),     # eight rows a key head: two blocks on an SM, runs of four tiles
+    (9, 8192, 8, 128, 19),     # more rows: one block on an SM, one wave of them
+    (16, 2048, 24, 128, 6),
+    (16, 8192, 60, 64, 5),     # two waves where one leaves a fifth of the SMs idle
+    (10, 8192, 100, 64, 3),
+    (16, 8192, 160, 64, 0),    # units enough without runs
+], ids=lambda x: str(x))
+def test_runs_of_few_fp32_rows_follow_the_blocks_an_sm_holds(lib, Sq, Sk, heads, D, runs):
+    """Sums and log-sum-exps of that many runs, in fp32."""
+    need = lib.nabla_cross_attn_fwd_workspace_bytes(0, 1, Sq, Sk, heads, heads, D)
+    assert need == runs * heads * Sq * (D + 1) * 4
