@@ -233,3 +233,62 @@ def test_gradient_against_differences(nabla):
         hi[which], lo[which] = hi[which] + e, lo[which] - e
         got = (loss(*hi) - loss(*lo)) / (2 * step)
         assert abs(got - float(grads[which][at])) <= tol
+
+
+def loss64(q, k, v, dout, lens, scale):
+    """<dout, o> by the definition, in 64 bits (none of the oracle)."""
+    total = 0.0
+    for b, n in enumerate(lens):
+        if n:
+            rep = q.shape[2] // k.shape[2]
+            z = torch.einsum("shd,uhd->hsu", q[b], k[b, :n].repeat_interleave(rep, 1)) * scale
+            o = torch.einsum("hsu,uhd->shd", z.softmax(-1), v[b, :n].repeat_interleave(rep, 1))
+            total += float((dout[b] * o).sum())
+    return total
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,Sq,Sk,h,hk,D,lens,scale", [
+    (2, 3, 9, 4, 2, 64, [8, 5], None),      # few rows
+    (3, 70, 150, 4, 2, 64, [150, 0, 33], None),
+    (1, 200, 77, 3, 1, 128, [60], -0.07),
+    (2, 5, 1100, 2, 2, 128, [1100, 700], 0.2),
+])
+def test_gradient_along_directions(nabla, B, Sq, Sk, h, hk, D, lens, scale, dtype):
+    """<gradient, d> of q, k and v, one at a time, against central differences of the
+    definition in 64 bits, along the gradient itself and along the halves of it that a
+    random choice of elements gives, d of length 1.  So the probe reads |d g|^2 / |d g|, a
+    half of the gradient's length or more, and a gradient that is 0, turned round, or off by
+    a factor in any large part of its elements is off by as much.
+
+    Tolerance, of the gradient's length: a gradient off by e elementwise moves the probe by
+    at most |e|.  fp32, by norm: scores and dP carry the roundings of 64 products a lane
+    (2^-21 of their size), lse 2^-21 at sizes to 16, ex2 2^-22, the sums over tens of tiles
+    less than 2^-20: below 2^-18 together, where scores spread over a few units; twice that
+    for o's and lse's own.  bf16: P, dz and the result are rounded by at most 2^-8 each, and
+    delta, from a rounded o, by 2^-8 of |dout| |o|, which is of dz's size: 2^-6.
+    The differences: step^2 / 6 of a third derivative of the first one's size, below 2^-22."""
+    scale = 1 / math.sqrt(D) if scale is None else scale
+    q, k, v, dout = inputs(B, Sq, Sk, h, hk, D, dtype, seed=Sk, spread=0.9)
+    n = lengths(lens)
+    o, lse = nabla.nabla_cross_attn_fwd_lse(q, k, v, kv_len=n, scale=scale)
+    grads = nabla.nabla_cross_attn_bwd(q, k, v, o, lse, dout, kv_len=n, scale=scale)
+    step, tol = 2.0 ** -11, 2.0 ** -6 if dtype == "bf16" else 2.0 ** -17
+    x = [t.double() for t in (q, k, v)]
+    gen = torch.Generator().manual_seed(Sq)
+    for which, grad in enumerate(grads):
+        g = grad.double()
+        pick = (torch.rand(g.shape, generator=gen) < 0.5).to(DEV)
+        for part in (torch.ones_like(pick), pick, ~pick):
+            d = torch.where(part, g, torch.zeros_like(g))
+            length = float(d.norm())
+            assert length >= 0.5 * float(g.norm()) > 0 and 10 * tol * float(g.norm()) <= length
+            d /= length
+            hi, lo = list(x), list(x)
+            hi[which], lo[which] = x[which] + step * d, x[which] - step * d
+            got = (loss64(*hi, dout.double(), lens, scale) -
+                   loss64(*lo, dout.double(), lens, scale)) / (2 * step)
+            assert abs(got - float((g * d).sum())) <= tol * float(g.norm()), (which, got, length)
+    for b, m in enumerate(lens):
+        assert (grads[1][b, m:] == 0).all() and (grads[2][b, m:] == 0).all()
+        assert m or (grads[0][b] == 0).all()
