@@ -644,7 +644,7 @@ def nabla_cross_attn_fwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk
     return load().nabla_cross_attn_fwd_workspace_bytes(code, B, Sq, Sk, h, hk, D)
 
 
-def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
+def _cross_fwd(q, k, v, kv_len, scale, o, lse, with_lse, workspace, stream):
     strides, sizes = _cross_args(q, k, v, kv_len)
     dev = q.device
     empty, scratch = _allocators(stream, dev)
@@ -656,6 +656,8 @@ def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
         _buf(o, "o", q.numel(), q.dtype, dev)
     if lse is not None:
         _buf(lse, "lse", q.numel() // sizes[-1], torch.float32, dev)
+    elif with_lse:
+        lse = empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32, device=dev)
     lib = load()
     if workspace is None:
         need = lib.nabla_cross_attn_fwd_workspace_bytes(*sizes)
@@ -668,7 +670,7 @@ def _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream):
          k.data_ptr(), strides[1], v.data_ptr(), strides[2], *sizes, _ptr(kv_len), scale,
          o.data_ptr(), _ptr(lse), _ptr(workspace),
          0 if workspace is None else workspace.numel() * workspace.element_size())
-    return o
+    return o, lse
 
 
 def nabla_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -678,7 +680,7 @@ def nabla_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Attention of q [B,Sq,h,D] to the first kv_len[b] (int32 [B]; None: all) of the
     states k, v [B,Sk,hk,D], hk dividing h; q, k, v may be views whose tokens are
     strided.  Returns o [B,Sq,h,D]."""
-    return _cross_fwd(q, k, v, kv_len, scale, o, None, workspace, stream)
+    return _cross_fwd(q, k, v, kv_len, scale, o, None, False, workspace, stream)[0]
 
 
 def nabla_cross_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -688,10 +690,7 @@ def nabla_cross_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                              workspace: Optional[torch.Tensor] = None, stream=None):
     """nabla_cross_attn_fwd that also returns the rows' base-2 log-sum-exp:
     (o, lse [B,h,Sq] fp32)."""
-    if lse is None:
-        lse = _allocators(stream, q.device)[0]((q.shape[0], q.shape[2], q.shape[1]),
-                                               dtype=torch.float32, device=q.device)
-    return _cross_fwd(q, k, v, kv_len, scale, o, lse, workspace, stream), lse
+    return _cross_fwd(q, k, v, kv_len, scale, o, lse, True, workspace, stream)
 
 
 def nabla_cross_attn_bwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk: int, h: int,

@@ -154,3 +154,12 @@ def test_runs_of_few_fp32_rows_follow_the_blocks_an_sm_holds(lib, Sq, Sk, heads,
     """Sums and log-sum-exps of that many runs, in fp32."""
     need = lib.nabla_cross_attn_fwd_workspace_bytes(0, 1, Sq, Sk, heads, heads, D)
     assert need == runs * heads * Sq * (D + 1) * 4
+
+
+def test_lse_form_names_what_is_wrong_with_q():
+    """As the form without lse does, before anything is allocated by q's sizes."""
+    q, k, v, n = tensors()
+    for call in (N.nabla_cross_attn_fwd, N.nabla_cross_attn_fwd_lse):
+        for bad in (q[0, 0], q[0], q[None]):
+            with pytest.raises(ValueError, match="q must be"):
+                call(bad, k, v, n)
