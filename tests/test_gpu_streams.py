@@ -110,3 +110,30 @@ def test_default_stream_from_another_one(nabla):
     torch.cuda.synchronize()
     for outs in got:
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("op", range(1, 5), ids=["attn_bwd", "qk_norm_bwd", "cross_lse",
+                                                 "cross_bwd"])
+def test_calls_on_a_forked_stream_are_captured(nabla, op):
+    """Two calls on a stream forked from the capturing one, their scratch and outputs
+    allocated in the capture and the first's outputs dropped there."""
+    f, g = (operators(nabla, i, torch.bfloat16)[op] for i in (8, 9))
+    want = [copies(x(None)) for x in (f, g)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        current = torch.cuda.current_stream()
+        side.wait_stream(current)
+        outs = f(side)
+        current.wait_stream(side)
+        first = copies(outs)
+        del outs
+        second = g(side)
+        current.wait_stream(side)
+    for _ in range(3):
+        for t in first + list(second):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in ((first, want[0]), (second, want[1])):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref))
