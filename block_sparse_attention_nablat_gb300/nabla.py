@@ -235,7 +235,8 @@ def _rows(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype,
     span = t.shape[3]
     for s, n in sorted((s, n) for s, n in zip(st[:3], t.shape) if n > 1):
         if s < span:
-            raise ValueError(f"the rows of {name} must not overlap")
+            raise ValueError(f"the rows of {name} must not overlap (an expanded tensor has to be "
+                             "made contiguous)")
         span += s * (n - 1)
     return _Strides(*st[:3])
 
@@ -538,8 +539,9 @@ def nabla_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     """RMS norm of q [B,S,hq,D] and k [B,S,hk,D] (or q alone) per head with weights
     wq, wk [D] (None: 1) and, with cos, sin [rows, R/2] fp32, the position rotation of
     their first R columns; token s takes table row s, or pos[b, s].  interleaved:
-    rotate columns (2i, 2i + 1), else (i, i + R/2).  q, k and the outputs may be views
-    whose tokens are strided.  Returns (q_out, k_out)."""
+    rotate columns (2i, 2i + 1), else (i, i + R/2).  q, k and the outputs may be views of
+    larger tensors with their dimensions in any order in memory, as long as a row's columns
+    lie together and no two rows overlap.  Returns (q_out, k_out)."""
     args, q_shape, k_shape, _ = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps)
     dev = q.device
     empty, _ = _allocators(stream, dev)
@@ -576,7 +578,8 @@ def nabla_qk_norm_rope_bwd(q: torch.Tensor, k: Optional[torch.Tensor],
                            workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of nabla_qk_norm_rope for the upstream gradients dq_out, dk_out of its
     outputs: returns (dq, dk, dwq, dwk); dwq, dwk [D] in the weights' type, None where
-    the weight is None."""
+    the weight is None.  dq_out, dk_out, dq and dk may be views as there; an expanded
+    gradient (that of a plain sum) has to be made contiguous first."""
     args, q_shape, k_shape, kind = _qk_args(q, k, wq, wk, cos, sin, pos, interleaved, eps)
     dev, dtype, D = q.device, q.dtype, q.shape[3]
     if dq_out is None or (k is None) != (dk_out is None):
@@ -678,8 +681,9 @@ def nabla_cross_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                          o: Optional[torch.Tensor] = None,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention of q [B,Sq,h,D] to the first kv_len[b] (int32 [B]; None: all) of the
-    states k, v [B,Sk,hk,D], hk dividing h; q, k, v may be views whose tokens are
-    strided.  Returns o [B,Sq,h,D]."""
+    states k, v [B,Sk,hk,D], hk dividing h; q, k and v may be views of larger tensors with
+    their dimensions in any order in memory, as long as a row's columns lie together and no
+    two rows overlap.  Returns o [B,Sq,h,D], dense."""
     return _cross_fwd(q, k, v, kv_len, scale, o, None, False, workspace, stream)[0]
 
 
@@ -707,7 +711,9 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
                          workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients of nabla_cross_attn_fwd, from its inputs, the o and lse of
     nabla_cross_attn_fwd_lse and the upstream gradient dout of o: returns dq [B,Sq,h,D] and
-    dk, dv [B,Sk,hk,D] (0 for states past kv_len)."""
+    dk, dv [B,Sk,hk,D] (0 for states past kv_len), dense.  o and dout may be views as q, k
+    and v may; an expanded dout (the gradient of a plain sum) has to be made contiguous
+    first."""
     strides, sizes = _cross_args(q, k, v, kv_len)
     dev = q.device
     so, sg = _rows(o, "o", q.shape, q.dtype, dev), _rows(dout, "dout", q.shape, q.dtype, dev)
