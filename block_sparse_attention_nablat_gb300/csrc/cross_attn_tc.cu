@@ -36,9 +36,12 @@
 // A unit costs about 1,500 cycles a step and 1,900 more: at few steps its start and end,
 // and the instruction fetches of code that runs once a unit, bound it, so the waits' slow
 // paths are out of line and no role's code exists twice.
-// Measured and not kept at 512 states: two chains of four softmax warps each 256 us,
-// output by the softmax warps 248, two or three sets of softmax warps on alternating steps
-// 168 to 200, the units walked without divisions (more code) 165.
+// At D 64 a step's products take half as long and its softmax as long as at D 128, so the
+// kernel does too: 512 states 150 us, 4096 states 1000, of floors of 54 and 433.
+// Measured and not kept at 512 states: two or three sets of softmax warps on alternating
+// steps 168 to 200, the units walked without divisions (more code) 165.  (Two chains of four
+// softmax warps each were 256 beside 238 before the waits' slow paths were out of line; not
+// measured since.)
 // Every mbarrier wait is bounded (1 s); on expiry the kernel records
 // NABLA_ERR_TIMEOUT, the roles stop waiting, copies and MMAs in flight are drained and
 // TMEM is released.

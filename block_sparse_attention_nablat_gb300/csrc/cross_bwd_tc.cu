@@ -33,9 +33,13 @@
 //
 // 32768 tokens, 24 heads, D 128, 512 states: 589 us in all, 875 TFLOP/s of the five
 // products (0.45 of a large library product's rate): rows' lse and delta 72, dK and dV 281
-// (tensor pipe 63% active), their sum 11, dQ 218 (59%).  4096 states: 3.96 ms, 1040.  A step of
-// dK / dV is bound by the chain X, P, dV, next X (X goes over P: TMEM is full); one of dQ
-// by V's tile, which is loaded when the last Y is done, and the products' own chain.
+// (tensor pipe 63% active), their sum 11, dQ 218 (59%).  4096 states: 3.8 to 4.0 ms, 1040 to
+// 1080.  Of the 319 us above the five products' 270, X and Y formed a second time are 108, the
+// pass before them 72, the sum 11, and what the two kernels take beyond their seven products'
+// time about 125: a step of dK / dV waits for the chain X, P, dV, next X (X goes over P: TMEM
+// is full), one of dQ for V's tile, which is loaded when the last Y is done, and for the
+// products' own chain.  At D 64 the products take half the time and the softmax as long: 433 us
+// at 512 states, 2.81 ms at 4096.
 // Measured and not kept: dO as dQ's TMEM operand, which makes room for a second V tile,
 // but starts a unit later: 4096 states 3.80 ms, 512 584 us, 256 416 against 399; dQ started
 // on the SMs that dK / dV leave: 600 against 595 at 512 states, 313 against 321 at 128.
