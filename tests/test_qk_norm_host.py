@@ -159,7 +159,7 @@ HM = 8 * 64  # a head of eight tokens, heads before tokens: [2, 6, 8, 64]
          ko_st=st(9 * 384, 384)),
     dict(q=M, q_st=st(8 * 640, 640), qo=M + 2 * 192, qo_st=st(8 * 640, 640)),
     dict(q=M, q_st=st(8 * 640, 640), qo=M + 2 * 7 * 640, qo_st=st(8 * 640, 640)),
-], ids=["last head", "first head", "a piece", "the next batch's head", "beside q", "q's last token"])
+], ids=["last head", "first head", "a piece", "next batch's head", "beside q", "q's last token"])
 def test_views_that_share_elements(lib, kw):
     """Two outputs, or an output and q, as views of one tensor whose strides agree and which
     meet in some rows only."""
