@@ -621,6 +621,182 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
   return from_cuda(launch_cross_bwd(a, dt, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+namespace nabla {
+namespace {
+
+bool valid_norm_shape(const NormShape &s) {
+  if (s.B < 1 || s.S < 1 || s.C < 8 || s.C > 8192 || s.C % 8 != 0) return false;
+  return (double)s.B * s.S <= 2.0e9 && (double)s.B * s.S * s.C <= 4.0e12;
+}
+
+struct Range {
+  const void *p;
+  uintptr_t n;
+};
+
+// What both directions of the block norm check: shape, norms, weights, modulations and
+// scalars; collects the arrays that outputs must keep clear of.
+struct NormCheck {
+  NormArgs &a;
+  size_t esz, wsz, msz;
+  Range arrays[8];
+  int count = 0;
+
+  explicit NormCheck(NormArgs &args)
+      : a(args),
+        esz(args.dt == NABLA_BF16 ? 2 : 4),
+        wsz(args.wdt == NABLA_BF16 ? 2 : 4),
+        msz(args.mdt == NABLA_BF16 ? 2 : 4) {}
+
+  bool array(const void *p, uintptr_t n) {
+    if (!p) return true;
+    if (!aligned(p, 16)) return false;
+    arrays[count++] = Range{p, n};
+    return true;
+  }
+  bool mod(const void *p, int64_t &st) {
+    if (!p) return true;
+    if (a.rows == 1) st = a.shape.C;
+    if (st < a.shape.C || st > (int64_t)1 << 38 || st * msz % 16 != 0) return false;
+    return array(p, (uintptr_t)((a.rows - 1) * st + a.shape.C) * msz);
+  }
+  bool common() {
+    if (!valid_dtype(a.dt) || !valid_dtype(a.wdt) || !valid_dtype(a.mdt)) return false;
+    if (!valid_norm_shape(a.shape)) return false;
+    if (a.norm < 0 || a.norm > 2 || a.post < 0 || a.post > 2) return false;
+    if (a.rows < 1 || (long)a.shape.B * a.shape.S % a.rows != 0) return false;
+    if (!std::isfinite(a.rs) || !(a.eps >= 0.f) || !std::isfinite(a.eps)) return false;
+    if (a.norm == 0 && (a.w || a.scale || a.shift)) return false;
+    if (a.post == 0 && a.pw) return false;
+    return array(a.w, a.shape.C * wsz) && array(a.pw, a.shape.C * wsz) &&
+           mod(a.gate, a.gate_st) && mod(a.scale, a.scale_st) && mod(a.shift, a.shift_st);
+  }
+  // A [B, S, C] tensor that may be absent; its strides filled in.
+  bool rows(const void *p, const nabla_strides *st, nabla_strides &to, Rows &r) {
+    r = rows_of(p, st, a.shape.B, a.shape.S, 1, a.shape.C);
+    to = r.st;
+    return !p || valid_rows(r, a.shape.B, a.shape.S, a.shape.C, esz);
+  }
+  bool apart(const Rows &o, const Rows &in) const {
+    return !o.p || !in.p || !rows_meet(o, in, a.shape.B, a.shape.S, a.shape.C, esz);
+  }
+  // `o` keeps clear of `in` or is it, row by row.
+  bool apart_or_same(const Rows &o, const Rows &in) const {
+    return apart(o, in) || (o.p == in.p && (a.shape.B == 1 || o.st.batch == in.st.batch) &&
+                            (a.shape.S == 1 || o.st.token == in.st.token));
+  }
+  bool clear_of_arrays(const Rows &o) const {
+    const uintptr_t n = o.p ? extent(o, a.shape.B, a.shape.S, a.shape.C, esz) : 0;
+    for (int i = 0; i < count && o.p; ++i)
+      if (ranges_meet(o.p, n, arrays[i].p, arrays[i].n)) return false;
+    return true;
+  }
+};
+
+}  // namespace
+}  // namespace nabla
+
+nabla_status nabla_block_norm(const void *x, const nabla_strides *x_st, const void *u,
+                              const nabla_strides *u_st, nabla_dtype dt, int B, int S, int C,
+                              nabla_norm norm, nabla_norm post, const void *weight,
+                              const void *post_weight, nabla_dtype wdt, const void *gate,
+                              int64_t gate_st, const void *scale, int64_t scale_st,
+                              const void *shift, int64_t shift_st, nabla_dtype mdt, int rows,
+                              float residual_scale, float eps, void *x_out,
+                              const nabla_strides *xo_st, void *y, const nabla_strides *y_st,
+                              nabla_stream_t stream) {
+  using namespace nabla;
+  NormArgs a{};
+  a.shape = NormShape{B, S, C};
+  a.x = x, a.u = u, a.s = x_out, a.y = y;
+  a.w = weight, a.pw = post_weight, a.gate = gate, a.scale = scale, a.shift = shift;
+  a.gate_st = gate_st, a.scale_st = scale_st, a.shift_st = shift_st;
+  a.dt = dt, a.wdt = wdt, a.mdt = mdt;
+  a.rows = rows, a.norm = norm, a.post = post, a.rs = residual_scale, a.eps = eps;
+  NormCheck c(a);
+  if (!x || !c.common()) return NABLA_ERR_INVALID_ARG;
+  if ((u == nullptr) != (x_out == nullptr) || (norm == 0) != (y == nullptr) || (!u && !y))
+    return NABLA_ERR_INVALID_ARG;
+  if (!u && (gate || post != 0)) return NABLA_ERR_INVALID_ARG;
+  Rows rx, ru, rs, ry;
+  if (!c.rows(x, x_st, a.x_st, rx) || !c.rows(u, u_st, a.u_st, ru) ||
+      !c.rows(x_out, xo_st, a.s_st, rs) || !c.rows(y, y_st, a.y_st, ry))
+    return NABLA_ERR_INVALID_ARG;
+  if (!c.apart_or_same(rs, rx) || !c.apart(rs, ru) || !c.apart(ry, rx) || !c.apart(ry, ru) ||
+      !c.apart(ry, rs) || !c.clear_of_arrays(rs) || !c.clear_of_arrays(ry))
+    return NABLA_ERR_INVALID_ARG;
+  return from_cuda(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t nabla_block_norm_bwd_workspace_bytes(int B, int S, int C) {
+  const nabla::NormShape s{B, S, C};
+  return nabla::valid_norm_shape(s) ? nabla::block_norm_bwd_workspace(s) : 0;
+}
+
+nabla_status nabla_block_norm_bwd(
+    const void *s, const nabla_strides *s_st, const void *u, const nabla_strides *u_st,
+    const void *dsum, const nabla_strides *dsum_st, const void *dy, const nabla_strides *dy_st,
+    nabla_dtype dt, int B, int S, int C, nabla_norm norm, nabla_norm post, const void *weight,
+    const void *post_weight, nabla_dtype wdt, const void *gate, int64_t gate_st,
+    const void *scale, int64_t scale_st, nabla_dtype mdt, int rows, float residual_scale,
+    float eps, void *dx, const nabla_strides *dx_st, void *du, const nabla_strides *du_st,
+    void *dgate, void *dscale, void *dshift, void *dweight, void *dpost_weight, void *workspace,
+    size_t ws_bytes, nabla_stream_t stream) {
+  using namespace nabla;
+  NormArgs a{};
+  a.shape = NormShape{B, S, C};
+  a.x = s, a.u = u, a.dsum = dsum, a.dy = dy, a.dx = dx, a.du = du;
+  a.w = weight, a.pw = post_weight, a.gate = gate, a.scale = scale;
+  a.gate_st = gate_st, a.scale_st = scale_st;
+  a.dw = dweight, a.dpw = dpost_weight, a.dgate = dgate, a.dscale = dscale, a.dshift = dshift;
+  a.dt = dt, a.wdt = wdt, a.mdt = mdt;
+  a.rows = rows, a.norm = norm, a.post = post, a.rs = residual_scale, a.eps = eps;
+  a.bwd = true;
+  NormCheck c(a);
+  if (!c.common()) return NABLA_ERR_INVALID_ARG;
+  if ((norm == 0) != (s == nullptr) || (norm == 0) != (dy == nullptr)) return NABLA_ERR_INVALID_ARG;
+  if (norm == 0 && (dscale || dshift || dweight)) return NABLA_ERR_INVALID_ARG;
+  if (!u && (post != 0 || dgate || dpost_weight)) return NABLA_ERR_INVALID_ARG;
+  if (post == 0 && dpost_weight) return NABLA_ERR_INVALID_ARG;
+  if ((!dsum && !dy) || (!dx && !du && !dgate && !dscale && !dshift && !dweight && !dpost_weight))
+    return NABLA_ERR_INVALID_ARG;
+  Rows r[4], o[2];
+  if (!c.rows(s, s_st, a.x_st, r[0]) || !c.rows(u, u_st, a.u_st, r[1]) ||
+      !c.rows(dsum, dsum_st, a.dsum_st, r[2]) || !c.rows(dy, dy_st, a.dy_st, r[3]) ||
+      !c.rows(dx, dx_st, a.dx_st, o[0]) || !c.rows(du, du_st, a.du_st, o[1]))
+    return NABLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (i == 0 && j == 2 ? !c.apart_or_same(o[i], r[j]) : !c.apart(o[i], r[j]))
+        return NABLA_ERR_INVALID_ARG;
+    if (!c.clear_of_arrays(o[i])) return NABLA_ERR_INVALID_ARG;
+  }
+  if (!c.apart(o[0], o[1])) return NABLA_ERR_INVALID_ARG;
+  // the small gradients keep clear of everything else, too
+  const uintptr_t mn = (uintptr_t)rows * C * c.msz, wn = (uintptr_t)C * c.wsz;
+  const Range small[5] = {{dgate, mn}, {dscale, mn}, {dshift, mn}, {dweight, wn},
+                          {dpost_weight, wn}};
+  bool any = false;
+  for (int i = 0; i < 5; ++i) {
+    const Range &g = small[i];
+    if (!g.p) continue;
+    any = true;
+    if (!aligned(g.p, 16)) return NABLA_ERR_INVALID_ARG;
+    for (int j = 0; j < c.count; ++j)
+      if (ranges_meet(g.p, g.n, c.arrays[j].p, c.arrays[j].n)) return NABLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (small[j].p && ranges_meet(g.p, g.n, small[j].p, small[j].n)) return NABLA_ERR_INVALID_ARG;
+    for (const Rows *t : {&r[0], &r[1], &r[2], &r[3], &o[0], &o[1]})
+      if (t->p && ranges_meet(g.p, g.n, t->p, extent(*t, B, S, C, c.esz)))
+        return NABLA_ERR_INVALID_ARG;
+  }
+  if (any && (!workspace || !aligned(workspace, 256) ||
+              ws_bytes < block_norm_bwd_workspace(a.shape)))
+    return NABLA_ERR_INVALID_ARG;
+  a.workspace = workspace;
+  return from_cuda(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 nabla_status nabla_selftest_bounded_wait(nabla_stream_t stream) {
   return nabla::from_cuda(nabla::launch_bounded_wait_probe(reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -160,4 +160,28 @@ cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const floa
 size_t qk_norm_bwd_workspace(int D);
 cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);
 
+// K11: a block's gated sum and adaptive norm, or (bwd) its gradient.  Absent tensors are
+// null; strides are in elements (of the [B, S, C] tensors batch and token alone count).
+struct NormShape {
+  int B, S, C;
+};
+struct NormArgs {
+  NormShape shape;
+  const void *x, *u, *dsum, *dy;  // x: backward: the sum that the forward wrote
+  void *s, *y;                    // forward: the sum, the normed rows
+  void *dx, *du;
+  nabla_strides x_st, u_st, dsum_st, dy_st, s_st, y_st, dx_st, du_st;
+  const void *w, *pw, *gate, *scale, *shift;
+  int64_t gate_st, scale_st, shift_st;
+  void *dw, *dpw, *dgate, *dscale, *dshift;
+  nabla_dtype dt, wdt, mdt;
+  int rows;        // of the modulations; divides B S
+  int norm, post;  // nabla_norm
+  float rs, eps;
+  bool bwd;
+  void *workspace;  // backward: block_norm_bwd_workspace()
+};
+size_t block_norm_bwd_workspace(const NormShape &s);
+cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st);
+
 }  // namespace nabla

@@ -97,6 +97,17 @@ def load() -> ctypes.CDLL:
     lib.nabla_cross_attn_bwd.restype = i32
     lib.nabla_cross_attn_bwd.argtypes = ([vp, st, vp, st, vp, st, vp, st, vp, vp, st] + xs +
                                          [vp, f32, vp, vp, vp, vp, sz, vp])
+    i64 = ctypes.c_int64
+    mods = [vp, i64, vp, i64]  # gate, scale
+    lib.nabla_block_norm.restype = i32
+    lib.nabla_block_norm.argtypes = ([vp, st, vp, st, i32, i32, i32, i32, i32, i32, vp, vp, i32] +
+                                     mods + [vp, i64, i32, i32, f32, f32, vp, st, vp, st, vp])
+    lib.nabla_block_norm_bwd_workspace_bytes.restype = sz
+    lib.nabla_block_norm_bwd_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.nabla_block_norm_bwd.restype = i32
+    lib.nabla_block_norm_bwd.argtypes = (
+        [vp, st] * 4 + [i32, i32, i32, i32, i32, i32, vp, vp, i32] + mods +
+        [i32, i32, f32, f32, vp, st, vp, st, vp, vp, vp, vp, vp, vp, sz, vp])
     lib.nabla_selftest_bounded_wait.restype = i32
     lib.nabla_selftest_bounded_wait.argtypes = [vp]
     lib.nabla_get_last_device_status.restype = i32
@@ -174,12 +185,16 @@ def _allocators(stream, device: torch.device):
     return outputs, scratch
 
 
-def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.bfloat16:
+def _dtype_code_of(dtype: torch.dtype) -> int:
+    if dtype == torch.bfloat16:
         return NABLA_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return NABLA_F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    raise TypeError(f"unsupported dtype {dtype}")
+
+
+def _dtype_code(t: torch.Tensor) -> int:
+    return _dtype_code_of(t.dtype)
 
 
 def _check(status: int, where: str) -> None:
@@ -740,6 +755,188 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
          dout.data_ptr(), sg, *sizes, _ptr(kv_len), scale, dq.data_ptr(), dk.data_ptr(),
          dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv
+
+
+_NORMS = {None: 0, "rms": 1, "layer": 2}
+
+
+def _plane(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype,
+           device: torch.device) -> Optional[_Strides]:
+    """_rows of a [B, S, C] tensor."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    st = _rows(t.unsqueeze(2), name, (shape[0], shape[1], 1, shape[2]), dtype, device)
+    return st
+
+
+def _mod(t: Optional[torch.Tensor], name: str, B: int, S: int, C: int,
+         device: torch.device) -> Tuple[int, int]:
+    """Checks a modulation [C], [B, C] or [B, m, C] with m dividing S, which may be a view of
+    a projection that holds several, and returns its number of rows and their distance."""
+    if t.dim() not in (1, 2, 3) or t.shape[-1] != C or (t.dim() > 1 and t.shape[0] != B) or (
+            t.dim() == 3 and (t.shape[1] < 1 or S % t.shape[1])):
+        raise ValueError(f"{name} must be [{C}], [{B}, {C}] or [{B}, m, {C}] with m dividing {S}, "
+                         f"got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the columns of {name} must lie together")
+    dims = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
+    if len(dims) == 2 and dims[0][1] != dims[1][0] * dims[1][1]:
+        raise ValueError(f"the rows of {name} must lie equally far apart (make it contiguous)")
+    return t.numel() // C, dims[-1][1] if dims else C
+
+
+def _norm_args(like, u, gate, scale, shift, weight, post_weight, norm, post_norm, residual_scale,
+               eps):
+    """Checks what nabla_block_norm and its backward have in common; `like`: a [B, S, C]
+    tensor.  Returns the shape, the C arguments from dt to mdt (without shift), shift's two, the
+    rest, and the modulations' and weights' types."""
+    if like.dim() != 3:
+        raise ValueError("the tensors must be [B, S, C]")
+    for name, n in (("norm", norm), ("post_norm", post_norm)):
+        if n not in _NORMS:
+            raise ValueError(f"{name} must be None, 'rms' or 'layer', got {n!r}")
+    B, S, C = shape = tuple(like.shape)
+    dev = like.device
+    kind, mkind, rows = None, None, 1
+    for name, w in (("weight", weight), ("post_weight", post_weight)):
+        if w is not None:
+            kind = w.dtype if kind is None else kind
+            _buf(w, name, C, kind, dev)
+            if w.numel() != C:
+                raise ValueError(f"{name} must be [{C}], got {list(w.shape)}")
+    if norm is None and (weight is not None or scale is not None or shift is not None):
+        raise ValueError("weight, scale and shift need a norm")
+    if post_norm is None and post_weight is not None:
+        raise ValueError("post_weight needs a post_norm")
+    if u is None and (gate is not None or post_norm is not None):
+        raise ValueError("gate and post_norm need u")
+    mods, first = [], None
+    for name, m in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if m is None:
+            mods.append((None, 0))
+            continue
+        n, step = _mod(m, name, B, S, C, dev)
+        if first is None:
+            first, rows, mkind = (name, m.shape), n, m.dtype
+        elif m.shape != first[1] or m.dtype != mkind:
+            raise ValueError(f"{name} must be {list(first[1])} {mkind} as {first[0]} is, got "
+                             f"{list(m.shape)} {m.dtype}")
+        mods.append((m.data_ptr(), step))
+    code = NABLA_F32 if kind is None else _dtype_code_of(kind)
+    mcode = NABLA_F32 if mkind is None else _dtype_code_of(mkind)
+    head = (_dtype_code(like), B, S, C, _NORMS[norm], _NORMS[post_norm], _ptr(weight),
+            _ptr(post_weight), code) + mods[0] + mods[1]
+    return shape, head, mods[2], (mcode, rows, residual_scale, eps), mkind, kind
+
+
+def nabla_block_norm(x: torch.Tensor, u: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                     shift: Optional[torch.Tensor] = None,
+                     weight: Optional[torch.Tensor] = None,
+                     post_weight: Optional[torch.Tensor] = None, norm: Optional[str] = "layer",
+                     post_norm: Optional[str] = None, residual_scale: float = 1.0,
+                     eps: float = 1e-6, x_out: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None, stream=None):
+    """The gated sum after a block's branch and the adaptive norm before the next:
+    s = x + residual_scale * gate * N(u) * post_weight with post_norm's N, and
+    y = N(s) * weight * (1 + scale) + shift with norm's; N is "rms", "layer" or None.
+    x and u [B,S,C]; u None: s = x, the norm alone; norm None: the sum alone.  gate, scale and
+    shift are all [C], [B,C] or [B,m,C] (a row for each of m equal runs of a batch's tokens),
+    views of one projection if need be; weight and post_weight [C]; None: 1 (shift: 0).
+    x_out may be x.  x, u and the outputs may be views whose columns lie together.
+    Returns (s, y); s is x where u is None, y None where norm is."""
+    shape, head, sh, rest, _, _ = _norm_args(x, u, gate, scale, shift, weight, post_weight, norm,
+                                             post_norm, residual_scale, eps)
+    dev, dtype = x.device, x.dtype
+    if u is None and norm is None:
+        raise ValueError("neither u nor a norm: nothing to compute")
+    x_st, u_st = _plane(x, "x", shape, dtype, dev), _plane(u, "u", shape, dtype, dev)
+    empty, _ = _allocators(stream, dev)
+    xo_st = y_st = None
+    if u is None:
+        if x_out is not None:
+            raise ValueError("x_out without u")
+    elif x_out is None:
+        x_out = empty(shape, dtype=dtype, device=dev)
+    else:
+        xo_st = _plane(x_out, "x_out", shape, dtype, dev)
+    if norm is None:
+        if y is not None:
+            raise ValueError("y without a norm")
+    elif y is None:
+        y = empty(shape, dtype=dtype, device=dev)
+    else:
+        y_st = _plane(y, "y", shape, dtype, dev)
+    _cuda(x)
+    _run(dev, stream, load().nabla_block_norm, "nabla_block_norm", x.data_ptr(), x_st, _ptr(u),
+         u_st, *head, *sh, *rest, _ptr(x_out), xo_st, _ptr(y), y_st)
+    return (x if u is None else x_out), y
+
+
+def nabla_block_norm_bwd_workspace_bytes(B: int, S: int, C: int) -> int:
+    return load().nabla_block_norm_bwd_workspace_bytes(B, S, C)
+
+
+def nabla_block_norm_bwd(s: Optional[torch.Tensor], u: Optional[torch.Tensor],
+                         dsum: Optional[torch.Tensor], dy: Optional[torch.Tensor],
+                         gate: Optional[torch.Tensor] = None,
+                         scale: Optional[torch.Tensor] = None,
+                         shift: Optional[torch.Tensor] = None,
+                         weight: Optional[torch.Tensor] = None,
+                         post_weight: Optional[torch.Tensor] = None,
+                         norm: Optional[str] = "layer", post_norm: Optional[str] = None,
+                         residual_scale: float = 1.0, eps: float = 1e-6,
+                         dx: Optional[torch.Tensor] = None, du: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of nabla_block_norm, from the sum s it returned, u, and the upstream
+    gradients dsum of s (None: 0) and dy of y, with the forward's other arguments: returns
+    (dx, du, dgate, dscale, dshift, dweight, dpost_weight), None for what was not given.  s and
+    dy are not looked at (and may be None) where norm is None.  dx may be dsum; s, u, dsum, dy,
+    dx and du may be views as there."""
+    if norm is None:
+        s = dy = None
+    like = dsum if s is None else s
+    if like is None:
+        raise ValueError("s and dy, or dsum, are needed")
+    shape, head, _, rest, mkind, wkind = _norm_args(like, u, gate, scale, shift, weight,
+                                                    post_weight, norm, post_norm, residual_scale,
+                                                    eps)
+    if norm is not None and dy is None:
+        raise ValueError("dy is needed with a norm")
+    dev, dtype = like.device, like.dtype
+    strides = [_plane(t, name, shape, dtype, dev) for name, t in (("s", s), ("u", u),
+                                                                  ("dsum", dsum), ("dy", dy))]
+    empty, scratch = _allocators(stream, dev)
+    dx_st = du_st = None
+    if dx is None:
+        dx = empty(shape, dtype=dtype, device=dev)
+    else:
+        dx_st = _plane(dx, "dx", shape, dtype, dev)
+    if u is None:
+        if du is not None:
+            raise ValueError("du without u")
+    elif du is None:
+        du = empty(shape, dtype=dtype, device=dev)
+    else:
+        du_st = _plane(du, "du", shape, dtype, dev)
+    small = [None if t is None else empty(t.shape, dtype=t.dtype, device=dev)
+             for t in (gate, scale, shift, weight, post_weight)]
+    lib = load()
+    if workspace is None and any(t is not None for t in small):
+        need = lib.nabla_block_norm_bwd_workspace_bytes(*shape)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _on(workspace, "workspace", dev)
+    _cuda(like)
+    pairs = [a for t, st in zip((s, u, dsum, dy), strides) for a in (_ptr(t), st)]
+    _run(dev, stream, lib.nabla_block_norm_bwd, "nabla_block_norm_bwd", *pairs, *head, *rest,
+         dx.data_ptr(), dx_st, _ptr(du), du_st, *(_ptr(t) for t in small), _ptr(workspace),
+         0 if workspace is None else workspace.numel() * workspace.element_size())
+    return (dx, du, *small)
 
 
 def _stream_device(stream) -> torch.device:

@@ -483,6 +483,91 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
                                   nabla_stream_t stream);
 
 /*
+ * nabla_block_norm -- what lies between two branches of a block: the sum of the residual x
+ * and a branch's output u, normed, gated and scaled, and the adaptive norm that the next
+ * branch reads, in one pass.  For every token (a row of C columns), with the rows gate,
+ * scale and shift of the modulations that it takes:
+ *   s = x + residual_scale * gate * N_post(u) * post_weight
+ *   y = N_norm(s) * weight * (1 + scale) + shift
+ * N_RMS(t) = t / sqrt(mean(t^2) + eps), N_LAYER(t) = (t - mean(t)) / sqrt(var(t) + eps) with
+ * the mean of the squares about the mean, N_NONE(t) = t.  Computed in fp32, s and y rounded
+ * once each (y is formed from s before its rounding).
+ *
+ *   x, u        [B, S, C] device, element type dt, strides x_st and u_st (batch and token;
+ *               head is not looked at).  u = NULL: s = x, which is not written again; then
+ *               post is NABLA_NORM_NONE and gate, post_weight and x_out are NULL.
+ *   C           a multiple of 8 in [8, 8192]; B, S >= 1.
+ *   norm, post  the two norms.  norm = NABLA_NORM_NONE: the sum alone; then y, weight,
+ *               scale and shift are NULL and u is given.
+ *   weight, post_weight  [C] device, element type wdt; NULL: 1.  post_weight needs a post.
+ *   gate, scale, shift   [rows, C] device, element type mdt, their rows gate_st, scale_st and
+ *               shift_st elements apart (each at least C, a multiple of 16 bytes; not looked
+ *               at where rows = 1); NULL: 1, 0 and 0.  They are views of one projection of
+ *               the time embedding, say.
+ *   rows        >= 1, divides B * S: token t = b * S + s takes row t / (B * S / rows): 1 for
+ *               all tokens, B for a row a batch, B * m for a row for each of the m equal
+ *               runs (frames) of a batch's tokens, B * S for a row a token.
+ *   residual_scale  finite;  eps  finite, >= 0.
+ *   x_out, y    as x, strides xo_st and y_st, overwritten.  x_out may be x itself (the same
+ *               strides); apart from that they share no element with another argument.
+ * All pointers are 16-byte aligned, as are the strides.  Errors: NABLA_ERR_INVALID_ARG for
+ * anything else.
+ */
+typedef enum {
+  NABLA_NORM_NONE = 0,
+  NABLA_NORM_RMS = 1,
+  NABLA_NORM_LAYER = 2
+} nabla_norm;
+nabla_status nabla_block_norm(const void *x, const nabla_strides *x_st, const void *u,
+                              const nabla_strides *u_st, nabla_dtype dt, int B, int S, int C,
+                              nabla_norm norm, nabla_norm post, const void *weight,
+                              const void *post_weight, nabla_dtype wdt, const void *gate,
+                              int64_t gate_st, const void *scale, int64_t scale_st,
+                              const void *shift, int64_t shift_st, nabla_dtype mdt, int rows,
+                              float residual_scale, float eps, void *x_out,
+                              const nabla_strides *xo_st, void *y, const nabla_strides *y_st,
+                              nabla_stream_t stream);
+
+/*
+ * nabla_block_norm_bwd -- gradients of nabla_block_norm from the sum s that it wrote (x, where
+ * there was no u), u, and the upstream gradients dsum of s (along the residual) and dy of y.
+ * With n and m the normed rows of s and u, and [.] for the layer norm alone:
+ *   g = dy weight (1 + scale),   ds = dsum + (g - [mean(g)] - n mean(g n)) / sqrt(var + eps)
+ *   dx = ds,   e = residual_scale gate post_weight ds,
+ *   du = (e - [mean(e)] - m mean(e m)) / sqrt(var(u) + eps)   (post none: du = e),
+ *   dgate = residual_scale post_weight sum ds m,  dscale = weight sum dy n,  dshift = sum dy
+ * over the tokens of each row of the modulations, and over all tokens
+ *   dweight = sum dy (1 + scale) n,   dpost_weight = sum residual_scale gate ds m.
+ * fp32 throughout, each gradient rounded once.  No atomics: repeated calls give the same bits.
+ *
+ *   s, u, dsum, dy  [B, S, C] device, element type dt, with strides.  dsum NULL: 0; dy and s
+ *               are NULL exactly where norm is NABLA_NORM_NONE; u may be NULL where neither
+ *               post, dgate nor dpost_weight needs it.
+ *   weight, ..., eps  as given to nabla_block_norm (shift is not needed).
+ *   dx, du      as s, overwritten; NULL: not wanted.  dx may be dsum itself (the same
+ *               strides); apart from that the outputs share no element with another argument.
+ *   dgate, dscale, dshift  [rows, C] device, dense, element type mdt, overwritten; NULL: not
+ *               wanted.  dscale and dshift need a norm.
+ *   dweight, dpost_weight  [C] device, element type wdt, overwritten; NULL: not wanted; each
+ *               needs its norm.
+ *   workspace   device scratch of ws_bytes >= nabla_block_norm_bwd_workspace_bytes()
+ *               (256-byte aligned); not looked at where none of the last five is wanted.  Calls
+ *               that overlap on the GPU need one each.
+ * Errors as for nabla_block_norm; nabla_block_norm_bwd_workspace_bytes returns 0 for a shape
+ * that is not valid.
+ */
+size_t nabla_block_norm_bwd_workspace_bytes(int B, int S, int C);
+nabla_status nabla_block_norm_bwd(
+    const void *s, const nabla_strides *s_st, const void *u, const nabla_strides *u_st,
+    const void *dsum, const nabla_strides *dsum_st, const void *dy, const nabla_strides *dy_st,
+    nabla_dtype dt, int B, int S, int C, nabla_norm norm, nabla_norm post, const void *weight,
+    const void *post_weight, nabla_dtype wdt, const void *gate, int64_t gate_st,
+    const void *scale, int64_t scale_st, nabla_dtype mdt, int rows, float residual_scale,
+    float eps, void *dx, const nabla_strides *dx_st, void *du, const nabla_strides *du_st,
+    void *dgate, void *dscale, void *dshift, void *dweight, void *dpost_weight, void *workspace,
+    size_t ws_bytes, nabla_stream_t stream);
+
+/*
  * Diagnostic of the failure-detection path (no counterpart on the pages):
  * enqueues one CTA that waits on an mbarrier nothing ever arrives on, through
  * the same bounded wait the attention kernel uses, with a 20 ms limit.  The

@@ -453,3 +453,140 @@ def cross_attention_bwd(q, k, v, dout, kv_len, scale: float, o=None):
             dk[b, :n, j] += scale * (dz.T @ Q)
             dv[b, :n, j] += P.T @ dO
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Between a block's branches: the gated sum and the adaptive norm.
+# ---------------------------------------------------------------------------
+def normed(t: np.ndarray, kind, eps: float):
+    """(N(t), what its centred rows were multiplied by); kind None, "rms" or "layer"."""
+    t = np.asarray(t, np.float64)
+    if kind is None:
+        return t, np.ones(t.shape[:-1] + (1,))
+    if kind == "layer":
+        t = t - t.mean(-1, keepdims=True)
+    r = 1.0 / np.sqrt((t * t).mean(-1, keepdims=True) + eps)
+    return t * r, r
+
+
+def normed_bwd(d, n, r, kind):
+    """The gradient of normed() at its n and r for the gradient d of n."""
+    if kind is None:
+        return d
+    g = d - n * (d * n).mean(-1, keepdims=True)
+    if kind == "layer":
+        g = g - d.mean(-1, keepdims=True)
+    return r * g
+
+
+def over_tokens(m, B: int, S: int) -> np.ndarray:
+    """A modulation [C], [B, C] or [B, m, C] as the rows that the tokens [B, S] take."""
+    m = np.asarray(m, np.float64)
+    C = m.shape[-1]
+    rows = m.reshape(-1, C)
+    return np.repeat(rows, B * S // rows.shape[0], axis=0).reshape(B, S, C)
+
+
+def by_rows(t: np.ndarray, shape) -> np.ndarray:
+    """The transpose of over_tokens: sums of t [B, S, C] in a modulation's shape."""
+    C = t.shape[-1]
+    n = int(np.prod(shape)) // C
+    return t.reshape(n, -1, C).sum(1).reshape(shape)
+
+
+def block_norm(x, u, gate, scale, shift, w, pw, norm, post, rs: float, eps: float):
+    """(s, y): s = x + rs gate N(u) pw, y = N(s) w (1 + scale) + shift; absent: None."""
+    x = np.asarray(x, np.float64)
+    B, S, _ = x.shape
+    s = x
+    if u is not None:
+        b = normed(u, post, eps)[0] * (1.0 if pw is None else np.asarray(pw, np.float64))
+        s = x + rs * b * (1.0 if gate is None else over_tokens(gate, B, S))
+    if norm is None:
+        return s, None
+    y = normed(s, norm, eps)[0] * (1.0 if w is None else np.asarray(w, np.float64))
+    if scale is not None:
+        y = y * (1.0 + over_tokens(scale, B, S))
+    return s, (y if shift is None else y + over_tokens(shift, B, S))
+
+
+def block_norm_bwd(s, u, dsum, dy, gate, scale, shift, w, pw, norm, post, rs: float, eps: float):
+    """(dx, du, dgate, dscale, dshift, dw, dpw) of block_norm at its sum s; None: absent."""
+    s = np.asarray(s, np.float64)
+    B, S, _ = s.shape
+    ds = np.zeros(s.shape) if dsum is None else np.asarray(dsum, np.float64)
+    out = dict.fromkeys(("du", "dgate", "dscale", "dshift", "dw", "dpw"))
+    if norm is not None:
+        dy = np.asarray(dy, np.float64)
+        wf = 1.0 if w is None else np.asarray(w, np.float64)
+        up = 1.0 if scale is None else 1.0 + over_tokens(scale, B, S)
+        n, r = normed(s, norm, eps)
+        ds = ds + normed_bwd(dy * up * wf, n, r, norm)
+        if scale is not None:
+            out["dscale"] = by_rows(dy * n * wf, np.shape(scale))
+        if shift is not None:
+            out["dshift"] = by_rows(dy, np.shape(shift))
+        if w is not None:
+            out["dw"] = (dy * up * n).sum((0, 1))
+    if u is not None:
+        pf = 1.0 if pw is None else np.asarray(pw, np.float64)
+        g = rs * (1.0 if gate is None else over_tokens(gate, B, S))
+        m, r = normed(u, post, eps)
+        out["du"] = normed_bwd(ds * g * pf, m, r, post)
+        if gate is not None:
+            out["dgate"] = by_rows(rs * pf * ds * m, np.shape(gate))
+        if pw is not None:
+            out["dpw"] = (ds * g * m).sum((0, 1))
+    return (ds, out["du"], out["dgate"], out["dscale"], out["dshift"], out["dw"], out["dpw"])
+
+
+# ---------------------------------------------------------------------------
+# Differential attention: the difference of two softmax maps.
+# ---------------------------------------------------------------------------
+def diff_attention(q, k, v, lam, kv_len, scale: float):
+    """o [B, Sq, h, D], the second map's rows o2 and the base-2 log-sum-exp [B, h, 2, Sq]:
+    o = o1 - lam o2, o1 and o2 the cross attentions of the first and the last D / 2 columns of
+    q and k over the whole of v; lam [h] or [1]."""
+    B, Sq, h, D = q.shape
+    d = D // 2
+    lam = np.broadcast_to(np.asarray(lam, np.float64), (h,))
+    o, lse = [], []
+    for at in (slice(0, d), slice(d, D)):
+        # a head of D columns whose other half is 0 scores by this half alone
+        qq, kk = np.zeros(q.shape), np.zeros(k.shape)
+        qq[..., at], kk[..., at] = q[..., at], k[..., at]
+        a, b = cross_attention(qq, kk, v, kv_len, scale)
+        o.append(a)
+        lse.append(b)
+    return o[0] - lam[:, None] * o[1], o[1], np.stack(lse, 2)
+
+
+def diff_attention_bwd(q, k, v, lam, dout, kv_len, scale: float, o=None, o2=None):
+    """(dq, dk, dv, dlam) of diff_attention; the maps' delta from the o and o2 passed in,
+    dlam in lam's shape (from the maps themselves)."""
+    B, Sq, h, D = q.shape
+    hk, d = k.shape[2], D // 2
+    lam_h = np.broadcast_to(np.asarray(lam, np.float64), (h,))
+    dq, dk, dv, dlam = np.zeros(q.shape), np.zeros(k.shape), np.zeros(k.shape), np.zeros(h)
+    for b in range(B):
+        n = int(kv_len[b])
+        for i in range(h if n else 0):
+            j = i // (h // hk)
+            Q, K, V, dO = (t.astype(np.float64) for t in
+                           (q[b, :, i], k[b, :n, j], v[b, :n, j], dout[b, :, i]))
+            P = []
+            for at in (slice(0, d), slice(d, D)):
+                z = scale * (Q[:, at] @ K[:, at].T)
+                p = np.exp(z - z.max(axis=1, keepdims=True))
+                P.append(p / p.sum(axis=1, keepdims=True))
+            dP = dO @ V.T
+            second = P[1] @ V if o2 is None else o2[b, :, i].astype(np.float64)
+            first = P[0] @ V if o is None else o[b, :, i].astype(np.float64) + lam_h[i] * second
+            for at, p, by, t in ((slice(0, d), P[0], 1.0, first),
+                                 (slice(d, D), P[1], -lam_h[i], second)):
+                dz = by * p * (dP - (dO * t).sum(axis=1, keepdims=True))
+                dq[b, :, i, at] = scale * (dz @ K[:, at])
+                dk[b, :n, j, at] += scale * (dz.T @ Q[:, at])
+            dv[b, :n, j] += (P[0] - lam_h[i] * P[1]).T @ dO
+            dlam[i] -= (P[1] * dP).sum()
+    return dq, dk, dv, (dlam if np.size(lam) == h and np.ndim(lam) else dlam.sum(keepdims=True))
