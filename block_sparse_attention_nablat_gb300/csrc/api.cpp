@@ -79,6 +79,11 @@ bool ranges_meet(const void *a, uintptr_t an, const void *b, uintptr_t bn) {
   return a0 < b0 + bn && b0 < a0 + an;
 }
 
+struct Range {
+  const void *p;
+  uintptr_t n;
+};
+
 // A tensor's dimensions larger than 1, the largest stride first; each stride is at least
 // what the dimensions after it span (valid_rows).
 struct Dim {
@@ -629,11 +634,6 @@ bool valid_norm_shape(const NormShape &s) {
   return (double)s.B * s.S <= 2.0e9 && (double)s.B * s.S * s.C <= 4.0e12;
 }
 
-struct Range {
-  const void *p;
-  uintptr_t n;
-};
-
 // What both directions of the block norm check: shape, norms, weights, modulations and
 // scalars; collects the arrays that outputs must keep clear of.
 struct NormCheck {
@@ -795,6 +795,128 @@ nabla_status nabla_block_norm_bwd(
     return NABLA_ERR_INVALID_ARG;
   a.workspace = workspace;
   return from_cuda(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace nabla {
+namespace {
+
+// lam: [1] or [h] fp32, kept clear of what is written.
+bool valid_lam(const float *lam, int n, int h) {
+  return lam && aligned(lam, 4) && (n == 1 || n == h);
+}
+
+}  // namespace
+}  // namespace nabla
+
+size_t nabla_diff_attn_fwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                           int D) {
+  const nabla::CrossShape s{B, Sq, Sk, h, hk, D};
+  if (!nabla::valid_dtype(dt) || !nabla::valid_cross_shape(s)) return 0;
+  return nabla::diff_fwd_workspace(s, dt);
+}
+
+nabla_status nabla_diff_attn_fwd(const void *q, const nabla_strides *q_st, const void *k,
+                                 const nabla_strides *k_st, const void *v,
+                                 const nabla_strides *v_st, nabla_dtype dt, int B, int Sq, int Sk,
+                                 int h, int hk, int D, const float *lam, int lam_n,
+                                 const int32_t *kv_len, float scale, void *o, void *o2, float *lse,
+                                 void *workspace, size_t ws_bytes, nabla_stream_t stream) {
+  using namespace nabla;
+  DiffArgs a{};
+  a.x.s = CrossShape{B, Sq, Sk, h, hk, D};
+  if (!valid_dtype(dt) || !valid_cross_shape(a.x.s) || !valid_lam(lam, lam_n, h))
+    return NABLA_ERR_INVALID_ARG;
+  const size_t esz = dt == NABLA_BF16 ? 2 : 4;
+  a.x.q = q, a.x.k = k, a.x.v = v;
+  a.x.kv_len = kv_len;
+  a.x.scale = scale;
+  CrossRows r;
+  if (!valid_cross_inputs(a.x, q_st, k_st, v_st, esz, r)) return NABLA_ERR_INVALID_ARG;
+  const uintptr_t rows = (uintptr_t)B * Sq * h, on = rows * D * esz;
+  if (!o || !aligned(o, 16) || !aligned(o2, 16) || !aligned(lse, 4)) return NABLA_ERR_INVALID_ARG;
+  const Range out[3] = {{o, on}, {o2, on}, {lse, rows * 8}};
+  for (int i = 0; i < 3; ++i) {
+    if (!out[i].p) continue;
+    if (meets_inputs(out[i].p, out[i].n, a.x, r) ||
+        ranges_meet(out[i].p, out[i].n, lam, (uintptr_t)lam_n * 4))
+      return NABLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[j].p && ranges_meet(out[i].p, out[i].n, out[j].p, out[j].n))
+        return NABLA_ERR_INVALID_ARG;
+  }
+  const size_t need = diff_fwd_workspace(a.x.s, dt);
+  if (need && (!workspace || !aligned(workspace, 256) || ws_bytes < need))
+    return NABLA_ERR_INVALID_ARG;
+  a.x.o = o, a.o2 = o2, a.x.lse = lse;
+  a.lam = lam, a.lam_n = lam_n;
+  a.x.workspace = workspace;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  a.x.status = device_status_ptr(&e);
+  if (!a.x.status) return NABLA_ERR_CUDA;
+  return from_cuda(dt == NABLA_BF16 ? launch_diff_attn_tc(a, st) : launch_diff_attn_simt(a, st));
+}
+
+size_t nabla_diff_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                           int D) {
+  const nabla::CrossShape s{B, Sq, Sk, h, hk, D};
+  if (!nabla::valid_dtype(dt) || !nabla::valid_cross_shape(s)) return 0;
+  return nabla::diff_bwd_workspace(s, dt);
+}
+
+nabla_status nabla_diff_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
+                                 const nabla_strides *k_st, const void *v,
+                                 const nabla_strides *v_st, const void *o,
+                                 const nabla_strides *o_st, const void *o2,
+                                 const nabla_strides *o2_st, const float *lse, const void *dout,
+                                 const nabla_strides *dout_st, nabla_dtype dt, int B, int Sq,
+                                 int Sk, int h, int hk, int D, const float *lam, int lam_n,
+                                 const int32_t *kv_len, float scale, void *dq, void *dk, void *dv,
+                                 float *dlam, void *workspace, size_t ws_bytes,
+                                 nabla_stream_t stream) {
+  using namespace nabla;
+  DiffArgs a{};
+  a.x.s = CrossShape{B, Sq, Sk, h, hk, D};
+  if (!valid_dtype(dt) || !valid_cross_shape(a.x.s) || !valid_lam(lam, lam_n, h))
+    return NABLA_ERR_INVALID_ARG;
+  const size_t esz = dt == NABLA_BF16 ? 2 : 4;
+  a.x.q = q, a.x.k = k, a.x.v = v;
+  a.x.kv_len = kv_len;
+  a.x.scale = scale;
+  CrossRows r;
+  if (!valid_cross_inputs(a.x, q_st, k_st, v_st, esz, r)) return NABLA_ERR_INVALID_ARG;
+  if (!lse || !dq || !dk || !dv || !dlam || !workspace) return NABLA_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(dlam, 4) || !aligned(workspace, 256))
+    return NABLA_ERR_INVALID_ARG;
+  const Rows in[3] = {rows_of(o, o_st, B, Sq, h, D), rows_of(o2, o2_st, B, Sq, h, D),
+                      rows_of(dout, dout_st, B, Sq, h, D)};
+  for (const Rows &t : in)
+    if (!valid_rows(t, B, Sq, D, esz)) return NABLA_ERR_INVALID_ARG;
+  a.x.o_st = in[0].st, a.o2_st = in[1].st, a.x.dout_st = in[2].st;
+  const uintptr_t rows = (uintptr_t)B * Sq * h, kn = (uintptr_t)B * Sk * hk * D * esz;
+  const Range out[4] = {{dq, rows * D * esz}, {dk, kn}, {dv, kn}, {dlam, (uintptr_t)lam_n * 4}};
+  for (int i = 0; i < 4; ++i) {
+    if ((i < 3 && !aligned(out[i].p, 16)) || meets_inputs(out[i].p, out[i].n, a.x, r) ||
+        ranges_meet(out[i].p, out[i].n, lse, rows * 8) ||
+        ranges_meet(out[i].p, out[i].n, lam, (uintptr_t)lam_n * 4))
+      return NABLA_ERR_INVALID_ARG;
+    for (const Rows &t : in)
+      if (ranges_meet(out[i].p, out[i].n, t.p, extent(t, B, Sq, D, esz)))
+        return NABLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (ranges_meet(out[i].p, out[i].n, out[j].p, out[j].n)) return NABLA_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < diff_bwd_workspace(a.x.s, dt)) return NABLA_ERR_INVALID_ARG;
+  a.x.of = o, a.o2f = o2;
+  a.x.lse = const_cast<float *>(lse);
+  a.x.dout = dout;
+  a.x.dq = dq, a.x.dk = dk, a.x.dv = dv;
+  a.lam = lam, a.lam_n = lam_n, a.dlam = dlam;
+  a.x.workspace = workspace;
+  cudaError_t e;
+  a.x.status = device_status_ptr(&e);
+  if (!a.x.status) return NABLA_ERR_CUDA;
+  return from_cuda(launch_diff_bwd(a, dt, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 nabla_status nabla_selftest_bounded_wait(nabla_stream_t stream) {

@@ -484,6 +484,7 @@ __global__ void __launch_bounds__(1024)
   __shared__ float sums[3][32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   pdl_launch_dependents();
+  pdl_wait();  // in every block, so that whoever waits for this kernel waits for the first
   const bool weights = (int)blockIdx.y == ny;
   long m = blockIdx.y;
   if (!weights && ny < rows) {  // by the runs' borders: the rows that run y + 1 goes on with
@@ -494,7 +495,6 @@ __global__ void __launch_bounds__(1024)
   const long g0 = m * P.n, g1 = g0 + P.n;
   const int t0 = weights ? 0 : (int)(g0 / P.L), t1 = weights ? teams - 1 : (int)((g1 - 1) / P.L);
   if (!weights && t0 == t1) return;  // seen whole
-  pdl_wait();
   float a[3] = {0.f, 0.f, 0.f};
   if (c < P.C)
     for (int t = t0 + ty; t <= t1; t += 32) {

@@ -1,0 +1,226 @@
+// The parts of the differential attention backward around its products: the rows' numbers in
+// packed order (before), and lam's gradient (after).
+#include <cuda_bf16.h>
+
+#include "diff_common.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+#include "vec8.cuh"
+
+namespace nabla {
+namespace {
+
+constexpr int kRowsArrays = 5;
+
+// -lse_1, -lse_2, -delta_1, -delta_2 and lam of the packed rows [B, hk, nsub, 64], with
+// delta_2 = <dout, o2> and delta_1 = <dout, o> + lam delta_2; -inf and 0 where a row is none
+// or has no states, so that its P is 0.  A block takes a 64-row subtile, D / 8 lanes a row;
+// HBM-bound (o, o2 and dout read once), so a thread's rows are all in flight at once.
+template <typename T>
+struct PrepParams {
+  const T *o, *o2, *dout;
+  nabla_strides o_st, o2_st, g_st;
+  const float *lse, *lam;  // [B, h, 2, Sq]
+  float *rows;
+  size_t nrows;
+  int lam_step, Sq, h, hk, G, tq, nsub;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(256) diff_prep_kernel(const __grid_constant__ PrepParams<T> P) {
+  constexpr int kLanes = D / 8, kPass = 256 / kLanes, kRows = 64 / kPass;
+  const int lane = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
+  pdl_launch_dependents();
+  const uint32_t bj = blockIdx.x / (uint32_t)P.nsub, sub = blockIdx.x - bj * P.nsub;
+  const uint32_t b = bj / (uint32_t)P.hk, j = bj - b * P.hk;
+  const T *o = P.o + b * P.o_st.batch + lane * 8, *o2 = P.o2 + b * P.o2_st.batch + lane * 8;
+  const T *g = P.dout + b * P.g_st.batch + lane * 8;
+  pdl_wait();
+  Raw<T> a[kRows], c[kRows], d[kRows];
+  float n[kRows][3];  // -lse_1, -lse_2, lam
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t r = r0 + i * kPass, t = r / (uint32_t)P.G;
+    const int token = (int)(sub * P.tq + t), hh = (int)(j * P.G + r - t * P.G);
+    const bool ok = t < (uint32_t)P.tq && token < P.Sq;
+    a[i] = load_raw(o + token * P.o_st.token + hh * P.o_st.head, ok);
+    c[i] = load_raw(o2 + token * P.o2_st.token + hh * P.o2_st.head, ok);
+    d[i] = load_raw(g + token * P.g_st.token + hh * P.g_st.head, ok);
+    n[i][0] = n[i][1] = -INFINITY;
+    n[i][2] = 0.f;
+    if (ok) {
+      const float *l = P.lse + ((size_t)b * P.h + hh) * 2 * P.Sq + token;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float v = l[(size_t)m * P.Sq];
+        if (v != -INFINITY) n[i][m] = -v;
+      }
+      n[i][2] = P.lam[hh * P.lam_step];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    float x[8], y[8], z[8], s = 0.f, s2 = 0.f;
+    unpack8(a[i], x);
+    unpack8(c[i], y);
+    unpack8(d[i], z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      s = fmaf(z[e], x[e], s);
+      s2 = fmaf(z[e], y[e], s2);
+    }
+#pragma unroll
+    for (int e = kLanes / 2; e; e >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, e);
+      s2 += __shfl_xor_sync(0xffffffffu, s2, e);
+    }
+    if (lane < kRowsArrays) {
+      const float v = lane == 0   ? n[i][0]
+                      : lane == 1 ? n[i][1]
+                      : lane == 2 ? -fmaf(n[i][2], s2, s)
+                      : lane == 3 ? -s2
+                                  : n[i][2];
+      P.rows[lane * P.nrows + (size_t)blockIdx.x * 64 + r0 + i * kPass] = v;
+    }
+  }
+}
+
+// lam's gradient: minus the sum of the rows' numbers t2 ([runs][nrows]; 0 where a row is
+// none), over all rows or over each head's.  Block (i, c): chunk c of gradient i; one chunk:
+// straight to dlam, else to part [i][chunks], which lam_sum_kernel adds up.
+struct LamParams {
+  const float *t2;
+  size_t nrows;
+  int runs, B, hk, G, tq, nsub, each;
+  float *part, *dlam;
+};
+
+__device__ __forceinline__ float block_sum(float v) {
+  __shared__ float sums[8];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v += sums[i];
+  return v;
+}
+
+__global__ void __launch_bounds__(256) lam_part_kernel(const LamParams P) {
+  const uint32_t i = blockIdx.x, chunk = blockIdx.y, chunks = gridDim.y;
+  pdl_launch_dependents();
+  const uint32_t j = i / (uint32_t)P.G, in = i - j * P.G;  // key head, head in its group
+  const size_t n = P.each ? (size_t)P.B * P.nsub * P.tq : P.nrows;
+  const size_t e0 = n * chunk / chunks, e1 = n * (chunk + 1) / chunks;
+  pdl_wait();
+  float v = 0.f;
+  for (size_t e = e0 + threadIdx.x; e < e1; e += 256) {
+    size_t row = e;
+    if (P.each) {
+      const size_t bs = e / P.tq, t = e - bs * P.tq, b = bs / P.nsub, sub = bs - b * P.nsub;
+      row = ((b * P.hk + j) * P.nsub + sub) * 64 + t * P.G + in;
+    }
+    for (int r = 0; r < P.runs; ++r) v += P.t2[(size_t)r * P.nrows + row];
+  }
+  v = block_sum(v);
+  if (threadIdx.x == 0) {
+    if (chunks == 1)
+      P.dlam[i] = -v;
+    else
+      P.part[(size_t)i * chunks + chunk] = v;
+  }
+}
+
+__global__ void __launch_bounds__(256) lam_sum_kernel(const LamParams P, int chunks) {
+  pdl_launch_dependents();
+  pdl_wait();
+  float v = (int)threadIdx.x < chunks ? P.part[(size_t)blockIdx.x * chunks + threadIdx.x] : 0.f;
+  v = block_sum(v);
+  if (threadIdx.x == 0) P.dlam[blockIdx.x] = -v;
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+struct BwdLayout {
+  int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
+  size_t nrows;
+  int nsplit, qsplit, truns, chunks;
+  size_t rows, t2, part, qpart, lam, total;
+};
+BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt, int lam_n) {
+  BwdLayout w;
+  w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
+  w.nrows = (size_t)s.B * s.hk * w.nsub * 64;
+  w.nsplit = cross_dkv_splits(s, dt);
+  w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : 1;
+  w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : 1;
+  // a chunk of 8192 numbers takes a block about as long as starting one more kernel does
+  const size_t numbers = w.nrows * w.truns / (lam_n > 1 ? s.h : 1);
+  const size_t chunks = (numbers + 8191) / 8192;
+  w.chunks = chunks > 256 ? 256 : (int)chunks;
+  w.rows = 0;
+  w.t2 = round_up(kRowsArrays * w.nrows * sizeof(float));
+  w.part = w.t2 + round_up(w.truns * w.nrows * sizeof(float));
+  w.qpart = w.part + (w.nsplit > 1 ? round_up((size_t)w.nsplit * 2 * s.B * s.Sk * s.hk * s.D *
+                                              sizeof(float))
+                                   : 0);
+  w.lam = w.qpart + (w.qsplit > 1 ? round_up((size_t)w.qsplit * s.B * s.Sq * s.h * s.D *
+                                             sizeof(float))
+                                  : 0);
+  w.total = w.lam + round_up((size_t)(lam_n > 1 ? s.h : 1) * 256 * sizeof(float));
+  return w;
+}
+
+template <typename T, int D>
+cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, cudaStream_t st) {
+  const CrossShape &s = a.x.s;
+  const cross::Packing pk = cross::packing(s);
+  PrepParams<T> p{};
+  p.o = static_cast<const T *>(a.x.of), p.o2 = static_cast<const T *>(a.o2f);
+  p.dout = static_cast<const T *>(a.x.dout);
+  p.o_st = a.x.o_st, p.o2_st = a.o2_st, p.g_st = a.x.dout_st;
+  p.lse = a.x.lse, p.lam = a.lam, p.lam_step = a.lam_n > 1 ? 1 : 0;
+  p.rows = rows, p.nrows = r.nrows;
+  p.Sq = s.Sq, p.h = s.h, p.hk = s.hk, p.G = pk.G, p.tq = pk.tq, p.nsub = r.nsub;
+  return launch_pdl(diff_prep_kernel<T, D>, dim3((unsigned)((long)s.B * s.hk * r.nsub)), dim3(256),
+                    0, st, p);
+}
+
+}  // namespace
+
+size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt) {
+  // one weight or one a head: the larger of the two
+  const size_t a = bwd_layout(s, dt, 1).total, b = bwd_layout(s, dt, s.h).total;
+  return a > b ? a : b;
+}
+
+cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) {
+  const CrossShape &s = a.x.s;
+  const BwdLayout w = bwd_layout(s, dt, a.lam_n);
+  char *ws = static_cast<char *>(a.x.workspace);
+  auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+  const DiffRows r{at(w.rows), w.nrows, at(w.t2), w.nsub};
+  cudaError_t e;
+  if (dt == NABLA_BF16)
+    e = s.D == 64 ? launch_prep<__nv_bfloat16, 64>(a, r, at(w.rows), st)
+                  : launch_prep<__nv_bfloat16, 128>(a, r, at(w.rows), st);
+  else
+    e = s.D == 64 ? launch_prep<float, 64>(a, r, at(w.rows), st)
+                  : launch_prep<float, 128>(a, r, at(w.rows), st);
+  if (e != cudaSuccess) return e;
+  e = dt == NABLA_BF16
+          ? launch_diff_bwd_tc(a, r, at(w.part), w.nsplit, at(w.qpart), w.qsplit, st)
+          : launch_diff_bwd_simt(a, r, at(w.part), w.nsplit, st);
+  if (e != cudaSuccess) return e;
+  const cross::Packing pk = cross::packing(s);
+  const bool each = a.lam_n > 1;
+  const LamParams p{r.t2, w.nrows, w.truns, s.B, s.hk, pk.G, pk.tq, w.nsub, each ? 1 : 0,
+                    at(w.lam), a.dlam};
+  const unsigned n = each ? (unsigned)s.h : 1u;
+  e = launch_pdl(lam_part_kernel, dim3(n, (unsigned)w.chunks), dim3(256), 0, st, p);
+  if (e != cudaSuccess || w.chunks == 1) return e;
+  return launch_pdl(lam_sum_kernel, dim3(n), dim3(256), 0, st, p, w.chunks);
+}
+
+}  // namespace nabla

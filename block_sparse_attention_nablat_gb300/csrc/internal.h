@@ -157,6 +157,40 @@ cudaError_t launch_cross_bwd_simt(const CrossArgs &a, const float *nlse, const f
 cudaError_t launch_cross_dkv_join(const CrossArgs &a, nabla_dtype dt, const float *part,
                                   int nsplit, cudaStream_t st);
 
+// Differential attention: the cross attention's shapes, the two maps in the halves of a
+// head's columns.
+struct DiffArgs {
+  CrossArgs x;  // its lse: [B, h, 2, Sq]
+  const float *lam;
+  int lam_n;  // 1 or h
+  void *o2;   // forward: the second map's rows, or null
+  const void *o2f;
+  nabla_strides o2_st;  // backward
+  float *dlam;
+};
+int diff_fwd_splits(const CrossShape &s, nabla_dtype dt);
+size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt);
+// [nsplit, 2, B, h, Sq, D] and [nsplit, 2, B, h, Sq]; none for one run
+CrossRuns diff_runs(const DiffArgs &a, int nsplit);
+cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, int nsplit, cudaStream_t st);
+// K12: bf16, tcgen05.  K12f: fp32, CUDA cores.
+cudaError_t launch_diff_attn_tc(const DiffArgs &a, cudaStream_t st);
+cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st);
+// K13: the backward.  Workspace: the packed rows' numbers (five), what lam's gradient is
+// summed from, the runs' sums of dK and dV and of dQ.
+struct DiffRows {
+  const float *rows;  // -lse_1, -lse_2, -delta_1, -delta_2, lam: [5][nrows]
+  size_t nrows;
+  float *t2;  // [runs][nrows]
+  int nsub;
+};
+size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt);
+cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st);
+cudaError_t launch_diff_bwd_tc(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,
+                               float *qpart, int qsplit, cudaStream_t st);
+cudaError_t launch_diff_bwd_simt(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,
+                                 cudaStream_t st);
+
 size_t qk_norm_bwd_workspace(int D);
 cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);
 

@@ -97,6 +97,16 @@ def load() -> ctypes.CDLL:
     lib.nabla_cross_attn_bwd.restype = i32
     lib.nabla_cross_attn_bwd.argtypes = ([vp, st, vp, st, vp, st, vp, st, vp, vp, st] + xs +
                                          [vp, f32, vp, vp, vp, vp, sz, vp])
+    lib.nabla_diff_attn_fwd_workspace_bytes.restype = sz
+    lib.nabla_diff_attn_fwd_workspace_bytes.argtypes = xs
+    lib.nabla_diff_attn_fwd.restype = i32
+    lib.nabla_diff_attn_fwd.argtypes = ([vp, st] * 3 + xs +
+                                        [vp, i32, vp, f32, vp, vp, vp, vp, sz, vp])
+    lib.nabla_diff_attn_bwd_workspace_bytes.restype = sz
+    lib.nabla_diff_attn_bwd_workspace_bytes.argtypes = xs
+    lib.nabla_diff_attn_bwd.restype = i32
+    lib.nabla_diff_attn_bwd.argtypes = ([vp, st] * 5 + [vp, vp, st] + xs +
+                                        [vp, i32, vp, f32, vp, vp, vp, vp, vp, sz, vp])
     i64 = ctypes.c_int64
     mods = [vp, i64, vp, i64]  # gate, scale
     lib.nabla_block_norm.restype = i32
@@ -755,6 +765,123 @@ def nabla_cross_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: t
          dout.data_ptr(), sg, *sizes, _ptr(kv_len), scale, dq.data_ptr(), dk.data_ptr(),
          dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dq, dk, dv
+
+
+def _lam(lam: torch.Tensor, h: int, device: torch.device) -> int:
+    if lam.dim() != 1 or lam.numel() not in (1, h):
+        raise ValueError(f"lam must be [{h}] or [1], got {list(lam.shape)}")
+    _buf(lam, "lam", lam.numel(), torch.float32, device)
+    return lam.numel()
+
+
+def nabla_diff_attn_fwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk: int, h: int,
+                                        hk: int, D: int) -> int:
+    code = NABLA_BF16 if dtype == torch.bfloat16 else NABLA_F32
+    return load().nabla_diff_attn_fwd_workspace_bytes(code, B, Sq, Sk, h, hk, D)
+
+
+def _diff_fwd(q, k, v, lam, kv_len, scale, o, o2, lse, whole, workspace, stream):
+    strides, sizes = _cross_args(q, k, v, kv_len)
+    dev = q.device
+    n = _lam(lam, sizes[4], dev)
+    empty, scratch = _allocators(stream, dev)
+    if scale is None:
+        scale = math.sqrt(2.0 / sizes[-1])
+    if o is None:
+        o = empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _buf(o, "o", q.numel(), q.dtype, dev)
+    if whole:
+        if o2 is None:
+            o2 = empty(q.shape, dtype=q.dtype, device=dev)
+        else:
+            _buf(o2, "o2", q.numel(), q.dtype, dev)
+        if lse is None:
+            lse = empty((q.shape[0], q.shape[2], 2, q.shape[1]), dtype=torch.float32, device=dev)
+        else:
+            _buf(lse, "lse", 2 * q.numel() // sizes[-1], torch.float32, dev)
+    lib = load()
+    if workspace is None:
+        need = lib.nabla_diff_attn_fwd_workspace_bytes(*sizes)
+        if need:
+            workspace = scratch(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _on(workspace, "workspace", dev)
+    _cuda(q)
+    _run(dev, stream, lib.nabla_diff_attn_fwd, "nabla_diff_attn_fwd", q.data_ptr(), strides[0],
+         k.data_ptr(), strides[1], v.data_ptr(), strides[2], *sizes, lam.data_ptr(), n,
+         _ptr(kv_len), scale, o.data_ptr(), _ptr(o2), _ptr(lse), _ptr(workspace),
+         0 if workspace is None else workspace.numel() * workspace.element_size())
+    return o, o2, lse
+
+
+def nabla_diff_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                        kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        o: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Differential attention of q [B,Sq,h,D] to the first kv_len[b] (int32 [B]; None: all) of
+    the states k, v [B,Sk,hk,D], hk dividing h: softmax of the scores of the first D / 2
+    columns of q and k minus lam (fp32 [h] or [1]) times that of the last D / 2, times v.
+    scale None: 1 / sqrt(D / 2).  q, k and v may be views as for nabla_cross_attn_fwd; heads
+    2i and 2i + 1 of [B,S,2h,D/2] viewed as [B,S,h,D] are head i.  Returns o [B,Sq,h,D], dense."""
+    return _diff_fwd(q, k, v, lam, kv_len, scale, o, None, None, False, workspace, stream)[0]
+
+
+def nabla_diff_attn_fwd_lse(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                            kv_len: Optional[torch.Tensor] = None,
+                            scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                            o2: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None):
+    """nabla_diff_attn_fwd that also returns what its backward needs: (o, o2, lse) with the
+    second map's rows o2 [B,Sq,h,D] and the maps' base-2 log-sum-exp lse [B,h,2,Sq] fp32."""
+    return _diff_fwd(q, k, v, lam, kv_len, scale, o, o2, lse, True, workspace, stream)
+
+
+def nabla_diff_attn_bwd_workspace_bytes(dtype: torch.dtype, B: int, Sq: int, Sk: int, h: int,
+                                        hk: int, D: int) -> int:
+    code = NABLA_BF16 if dtype == torch.bfloat16 else NABLA_F32
+    return load().nabla_diff_attn_bwd_workspace_bytes(code, B, Sq, Sk, h, hk, D)
+
+
+def nabla_diff_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                        o: torch.Tensor, o2: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor,
+                        kv_len: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                        dv: Optional[torch.Tensor] = None, dlam: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of nabla_diff_attn_fwd, from its inputs, what nabla_diff_attn_fwd_lse returned
+    and the upstream gradient dout of o: returns dq [B,Sq,h,D], dk, dv [B,Sk,hk,D] (0 for states
+    past kv_len), dense, and dlam in lam's shape.  o, o2 and dout may be views as q, k and v
+    may; an expanded dout (the gradient of a plain sum) has to be made contiguous first."""
+    strides, sizes = _cross_args(q, k, v, kv_len)
+    dev = q.device
+    n = _lam(lam, sizes[4], dev)
+    so, s2, sg = (_rows(t, name, q.shape, q.dtype, dev)
+                  for name, t in (("o", o), ("o2", o2), ("dout", dout)))
+    _buf(lse, "lse", 2 * q.numel() // sizes[-1], torch.float32, dev)
+    if scale is None:
+        scale = math.sqrt(2.0 / sizes[-1])
+    empty, scratch = _allocators(stream, dev)
+    outs = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k), ("dlam", dlam, lam)):
+        if t is None:
+            t = empty(like.shape, dtype=like.dtype, device=dev)
+        else:
+            _buf(t, name, like.numel(), like.dtype, dev)
+        outs.append(t)
+    lib = load()
+    if workspace is None:
+        need = lib.nabla_diff_attn_bwd_workspace_bytes(*sizes)
+        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
+    _on(workspace, "workspace", dev)
+    _cuda(q)
+    _run(dev, stream, lib.nabla_diff_attn_bwd, "nabla_diff_attn_bwd", q.data_ptr(), strides[0],
+         k.data_ptr(), strides[1], v.data_ptr(), strides[2], o.data_ptr(), so, o2.data_ptr(), s2,
+         lse.data_ptr(), dout.data_ptr(), sg, *sizes, lam.data_ptr(), n, _ptr(kv_len), scale,
+         *(t.data_ptr() for t in outs), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    return tuple(outs)
 
 
 _NORMS = {None: 0, "rms": 1, "layer": 2}

@@ -483,6 +483,81 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
                                   nabla_stream_t stream);
 
 /*
+ * nabla_diff_attn_fwd -- differential attention: the difference of two softmax maps with a
+ * learned weight, of tokens to states of any length (their own, or an encoder's).  A head's
+ * D columns of q and k hold the two maps' queries and keys of d = D / 2 side by side (the
+ * heads 2i and 2i + 1 of a [B, S, 2h, d] tensor are head i of [B, S, h, D]).  For every batch
+ * b, query token s and head i, with key head j = i / (h / hk):
+ *   o_m[b, s, i, :] = sum_u softmax_u( scale * <q_m[b,s,i], k_m[b,u,j]> ) v[b, u, j, :],
+ *   o = o_1 - lam[i] o_2,   o2 = o_2,   u = 0 .. kv_len[b] - 1;
+ *   lse[((b*h + i)*2 + m)*Sq + s] = log2( sum_u 2^(scale * log2(e) * <q_m, k_m,u>) ).
+ * A batch with kv_len[b] = 0 gets o = o2 = 0 and lse = -INFINITY.  k and v from kv_len[b] on
+ * are padding: nothing they hold (NaN, infinities) reaches o, o2 or lse.
+ * bf16: the products run on the tcgen05 tensor cores with fp32 accumulators (P is rounded to
+ * bf16 before its product with v; o_1 and o_2 are subtracted in fp32 and o rounded once);
+ * f32: fp32 arithmetic on CUDA cores.  Repeated calls on the same inputs give the same bits.
+ *
+ *   q, k, v, their strides, D (64 or 128), the lengths, hk, kv_len: as for
+ *              nabla_cross_attn_fwd.
+ *   lam        [lam_n] device fp32, lam_n = h (a weight for each head) or 1; any values.
+ *   scale      softmax scale of both maps, finite (normally 1/sqrt(D / 2)).
+ *   o          [B, Sq, h, D] device, dense, element type dt, overwritten.
+ *   o2         likewise, or NULL: not wanted.  The backward needs it.
+ *   lse        [B, h, 2, Sq] device fp32, 4-byte aligned, overwritten; NULL: not wanted.
+ *   workspace  device scratch of ws_bytes >= nabla_diff_attn_fwd_workspace_bytes() (256-byte
+ *              aligned); not looked at where that is 0.  Calls that overlap on the GPU need a
+ *              workspace each.
+ * q, k, v, o and o2 are 16-byte aligned, lam and kv_len 4-byte; o, o2 and lse overlap no other
+ * argument.  nabla_diff_attn_fwd_workspace_bytes returns 0 for a shape that is not valid, too.
+ * Errors: NABLA_ERR_INVALID_ARG for anything else.
+ */
+size_t nabla_diff_attn_fwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                           int D);
+nabla_status nabla_diff_attn_fwd(const void *q, const nabla_strides *q_st, const void *k,
+                                 const nabla_strides *k_st, const void *v,
+                                 const nabla_strides *v_st, nabla_dtype dt, int B, int Sq, int Sk,
+                                 int h, int hk, int D, const float *lam, int lam_n,
+                                 const int32_t *kv_len, float scale, void *o, void *o2, float *lse,
+                                 void *workspace, size_t ws_bytes, nabla_stream_t stream);
+
+/*
+ * nabla_diff_attn_bwd -- gradients of nabla_diff_attn_fwd with respect to q, k, v and lam.
+ * With P_m the softmax weights (rebuilt from lse) and the upstream gradient dout:
+ *   delta_2 = <dout_s, o2_s>,   delta_1 = <dout_s, o_s> + lam delta_2,
+ *   dz_1 = P_1 (<dout_s, v_u> - delta_1),   dz_2 = -lam P_2 (<dout_s, v_u> - delta_2),
+ *   dq_m = scale sum_u dz_m k_m,u,   dk_m = scale sum_s dz_m q_m,s,
+ *   dv_u = sum_s (P_1 - lam P_2) dout_s,   dlam = - sum_s,u P_2 <dout_s, v_u>,
+ * the sums over s running over the tokens of all the heads that share the key head, those of
+ * dlam over a head's rows, or all heads' (lam_n = 1).  A batch without states gets dq = 0;
+ * states from kv_len[b] on get dk = dv = 0, whatever k and v hold there.  o and o2 must be the
+ * forward's.  bf16: the products run on tcgen05 with fp32 accumulators, P and dz enter them as
+ * bf16; f32: fp32 arithmetic on CUDA cores.  No atomics: repeated calls give the same bits.
+ *
+ *   q, k, v, lam, kv_len, scale  as given to nabla_diff_attn_fwd.
+ *   o, o2, dout [B, Sq, h, D] device, element type dt, strides o_st, o2_st and dout_st.
+ *   lse         [B, h, 2, Sq] device fp32, 4-byte aligned, from nabla_diff_attn_fwd.
+ *   dq          [B, Sq, h, D], dk and dv [B, Sk, hk, D] device, dense, element type dt,
+ *               overwritten.
+ *   dlam        [lam_n] device fp32, overwritten.  The outputs overlap no other argument.
+ *   workspace   device scratch of ws_bytes >= nabla_diff_attn_bwd_workspace_bytes()
+ *               (256-byte aligned); calls that overlap on the GPU need one each.
+ * o, o2, dout, dq, dk and dv are 16-byte aligned, dlam 4-byte.  Everything else, and the
+ * errors, as for nabla_diff_attn_fwd.
+ */
+size_t nabla_diff_attn_bwd_workspace_bytes(nabla_dtype dt, int B, int Sq, int Sk, int h, int hk,
+                                           int D);
+nabla_status nabla_diff_attn_bwd(const void *q, const nabla_strides *q_st, const void *k,
+                                 const nabla_strides *k_st, const void *v,
+                                 const nabla_strides *v_st, const void *o,
+                                 const nabla_strides *o_st, const void *o2,
+                                 const nabla_strides *o2_st, const float *lse, const void *dout,
+                                 const nabla_strides *dout_st, nabla_dtype dt, int B, int Sq,
+                                 int Sk, int h, int hk, int D, const float *lam, int lam_n,
+                                 const int32_t *kv_len, float scale, void *dq, void *dk, void *dv,
+                                 float *dlam, void *workspace, size_t ws_bytes,
+                                 nabla_stream_t stream);
+
+/*
  * nabla_block_norm -- what lies between two branches of a block: the sum of the residual x
  * and a branch's output u, normed, gated and scaled, and the adaptive norm that the next
  * branch reads, in one pass.  For every token (a row of C columns), with the rows gate,
