@@ -725,6 +725,9 @@ nabla_status nabla_block_norm(const void *x, const nabla_strides *x_st, const vo
   if (!c.apart_or_same(rs, rx) || !c.apart(rs, ru) || !c.apart(ry, rx) || !c.apart(ry, ru) ||
       !c.apart(ry, rs) || !c.clear_of_arrays(rs) || !c.clear_of_arrays(ry))
     return NABLA_ERR_INVALID_ARG;
+  cudaError_t e;
+  a.status = device_status_ptr(&e);
+  if (!a.status) return NABLA_ERR_CUDA;
   return from_cuda(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -794,6 +797,9 @@ nabla_status nabla_block_norm_bwd(
               ws_bytes < block_norm_bwd_workspace(a.shape)))
     return NABLA_ERR_INVALID_ARG;
   a.workspace = workspace;
+  cudaError_t e;
+  a.status = device_status_ptr(&e);
+  if (!a.status) return NABLA_ERR_CUDA;
   return from_cuda(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -12,26 +12,36 @@
 // modulation, those of dw and dpw over all.
 //
 // HBM-bound: x, u read and s, y written once (backward: s, u, dsum, dy read, dx, du
-// written).  A team of threads holds a row, 8 (or 16) columns a thread, and walks a run
-// of rows with the next row's loads under way; the modulations of its columns stay in
-// registers until the run comes to another row of them.  A team is a whole block, whose
-// warps exchange their sums once a norm, or, up to 256 columns, 8 to 32 lanes.  Variances
-// are summed about each warp's own mean and joined exactly, so a large mean costs nothing.
+// written).  Variances are summed about each warp's own mean and joined exactly, so a large
+// mean costs nothing.
 //
-// The gradient's sums over tokens: every team adds up its run's, a modulation row at a
-// time.  A row whose tokens all lie in the run is finished there, the others' parts (of
+// Forward: a warp holds a row (up to 8 vectors of 8 columns a lane; few columns: 8 or 16
+// lanes, many: two to eight warps), so its norms need no barrier, and an SM's 16 warps have
+// enough rows in flight without loading ahead.  The modulations of a block's rows lie in
+// shared memory as fp32, w (1 + scale), rs gate pw and shift, until the block comes to
+// another row of them; where such a row has fewer tokens than that is worth they are read
+// with every token.
+//
+// Backward: three sums a column stay in registers, so a team of threads holds a row, 8
+// columns a thread, a whole block above 256 columns.  Its rows come by bulk copies into a
+// ring in shared memory, several rows ahead, which takes no registers; the warps exchange
+// their sums once a norm.  Sums over tokens: every team adds up its run's, a modulation row
+// at a time.  A row whose tokens all lie in the run is finished there, the others' parts (of
 // the run's first and last row of modulations) go to the workspace and are added up in
 // order by a second kernel, as are the teams' sums for the weights.
 #include <cuda_bf16.h>
 
 #include "internal.h"
 #include "pdl.cuh"
+#include "tc_ptx.cuh"
 #include "vec8.cuh"
 
 namespace nabla {
 namespace {
 
-constexpr int kTeamBlock = 128;  // threads of a block of several teams
+constexpr int kTeamBlock = 128;  // backward: threads of a block of several teams
+constexpr int kFwdBlock = 256;   // forward
+constexpr int kMaxStages = 4;    // rows of the backward's ring
 
 struct Mod {  // a modulation: `rows` rows, `st` elements apart
   const void *p;
@@ -52,7 +62,9 @@ struct NormParams {
   long T, n;  // tokens; tokens that share a row of the modulations
   int S, C, L;  // tokens of a batch; columns; rows of a run
   int norm, post;  // 0: none, 1: RMS, 2: layer
+  int stages;      // backward: rows of the ring
   float rs, eps;
+  int *status;
 };
 
 __device__ __forceinline__ void load_vec(const void *p, nabla_dtype dt, int64_t at, bool on,
@@ -87,7 +99,7 @@ struct Box {
 };
 
 // A team: kTeam lanes of a warp, or (0) the whole block.
-template <int kTeam, int N>
+template <int kTeam, int N, int kBlock>
 struct Team {
   static constexpr int kLanes = kTeam ? kTeam : 32;
   long id;
@@ -101,7 +113,7 @@ struct Team {
     size = kTeam ? kTeam : (int)blockDim.x;
     warps = kTeam ? 1 : (int)blockDim.x >> 5;
     lane = kTeam ? (int)threadIdx.x % kLanes : (int)threadIdx.x;
-    id = kTeam ? (long)blockIdx.x * (kTeamBlock / kLanes) + (int)threadIdx.x / kLanes : blockIdx.x;
+    id = kTeam ? (long)blockIdx.x * (kBlock / kLanes) + (int)threadIdx.x / kLanes : blockIdx.x;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -129,8 +141,10 @@ struct Team {
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     __syncthreads();
     Sums r{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int i = 0; i < warps; ++i) r.mean = fmaf(b[i].mean, box->cols[i], r.mean);
     r.mean /= (float)C;
+#pragma unroll 4
     for (int i = 0; i < warps; ++i) {
       const Sums a = b[i];
       const float off = a.mean - r.mean;
@@ -221,92 +235,148 @@ __device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, lon
   }
 }
 
-template <typename T, int kTeam, int N>
-__global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
+// kShared: the modulations of a block's rows in shared memory, [up, by, add][C].
+template <typename T, int kTeam, int N, bool kShared>
+__global__ void __launch_bounds__(kFwdBlock, 2)
     block_norm_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
+  extern __shared__ __align__(16) float mods[];
   pdl_launch_dependents();
-  const Team<kTeam, N> tm(P.C, &box);
+  const Team<kTeam, N, kFwdBlock> tm(P.C, &box);
+  constexpr int kTeams = kTeam ? kFwdBlock / (kTeam ? kTeam : 1) : 1;
+  const uint32_t team = kTeam ? threadIdx.x / tm.kLanes : 0;
   pdl_wait();
-  const long first = tm.id * P.L, end = first + P.L < P.T ? first + P.L : P.T;
-  Place at{first / P.S, (int)(first % P.S)}, ahead = at;
+  const uint32_t first = blockIdx.x * (uint32_t)P.L;
+  const uint32_t end = first + P.L < P.T ? first + P.L : (uint32_t)P.T;
   const float inv = 1.f / (float)P.C;
-  float up[N][8], by[N][8], add[N][8];
-  long m = first / P.n, left = 0;  // left: tokens of row m of the modulations still to come
-  Raw<T> xr[N], ur[N];
-  auto load = [&](long row) {
-    fetch<T, N>(P.x, P.x_b, P.x_t, ahead, tm, row < end, xr);
-    if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, ahead, tm, row < end, ur);
-    ahead.next(P.S);
-  };
-  load(first);
   int turn = 0;
-#pragma unroll 1
-  for (long row = first; row < first + P.L; ++row, turn ^= 1) {
-    const bool live = row < end;
-    if (!kTeam && !live) break;  // teams in a warp stay together
-    if (left == 0 && live) {
-      if (row != first) ++m;
-      left = (m + 1) * P.n - row;
-      load_mods<N>(P, tm, m, up, by);
+  for (uint32_t g0 = first, g1; g0 < end; g0 = g1) {
+    g1 = end;
+    if (kShared) {  // the block's next row of the modulations
+      const uint32_t m = g0 / (uint32_t)P.n, last = (m + 1) * (uint32_t)P.n;
+      g1 = last < end ? last : end;
+      __syncthreads();  // the last one's are no longer read
+      for (int c = threadIdx.x * 8; c < P.C; c += blockDim.x * 8) {
+        float a[8], t[8];
+        load_vec(P.w, P.wdt, c, true, 1.f, a);
+        load_vec(P.scale.p, P.mdt, m * P.scale.st + c, true, 0.f, t);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        load_vec(P.shift.p, P.mdt, m * P.shift.st + tm.col[i], tm.on[i], 0.f, add[i]);
-    }
-    --left;
-    float s[N][8];
+        for (int j = 0; j < 8; ++j) a[j] *= 1.f + t[j];
+        store8(mods + c, a);
+        load_vec(P.pw, P.wdt, c, true, 1.f, a);
+        load_vec(P.gate.p, P.mdt, m * P.gate.st + c, true, 1.f, t);
 #pragma unroll
-    for (int i = 0; i < N; ++i) unpack8(xr[i], s[i]);
-    if (P.u) {
-      float v[N][8];
-#pragma unroll
-      for (int i = 0; i < N; ++i) unpack8(ur[i], v[i]);
-      load(row + 1);
-      float mean = 0.f, r = 1.f;
-      if (P.post) {
-        const Sums q = tm.join(tm.squares(v, P.post == 2), turn, 0, P.C);
-        mean = q.mean;
-        r = rsqrtf(fmaf(q.sq, inv, P.eps));
+        for (int j = 0; j < 8; ++j) a[j] *= P.rs * t[j];
+        store8(mods + P.C + c, a);
+        load_vec(P.shift.p, P.mdt, m * P.shift.st + c, true, 0.f, t);
+        store8(mods + 2 * P.C + c, t);
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (tm.on[i]) s[i][j] = fmaf((v[i][j] - mean) * r, by[i][j], s[i][j]);
-      if (live) put<T, N>(P.s, P.s_b, P.s_t, at, tm, s);
-    } else {
-      load(row + 1);
+      __syncthreads();
     }
-    if (P.norm) {
-      const Sums q = tm.join(tm.squares(s, P.norm == 2), turn, 1, P.C);
-      const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
+#pragma unroll 1
+    for (uint32_t r0 = g0; r0 < g1; r0 += kTeams, turn ^= 1) {
+      const uint32_t row = r0 + team;
+      const bool live = row < g1;
+      const Place at{(long)(row / (uint32_t)P.S), (int)(row % (uint32_t)P.S)};
+      const uint32_t m = kShared || !live ? 0 : row / (uint32_t)P.n;
+      Raw<T> xr[N], ur[N];
+      fetch<T, N>(P.x, P.x_b, P.x_t, at, tm, live, xr);
+      if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, at, tm, live, ur);
+      // eight columns of up, by or add
+      auto mod = [&](int which, int i, float (&v)[8]) {
+        if (kShared) {
+          if (tm.on[i]) load8(mods + which * P.C + tm.col[i], v);
+          return;
+        }
+        const bool on = live && tm.on[i];
+        float t[8];
+        if (which == 2) {
+          load_vec(P.shift.p, P.mdt, m * P.shift.st + tm.col[i], on, 0.f, v);
+          return;
+        }
+        const Mod &f = which ? P.gate : P.scale;
+        load_vec(which ? P.pw : P.w, P.wdt, tm.col[i], on, 1.f, v);
+        load_vec(f.p, P.mdt, m * f.st + tm.col[i], on, which ? 1.f : 0.f, t);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+        for (int j = 0; j < 8; ++j) v[j] *= which ? P.rs * t[j] : 1.f + t[j];
+      };
+      float s[N][8];
+      if (P.u) {
+        float mean = 0.f, r = 1.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          s[i][j] = fmaf((s[i][j] - q.mean) * r, up[i][j], add[i][j]);
-      if (live) put<T, N>(P.y, P.y_b, P.y_t, at, tm, s);
+        for (int i = 0; i < N; ++i) unpack8(ur[i], s[i]);
+        if (P.post) {
+          const Sums q = tm.join(tm.squares(s, P.post == 2), turn, 0, P.C);
+          mean = q.mean;
+          r = rsqrtf(fmaf(q.sq, inv, P.eps));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float x[8], by[8];
+          unpack8(xr[i], x);
+          mod(1, i, by);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            s[i][j] = tm.on[i] ? fmaf((s[i][j] - mean) * r, by[j], x[j]) : 0.f;
+        }
+        if (live) put<T, N>(P.s, P.s_b, P.s_t, at, tm, s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) unpack8(xr[i], s[i]);
+      }
+      if (P.norm) {
+        const Sums q = tm.join(tm.squares(s, P.norm == 2), turn, 1, P.C);
+        const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
+        T *y = static_cast<T *>(P.y) + at.b * P.y_b + at.s * P.y_t;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          float up[8], add[8];
+          mod(0, i, up);
+          mod(2, i, add);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) add[j] = fmaf((s[i][j] - q.mean) * r, up[j], add[j]);
+          if (live && tm.on[i]) store8(y + tm.col[i], add);
+        }
+      }
     }
-    at.next(P.S);
   }
 }
 
-// The gradient; dynamic shared memory (where a weight's is wanted): the teams' dw and dpw,
-// [teams of the block][2][C], every column of them one thread's own.
+// What a block of the backward waits with: the rows that have arrived.
+struct Ring {
+  uint64_t full[kMaxStages];
+  int abort;
+};
+
+// The gradient.  Dynamic shared memory: where a weight's is wanted the teams' dw and dpw,
+// [teams of the block][2][C], every column of them one thread's own; then (a team that is a
+// block) the ring, [stages][s, dy, dsum, u: those there are][C].
 template <typename T, int kTeam, int N>
 __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
     block_norm_bwd_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
+  __shared__ Ring ring;
   extern __shared__ __align__(16) float wsum[];
   pdl_launch_dependents();
-  const Team<kTeam, N> tm(P.C, &box);
+  const Team<kTeam, N, kTeamBlock> tm(P.C, &box);
   float *own = wsum + (kTeam ? (int)threadIdx.x / tm.kLanes : 0) * 2 * P.C;
+  uint8_t *rows = reinterpret_cast<uint8_t *>(wsum + (P.wpart ? 2 * P.C : 0));
+  const uint32_t bytes = P.C * sizeof(T);
+  const int tensors = (P.norm ? 2 : 0) + (P.dsum ? 1 : 0) + (P.u ? 1 : 0);
   if (P.wpart)
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (tm.on[i])
 #pragma unroll
         for (int j = 0; j < 8; ++j) own[tm.col[i] + j] = own[P.C + tm.col[i] + j] = 0.f;
+  if (!kTeam) {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < P.stages; ++i) tc::mbar_init(&ring.full[i], 1);
+      ring.abort = 0;
+      tc::fence_barrier_init();
+    }
+    __syncthreads();
+  }
   pdl_wait();
   const long first = tm.id * P.L, end = first + P.L < P.T ? first + P.L : P.T;
   Place at{first / P.S, (int)(first % P.S)}, ahead = at;
@@ -314,15 +384,54 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
   float up[N][8], by[N][8], acc[3][N][8];
   long m = first / P.n, left = 0;
   Raw<T> sr[N], ur[N], gr[N], yr[N];
+  // A team that is a block: thread 0 asks for `row`, the next one to be loaded.
+  int ask = 0, stage = 0;
+  uint32_t phase = 0;
+  auto request = [&](long row) {
+    if (row >= end) return;
+    tc::mbar_expect_tx(&ring.full[ask], tensors * bytes);
+    uint8_t *to = rows + (size_t)ask * tensors * bytes;
+    auto copy = [&](const void *p, int64_t bst, int64_t tst) {
+      tc::bulk_load(to, static_cast<const T *>(p) + ahead.b * bst + ahead.s * tst, bytes,
+                    &ring.full[ask]);
+      to += bytes;
+    };
+    if (P.norm) {
+      copy(P.x, P.x_b, P.x_t);
+      copy(P.dy, P.dy_b, P.dy_t);
+    }
+    if (P.dsum) copy(P.dsum, P.ds_b, P.ds_t);
+    if (P.u) copy(P.u, P.u_b, P.u_t);
+    ahead.next(P.S);
+    if (++ask == P.stages) ask = 0;
+  };
+  // The next row into registers: from memory, or out of the ring.
   auto load = [&](long row) {
     const bool live = row < end;
-    if (P.norm) {
-      fetch<T, N>(P.x, P.x_b, P.x_t, ahead, tm, live, sr);
-      fetch<T, N>(P.dy, P.dy_b, P.dy_t, ahead, tm, live, yr);
+    if (kTeam) {
+      if (P.norm) {
+        fetch<T, N>(P.x, P.x_b, P.x_t, ahead, tm, live, sr);
+        fetch<T, N>(P.dy, P.dy_b, P.dy_t, ahead, tm, live, yr);
+      }
+      if (P.dsum) fetch<T, N>(P.dsum, P.ds_b, P.ds_t, ahead, tm, live, gr);
+      if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, ahead, tm, live, ur);
+      ahead.next(P.S);
+      return;
     }
-    if (P.dsum) fetch<T, N>(P.dsum, P.ds_b, P.ds_t, ahead, tm, live, gr);
-    if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, ahead, tm, live, ur);
-    ahead.next(P.S);
+    tc::mbar_wait_small(&ring.full[stage], phase, &ring.abort, P.status, kDevTimeout);
+    const T *from = reinterpret_cast<const T *>(rows + (size_t)stage * tensors * bytes);
+    auto take = [&](Raw<T> (&r)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = load_raw(from + tm.col[i], tm.on[i]);
+      from += P.C;
+    };
+    if (P.norm) {
+      take(sr);
+      take(yr);
+    }
+    if (P.dsum) take(gr);
+    if (P.u) take(ur);
+    if (++stage == P.stages) stage = 0, phase ^= 1u;
   };
   // the sums of row m of the modulations, whose tokens up to `upto` this run has seen
   auto finish = [&](long upto) {
@@ -365,12 +474,16 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       }
     }
   };
-  load(first);
+  if (kTeam)
+    load(first);
+  else if (threadIdx.x == 0)
+    for (int i = 0; i < P.stages; ++i) request(first + i);
   int turn = 0;
 #pragma unroll 1
   for (long row = first; row < first + P.L; ++row, turn ^= 1) {
     const bool live = row < end;
     if (!kTeam && !live) break;
+    if (!kTeam) load(row);
     if (left == 0 && live) {
       if (row != first) {
         finish(row);
@@ -398,7 +511,11 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       if (P.dsum) unpack8(gr[i], ds[i]);
       if (P.u) unpack8(ur[i], v[i]);
     }
-    load(row + 1);
+    if (kTeam) load(row + 1);
+    if (!kTeam && !P.norm) {  // with a norm, the warps meet there
+      __syncthreads();
+      if (threadIdx.x == 0) request(row + P.stages);
+    }
     if (P.norm) {
       float g[N][8];
 #pragma unroll
@@ -408,6 +525,8 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       Sums q = tm.squares(s, P.norm == 2);
       tm.products(g, s, q.mean, 1.f, q);
       q = tm.join(q, turn, 0, P.C);
+      // every warp has taken the row out of the ring
+      if (!kTeam && threadIdx.x == 0) request(row + P.stages);
       const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
       const float mg = P.norm == 2 ? q.d * inv : 0.f, mgn = q.dt * r * inv;
 #pragma unroll
@@ -532,27 +651,36 @@ __global__ void __launch_bounds__(1024)
 struct Form {
   int team, vecs, threads;
 };
-Form form_of(int C) {
+Form bwd_form(int C) {
   if (C <= 64) return {8, 1, kTeamBlock};
   if (C <= 128) return {16, 1, kTeamBlock};
   if (C <= 256) return {32, 1, kTeamBlock};
   if (C <= 4096) return {0, 1, (C + 255) / 256 * 32};
   return {0, 2, (C + 511) / 512 * 32};
 }
+// bf16: up to 8 vectors a lane, fp32 (twice the registers): 4.
+Form fwd_form(int C, nabla_dtype dt) {
+  if (C <= 64) return {8, 1, kFwdBlock};
+  if (C <= 128) return {16, 1, kFwdBlock};
+  const int most = dt == NABLA_BF16 ? 8 : 4, warps = (C + most * 256 - 1) / (most * 256);
+  int vecs = (C + warps * 256 - 1) / (warps * 256);
+  if (vecs > 1) vecs = (vecs + 1) / 2 * 2;  // 1, 2, 4, 6, 8
+  return {warps == 1 ? 32 : 0, vecs, warps == 1 ? kFwdBlock : warps * 32};
+}
 
-// Teams and rows of a run.  Sized for GB300's 152 SMs, so that the workspace depends on the
-// shape alone.
+// Teams and rows of a run of the backward.  Sized for GB300's 152 SMs, so that the workspace
+// depends on the shape alone: 512 threads an SM.
 struct Runs {
   long teams;
   int L;
 };
-Runs runs_of(const NormShape &s, bool bwd) {
-  const Form f = form_of(s.C);
+Runs bwd_runs(const NormShape &s) {
+  const Form f = bwd_form(s.C);
   const long T = (long)s.B * s.S;
   const int per = f.team ? f.threads / f.team : 1;  // teams of a block
-  const long most = 152L * ((bwd ? 512 : 1024) / f.threads) * per;
+  const long most = 152L * (512 / f.threads) * per;
   long L = (T + most - 1) / most;
-  if (bwd && L < 4) L = 4;  // shorter ones would have more partial sums than rows
+  if (L < 4) L = 4;  // shorter ones would have more partial sums than rows
   return {(T + L - 1) / L, (int)L};
 }
 
@@ -562,7 +690,7 @@ struct NormLayout {
   size_t part, wpart, total;
 };
 NormLayout norm_layout(const NormShape &s) {
-  const Runs r = runs_of(s, true);
+  const Runs r = bwd_runs(s);
   NormLayout w;
   w.part = 0;
   w.wpart = round_up((size_t)r.teams * 6 * s.C * sizeof(float));
@@ -570,13 +698,40 @@ NormLayout norm_layout(const NormShape &s) {
   return w;
 }
 
+// Tokens of a row of the modulations from which on it is worth laying out in shared memory.
+constexpr int kSharedFrom = 16;
+
 template <typename T, int kTeam, int N>
-cudaError_t launch_typed(const NormParams &p, const Form &f, long teams, bool bwd,
-                         cudaStream_t st) {
+cudaError_t launch_fwd(NormParams p, const Form &f, cudaStream_t st) {
+  const bool shared = p.n >= kSharedFrom;
+  const size_t smem = shared ? (size_t)3 * p.C * sizeof(float) : 0;
+  // 16 warps an SM, if shared memory holds their blocks' modulations
+  int per_sm = 512 / f.threads;
+  while (per_sm > 1 && per_sm * smem > 200 * 1024) --per_sm;
+  const long most = 152L * per_sm;
+  p.L = (int)((p.T + most - 1) / most);
+  const dim3 grid((unsigned)((p.T + p.L - 1) / p.L)), block(f.threads);
+  auto kern = shared ? block_norm_kernel<T, kTeam, N, true> : block_norm_kernel<T, kTeam, N, false>;
+  if (smem > 40000) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, grid, block, smem, st, p);
+}
+
+template <typename T, int kTeam, int N>
+cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st) {
   const int per = kTeam ? f.threads / (kTeam ? kTeam : 1) : 1;
   const dim3 grid((unsigned)((teams + per - 1) / per)), block(f.threads);
-  if (!bwd) return launch_pdl(block_norm_kernel<T, kTeam, N>, grid, block, 0, st, p);
-  const size_t smem = p.wpart ? (size_t)per * 2 * p.C * sizeof(float) : 0;
+  size_t smem = p.wpart ? (size_t)per * 2 * p.C * sizeof(float) : 0;
+  if (!kTeam) {  // as many rows as fit the SM's share of shared memory
+    const size_t row = ((p.norm ? 2 : 0) + (p.dsum ? 1 : 0) + (p.u ? 1 : 0)) * p.C * sizeof(T);
+    const size_t room = (size_t)220 * 1024 / (512 / f.threads) - 2048;
+    p.stages = smem + row < room ? (int)((room - smem) / row) : 1;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    smem += p.stages * row;
+  }
   auto kern = block_norm_bwd_kernel<T, kTeam, N>;
   if (smem > 40000) {
     const cudaError_t e =
@@ -587,15 +742,31 @@ cudaError_t launch_typed(const NormParams &p, const Form &f, long teams, bool bw
 }
 
 template <typename T>
-cudaError_t launch_form(const NormParams &p, const Form &f, long teams, bool bwd,
-                        cudaStream_t st) {
-  switch (f.team) {
-    case 8: return launch_typed<T, 8, 1>(p, f, teams, bwd, st);
-    case 16: return launch_typed<T, 16, 1>(p, f, teams, bwd, st);
-    case 32: return launch_typed<T, 32, 1>(p, f, teams, bwd, st);
+cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st) {
+  if (f.team == 8) return launch_fwd<T, 8, 1>(p, f, st);
+  if (f.team == 16) return launch_fwd<T, 16, 1>(p, f, st);
+  const bool warp = f.team == 32;
+  switch (f.vecs) {
+    case 1: return launch_fwd<T, 32, 1>(p, f, st);
+    case 2: return launch_fwd<T, 32, 2>(p, f, st);
+    case 4: return warp ? launch_fwd<T, 32, 4>(p, f, st) : launch_fwd<T, 0, 4>(p, f, st);
   }
-  return f.vecs == 1 ? launch_typed<T, 0, 1>(p, f, teams, bwd, st)
-                     : launch_typed<T, 0, 2>(p, f, teams, bwd, st);
+  if constexpr (sizeof(T) == 2) {
+    if (f.vecs == 6) return warp ? launch_fwd<T, 32, 6>(p, f, st) : launch_fwd<T, 0, 6>(p, f, st);
+    return warp ? launch_fwd<T, 32, 8>(p, f, st) : launch_fwd<T, 0, 8>(p, f, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t launch_bwd_form(const NormParams &p, const Form &f, long teams, cudaStream_t st) {
+  switch (f.team) {
+    case 8: return launch_bwd<T, 8, 1>(p, f, teams, st);
+    case 16: return launch_bwd<T, 16, 1>(p, f, teams, st);
+    case 32: return launch_bwd<T, 32, 1>(p, f, teams, st);
+  }
+  return f.vecs == 1 ? launch_bwd<T, 0, 1>(p, f, teams, st)
+                     : launch_bwd<T, 0, 2>(p, f, teams, st);
 }
 
 }  // namespace
@@ -621,17 +792,20 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
   p.S = a.shape.S, p.C = a.shape.C;
   p.norm = a.norm, p.post = a.post;
   p.rs = a.rs, p.eps = a.eps;
-  const Form f = form_of(p.C);
-  const Runs r = runs_of(a.shape, a.bwd);
+  p.status = a.status;
+  if (!a.bwd)
+    return a.dt == NABLA_BF16 ? launch_fwd_form<__nv_bfloat16>(p, fwd_form(p.C, a.dt), st)
+                              : launch_fwd_form<float>(p, fwd_form(p.C, a.dt), st);
+  const Form f = bwd_form(p.C);
+  const Runs r = bwd_runs(a.shape);
   p.L = r.L;
-  if (a.bwd) {
-    const NormLayout w = norm_layout(a.shape);
-    char *ws = static_cast<char *>(a.workspace);
-    if (p.dgate || p.dscale || p.dshift) p.part = reinterpret_cast<float *>(ws + w.part);
-    if (a.dw || a.dpw) p.wpart = reinterpret_cast<float *>(ws + w.wpart);
-  }
-  cudaError_t e = a.dt == NABLA_BF16 ? launch_form<__nv_bfloat16>(p, f, r.teams, a.bwd, st)
-                                     : launch_form<float>(p, f, r.teams, a.bwd, st);
+  const NormLayout w = norm_layout(a.shape);
+  char *ws = static_cast<char *>(a.workspace);
+  if (p.dgate || p.dscale || p.dshift) p.part = reinterpret_cast<float *>(ws + w.part);
+  if (a.dw || a.dpw) p.wpart = reinterpret_cast<float *>(ws + w.wpart);
+  const cudaError_t e = a.dt == NABLA_BF16
+                            ? launch_bwd_form<__nv_bfloat16>(p, f, r.teams, st)
+                            : launch_bwd_form<float>(p, f, r.teams, st);
   if (e != cudaSuccess || !(p.part || p.wpart)) return e;
   // rows of the modulations that may lie in several runs: all, or one a border
   const long ny = !p.part ? 0 : a.rows <= r.teams - 1 ? a.rows : r.teams - 1;

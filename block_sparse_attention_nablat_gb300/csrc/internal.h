@@ -214,6 +214,7 @@ struct NormArgs {
   float rs, eps;
   bool bwd;
   void *workspace;  // backward: block_norm_bwd_workspace()
+  int *status;
 };
 size_t block_norm_bwd_workspace(const NormShape &s);
 cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st);
