@@ -31,6 +31,7 @@
 // order by a second kernel, as are the teams' sums for the weights.
 #include <cuda_bf16.h>
 
+#include "attn_common.cuh"
 #include "internal.h"
 #include "pdl.cuh"
 #include "tc_ptx.cuh"
@@ -39,8 +40,16 @@
 namespace nabla {
 namespace {
 
+using tcattn::add2;
+using tcattn::f2;
+using tcattn::fma2;
+using tcattn::unf2;
+
 constexpr int kTeamBlock = 128;  // backward: threads of a block of several teams
-constexpr int kFwdBlock = 256;   // forward
+// Threads of a forward block: two blocks an SM leave a thread 128 registers, or 168 where a
+// lane holds eight vectors (with 128 it spills 350 bytes).
+template <int N>
+constexpr int kFwdBlock = N == 8 ? 192 : 256;
 constexpr int kMaxStages = 4;    // rows of the backward's ring
 
 struct Mod {  // a modulation: `rows` rows, `st` elements apart
@@ -84,6 +93,36 @@ __device__ __forceinline__ void store_vec(void *p, nabla_dtype dt, int64_t at,
     store8(static_cast<__nv_bfloat16 *>(p) + at, v);
   else
     store8(static_cast<float *>(p) + at, v);
+}
+
+// Eight columns as four fp32 pairs: the pair instructions halve the kernels' arithmetic,
+// which as single ones took longer than the rows' way in and out.
+using V8 = uint64_t[4];
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float a) { return f2(a, a); }
+__device__ __forceinline__ float total(uint64_t v) {
+  float a, b;
+  unf2(v, a, b);
+  return a + b;
+}
+__device__ __forceinline__ void pairs(const float (&f)[8], V8 &v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void singles(const V8 &v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unf2(v[i], f[2 * i], f[2 * i + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw<T> &r, V8 &v) {
+  float f[8];
+  unpack8(r, f);
+  pairs(f, v);
 }
 
 // The sums a row's norm needs: its mean (0 for the RMS norm), squares about it, and, of
@@ -140,54 +179,62 @@ struct Team {
     Sums *b = box->of[turn][which];
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     __syncthreads();
-    Sums r{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < warps; ++i) r.mean = fmaf(b[i].mean, box->cols[i], r.mean);
-    r.mean /= (float)C;
-#pragma unroll 4
-    for (int i = 0; i < warps; ++i) {
-      const Sums a = b[i];
-      const float off = a.mean - r.mean;
-      r.sq += fmaf(box->cols[i] * off, off, a.sq);
-      r.d += a.d;
-      r.dt += fmaf(off, a.d, a.dt);
-    }
+    // a lane per warp
+    const int l = threadIdx.x & 31;
+    const Sums a = l < warps ? b[l] : Sums{0.f, 0.f, 0.f, 0.f};
+    const float n = l < warps ? box->cols[l] : 0.f;
+    Sums r{join16(a.mean * n) / (float)C, 0.f, 0.f, 0.f};
+    const float off = a.mean - r.mean;
+    r.sq = join16(fmaf(n * off, off, a.sq));
+    r.d = join16(a.d);
+    r.dt = join16(fmaf(off, a.d, a.dt));
     return r;
   }
+  // The sum of the first 16 lanes' values, in all lanes.
+  static __device__ __forceinline__ float join16(float v) {
+#pragma unroll
+    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return __shfl_sync(0xffffffffu, v, 0);
+  }
 
-  // This warp's mean and squares about it (columns that do not exist hold 0).
-  __device__ __forceinline__ Sums squares(const float (&v)[N][8], bool layer) const {
+  // Takes this warp's mean (layer; else 0) off v, whose columns that do not exist stay 0,
+  // and returns it with the squares.
+  __device__ __forceinline__ Sums center(V8 (&v)[N], bool layer) const {
     Sums r{0.f, 0.f, 0.f, 0.f};
     if (layer) {
+      uint64_t t = 0ull;
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r.mean += v[i][j];
-      r.mean = sum(r.mean) / own;
+        for (int j = 0; j < 4; ++j) t = add2(t, v[i][j]);
+      r.mean = sum(total(t)) / own;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint64_t off = both(on[i] ? -r.mean : 0.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = add2(v[i][j], off);
+      }
     }
+    uint64_t t = 0ull;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (on[i])
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = v[i][j] - r.mean;
-          r.sq = fmaf(t, t, r.sq);
-        }
-    r.sq = sum(r.sq);
+      for (int j = 0; j < 4; ++j) t = fma2(v[i][j], v[i][j], t);
+    r.sq = sum(total(t));
     return r;
   }
-  // The sums of d and of d (t - mean) of this warp, t = (v - mean) mul.
-  __device__ __forceinline__ void products(const float (&d)[N][8], const float (&v)[N][8],
-                                           float mean, float mul, Sums &r) const {
+  // The sums of d and of d v of this warp, v centred.
+  __device__ __forceinline__ void products(const V8 (&d)[N], const V8 (&v)[N], Sums &r) const {
+    uint64_t a = 0ull, b = 0ull;
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r.d += d[i][j];
-        r.dt = fmaf(d[i][j] * mul, v[i][j] - mean, r.dt);
+      for (int j = 0; j < 4; ++j) {
+        a = add2(a, d[i][j]);
+        b = fma2(d[i][j], v[i][j], b);
       }
-    r.d = sum(r.d);
-    r.dt = sum(r.dt);
+    r.d = sum(total(a));
+    r.dt = sum(total(b));
   }
 };
 
@@ -210,40 +257,47 @@ __device__ __forceinline__ void fetch(const void *p, int64_t bst, int64_t tst, c
 }
 template <typename T, int N, class Tm>
 __device__ __forceinline__ void put(void *p, int64_t bst, int64_t tst, const Place &at,
-                                    const Tm &tm, const float (&v)[N][8]) {
+                                    const Tm &tm, const V8 (&v)[N]) {
   T *row = static_cast<T *>(p) + at.b * bst + at.s * tst;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (tm.on[i]) store8(row + tm.col[i], v[i]);
+    if (tm.on[i]) {
+      float f[8];
+      singles(v[i], f);
+      store8(row + tm.col[i], f);
+    }
 }
 
-// up = w (1 + scale) and by = rs gate pw of the team's columns in row `m` of the modulations.
+// up = w (1 + scale) and by = rs gate pw of the team's columns in row `m` of the modulations
+// (0 for columns that do not exist).
 template <int N, class Tm>
-__device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, long m,
-                                          float (&up)[N][8], float (&by)[N][8]) {
+__device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, long m, V8 (&up)[N],
+                                          V8 (&by)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float t[8];
-    load_vec(P.w, P.wdt, tm.col[i], tm.on[i], 1.f, up[i]);
+    float a[8], t[8];
+    load_vec(P.w, P.wdt, tm.col[i], tm.on[i], 1.f, a);
     load_vec(P.scale.p, P.mdt, m * P.scale.st + tm.col[i], tm.on[i], 0.f, t);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) up[i][j] *= 1.f + t[j];
-    load_vec(P.pw, P.wdt, tm.col[i], tm.on[i], 1.f, by[i]);
+    for (int j = 0; j < 8; ++j) a[j] *= 1.f + t[j];
+    pairs(a, up[i]);
+    load_vec(P.pw, P.wdt, tm.col[i], tm.on[i], 1.f, a);
     load_vec(P.gate.p, P.mdt, m * P.gate.st + tm.col[i], tm.on[i], 1.f, t);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) by[i][j] *= P.rs * t[j];
+    for (int j = 0; j < 8; ++j) a[j] *= tm.on[i] ? P.rs * t[j] : 0.f;
+    pairs(a, by[i]);
   }
 }
 
 // kShared: the modulations of a block's rows in shared memory, [up, by, add][C].
 template <typename T, int kTeam, int N, bool kShared>
-__global__ void __launch_bounds__(kFwdBlock, 2)
+__global__ void __launch_bounds__(kFwdBlock<N>, 2)
     block_norm_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   extern __shared__ __align__(16) float mods[];
   pdl_launch_dependents();
-  const Team<kTeam, N, kFwdBlock> tm(P.C, &box);
-  constexpr int kTeams = kTeam ? kFwdBlock / (kTeam ? kTeam : 1) : 1;
+  const Team<kTeam, N, kFwdBlock<N>> tm(P.C, &box);
+  constexpr int kTeams = kTeam ? kFwdBlock<N> / (kTeam ? kTeam : 1) : 1;
   const uint32_t team = kTeam ? threadIdx.x / tm.kLanes : 0;
   pdl_wait();
   const uint32_t first = blockIdx.x * (uint32_t)P.L;
@@ -283,60 +337,63 @@ __global__ void __launch_bounds__(kFwdBlock, 2)
       fetch<T, N>(P.x, P.x_b, P.x_t, at, tm, live, xr);
       if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, at, tm, live, ur);
       // eight columns of up, by or add
-      auto mod = [&](int which, int i, float (&v)[8]) {
+      auto mod = [&](int which, int i, V8 &v) {
+        float a[8], t[8];
         if (kShared) {
-          if (tm.on[i]) load8(mods + which * P.C + tm.col[i], v);
+          if (tm.on[i]) load8(mods + which * P.C + tm.col[i], a);
+          pairs(a, v);
           return;
         }
         const bool on = live && tm.on[i];
-        float t[8];
         if (which == 2) {
-          load_vec(P.shift.p, P.mdt, m * P.shift.st + tm.col[i], on, 0.f, v);
-          return;
-        }
-        const Mod &f = which ? P.gate : P.scale;
-        load_vec(which ? P.pw : P.w, P.wdt, tm.col[i], on, 1.f, v);
-        load_vec(f.p, P.mdt, m * f.st + tm.col[i], on, which ? 1.f : 0.f, t);
+          load_vec(P.shift.p, P.mdt, m * P.shift.st + tm.col[i], on, 0.f, a);
+        } else {
+          const Mod &f = which ? P.gate : P.scale;
+          load_vec(which ? P.pw : P.w, P.wdt, tm.col[i], on, 1.f, a);
+          load_vec(f.p, P.mdt, m * f.st + tm.col[i], on, which ? 1.f : 0.f, t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= which ? P.rs * t[j] : 1.f + t[j];
+          for (int j = 0; j < 8; ++j) a[j] *= which ? P.rs * t[j] : 1.f + t[j];
+        }
+        pairs(a, v);
       };
-      float s[N][8];
+      V8 s[N];
       if (P.u) {
-        float mean = 0.f, r = 1.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) unpack8(ur[i], s[i]);
+        for (int i = 0; i < N; ++i) unpack(ur[i], s[i]);
+        float off = 0.f, r = 1.f;  // the normed row: r s + off
         if (P.post) {
-          const Sums q = tm.join(tm.squares(s, P.post == 2), turn, 0, P.C);
-          mean = q.mean;
+          const Sums w = tm.center(s, P.post == 2), q = tm.join(w, turn, 0, P.C);
           r = rsqrtf(fmaf(q.sq, inv, P.eps));
+          off = (w.mean - q.mean) * r;
         }
+        const uint64_t r2 = both(r), off2 = both(off);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          float x[8], by[8];
-          unpack8(xr[i], x);
+          V8 x, by;
+          unpack(xr[i], x);
           mod(1, i, by);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            s[i][j] = tm.on[i] ? fmaf((s[i][j] - mean) * r, by[j], x[j]) : 0.f;
+          for (int j = 0; j < 4; ++j)
+            s[i][j] = tm.on[i] ? fma2(fma2(s[i][j], r2, off2), by[j], x[j]) : 0ull;
         }
         if (live) put<T, N>(P.s, P.s_b, P.s_t, at, tm, s);
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) unpack8(xr[i], s[i]);
+        for (int i = 0; i < N; ++i) unpack(xr[i], s[i]);
       }
       if (P.norm) {
-        const Sums q = tm.join(tm.squares(s, P.norm == 2), turn, 1, P.C);
+        const Sums w = tm.center(s, P.norm == 2), q = tm.join(w, turn, 1, P.C);
         const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
-        T *y = static_cast<T *>(P.y) + at.b * P.y_b + at.s * P.y_t;
+        const uint64_t r2 = both(r), off2 = both((w.mean - q.mean) * r);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          float up[8], add[8];
+          V8 up, add;
           mod(0, i, up);
           mod(2, i, add);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) add[j] = fmaf((s[i][j] - q.mean) * r, up[j], add[j]);
-          if (live && tm.on[i]) store8(y + tm.col[i], add);
+          for (int j = 0; j < 4; ++j) s[i][j] = fma2(fma2(s[i][j], r2, off2), up[j], add[j]);
         }
+        if (live) put<T, N>(P.y, P.y_b, P.y_t, at, tm, s);
       }
     }
   }
@@ -350,9 +407,10 @@ struct Ring {
 
 // The gradient.  Dynamic shared memory: where a weight's is wanted the teams' dw and dpw,
 // [teams of the block][2][C], every column of them one thread's own; then (a team that is a
-// block) the ring, [stages][s, dy, dsum, u: those there are][C].
-template <typename T, int kTeam, int N>
-__global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
+// block) the ring, [stages][s, dy, dsum, u: those there are][C].  kMost: threads at most; kU: there is a
+// branch's output; kPost: it is normed.
+template <typename T, int kTeam, int N, int kMost, bool kU, bool kPost>
+__global__ void __launch_bounds__(kMost)
     block_norm_bwd_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   __shared__ Ring ring;
@@ -362,7 +420,7 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
   float *own = wsum + (kTeam ? (int)threadIdx.x / tm.kLanes : 0) * 2 * P.C;
   uint8_t *rows = reinterpret_cast<uint8_t *>(wsum + (P.wpart ? 2 * P.C : 0));
   const uint32_t bytes = P.C * sizeof(T);
-  const int tensors = (P.norm ? 2 : 0) + (P.dsum ? 1 : 0) + (P.u ? 1 : 0);
+  const int tensors = (P.norm ? 2 : 0) + (P.dsum ? 1 : 0) + (kU ? 1 : 0);
   if (P.wpart)
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -381,7 +439,7 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
   const long first = tm.id * P.L, end = first + P.L < P.T ? first + P.L : P.T;
   Place at{first / P.S, (int)(first % P.S)}, ahead = at;
   const float inv = 1.f / (float)P.C;
-  float up[N][8], by[N][8], acc[3][N][8];
+  V8 up[N], by[N], acc[3][N];
   long m = first / P.n, left = 0;
   Raw<T> sr[N], ur[N], gr[N], yr[N];
   // A team that is a block: thread 0 asks for `row`, the next one to be loaded.
@@ -401,7 +459,7 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       copy(P.dy, P.dy_b, P.dy_t);
     }
     if (P.dsum) copy(P.dsum, P.ds_b, P.ds_t);
-    if (P.u) copy(P.u, P.u_b, P.u_t);
+    if (kU) copy(P.u, P.u_b, P.u_t);
     ahead.next(P.S);
     if (++ask == P.stages) ask = 0;
   };
@@ -414,7 +472,7 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
         fetch<T, N>(P.dy, P.dy_b, P.dy_t, ahead, tm, live, yr);
       }
       if (P.dsum) fetch<T, N>(P.dsum, P.ds_b, P.ds_t, ahead, tm, live, gr);
-      if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, ahead, tm, live, ur);
+      if (kU) fetch<T, N>(P.u, P.u_b, P.u_t, ahead, tm, live, ur);
       ahead.next(P.S);
       return;
     }
@@ -430,7 +488,7 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       take(yr);
     }
     if (P.dsum) take(gr);
-    if (P.u) take(ur);
+    if (kU) take(ur);
     if (++stage == P.stages) stage = 0, phase ^= 1u;
   };
   // the sums of row m of the modulations, whose tokens up to `upto` this run has seen
@@ -442,34 +500,36 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
     for (int i = 0; i < N; ++i) {
       if (!tm.on[i]) continue;
       const int c = tm.col[i];
-      float t[8], w[8];
+      float t[8], w[8], a[3][8];
+#pragma unroll
+      for (int k = 0; k < 3; ++k) singles(acc[k][i], a[k]);
       if (P.wpart) {  // what the modulations contribute to the weights' gradients
         load_vec(P.scale.p, P.mdt, m * P.scale.st + c, true, 0.f, t);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) own[c + j] = fmaf(1.f + t[j], acc[0][i][j], own[c + j]);
+        for (int j = 0; j < 8; ++j) own[c + j] = fmaf(1.f + t[j], a[0][j], own[c + j]);
         load_vec(P.gate.p, P.mdt, m * P.gate.st + c, true, 1.f, t);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          own[P.C + c + j] = fmaf(P.rs * t[j], acc[2][i][j], own[P.C + c + j]);
+          own[P.C + c + j] = fmaf(P.rs * t[j], a[2][j], own[P.C + c + j]);
       }
       if (!P.part) continue;
       if (!whole) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k) store8(part + k * P.C + c, acc[k][i]);
+        for (int k = 0; k < 3; ++k) store8(part + k * P.C + c, a[k]);
         continue;
       }
       const int64_t o = m * P.C + c;
       if (P.dscale) {
         load_vec(P.w, P.wdt, c, true, 1.f, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = w[j] * acc[0][i][j];
+        for (int j = 0; j < 8; ++j) t[j] = w[j] * a[0][j];
         store_vec(P.dscale, P.mdt, o, t);
       }
-      if (P.dshift) store_vec(P.dshift, P.mdt, o, acc[1][i]);
+      if (P.dshift) store_vec(P.dshift, P.mdt, o, a[1]);
       if (P.dgate) {
         load_vec(P.pw, P.wdt, c, true, 1.f, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = P.rs * w[j] * acc[2][i][j];
+        for (int j = 0; j < 8; ++j) t[j] = P.rs * w[j] * a[2][j];
         store_vec(P.dgate, P.mdt, o, t);
       }
     }
@@ -496,20 +556,20 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[k][i][j] = 0.f;
+          for (int j = 0; j < 4; ++j) acc[k][i][j] = 0ull;
     }
     --left;
-    float s[N][8], ds[N][8], v[N][8], d[N][8];
+    V8 s[N], ds[N], v[N], d[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (P.norm) {
-        unpack8(sr[i], s[i]);
-        unpack8(yr[i], d[i]);
+        unpack(sr[i], s[i]);
+        unpack(yr[i], d[i]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ds[i][j] = 0.f;
-      if (P.dsum) unpack8(gr[i], ds[i]);
-      if (P.u) unpack8(ur[i], v[i]);
+      for (int j = 0; j < 4; ++j) ds[i][j] = 0ull;
+      if (P.dsum) unpack(gr[i], ds[i]);
+      if (kU) unpack(ur[i], v[i]);
     }
     if (kTeam) load(row + 1);
     if (!kTeam && !P.norm) {  // with a norm, the warps meet there
@@ -517,64 +577,68 @@ __global__ void __launch_bounds__(kTeam ? kTeamBlock : 512)
       if (threadIdx.x == 0) request(row + P.stages);
     }
     if (P.norm) {
-      float g[N][8];
+      V8 g[N];
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[i][j] = d[i][j] * up[i][j];
-      Sums q = tm.squares(s, P.norm == 2);
-      tm.products(g, s, q.mean, 1.f, q);
-      q = tm.join(q, turn, 0, P.C);
+        for (int j = 0; j < 4; ++j) g[i][j] = mul2(d[i][j], up[i][j]);
+      Sums w = tm.center(s, P.norm == 2);
+      tm.products(g, s, w);
+      const Sums q = tm.join(w, turn, 0, P.C);
       // every warp has taken the row out of the ring
       if (!kTeam && threadIdx.x == 0) request(row + P.stages);
       const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
-      const float mg = P.norm == 2 ? q.d * inv : 0.f, mgn = q.dt * r * inv;
+      const uint64_t r2 = both(r), off2 = both((w.mean - q.mean) * r);
+      const uint64_t mg = both(P.norm == 2 ? -r * q.d * inv : 0.f), mgn = both(-r * r * q.dt * inv);
 #pragma unroll
       for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float n = (s[i][j] - q.mean) * r;
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t n = fma2(s[i][j], r2, off2);
           if (live) {
-            acc[0][i][j] = fmaf(d[i][j], n, acc[0][i][j]);
-            acc[1][i][j] += d[i][j];
+            acc[0][i][j] = fma2(d[i][j], n, acc[0][i][j]);
+            acc[1][i][j] = add2(d[i][j], acc[1][i][j]);
           }
-          ds[i][j] = fmaf(r, g[i][j] - mg - n * mgn, ds[i][j]);
+          // dsum + (r g - r mean(g) - n r mean(g n))
+          ds[i][j] = add2(ds[i][j], fma2(n, mgn, fma2(g[i][j], r2, mg)));
         }
     }
     if (live && P.dx) put<T, N>(P.dx, P.dx_b, P.dx_t, at, tm, ds);
-    if (P.du || P.dgate || P.wpart) {
-      float mean = 0.f, r = 1.f, me = 0.f, men = 0.f;
-      if (P.post) {
-        float e[N][8];
+    if (kU) {
+      V8 e[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[i][j] = mul2(ds[i][j], by[i][j]);
+      if (kPost) {
+        Sums w = tm.center(v, P.post == 2);
+        tm.products(e, v, w);
+        const Sums q = tm.join(w, turn, 1, P.C);
+        const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
+        const uint64_t r2 = both(r), off2 = both((w.mean - q.mean) * r);
+        const uint64_t me = both(P.post == 2 ? -r * q.d * inv : 0.f);
+        const uint64_t men = both(-r * r * q.dt * inv);
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) e[i][j] = tm.on[i] ? ds[i][j] * by[i][j] : 0.f;
-        Sums q = tm.squares(v, P.post == 2);
-        tm.products(e, v, q.mean, 1.f, q);
-        q = tm.join(q, turn, 1, P.C);
-        mean = q.mean;
-        r = rsqrtf(fmaf(q.sq, inv, P.eps));
-        men = q.dt * r * inv;
-        if (P.post == 2) me = q.d * inv;
-      }
-      if (P.u) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float n = (v[i][j] - mean) * r;
-            if (live) acc[2][i][j] = fmaf(ds[i][j], n, acc[2][i][j]);
-            ds[i][j] *= by[i][j];
-            if (P.post) ds[i][j] = r * (ds[i][j] - me - n * men);
+          for (int j = 0; j < 4; ++j) {
+            v[i][j] = fma2(v[i][j], r2, off2);
+            e[i][j] = fma2(v[i][j], men, fma2(e[i][j], r2, me));
           }
-      } else {
+      }
+      if (live)
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ds[i][j] *= by[i][j];
-      }
-      if (live && P.du) put<T, N>(P.du, P.du_b, P.du_t, at, tm, ds);
+          for (int j = 0; j < 4; ++j) acc[2][i][j] = fma2(ds[i][j], v[i][j], acc[2][i][j]);
+      if (live && P.du) put<T, N>(P.du, P.du_b, P.du_t, at, tm, e);
+    } else if (live && P.du) {  // without the branch's output: du alone
+      V8 e[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[i][j] = mul2(ds[i][j], by[i][j]);
+      put<T, N>(P.du, P.du_b, P.du_t, at, tm, e);
     }
     at.next(P.S);
   }
@@ -660,12 +724,13 @@ Form bwd_form(int C) {
 }
 // bf16: up to 8 vectors a lane, fp32 (twice the registers): 4.
 Form fwd_form(int C, nabla_dtype dt) {
-  if (C <= 64) return {8, 1, kFwdBlock};
-  if (C <= 128) return {16, 1, kFwdBlock};
+  if (C <= 64) return {8, 1, kFwdBlock<1>};
+  if (C <= 128) return {16, 1, kFwdBlock<1>};
   const int most = dt == NABLA_BF16 ? 8 : 4, warps = (C + most * 256 - 1) / (most * 256);
   int vecs = (C + warps * 256 - 1) / (warps * 256);
   if (vecs > 1) vecs = (vecs + 1) / 2 * 2;  // 1, 2, 4, 6, 8
-  return {warps == 1 ? 32 : 0, vecs, warps == 1 ? kFwdBlock : warps * 32};
+  const int threads = vecs == 8 ? kFwdBlock<8> : kFwdBlock<1>;
+  return {warps == 1 ? 32 : 0, vecs, warps == 1 ? threads : warps * 32};
 }
 
 // Teams and rows of a run of the backward.  Sized for GB300's 152 SMs, so that the workspace
@@ -720,7 +785,7 @@ cudaError_t launch_fwd(NormParams p, const Form &f, cudaStream_t st) {
   return launch_pdl(kern, grid, block, smem, st, p);
 }
 
-template <typename T, int kTeam, int N>
+template <typename T, int kTeam, int N, int kMost>
 cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st) {
   const int per = kTeam ? f.threads / (kTeam ? kTeam : 1) : 1;
   const dim3 grid((unsigned)((teams + per - 1) / per)), block(f.threads);
@@ -732,7 +797,9 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     smem += p.stages * row;
   }
-  auto kern = block_norm_bwd_kernel<T, kTeam, N>;
+  auto kern = p.post ? block_norm_bwd_kernel<T, kTeam, N, kMost, true, true>
+              : p.u  ? block_norm_bwd_kernel<T, kTeam, N, kMost, true, false>
+                     : block_norm_bwd_kernel<T, kTeam, N, kMost, false, false>;
   if (smem > 40000) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -761,12 +828,14 @@ cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st)
 template <typename T>
 cudaError_t launch_bwd_form(const NormParams &p, const Form &f, long teams, cudaStream_t st) {
   switch (f.team) {
-    case 8: return launch_bwd<T, 8, 1>(p, f, teams, st);
-    case 16: return launch_bwd<T, 16, 1>(p, f, teams, st);
-    case 32: return launch_bwd<T, 32, 1>(p, f, teams, st);
+    case 8: return launch_bwd<T, 8, 1, kTeamBlock>(p, f, teams, st);
+    case 16: return launch_bwd<T, 16, 1, kTeamBlock>(p, f, teams, st);
+    case 32: return launch_bwd<T, 32, 1, kTeamBlock>(p, f, teams, st);
   }
-  return f.vecs == 1 ? launch_bwd<T, 0, 1>(p, f, teams, st)
-                     : launch_bwd<T, 0, 2>(p, f, teams, st);
+  if (f.vecs == 1) return launch_bwd<T, 0, 1, 512>(p, f, teams, st);
+  // two vectors a thread want more than the 128 registers that 512 threads have
+  return f.threads <= 384 ? launch_bwd<T, 0, 2, 384>(p, f, teams, st)
+                          : launch_bwd<T, 0, 2, 512>(p, f, teams, st);
 }
 
 }  // namespace

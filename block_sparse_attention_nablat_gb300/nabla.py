@@ -11,6 +11,7 @@ library is missing, every call raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -193,6 +194,19 @@ def _allocators(stream, device: torch.device):
         return t
 
     return outputs, scratch
+
+
+def _like(t: torch.Tensor, empty) -> torch.Tensor:
+    """A dense tensor of t's shape and type from `empty` (see _allocators)."""
+    if empty is torch.empty:  # a microsecond less of a small call
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(name: str, *shape) -> int:
+    """What the library's function `name` says of a shape, which alone it depends on."""
+    return getattr(load(), name)(*shape)
 
 
 def _dtype_code_of(dtype: torch.dtype) -> int:
@@ -788,12 +802,12 @@ def _diff_fwd(q, k, v, lam, kv_len, scale, o, o2, lse, whole, workspace, stream)
     if scale is None:
         scale = math.sqrt(2.0 / sizes[-1])
     if o is None:
-        o = empty(q.shape, dtype=q.dtype, device=dev)
+        o = _like(q, empty)
     else:
         _buf(o, "o", q.numel(), q.dtype, dev)
     if whole:
         if o2 is None:
-            o2 = empty(q.shape, dtype=q.dtype, device=dev)
+            o2 = _like(q, empty)
         else:
             _buf(o2, "o2", q.numel(), q.dtype, dev)
         if lse is None:
@@ -802,7 +816,7 @@ def _diff_fwd(q, k, v, lam, kv_len, scale, o, o2, lse, whole, workspace, stream)
             _buf(lse, "lse", 2 * q.numel() // sizes[-1], torch.float32, dev)
     lib = load()
     if workspace is None:
-        need = lib.nabla_diff_attn_fwd_workspace_bytes(*sizes)
+        need = _bytes("nabla_diff_attn_fwd_workspace_bytes", *sizes)
         if need:
             workspace = scratch(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
@@ -866,14 +880,14 @@ def nabla_diff_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: 
     outs = []
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, k), ("dlam", dlam, lam)):
         if t is None:
-            t = empty(like.shape, dtype=like.dtype, device=dev)
+            t = _like(like, empty)
         else:
             _buf(t, name, like.numel(), like.dtype, dev)
         outs.append(t)
     lib = load()
     if workspace is None:
-        need = lib.nabla_diff_attn_bwd_workspace_bytes(*sizes)
-        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = scratch(_bytes("nabla_diff_attn_bwd_workspace_bytes", *sizes) or 1,
+                            dtype=torch.uint8, device=dev)
     _on(workspace, "workspace", dev)
     _cuda(q)
     _run(dev, stream, lib.nabla_diff_attn_bwd, "nabla_diff_attn_bwd", q.data_ptr(), strides[0],
@@ -892,72 +906,86 @@ def _plane(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype,
     """_rows of a [B, S, C] tensor."""
     if t is None:
         return None
-    if t.dim() != 3 or t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    st = _rows(t.unsqueeze(2), name, (shape[0], shape[1], 1, shape[2]), dtype, device)
-    return st
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        if t.dim() != 3 or t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return _rows(t.unsqueeze(2), name, (shape[0], shape[1], 1, shape[2]), dtype, device)
+    return None
 
 
-def _mod(t: Optional[torch.Tensor], name: str, B: int, S: int, C: int,
+def _mod(t: torch.Tensor, name: str, B: int, S: int, C: int,
          device: torch.device) -> Tuple[int, int]:
     """Checks a modulation [C], [B, C] or [B, m, C] with m dividing S, which may be a view of
     a projection that holds several, and returns its number of rows and their distance."""
-    if t.dim() not in (1, 2, 3) or t.shape[-1] != C or (t.dim() > 1 and t.shape[0] != B) or (
-            t.dim() == 3 and (t.shape[1] < 1 or S % t.shape[1])):
+    shape = t.shape
+    k = len(shape)
+    if not 1 <= k <= 3 or shape[-1] != C or (k > 1 and shape[0] != B) or (
+            k == 3 and (shape[1] < 1 or S % shape[1])):
         raise ValueError(f"{name} must be [{C}], [{B}, {C}] or [{B}, m, {C}] with m dividing {S}, "
-                         f"got {list(t.shape)}")
+                         f"got {list(shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.stride(-1) != 1:
+    st = t.stride()
+    if st[-1] != 1:
         raise ValueError(f"the columns of {name} must lie together")
-    dims = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]
-    if len(dims) == 2 and dims[0][1] != dims[1][0] * dims[1][1]:
+    if k == 1:
+        return 1, C
+    if k == 2:
+        return B, st[0]
+    m = shape[1]
+    if B > 1 and m > 1 and st[0] != m * st[1]:
         raise ValueError(f"the rows of {name} must lie equally far apart (make it contiguous)")
-    return t.numel() // C, dims[-1][1] if dims else C
+    return B * m, st[1] if m > 1 else st[0]
+
+
+def _norm_weight(w: torch.Tensor, name: str, C: int, kind, device: torch.device) -> int:
+    _buf(w, name, C, w.dtype if kind is None else kind, device)
+    if w.numel() != C:
+        raise ValueError(f"{name} must be [{C}], got {list(w.shape)}")
+    return w.data_ptr()
 
 
 def _norm_args(like, u, gate, scale, shift, weight, post_weight, norm, post_norm, residual_scale,
                eps):
     """Checks what nabla_block_norm and its backward have in common; `like`: a [B, S, C]
-    tensor.  Returns the shape, the C arguments from dt to mdt (without shift), shift's two, the
-    rest, and the modulations' and weights' types."""
-    if like.dim() != 3:
+    tensor.  Returns the shape, the C arguments from dt to the scale, the shift's two, and the
+    rest to eps."""
+    shape = like.shape
+    if len(shape) != 3:
         raise ValueError("the tensors must be [B, S, C]")
-    for name, n in (("norm", norm), ("post_norm", post_norm)):
-        if n not in _NORMS:
-            raise ValueError(f"{name} must be None, 'rms' or 'layer', got {n!r}")
-    B, S, C = shape = tuple(like.shape)
+    if norm not in _NORMS or post_norm not in _NORMS:
+        name, n = ("norm", norm) if norm not in _NORMS else ("post_norm", post_norm)
+        raise ValueError(f"{name} must be None, 'rms' or 'layer', got {n!r}")
+    B, S, C = shape
     dev = like.device
-    kind, mkind, rows = None, None, 1
-    for name, w in (("weight", weight), ("post_weight", post_weight)):
-        if w is not None:
-            kind = w.dtype if kind is None else kind
-            _buf(w, name, C, kind, dev)
-            if w.numel() != C:
-                raise ValueError(f"{name} must be [{C}], got {list(w.shape)}")
+    kind = w = pw = None
+    if weight is not None:
+        w = _norm_weight(weight, "weight", C, None, dev)
+        kind = weight.dtype
+    if post_weight is not None:
+        pw = _norm_weight(post_weight, "post_weight", C, kind, dev)
+        kind = post_weight.dtype
     if norm is None and (weight is not None or scale is not None or shift is not None):
         raise ValueError("weight, scale and shift need a norm")
     if post_norm is None and post_weight is not None:
         raise ValueError("post_weight needs a post_norm")
     if u is None and (gate is not None or post_norm is not None):
         raise ValueError("gate and post_norm need u")
-    mods, first = [], None
+    rows, first, at = 1, None, []
     for name, m in (("gate", gate), ("scale", scale), ("shift", shift)):
         if m is None:
-            mods.append((None, 0))
+            at.append((None, 0))
             continue
-        n, step = _mod(m, name, B, S, C, dev)
-        if first is None:
-            first, rows, mkind = (name, m.shape), n, m.dtype
-        elif m.shape != first[1] or m.dtype != mkind:
-            raise ValueError(f"{name} must be {list(first[1])} {mkind} as {first[0]} is, got "
-                             f"{list(m.shape)} {m.dtype}")
-        mods.append((m.data_ptr(), step))
-    code = NABLA_F32 if kind is None else _dtype_code_of(kind)
-    mcode = NABLA_F32 if mkind is None else _dtype_code_of(mkind)
-    head = (_dtype_code(like), B, S, C, _NORMS[norm], _NORMS[post_norm], _ptr(weight),
-            _ptr(post_weight), code) + mods[0] + mods[1]
-    return shape, head, mods[2], (mcode, rows, residual_scale, eps), mkind, kind
+        if first is not None and (m.shape != first.shape or m.dtype != first.dtype):
+            raise ValueError(f"{name} must be {list(first.shape)} {first.dtype} as the other "
+                             f"modulations are, got {list(m.shape)} {m.dtype}")
+        first = m
+        rows, step = _mod(m, name, B, S, C, dev)
+        at.append((m.data_ptr(), step))
+    head = (_dtype_code(like), B, S, C, _NORMS[norm], _NORMS[post_norm], w, pw,
+            NABLA_F32 if kind is None else _dtype_code_of(kind), *at[0], *at[1])
+    return shape, head, at[2], (NABLA_F32 if first is None else _dtype_code(first), rows,
+                                residual_scale, eps)
 
 
 def nabla_block_norm(x: torch.Tensor, u: Optional[torch.Tensor] = None,
@@ -976,8 +1004,8 @@ def nabla_block_norm(x: torch.Tensor, u: Optional[torch.Tensor] = None,
     views of one projection if need be; weight and post_weight [C]; None: 1 (shift: 0).
     x_out may be x.  x, u and the outputs may be views whose columns lie together.
     Returns (s, y); s is x where u is None, y None where norm is."""
-    shape, head, sh, rest, _, _ = _norm_args(x, u, gate, scale, shift, weight, post_weight, norm,
-                                             post_norm, residual_scale, eps)
+    shape, head, sh, rest = _norm_args(x, u, gate, scale, shift, weight, post_weight, norm, post_norm,
+                                       residual_scale, eps)
     dev, dtype = x.device, x.dtype
     if u is None and norm is None:
         raise ValueError("neither u nor a norm: nothing to compute")
@@ -988,14 +1016,14 @@ def nabla_block_norm(x: torch.Tensor, u: Optional[torch.Tensor] = None,
         if x_out is not None:
             raise ValueError("x_out without u")
     elif x_out is None:
-        x_out = empty(shape, dtype=dtype, device=dev)
+        x_out = _like(x, empty)
     else:
         xo_st = _plane(x_out, "x_out", shape, dtype, dev)
     if norm is None:
         if y is not None:
             raise ValueError("y without a norm")
     elif y is None:
-        y = empty(shape, dtype=dtype, device=dev)
+        y = _like(x, empty)
     else:
         y_st = _plane(y, "y", shape, dtype, dev)
     _cuda(x)
@@ -1029,39 +1057,37 @@ def nabla_block_norm_bwd(s: Optional[torch.Tensor], u: Optional[torch.Tensor],
     like = dsum if s is None else s
     if like is None:
         raise ValueError("s and dy, or dsum, are needed")
-    shape, head, _, rest, mkind, wkind = _norm_args(like, u, gate, scale, shift, weight,
-                                                    post_weight, norm, post_norm, residual_scale,
-                                                    eps)
+    shape, head, _, rest = _norm_args(like, u, gate, scale, shift, weight, post_weight, norm,
+                                      post_norm, residual_scale, eps)
     if norm is not None and dy is None:
         raise ValueError("dy is needed with a norm")
     dev, dtype = like.device, like.dtype
-    strides = [_plane(t, name, shape, dtype, dev) for name, t in (("s", s), ("u", u),
-                                                                  ("dsum", dsum), ("dy", dy))]
+    s_st, u_st = _plane(s, "s", shape, dtype, dev), _plane(u, "u", shape, dtype, dev)
+    ds_st, dy_st = _plane(dsum, "dsum", shape, dtype, dev), _plane(dy, "dy", shape, dtype, dev)
     empty, scratch = _allocators(stream, dev)
     dx_st = du_st = None
     if dx is None:
-        dx = empty(shape, dtype=dtype, device=dev)
+        dx = _like(like, empty)
     else:
         dx_st = _plane(dx, "dx", shape, dtype, dev)
     if u is None:
         if du is not None:
             raise ValueError("du without u")
     elif du is None:
-        du = empty(shape, dtype=dtype, device=dev)
+        du = _like(like, empty)
     else:
         du_st = _plane(du, "du", shape, dtype, dev)
-    small = [None if t is None else empty(t.shape, dtype=t.dtype, device=dev)
+    small = [None if t is None else _like(t, empty)
              for t in (gate, scale, shift, weight, post_weight)]
-    lib = load()
     if workspace is None and any(t is not None for t in small):
-        need = lib.nabla_block_norm_bwd_workspace_bytes(*shape)
-        workspace = scratch(max(need, 1), dtype=torch.uint8, device=dev)
+        workspace = scratch(_bytes("nabla_block_norm_bwd_workspace_bytes", *shape) or 1,
+                            dtype=torch.uint8, device=dev)
     if workspace is not None:
         _on(workspace, "workspace", dev)
     _cuda(like)
-    pairs = [a for t, st in zip((s, u, dsum, dy), strides) for a in (_ptr(t), st)]
-    _run(dev, stream, lib.nabla_block_norm_bwd, "nabla_block_norm_bwd", *pairs, *head, *rest,
-         dx.data_ptr(), dx_st, _ptr(du), du_st, *(_ptr(t) for t in small), _ptr(workspace),
+    _run(dev, stream, load().nabla_block_norm_bwd, "nabla_block_norm_bwd", _ptr(s), s_st, _ptr(u),
+         u_st, _ptr(dsum), ds_st, _ptr(dy), dy_st, *head, *rest, dx.data_ptr(), dx_st, _ptr(du),
+         du_st, *map(_ptr, small), _ptr(workspace),
          0 if workspace is None else workspace.numel() * workspace.element_size())
     return (dx, du, *small)
 
