@@ -50,6 +50,9 @@ constexpr int kTeamBlock = 128;  // backward: threads of a block of several team
 // lane holds eight vectors (with 128 it spills 350 bytes).
 template <int N>
 constexpr int kFwdBlock = N == 8 ? 192 : 256;
+// Blocks of 256 threads on an SM: rows of few vectors need more of them under way.
+template <int N>
+constexpr int kFwdPerSm = N == 1 ? 4 : N == 2 ? 3 : 2;
 constexpr int kMaxStages = 4;    // rows of the backward's ring
 
 struct Mod {  // a modulation: `rows` rows, `st` elements apart
@@ -145,7 +148,7 @@ struct Team {
   int size, lane, warps;
   int col[N];
   bool on[N];  // the columns exist
-  float own;   // columns of this thread's warp, or of the team in it
+  float own, per;  // columns of this thread's warp, or of the team in it; 1 / own
   Box *box;
 
   __device__ __forceinline__ Team(int C, Box *b) : box(b) {
@@ -161,6 +164,7 @@ struct Team {
       n += __popc(__ballot_sync(0xffffffffu, on[i])) * 8;
     }
     own = kTeam ? (float)C : (float)n;
+    per = 1.f / own;
     if (warps > 1) {
       if ((threadIdx.x & 31) == 0) box->cols[threadIdx.x >> 5] = own;
       __syncthreads();
@@ -174,27 +178,29 @@ struct Team {
   }
 
   // The row's sums from its warps'.
-  __device__ __forceinline__ Sums join(const Sums &v, int turn, int which, int C) const {
+  __device__ __forceinline__ Sums join(const Sums &v, int turn, int which, float inv) const {
     if (kTeam || warps == 1) return v;
     Sums *b = box->of[turn][which];
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     __syncthreads();
-    // a lane per warp
-    const int l = threadIdx.x & 31;
+    // a lane per warp, in both halves of the warp
+    const int l = threadIdx.x & 15;
+    const bool hi = threadIdx.x & 16;
     const Sums a = l < warps ? b[l] : Sums{0.f, 0.f, 0.f, 0.f};
     const float n = l < warps ? box->cols[l] : 0.f;
-    Sums r{join16(a.mean * n) / (float)C, 0.f, 0.f, 0.f};
+    Sums r{sum16(a.mean * n) * inv, 0.f, 0.f, 0.f};
     const float off = a.mean - r.mean;
-    r.sq = join16(fmaf(n * off, off, a.sq));
-    r.d = join16(a.d);
-    r.dt = join16(fmaf(off, a.d, a.dt));
+    r.sq = sum16(fmaf(n * off, off, a.sq));
+    const float dd = sum16(hi ? fmaf(off, a.d, a.dt) : a.d);
+    r.d = __shfl_sync(0xffffffffu, dd, 0);
+    r.dt = __shfl_sync(0xffffffffu, dd, 16);
     return r;
   }
-  // The sum of the first 16 lanes' values, in all lanes.
-  static __device__ __forceinline__ float join16(float v) {
+  // The sum of 16 lanes' values, in all of them.
+  static __device__ __forceinline__ float sum16(float v) {
 #pragma unroll
     for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return __shfl_sync(0xffffffffu, v, 0);
+    return v;
   }
 
   // Takes this warp's mean (layer; else 0) off v, whose columns that do not exist stay 0,
@@ -207,7 +213,7 @@ struct Team {
       for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) t = add2(t, v[i][j]);
-      r.mean = sum(total(t)) / own;
+      r.mean = sum(total(t)) * per;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const uint64_t off = both(on[i] ? -r.mean : 0.f);
@@ -220,10 +226,14 @@ struct Team {
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) t = fma2(v[i][j], v[i][j], t);
-    r.sq = sum(total(t));
+    r.sq = total(t);
     return r;
   }
-  // The sums of d and of d v of this warp, v centred.
+  // This thread's squares (center()'s, of one row) as the warp's.
+  __device__ __forceinline__ void sum_squares(Sums &r) const { r.sq = sum(r.sq); }
+  // The sums of d and of d v of this warp, v centred, and of its squares.  Three sums a step
+  // would be 15 shuffles; here the halves of the warp first share out two pairs of values,
+  // then the quarters one.
   __device__ __forceinline__ void products(const V8 (&d)[N], const V8 (&v)[N], Sums &r) const {
     uint64_t a = 0ull, b = 0ull;
 #pragma unroll
@@ -233,8 +243,23 @@ struct Team {
         a = add2(a, d[i][j]);
         b = fma2(d[i][j], v[i][j], b);
       }
-    r.d = sum(total(a));
-    r.dt = sum(total(b));
+    r.d = total(a);
+    r.dt = total(b);
+    if (kLanes < 32) {
+      r.sq = sum(r.sq), r.d = sum(r.d), r.dt = sum(r.dt);
+      return;
+    }
+    const bool hi = threadIdx.x & 16, odd = threadIdx.x & 8;
+    // lanes 0-15: sq, d; lanes 16-31: dt (and nothing)
+    const float x = (hi ? r.dt : r.sq) + __shfl_xor_sync(0xffffffffu, hi ? r.sq : r.dt, 16);
+    const float y = (hi ? 0.f : r.d) + __shfl_xor_sync(0xffffffffu, hi ? r.d : 0.f, 16);
+    // lanes 0-7: sq, 8-15: d, 16-23: dt
+    float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    r.sq = __shfl_sync(0xffffffffu, z, 0);
+    r.d = __shfl_sync(0xffffffffu, z, 8);
+    r.dt = __shfl_sync(0xffffffffu, z, 16);
   }
 };
 
@@ -290,8 +315,9 @@ __device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, lon
 }
 
 // kShared: the modulations of a block's rows in shared memory, [up, by, add][C].
-template <typename T, int kTeam, int N, bool kShared>
-__global__ void __launch_bounds__(kFwdBlock<N>, 2)
+// kSpread: few rows; a block a row, with as many threads as that takes.
+template <typename T, int kTeam, int N, bool kShared, bool kSpread>
+__global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N>, kSpread ? 1 : kFwdPerSm<N>)
     block_norm_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   extern __shared__ __align__(16) float mods[];
@@ -362,7 +388,9 @@ __global__ void __launch_bounds__(kFwdBlock<N>, 2)
         for (int i = 0; i < N; ++i) unpack(ur[i], s[i]);
         float off = 0.f, r = 1.f;  // the normed row: r s + off
         if (P.post) {
-          const Sums w = tm.center(s, P.post == 2), q = tm.join(w, turn, 0, P.C);
+          Sums w = tm.center(s, P.post == 2);
+          tm.sum_squares(w);
+          const Sums q = tm.join(w, turn, 0, inv);
           r = rsqrtf(fmaf(q.sq, inv, P.eps));
           off = (w.mean - q.mean) * r;
         }
@@ -382,7 +410,9 @@ __global__ void __launch_bounds__(kFwdBlock<N>, 2)
         for (int i = 0; i < N; ++i) unpack(xr[i], s[i]);
       }
       if (P.norm) {
-        const Sums w = tm.center(s, P.norm == 2), q = tm.join(w, turn, 1, P.C);
+        Sums w = tm.center(s, P.norm == 2);
+        tm.sum_squares(w);
+        const Sums q = tm.join(w, turn, 1, inv);
         const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
         const uint64_t r2 = both(r), off2 = both((w.mean - q.mean) * r);
 #pragma unroll
@@ -407,7 +437,7 @@ struct Ring {
 
 // The gradient.  Dynamic shared memory: where a weight's is wanted the teams' dw and dpw,
 // [teams of the block][2][C], every column of them one thread's own; then (a team that is a
-// block) the ring, [stages][s, dy, dsum, u: those there are][C].  kMost: threads at most; kU: there is a
+// block) the ring, [stages][s, dy, dsum, u: those there are][columns of the team].  kMost: threads at most; kU: there is a
 // branch's output; kPost: it is normed.
 template <typename T, int kTeam, int N, int kMost, bool kU, bool kPost>
 __global__ void __launch_bounds__(kMost)
@@ -419,7 +449,8 @@ __global__ void __launch_bounds__(kMost)
   const Team<kTeam, N, kTeamBlock> tm(P.C, &box);
   float *own = wsum + (kTeam ? (int)threadIdx.x / tm.kLanes : 0) * 2 * P.C;
   uint8_t *rows = reinterpret_cast<uint8_t *>(wsum + (P.wpart ? 2 * P.C : 0));
-  const uint32_t bytes = P.C * sizeof(T);
+  // a row's copy, and its place: as many columns as the team's threads read, the last ones 0
+  const uint32_t bytes = P.C * sizeof(T), pitch = blockDim.x * 8 * N * sizeof(T);
   const int tensors = (P.norm ? 2 : 0) + (P.dsum ? 1 : 0) + (kU ? 1 : 0);
   if (P.wpart)
 #pragma unroll
@@ -428,6 +459,13 @@ __global__ void __launch_bounds__(kMost)
 #pragma unroll
         for (int j = 0; j < 8; ++j) own[tm.col[i] + j] = own[P.C + tm.col[i] + j] = 0.f;
   if (!kTeam) {
+    for (int x = 0; x < P.stages * tensors; ++x)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!tm.on[i]) {
+          const float none[8] = {};
+          store8(reinterpret_cast<T *>(rows + x * pitch) + tm.col[i], none);
+        }
     if (threadIdx.x == 0) {
       for (int i = 0; i < P.stages; ++i) tc::mbar_init(&ring.full[i], 1);
       ring.abort = 0;
@@ -448,11 +486,11 @@ __global__ void __launch_bounds__(kMost)
   auto request = [&](long row) {
     if (row >= end) return;
     tc::mbar_expect_tx(&ring.full[ask], tensors * bytes);
-    uint8_t *to = rows + (size_t)ask * tensors * bytes;
+    uint8_t *to = rows + ask * tensors * pitch;
     auto copy = [&](const void *p, int64_t bst, int64_t tst) {
       tc::bulk_load(to, static_cast<const T *>(p) + ahead.b * bst + ahead.s * tst, bytes,
                     &ring.full[ask]);
-      to += bytes;
+      to += pitch;
     };
     if (P.norm) {
       copy(P.x, P.x_b, P.x_t);
@@ -477,11 +515,11 @@ __global__ void __launch_bounds__(kMost)
       return;
     }
     tc::mbar_wait_small(&ring.full[stage], phase, &ring.abort, P.status, kDevTimeout);
-    const T *from = reinterpret_cast<const T *>(rows + (size_t)stage * tensors * bytes);
+    const T *from = reinterpret_cast<const T *>(rows + stage * tensors * pitch);
     auto take = [&](Raw<T> (&r)[N]) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = load_raw(from + tm.col[i], tm.on[i]);
-      from += P.C;
+      for (int i = 0; i < N; ++i) r[i] = load_raw(from + tm.col[i], true);
+      from += pitch / sizeof(T);
     };
     if (P.norm) {
       take(sr);
@@ -505,12 +543,17 @@ __global__ void __launch_bounds__(kMost)
       for (int k = 0; k < 3; ++k) singles(acc[k][i], a[k]);
       if (P.wpart) {  // what the modulations contribute to the weights' gradients
         load_vec(P.scale.p, P.mdt, m * P.scale.st + c, true, 0.f, t);
+        load8(own + c, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) own[c + j] = fmaf(1.f + t[j], a[0][j], own[c + j]);
-        load_vec(P.gate.p, P.mdt, m * P.gate.st + c, true, 1.f, t);
+        for (int j = 0; j < 8; ++j) w[j] = fmaf(1.f + t[j], a[0][j], w[j]);
+        store8(own + c, w);
+        if (kPost) {
+          load_vec(P.gate.p, P.mdt, m * P.gate.st + c, true, 1.f, t);
+          load8(own + P.C + c, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          own[P.C + c + j] = fmaf(P.rs * t[j], a[2][j], own[P.C + c + j]);
+          for (int j = 0; j < 8; ++j) w[j] = fmaf(P.rs * t[j], a[2][j], w[j]);
+          store8(own + P.C + c, w);
+        }
       }
       if (!P.part) continue;
       if (!whole) {
@@ -584,7 +627,7 @@ __global__ void __launch_bounds__(kMost)
         for (int j = 0; j < 4; ++j) g[i][j] = mul2(d[i][j], up[i][j]);
       Sums w = tm.center(s, P.norm == 2);
       tm.products(g, s, w);
-      const Sums q = tm.join(w, turn, 0, P.C);
+      const Sums q = tm.join(w, turn, 0, inv);
       // every warp has taken the row out of the ring
       if (!kTeam && threadIdx.x == 0) request(row + P.stages);
       const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
@@ -613,7 +656,7 @@ __global__ void __launch_bounds__(kMost)
       if (kPost) {
         Sums w = tm.center(v, P.post == 2);
         tm.products(e, v, w);
-        const Sums q = tm.join(w, turn, 1, P.C);
+        const Sums q = tm.join(w, turn, 1, inv);
         const float r = rsqrtf(fmaf(q.sq, inv, P.eps));
         const uint64_t r2 = both(r), off2 = both((w.mean - q.mean) * r);
         const uint64_t me = both(P.post == 2 ? -r * q.d * inv : 0.f);
@@ -660,12 +703,13 @@ __global__ void __launch_bounds__(kMost)
 
 // The sums that no run saw whole: blockIdx.y < ny: of a row of the modulations (there are
 // `rows`, and as many as ny of them can lie in more than one run); the last: of the
-// weights.  32 columns a block, 32 teams at a time.
+// weights.  32 columns a block, blockDim / 32 teams at a time.
 __global__ void __launch_bounds__(1024)
     block_norm_join_kernel(const __grid_constant__ NormParams P, int teams, int ny, long rows,
                            void *dw, void *dpw) {
   __shared__ float sums[3][32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
+  const int lanes = blockDim.x >> 5;  // 3 at least
   pdl_launch_dependents();
   pdl_wait();  // in every block, so that whoever waits for this kernel waits for the first
   const bool weights = (int)blockIdx.y == ny;
@@ -680,7 +724,7 @@ __global__ void __launch_bounds__(1024)
   if (!weights && t0 == t1) return;  // seen whole
   float a[3] = {0.f, 0.f, 0.f};
   if (c < P.C)
-    for (int t = t0 + ty; t <= t1; t += 32) {
+    for (int t = t0 + ty; t <= t1; t += lanes) {
       const float *p = weights ? P.wpart + (size_t)t * 2 * P.C
                                : P.part + ((size_t)t * 2 + ((long)t * P.L >= g0 ? 0 : 1)) * 3 * P.C;
       a[0] += p[c];
@@ -692,8 +736,7 @@ __global__ void __launch_bounds__(1024)
   __syncthreads();
   if (ty >= 3 || c >= P.C) return;  // a warp for each of the three
   float v = 0.f;
-#pragma unroll
-  for (int k = 0; k < 32; ++k) v += sums[ty][k][tx];
+  for (int k = 0; k < lanes; ++k) v += sums[ty][k][tx];
   void *o = weights ? (ty == 0 ? dw : ty == 1 ? dpw : nullptr)
                     : (ty == 0 ? P.dscale : ty == 1 ? P.dshift : P.dgate);
   if (!o) return;
@@ -734,18 +777,20 @@ Form fwd_form(int C, nabla_dtype dt) {
 }
 
 // Teams and rows of a run of the backward.  Sized for GB300's 152 SMs, so that the workspace
-// depends on the shape alone: 512 threads an SM.
+// depends on the shape alone: 512 threads an SM.  n: tokens of a row of the modulations.
 struct Runs {
   long teams;
   int L;
 };
-Runs bwd_runs(const NormShape &s) {
+Runs bwd_runs(const NormShape &s, long n) {
   const Form f = bwd_form(s.C);
   const long T = (long)s.B * s.S;
   const int per = f.team ? f.threads / f.team : 1;  // teams of a block
   const long most = 152L * (512 / f.threads) * per;
   long L = (T + most - 1) / most;
   if (L < 4) L = 4;  // shorter ones would have more partial sums than rows
+  // whole rows of the modulations where that changes little: nothing to join then
+  if (n * 4 <= L) L = (L + n - 1) / n * n;
   return {(T + L - 1) / L, (int)L};
 }
 
@@ -755,7 +800,7 @@ struct NormLayout {
   size_t part, wpart, total;
 };
 NormLayout norm_layout(const NormShape &s) {
-  const Runs r = bwd_runs(s);
+  const Runs r = bwd_runs(s, s.B * (long)s.S);  // the most runs
   NormLayout w;
   w.part = 0;
   w.wpart = round_up((size_t)r.teams * 6 * s.C * sizeof(float));
@@ -766,17 +811,18 @@ NormLayout norm_layout(const NormShape &s) {
 // Tokens of a row of the modulations from which on it is worth laying out in shared memory.
 constexpr int kSharedFrom = 16;
 
-template <typename T, int kTeam, int N>
+template <typename T, int kTeam, int N, bool kSpread = false>
 cudaError_t launch_fwd(NormParams p, const Form &f, cudaStream_t st) {
-  const bool shared = p.n >= kSharedFrom;
+  const bool shared = !kSpread && p.n >= kSharedFrom;
   const size_t smem = shared ? (size_t)3 * p.C * sizeof(float) : 0;
-  // 16 warps an SM, if shared memory holds their blocks' modulations
-  int per_sm = 512 / f.threads;
+  // as many warps an SM as their registers allow, if shared memory holds their modulations
+  int per_sm = kSpread ? 2048 / f.threads : kFwdPerSm<N> * kFwdBlock<N> / f.threads;
   while (per_sm > 1 && per_sm * smem > 200 * 1024) --per_sm;
   const long most = 152L * per_sm;
   p.L = (int)((p.T + most - 1) / most);
   const dim3 grid((unsigned)((p.T + p.L - 1) / p.L)), block(f.threads);
-  auto kern = shared ? block_norm_kernel<T, kTeam, N, true> : block_norm_kernel<T, kTeam, N, false>;
+  auto kern = shared ? block_norm_kernel<T, kTeam, N, !kSpread, kSpread>
+                     : block_norm_kernel<T, kTeam, N, false, kSpread>;
   if (smem > 40000) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -791,7 +837,8 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
   const dim3 grid((unsigned)((teams + per - 1) / per)), block(f.threads);
   size_t smem = p.wpart ? (size_t)per * 2 * p.C * sizeof(float) : 0;
   if (!kTeam) {  // as many rows as fit the SM's share of shared memory
-    const size_t row = ((p.norm ? 2 : 0) + (p.dsum ? 1 : 0) + (p.u ? 1 : 0)) * p.C * sizeof(T);
+    const size_t row =
+        ((p.norm ? 2 : 0) + (p.dsum ? 1 : 0) + (p.u ? 1 : 0)) * f.threads * 8 * N * sizeof(T);
     const size_t room = (size_t)220 * 1024 / (512 / f.threads) - 2048;
     p.stages = smem + row < room ? (int)((room - smem) / row) : 1;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
@@ -810,6 +857,12 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
 
 template <typename T>
 cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st) {
+  // Few rows: what counts is how long one takes.
+  if (p.C > 256 && p.T <= 304) {
+    const int vecs = p.C <= 4096 ? 1 : 2;
+    const Form g{0, vecs, (p.C + vecs * 256 - 1) / (vecs * 256) * 32};
+    return vecs == 1 ? launch_fwd<T, 0, 1, true>(p, g, st) : launch_fwd<T, 0, 2, true>(p, g, st);
+  }
   if (f.team == 8) return launch_fwd<T, 8, 1>(p, f, st);
   if (f.team == 16) return launch_fwd<T, 16, 1>(p, f, st);
   const bool warp = f.team == 32;
@@ -866,7 +919,7 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
     return a.dt == NABLA_BF16 ? launch_fwd_form<__nv_bfloat16>(p, fwd_form(p.C, a.dt), st)
                               : launch_fwd_form<float>(p, fwd_form(p.C, a.dt), st);
   const Form f = bwd_form(p.C);
-  const Runs r = bwd_runs(a.shape);
+  const Runs r = bwd_runs(a.shape, p.n);
   p.L = r.L;
   const NormLayout w = norm_layout(a.shape);
   char *ws = static_cast<char *>(a.workspace);
@@ -876,12 +929,20 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
                             ? launch_bwd_form<__nv_bfloat16>(p, f, r.teams, st)
                             : launch_bwd_form<float>(p, f, r.teams, st);
   if (e != cudaSuccess || !(p.part || p.wpart)) return e;
-  // rows of the modulations that may lie in several runs: all, or one a border
-  const long ny = !p.part ? 0 : a.rows <= r.teams - 1 ? a.rows : r.teams - 1;
+  // rows of the modulations that may lie in several runs: none, all, or one a border
+  long ny = !p.part || p.L % p.n == 0 ? 0 : a.rows <= r.teams - 1 ? a.rows : r.teams - 1;
+  const unsigned nx = (unsigned)((p.C + 31) / 32);
+  auto join = [&](unsigned y, unsigned threads, long borders) {
+    return launch_pdl(block_norm_join_kernel, dim3(nx, y), dim3(threads), 0, st, p, (int)r.teams,
+                      (int)borders, (long)a.rows, a.dw, a.dpw);
+  };
+  if (ny > 0 && p.n <= 4L * p.L) {  // a row of them lies in few runs: small blocks
+    const cudaError_t e2 = join((unsigned)ny, 128, ny);
+    if (e2 != cudaSuccess) return e2;
+    ny = 0;
+  }
   if (ny == 0 && !p.wpart) return e;
-  const dim3 grid((unsigned)((p.C + 31) / 32), (unsigned)(ny + (p.wpart ? 1 : 0)));
-  return launch_pdl(block_norm_join_kernel, grid, dim3(1024), 0, st, p, (int)r.teams, (int)ny,
-                    (long)a.rows, a.dw, a.dpw);
+  return join((unsigned)ny + (p.wpart ? 1 : 0), 1024, ny);
 }
 
 }  // namespace nabla
