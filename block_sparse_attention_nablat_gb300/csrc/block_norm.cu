@@ -47,9 +47,9 @@ using tcattn::unf2;
 
 constexpr int kTeamBlock = 128;  // backward: threads of a block of several teams
 // Threads of a forward block: two blocks an SM leave a thread 128 registers, or 168 where a
-// lane holds eight vectors (with 128 it spills 350 bytes).
-template <int N>
-constexpr int kFwdBlock = N == 8 ? 192 : 256;
+// lane holds eight vectors of both x and u (with 128 it spills 350 bytes).
+template <int N, bool kU>
+constexpr int kFwdBlock = N == 8 && kU ? 192 : 256;
 // Blocks of 256 threads on an SM: rows of few vectors need more of them under way.
 template <int N>
 constexpr int kFwdPerSm = N == 1 ? 4 : N == 2 ? 3 : 2;
@@ -316,14 +316,15 @@ __device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, lon
 
 // kShared: the modulations of a block's rows in shared memory, [up, by, add][C].
 // kSpread: few rows; a block a row, with as many threads as that takes.
-template <typename T, int kTeam, int N, bool kShared, bool kSpread>
-__global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N>, kSpread ? 1 : kFwdPerSm<N>)
+// kU: there is a branch's output.
+template <typename T, int kTeam, int N, bool kShared, bool kSpread, bool kU>
+__global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N, kU>, kSpread ? 1 : kFwdPerSm<N>)
     block_norm_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   extern __shared__ __align__(16) float mods[];
   pdl_launch_dependents();
-  const Team<kTeam, N, kFwdBlock<N>> tm(P.C, &box);
-  constexpr int kTeams = kTeam ? kFwdBlock<N> / (kTeam ? kTeam : 1) : 1;
+  const Team<kTeam, N, kFwdBlock<N, kU>> tm(P.C, &box);
+  constexpr int kTeams = kTeam ? kFwdBlock<N, kU> / (kTeam ? kTeam : 1) : 1;
   const uint32_t team = kTeam ? threadIdx.x / tm.kLanes : 0;
   pdl_wait();
   const uint32_t first = blockIdx.x * (uint32_t)P.L;
@@ -361,7 +362,7 @@ __global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N>, kSpread ? 1 : kF
       const uint32_t m = kShared || !live ? 0 : row / (uint32_t)P.n;
       Raw<T> xr[N], ur[N];
       fetch<T, N>(P.x, P.x_b, P.x_t, at, tm, live, xr);
-      if (P.u) fetch<T, N>(P.u, P.u_b, P.u_t, at, tm, live, ur);
+      if (kU) fetch<T, N>(P.u, P.u_b, P.u_t, at, tm, live, ur);
       // eight columns of up, by or add
       auto mod = [&](int which, int i, V8 &v) {
         float a[8], t[8];
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N>, kSpread ? 1 : kF
         pairs(a, v);
       };
       V8 s[N];
-      if (P.u) {
+      if (kU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) unpack(ur[i], s[i]);
         float off = 0.f, r = 1.f;  // the normed row: r s + off
@@ -766,13 +767,13 @@ Form bwd_form(int C) {
   return {0, 2, (C + 511) / 512 * 32};
 }
 // bf16: up to 8 vectors a lane, fp32 (twice the registers): 4.
-Form fwd_form(int C, nabla_dtype dt) {
-  if (C <= 64) return {8, 1, kFwdBlock<1>};
-  if (C <= 128) return {16, 1, kFwdBlock<1>};
+Form fwd_form(int C, nabla_dtype dt, bool u) {
+  if (C <= 64) return {8, 1, 256};
+  if (C <= 128) return {16, 1, 256};
   const int most = dt == NABLA_BF16 ? 8 : 4, warps = (C + most * 256 - 1) / (most * 256);
   int vecs = (C + warps * 256 - 1) / (warps * 256);
   if (vecs > 1) vecs = (vecs + 1) / 2 * 2;  // 1, 2, 4, 6, 8
-  const int threads = vecs == 8 ? kFwdBlock<8> : kFwdBlock<1>;
+  const int threads = vecs == 8 && u ? kFwdBlock<8, true> : 256;
   return {warps == 1 ? 32 : 0, vecs, warps == 1 ? threads : warps * 32};
 }
 
@@ -811,24 +812,30 @@ NormLayout norm_layout(const NormShape &s) {
 // Tokens of a row of the modulations from which on it is worth laying out in shared memory.
 constexpr int kSharedFrom = 16;
 
-template <typename T, int kTeam, int N, bool kSpread = false>
-cudaError_t launch_fwd(NormParams p, const Form &f, cudaStream_t st) {
+template <typename T, int kTeam, int N, bool kSpread, bool kU>
+cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
   const bool shared = !kSpread && p.n >= kSharedFrom;
   const size_t smem = shared ? (size_t)3 * p.C * sizeof(float) : 0;
   // as many warps an SM as their registers allow, if shared memory holds their modulations
-  int per_sm = kSpread ? 2048 / f.threads : kFwdPerSm<N> * kFwdBlock<N> / f.threads;
+  int per_sm = kSpread ? 2048 / f.threads : kFwdPerSm<N> * kFwdBlock<N, kU> / f.threads;
   while (per_sm > 1 && per_sm * smem > 200 * 1024) --per_sm;
   const long most = 152L * per_sm;
   p.L = (int)((p.T + most - 1) / most);
   const dim3 grid((unsigned)((p.T + p.L - 1) / p.L)), block(f.threads);
-  auto kern = shared ? block_norm_kernel<T, kTeam, N, !kSpread, kSpread>
-                     : block_norm_kernel<T, kTeam, N, false, kSpread>;
+  auto kern = shared ? block_norm_kernel<T, kTeam, N, !kSpread, kSpread, kU>
+                     : block_norm_kernel<T, kTeam, N, false, kSpread, kU>;
   if (smem > 40000) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, grid, block, smem, st, p);
+}
+
+template <typename T, int kTeam, int N, bool kSpread = false>
+cudaError_t launch_fwd(const NormParams &p, const Form &f, cudaStream_t st) {
+  return p.u ? launch_fwd_u<T, kTeam, N, kSpread, true>(p, f, st)
+             : launch_fwd_u<T, kTeam, N, kSpread, false>(p, f, st);
 }
 
 template <typename T, int kTeam, int N, int kMost>
@@ -916,8 +923,8 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
   p.rs = a.rs, p.eps = a.eps;
   p.status = a.status;
   if (!a.bwd)
-    return a.dt == NABLA_BF16 ? launch_fwd_form<__nv_bfloat16>(p, fwd_form(p.C, a.dt), st)
-                              : launch_fwd_form<float>(p, fwd_form(p.C, a.dt), st);
+    return a.dt == NABLA_BF16 ? launch_fwd_form<__nv_bfloat16>(p, fwd_form(p.C, a.dt, p.u), st)
+                              : launch_fwd_form<float>(p, fwd_form(p.C, a.dt, p.u), st);
   const Form f = bwd_form(p.C);
   const Runs r = bwd_runs(a.shape, p.n);
   p.L = r.L;
