@@ -314,7 +314,8 @@ __device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, lon
   }
 }
 
-// kShared: the modulations of a block's rows in shared memory, [up, by, add][C].
+// kShared: the modulations of a block's rows in shared memory, [up, by, add][C], halves of
+// every eight columns apart.
 // kSpread: few rows; a block a row, with as many threads as that takes.
 // kU: there is a branch's output.
 template <typename T, int kTeam, int N, bool kShared, bool kSpread, bool kU>
@@ -330,6 +331,13 @@ __global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N, kU>, kSpread ? 1 
   const uint32_t first = blockIdx.x * (uint32_t)P.L;
   const uint32_t end = first + P.L < P.T ? first + P.L : (uint32_t)P.T;
   const float inv = 1.f / (float)P.C;
+  // The first four of every eight columns, then the others: lanes 16 bytes apart, so that a
+  // warp's read meets every bank once.
+  auto put_mod = [&](int which, int c, const float (&v)[8]) {
+    float *to = mods + which * P.C + c / 2;
+    *reinterpret_cast<float4 *>(to) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4 *>(to + P.C / 2) = make_float4(v[4], v[5], v[6], v[7]);
+  };
   int turn = 0;
   for (uint32_t g0 = first, g1; g0 < end; g0 = g1) {
     g1 = end;
@@ -343,14 +351,14 @@ __global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N, kU>, kSpread ? 1 
         load_vec(P.scale.p, P.mdt, m * P.scale.st + c, true, 0.f, t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] *= 1.f + t[j];
-        store8(mods + c, a);
+        put_mod(0, c, a);
         load_vec(P.pw, P.wdt, c, true, 1.f, a);
         load_vec(P.gate.p, P.mdt, m * P.gate.st + c, true, 1.f, t);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] *= P.rs * t[j];
-        store8(mods + P.C + c, a);
+        put_mod(1, c, a);
         load_vec(P.shift.p, P.mdt, m * P.shift.st + c, true, 0.f, t);
-        store8(mods + 2 * P.C + c, t);
+        put_mod(2, c, t);
       }
       __syncthreads();
     }
@@ -367,8 +375,12 @@ __global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N, kU>, kSpread ? 1 
       auto mod = [&](int which, int i, V8 &v) {
         float a[8], t[8];
         if (kShared) {
-          if (tm.on[i]) load8(mods + which * P.C + tm.col[i], a);
-          pairs(a, v);
+          const float *from = mods + which * P.C + tm.col[i] / 2;
+          if (tm.on[i]) {
+            const ulonglong2 lo = *reinterpret_cast<const ulonglong2 *>(from);
+            const ulonglong2 hi = *reinterpret_cast<const ulonglong2 *>(from + P.C / 2);
+            v[0] = lo.x, v[1] = lo.y, v[2] = hi.x, v[3] = hi.y;
+          }
           return;
         }
         const bool on = live && tm.on[i];

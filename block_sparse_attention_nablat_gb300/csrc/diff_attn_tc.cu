@@ -5,7 +5,8 @@
 //
 //  * Work unit = 128 packed query rows (two 64-row subtiles, cross_common.cuh) of one
 //    (batch, key head), over the batch's state tiles or one of `nsplit` runs of them
-//    (diff_join joins the runs).  Persistent CTAs (one per SM).
+//    (diff_join joins the runs): those of the last round, which would leave SMs idle.
+//    Persistent CTAs (one per SM).
 //  * A step covers 64 states.  For each map m: S_m = Q_m K_m^T is one SS MMA (M = 128,
 //    N = 64, depth D / 2), O_m += P_m V a TS MMA with P_m (bf16) over the scores.  The maps
 //    share K's tile (each its half of the columns) and V's.
@@ -15,7 +16,9 @@
 //  * Each map has four softmax warps, thread = row: a row's maximum and sum never leave its
 //    thread, and the two maps' chains (S, softmax, P V) fill each other's gaps, as do the
 //    two buffers of a chain.
-//  * Softmax as in the cross attention (base 2, bias raised only by steps of more than 8).
+//  * Softmax in base 2 with the scale folded in.  The running maximum is only the exponents'
+//    bias: the row maximum of a unit's first step, raised (O and l rescaled) only where a later
+//    step's P add up to more than 2^8.
 //  * Four output warps take O_1 and O_2 out of TMEM, scale and subtract in fp32, round once
 //    and store rows by TMA; likewise o_2, which the backward needs, where it is wanted.
 //  * V's rows that share the last 16-row MMA step with states past the length are zeroed in
@@ -38,7 +41,9 @@ namespace {
 
 using namespace tc;
 using diff::kStates;
+using tcattn::add2;
 using tcattn::f2;
+using tcattn::fma2;
 using tcattn::Ring;
 using tcattn::unf2;
 
@@ -77,12 +82,13 @@ static_assert(f_smem_bytes<128>() <= 232448, "shared memory budget");
 struct FParams {
   __nv_bfloat16 *o, *o2;  // [B, Sq, h, D]; o2 or null
   float *lse;             // [B, h, 2, Sq] or null
-  float *po, *plse;       // runs: [nsplit, 2, B, h, Sq, D] and [nsplit, 2, B, h, Sq]
+  float *po, *plse;       // runs: [nsplit, 2, rows, D] and [nsplit, 2, rows], 128 rows a unit
   const float *lam;
   const int32_t *kv_len;
   int lam_step;  // 1: a weight for each head; 0: one
   int B, Sq, Sk, h, hk, G, tq, nqt, nsplit;
-  uint32_t units;    // B hk nqt nsplit
+  uint32_t units, whole;  // units and runs; the first `whole` are not split, the others in nsplit
+  size_t rows;            // of the split ones
   float scale_log2;  // of |scale|, never 0
   uint32_t neg;      // kIdescNegA for a negative scale: the scores come negated
   int *status;
@@ -90,19 +96,31 @@ struct FParams {
 
 struct FUnit {
   int b, j, qt, sp, len, t0, n;  // n state tiles from t0
+  int part;                      // index among the split units, or -1
 };
-// Unit u: runs of one tile of queries first, then query tiles, key heads, batches.
-__device__ __noinline__ FUnit f_unit(const FParams &P, uint32_t u) {
+// Query tiles of 128 packed rows first, then key heads, batches; of split ones the runs first.
+__device__ __noinline__ FUnit f_unit(const FParams &P, uint32_t i) {
   FUnit r;
-  const uint32_t v = u / (uint32_t)P.nsplit, bj = v / (uint32_t)P.nqt;
-  r.sp = (int)(u - v * (uint32_t)P.nsplit);
+  uint32_t v = i;
+  r.sp = 0;
+  r.part = -1;
+  if (i >= P.whole) {
+    r.part = (int)((i - P.whole) / (uint32_t)P.nsplit);
+    r.sp = (int)(i - P.whole) - r.part * P.nsplit;
+    v = P.whole + (uint32_t)r.part;
+  }
+  const uint32_t bj = v / (uint32_t)P.nqt;
   r.qt = (int)(v - bj * (uint32_t)P.nqt);
   r.b = (int)(bj / (uint32_t)P.hk);
   r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
   r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
   const int nt = (r.len + kStates - 1) / kStates;
-  r.t0 = (int)((long)nt * r.sp / P.nsplit);
-  r.n = (int)((long)nt * (r.sp + 1) / P.nsplit) - r.t0;
+  r.t0 = 0;
+  r.n = nt;
+  if (r.part >= 0) {
+    r.t0 = (int)((long)nt * r.sp / P.nsplit);
+    r.n = (int)((long)nt * (r.sp + 1) / P.nsplit) - r.t0;
+  }
   return r;
 }
 
@@ -292,8 +310,16 @@ __device__ __forceinline__ void f_arrive(uint64_t *bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// A later step's maximum may exceed the bias by this much (base 2) before O is rescaled.
-constexpr float kFSlack = 8.f;
+// A row's P of a later step may add up to this much before O is rescaled: P is at most 2^8,
+// or the bias is raised to the step's maximum.
+constexpr float kFMost = 256.f;
+
+__device__ __forceinline__ float f_max(const uint32_t (&r0)[32], const uint32_t (&r1)[32]) {
+  float a = -INFINITY, b = -INFINITY, c = -INFINITY, d = -INFINITY;  // four short chains
+  cross::x_max(r0, a, b);
+  cross::x_max(r1, c, d);
+  return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
 
 // Warps 4-7 (map 0) and 8-11 (map 1): P of every step; thread = row.
 template <int D>
@@ -319,52 +345,58 @@ __device__ void f_softmax(const FParams &P, uint8_t *smem, FSync *sy, uint32_t t
       cross::warp_wait(live, &sy->s_full[map][sb.slot], sb.phase, abort, P.status);
       tc_fence_after();
       const uint32_t own = at + C::kSCol + map * 128 + sb.slot * 64;
-      uint32_t r0[32], r1[32];
-      tmem_ld32(own, r0);
-      tmem_ld32(own + 32, r1);
-      tmem_wait_ld();
-      reg_fence(r0);
-      reg_fence(r1);
-      if (mine < kStates) {
-        cross::x_mask(mine, r0);
-        cross::x_mask(mine - 32, r1);
-      }
-      float a0 = -INFINITY, a1 = -INFINITY;
-      cross::x_max(r0, a0, a1);
-      cross::x_max(r1, a0, a1);
-      const float mh = fmaxf(a0, a1) * sl2;
-      if (s == 0) {
-        m_run = mh;
-      } else if (__any_sync(0xffffffffu, mh > m_run + kFSlack)) {
-        // O must hold the product of the step before when it is rescaled
-        cross::warp_wait(live, &sy->pv_done[map][sb.slot ^ 1u], sb.slot ? sb.phase : sb.phase ^ 1u,
-                         abort, P.status);
-        tc_fence_after();
-        const float m_new = mh > m_run + kFSlack ? mh : m_run, alpha = ex2(m_run - m_new);
+      uint32_t pk0[16], pk1[16];
+      float sum;
+      // Once, or twice where the bias is raised: the sum of a later step's P says whether it
+      // will do, and the scores are read again rather than kept (which took 160 bytes of
+      // spills: 677 us against 503 for 8192 x 8192 states, 12 heads).
 #pragma unroll 1
-        for (int x = 0; x < D / 16; ++x) {
-          uint32_t t[16];
-          tmem_ld16(oc + x * 16, t);
-          tmem_wait_ld();
-          reg_fence16(t);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
-          tmem_st16(oc + x * 16, t);
+      for (bool again = false;; again = true) {
+        uint32_t r0[32], r1[32];
+        tmem_ld32(own, r0);
+        tmem_ld32(own + 32, r1);
+        tmem_wait_ld();
+        reg_fence(r0);
+        reg_fence(r1);
+        if (mine < kStates) {
+          cross::x_mask(mine, r0);
+          cross::x_mask(mine - 32, r1);
         }
-        tmem_wait_st();
-        l_run *= alpha;
-        m_run = m_new;
+        if (s == 0) {
+          m_run = f_max(r0, r1) * sl2;
+        } else if (again) {
+          const float mh = f_max(r0, r1) * sl2;
+          const float m_new = sum > kFMost ? fmaxf(m_run, mh) : m_run, alpha = ex2(m_run - m_new);
+          // O must hold the product of the step before when it is rescaled
+          cross::warp_wait(live, &sy->pv_done[map][sb.slot ^ 1u],
+                           sb.slot ? sb.phase : sb.phase ^ 1u, abort, P.status);
+          tc_fence_after();
+#pragma unroll 1
+          for (int x = 0; x < D / 16; ++x) {
+            uint32_t t[16];
+            tmem_ld16(oc + x * 16, t);
+            tmem_wait_ld();
+            reg_fence16(t);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) t[e] = __float_as_uint(__uint_as_float(t[e]) * alpha);
+            tmem_st16(oc + x * 16, t);
+          }
+          tmem_wait_st();
+          l_run *= alpha;
+          m_run = m_new;
+        }
+        const uint64_t nm2 = f2(-m_run, -m_run);
+        uint64_t acc0 = f2(0.f, 0.f), acc1 = acc0;
+        cross::x_exp(r0, sc2, nm2, acc0, acc1, pk0);
+        cross::x_exp(r1, sc2, nm2, acc0, acc1, pk1);
+        float s0, s1;
+        unf2(add2(acc0, acc1), s0, s1);
+        sum = s0 + s1;
+        if (s == 0 || again || !__any_sync(0xffffffffu, sum > kFMost)) break;
       }
-      uint32_t pk[16];
-      uint64_t nm2 = f2(-m_run, -m_run), acc0 = f2(0.f, 0.f), acc1 = acc0;
-      cross::x_exp(r0, sc2, nm2, acc0, acc1, pk);
-      tmem_st16(own, pk);
-      cross::x_exp(r1, sc2, nm2, acc0, acc1, pk);
-      tmem_st16(own + 16, pk);
-      float s0, s1, s2, s3;
-      unf2(acc0, s0, s1);
-      unf2(acc1, s2, s3);
-      l_run += (s0 + s1) + (s2 + s3);
+      tmem_st16(own, pk0);
+      tmem_st16(own + 16, pk1);
+      l_run += sum;
       tmem_wait_st();
       tc_fence_before();
       f_arrive(&sy->p_full[map][sb.slot], lane);
@@ -381,6 +413,11 @@ __device__ void f_softmax(const FParams &P, uint8_t *smem, FSync *sy, uint32_t t
 // The four output warps.
 __device__ __forceinline__ void f_out_sync() { asm volatile("bar.sync 13, 128;" ::: "memory"); }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ float f_lse(float l, float m) {
   return l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
 }
@@ -399,7 +436,6 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
   const float *xl = reinterpret_cast<const float *>(smem + C::kOffL) + row;
   uint8_t *tile = smem + C::kOffO;
   const int tok = r64 / P.G, head = r64 - tok * P.G;  // of this row, in its subtile
-  const size_t all = (size_t)P.B * P.h * P.Sq;
   Ring<2> sb;   // of the next step
   uint32_t kq = 0;
   bool live = true;  // false after a wait gave up: keep meeting the barrier, do no work
@@ -407,7 +443,8 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
     const FUnit u = f_unit(P, i);
     const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok, hh = u.j * P.G + head;
     const bool row_ok = tok < P.tq && token < P.Sq;
-    const size_t lrow = ((size_t)u.b * P.h + hh) * P.Sq + token;  // of [B, h, Sq]
+    const bool split = u.part >= 0;
+    const size_t prow = (size_t)u.sp * 2 * P.rows + (size_t)u.part * 128 + row;  // of a run's
     float l1 = 0.f, m1 = 0.f, l2 = 0.f, m2 = 0.f;
     const float lam = row_ok ? __ldg(P.lam + hh * P.lam_step) : 0.f;
     if (u.n > 0) {
@@ -427,7 +464,8 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
       sb.slot = (sb.slot + (uint32_t)u.n) & 1u;
       ++kq;
       const float inv1 = f_inv(l1), inv2 = f_inv(l2), by2 = -lam * inv2;
-      float *run = P.po + ((size_t)u.sp * 2 * all + lrow) * D;
+      const uint64_t i1 = f2(inv1, inv1), i2 = f2(inv2, inv2), b2 = f2(by2, by2);
+      float *run = P.po + prow * D;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t a[32], c[32];
@@ -440,14 +478,14 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
           tc_fence_before();
           f_arrive(&sy->o_free, lane);
         }
-        if (P.nsplit > 1) {
+        if (split) {
           if (row_ok && live)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               *reinterpret_cast<float4 *>(run + x * 32 + e) = make_float4(
                   __uint_as_float(a[e]) * inv1, __uint_as_float(a[e + 1]) * inv1,
                   __uint_as_float(a[e + 2]) * inv1, __uint_as_float(a[e + 3]) * inv1);
-              *reinterpret_cast<float4 *>(run + all * D + x * 32 + e) = make_float4(
+              *reinterpret_cast<float4 *>(run + P.rows * D + x * 32 + e) = make_float4(
                   __uint_as_float(c[e]) * inv2, __uint_as_float(c[e + 1]) * inv2,
                   __uint_as_float(c[e + 2]) * inv2, __uint_as_float(c[e + 3]) * inv2);
             }
@@ -461,11 +499,14 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
           uint32_t w[4], w2[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const float c0 = __uint_as_float(c[8 * e + 2 * y]);
-            const float c1 = __uint_as_float(c[8 * e + 2 * y + 1]);
-            w[y] = pack_bf16x2(fmaf(__uint_as_float(a[8 * e + 2 * y]), inv1, c0 * by2),
-                               fmaf(__uint_as_float(a[8 * e + 2 * y + 1]), inv1, c1 * by2));
-            w2[y] = pack_bf16x2(c0 * inv2, c1 * inv2);
+            const int at2 = 8 * e + 2 * y;
+            const uint64_t c2 = f2(__uint_as_float(c[at2]), __uint_as_float(c[at2 + 1]));
+            float x0, x1;
+            unf2(fma2(f2(__uint_as_float(a[at2]), __uint_as_float(a[at2 + 1])), i1, mul2(c2, b2)),
+                 x0, x1);
+            w[y] = pack_bf16x2(x0, x1);
+            unf2(mul2(c2, i2), x0, x1);
+            w2[y] = pack_bf16x2(x0, x1);
           }
           *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
           if (P.o2)
@@ -474,7 +515,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
       }
       fence_async_smem();
       f_out_sync();
-      if (q4 == 0 && lane == 0 && live && P.nsplit == 1) {
+      if (q4 == 0 && lane == 0 && live && !split) {
 #pragma unroll 1
         for (int x = 0; x < 2 * C::kBoxes; ++x) {
           const int t0 = (u.qt * 2 + (x & 1)) * P.tq;
@@ -485,7 +526,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
         }
         bulk_commit();
       }
-    } else if (P.nsplit == 1 && row_ok) {  // o = o2 = 0 (joining runs leaves one without states out)
+    } else if (!split && row_ok) {  // o = o2 = 0 (joining runs leaves one without states out)
       const size_t to = (((size_t)u.b * P.Sq + token) * P.h + hh) * D;
 #pragma unroll 1
       for (int e = 0; e < D / 8; ++e) {
@@ -494,10 +535,10 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
       }
     }
     if (row_ok && live) {
-      if (P.nsplit > 1) {
-        float *to = P.plse + (size_t)u.sp * 2 * all + lrow;
+      if (split) {
+        float *to = P.plse + prow;
         to[0] = f_lse(l1, m1);
-        to[all] = f_lse(l2, m2);
+        to[P.rows] = f_lse(l2, m2);
       } else if (P.lse) {
         float *to = P.lse + ((size_t)u.b * P.h + hh) * 2 * P.Sq + token;
         to[0] = f_lse(l1, m1);
@@ -629,19 +670,21 @@ cudaError_t launch_f(const DiffArgs &a, cudaStream_t st) {
   p.kv_len = a.x.kv_len;
   p.B = s.B, p.Sq = s.Sq, p.Sk = s.Sk, p.h = s.h, p.hk = s.hk;
   p.G = pk.G, p.tq = pk.tq;
-  p.nqt = (pk.nsub + 1) / 2, p.nsplit = diff_fwd_splits(s, NABLA_BF16);
+  p.nqt = (pk.nsub + 1) / 2;
   // a scale of 0 weighs all states alike, as one too small to tell scores apart does
   p.scale_log2 = a.x.scale == 0.f ? 1e-30f : fabsf(a.x.scale) * 1.4426950408889634f;
   p.neg = a.x.scale < 0.f ? kIdescNegA : 0u;
   p.status = a.x.status;
-  const CrossRuns runs = diff_runs(a, p.nsplit);
+  const DiffRuns runs = diff_runs(a, NABLA_BF16);
+  p.nsplit = runs.plan.runs, p.rows = (size_t)runs.rows;
   p.po = runs.po, p.plse = runs.plse;
-  p.units = (uint32_t)((long)s.B * s.hk * p.nqt * p.nsplit);
+  p.whole = (uint32_t)runs.plan.whole;
+  p.units = (uint32_t)(runs.plan.whole + runs.plan.rest * runs.plan.runs);
   const unsigned grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
   err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), f_smem_bytes<D>(), st, mq, mk, mv, mo,
                    mo2, p);
   if (err != cudaSuccess || p.nsplit == 1) return err;
-  return launch_diff_join(a, NABLA_BF16, p.nsplit, st);
+  return launch_diff_join(a, NABLA_BF16, runs, st);
 }
 
 }  // namespace

@@ -1,0 +1,276 @@
+// K12s -- differential attention forward of few rows: at most four packed rows a key head
+// (single tokens of grouped heads), bf16 and fp32.
+//
+// Bound by the bytes of K and V.  D columns of a state lie over the lanes of a group, 16
+// bytes a lane (bf16, D 128: 16 lanes, two states a warp and load), the first half of the
+// lanes holding map 1's columns of K, the others map 2's.  A group walks its own states
+// with its own running maxima and sums, straight from memory to registers: no shared memory,
+// no barrier, and a warp's eight loads are all under way together.  Scores: products of the
+// lane's columns, added up over the half group; then every lane has its own map's P, takes
+// the other's from the other half, and adds both times its columns of V.  The groups of a CTA
+// are joined in shared memory at the end, CTAs (runs of a batch's states) by diff_join.
+// At most four rows: their arithmetic (some 100 instructions for two states and three rows)
+// stays behind the loads.
+#include <cuda_bf16.h>
+
+#include <cfloat>
+
+#include "attn_common.cuh"
+#include "diff_common.cuh"
+#include "internal.h"
+#include "pdl.cuh"
+#include "tc_ptx.cuh"
+
+namespace nabla {
+namespace {
+
+using tcattn::add2;
+using tcattn::f2;
+using tcattn::fma2;
+using tcattn::unf2;
+
+struct FewParams {
+  const void *q, *k, *v;
+  nabla_strides q_st, k_st, v_st;
+  const float *lam;
+  const int32_t *kv_len;
+  void *o, *o2;
+  float *lse;         // [B, h, 2, Sq]
+  float *po, *plse;   // runs
+  int lam_step, B, Sq, Sk, h, hk, G, nsplit;
+  float scale_log2;
+  int *status;
+};
+
+// 16 bytes as fp32 pairs.
+__device__ __forceinline__ void widen(const uint4 &r, uint64_t (&v)[4], __nv_bfloat16) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = f2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void widen(const uint4 &r, uint64_t (&v)[2], float) {
+  v[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
+  v[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
+}
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const float4 &v) {
+  *reinterpret_cast<uint2 *>(p) = make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void put(float *p, const float4 &v) {
+  *reinterpret_cast<float4 *>(p) = v;
+}
+
+// CTA: run `sp` of the states of batch b and key head j; kR: rows at most.
+template <typename T, int D, int kR>
+__global__ void __launch_bounds__(256, kR == 4 ? 1 : 2)
+    diff_few_kernel(const __grid_constant__ FewParams P) {
+  constexpr int kCols = 16 / (int)sizeof(T), kPairs = kCols / 2;  // columns a lane
+  constexpr int kLanes = D / kCols, kHalf = kLanes / 2;           // of a group, of a map's half
+  constexpr int kGroups = 256 / kLanes, kAhead = 4;               // states a group loads at once
+  __shared__ float ml[kGroups][2][kR][2];                         // maximum and sum
+  __shared__ float sums[kGroups][2][D + 4];                       // of one row, in turn
+  const int tid = threadIdx.x, lane = tid % kLanes, group = tid / kLanes;
+  const bool second = lane >= kHalf;
+  const int sp = (int)(blockIdx.x % P.nsplit);
+  const int bj = (int)(blockIdx.x / P.nsplit), b = bj / P.hk, j = bj - b * P.hk;
+  const int rows = P.Sq * P.G;
+  pdl_launch_dependents();
+  pdl_wait();
+  if (tid == 0) cross::check_len(P.kv_len, b, P.Sk, P.status);
+  const int len = cross::batch_len(P.kv_len, b, P.Sk);
+  const int u0 = (int)((long)len * sp / P.nsplit), u1 = (int)((long)len * (sp + 1) / P.nsplit);
+  const T *k = static_cast<const T *>(P.k) + b * P.k_st.batch + j * P.k_st.head + lane * kCols;
+  const T *v = static_cast<const T *>(P.v) + b * P.v_st.batch + j * P.v_st.head + lane * kCols;
+  uint64_t q[kR][kPairs], own[kR][kPairs], other[kR][kPairs];  // O of this lane's map, the other's
+  float m[kR], l[kR];
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    const int t = r / P.G, hh = j * P.G + r - t * P.G;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows)
+      w = *reinterpret_cast<const uint4 *>(static_cast<const T *>(P.q) + b * P.q_st.batch +
+                                           t * P.q_st.token + hh * P.q_st.head + lane * kCols);
+    widen(w, q[r], T());
+    const uint64_t s2 = f2(P.scale_log2, P.scale_log2);
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      q[r][i] = fma2(q[r][i], s2, 0ull);  // scores come in base 2
+      own[r][i] = other[r][i] = 0ull;
+    }
+    m[r] = -FLT_MAX;
+    l[r] = 0.f;
+  }
+  for (int u = u0 + group; u - group < u1; u += kGroups * kAhead) {  // a warp stays together
+    uint4 kr[kAhead], vr[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int64_t at = u + a * kGroups;
+      const bool on = at < u1;
+      kr[a] = on ? *reinterpret_cast<const uint4 *>(k + at * P.k_st.token)
+                 : make_uint4(0u, 0u, 0u, 0u);
+      vr[a] = on ? *reinterpret_cast<const uint4 *>(v + at * P.v_st.token)
+                 : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float s[kAhead][kR];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      uint64_t kk[kPairs];
+      widen(kr[a], kk, T());
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        uint64_t t = fma2(q[r][0], kk[0], 0ull);
+#pragma unroll
+        for (int i = 1; i < kPairs; ++i) t = fma2(q[r][i], kk[i], t);
+        float x, y;
+        unf2(t, x, y);
+        s[a][r] = x + y;
+      }
+#pragma unroll
+      for (int o = kHalf / 2; o; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < kR; ++r) s[a][r] += __shfl_xor_sync(0xffffffffu, s[a][r], o);
+    }
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      float top = m[r];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (u + a * kGroups < u1) top = fmaxf(top, s[a][r]);
+      const float by = exp2f(m[r] - top), by_other = __shfl_xor_sync(0xffffffffu, by, kHalf);
+      m[r] = top;
+      l[r] *= by;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        own[r][i] = fma2(own[r][i], f2(by, by), 0ull);
+        other[r][i] = fma2(other[r][i], f2(by_other, by_other), 0ull);
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        s[a][r] = u + a * kGroups < u1 ? exp2f(s[a][r] - top) : 0.f;
+        l[r] += s[a][r];
+      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      uint64_t vv[kPairs];
+      widen(vr[a], vv, T());
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const float p = s[a][r], p_other = __shfl_xor_sync(0xffffffffu, p, kHalf);
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          own[r][i] = fma2(f2(p, p), vv[i], own[r][i]);
+          other[r][i] = fma2(f2(p_other, p_other), vv[i], other[r][i]);
+        }
+      }
+    }
+  }
+  // the groups' sums of a row, scaled to their common maximum
+  if (lane % kHalf == 0)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      ml[group][second][r][0] = m[r];
+      ml[group][second][r][1] = l[r];
+    }
+  __syncthreads();
+  const size_t all = (size_t)P.B * P.h * P.Sq;
+#pragma unroll
+  for (int r = 0; r < kR; ++r) {
+    if (r >= rows) break;
+    float top[2], sum[2];
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+      top[map] = -FLT_MAX;
+      for (int g = 0; g < kGroups; ++g) top[map] = fmaxf(top[map], ml[g][map][r][0]);
+      sum[map] = 0.f;
+      for (int g = 0; g < kGroups; ++g)
+        sum[map] = fmaf(ml[g][map][r][1], exp2f(ml[g][map][r][0] - top[map]), sum[map]);
+    }
+#pragma unroll
+    for (int map = 0; map < 2; ++map) {
+      const float w = exp2f(ml[group][map][r][0] - top[map]);
+      float *to = sums[group][map] + lane * kCols;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const uint64_t t = fma2((map == 1) == second ? own[r][i] : other[r][i], f2(w, w), 0ull);
+        unf2(t, to[2 * i], to[2 * i + 1]);
+      }
+    }
+    __syncthreads();
+    const int t = r / P.G, hh = j * P.G + r - t * P.G;
+    const size_t row = ((size_t)b * P.h + hh) * P.Sq + t;
+    if (tid < 2) {
+      const float s = sum[tid], lse = s > 0.f ? top[tid] + log2f(s) : s == 0.f ? -INFINITY : s;
+      if (P.nsplit > 1)
+        P.plse[((size_t)sp * 2 + tid) * all + row] = lse;
+      else if (P.lse)
+        P.lse[(((size_t)b * P.h + hh) * 2 + tid) * P.Sq + t] = lse;
+    }
+    if (tid < D / 4) {
+      float4 o[2];
+#pragma unroll
+      for (int map = 0; map < 2; ++map) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int g = 0; g < kGroups; ++g) {
+          const float4 y = *reinterpret_cast<const float4 *>(sums[g][map] + tid * 4);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const float inv = sum[map] > 0.f ? 1.0f / sum[map] : sum[map];
+        o[map] = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      }
+      if (P.nsplit > 1) {
+        if (u0 < u1) {  // (a run without states is not read)
+          float *po = P.po + ((size_t)sp * 2 * all + row) * D + tid * 4;
+          put(po, o[0]);
+          put(po + all * D, o[1]);
+        }
+      } else {
+        const float lam = P.lam[hh * P.lam_step];
+        const size_t to = (((size_t)b * P.Sq + t) * P.h + hh) * D + tid * 4;
+        put(static_cast<T *>(P.o) + to,
+            make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
+                        fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
+        if (P.o2) put(static_cast<T *>(P.o2) + to, o[1]);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const FewParams &p, cudaStream_t st) {
+  const dim3 grid((unsigned)((long)p.B * p.hk * p.nsplit)), block(256);
+  const int rows = p.Sq * p.G;
+  return rows == 1   ? launch_pdl(diff_few_kernel<T, D, 1>, grid, block, 0, st, p)
+         : rows == 2 ? launch_pdl(diff_few_kernel<T, D, 2>, grid, block, 0, st, p)
+         : rows == 3 ? launch_pdl(diff_few_kernel<T, D, 3>, grid, block, 0, st, p)
+                     : launch_pdl(diff_few_kernel<T, D, 4>, grid, block, 0, st, p);
+}
+
+}  // namespace
+
+bool diff_few_rows(const CrossShape &s) { return (long)s.Sq * (s.h / s.hk) <= 4; }
+
+cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) {
+  const CrossShape &s = a.x.s;
+  FewParams p{};
+  p.q = a.x.q, p.k = a.x.k, p.v = a.x.v;
+  p.q_st = a.x.q_st, p.k_st = a.x.k_st, p.v_st = a.x.v_st;
+  p.lam = a.lam, p.lam_step = a.lam_n > 1 ? 1 : 0;
+  p.kv_len = a.x.kv_len;
+  p.o = a.x.o, p.o2 = a.o2, p.lse = a.x.lse;
+  p.B = s.B, p.Sq = s.Sq, p.Sk = s.Sk, p.h = s.h, p.hk = s.hk, p.G = s.h / s.hk;
+  p.scale_log2 = a.x.scale * 1.4426950408889634f;
+  p.status = a.x.status;
+  const DiffRuns runs = diff_runs(a, dt);
+  p.nsplit = runs.plan.runs, p.po = runs.po, p.plse = runs.plse;
+  cudaError_t e;
+  if (dt == NABLA_BF16)
+    e = s.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, st) : launch_rows<__nv_bfloat16, 128>(p, st);
+  else
+    e = s.D == 64 ? launch_rows<float, 64>(p, st) : launch_rows<float, 128>(p, st);
+  if (e != cudaSuccess || p.nsplit == 1) return e;
+  return launch_diff_join(a, dt, runs, st);
+}
+
+}  // namespace nabla

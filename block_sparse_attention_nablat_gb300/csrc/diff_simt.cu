@@ -494,15 +494,14 @@ cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st) {
   p.x.out = static_cast<float *>(a.x.o);
   p.x.lse_out = a.x.lse;
   p.o2 = static_cast<float *>(a.o2);
-  p.x.nsplit = diff_fwd_splits(a.x.s, NABLA_F32);
-  const CrossRuns runs = diff_runs(a, p.x.nsplit);
-  p.x.po = runs.po, p.x.plse = runs.plse;
+  const DiffRuns runs = diff_runs(a, NABLA_F32);
+  p.x.nsplit = runs.plan.runs, p.x.po = runs.po, p.x.plse = runs.plse;
   const long subs = (long)a.x.s.B * a.x.s.hk * p.x.nsub;
   const int A = cross_simt_plan(a.x.s).A;
   const cudaError_t e =
       a.x.s.D == 64 ? launch_fwd<64>(p, A, subs, st) : launch_fwd<128>(p, A, subs, st);
   if (e != cudaSuccess || p.x.nsplit == 1) return e;
-  return launch_diff_join(a, NABLA_F32, p.x.nsplit, st);
+  return launch_diff_join(a, NABLA_F32, runs, st);
 }
 
 cudaError_t launch_diff_bwd_simt(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,

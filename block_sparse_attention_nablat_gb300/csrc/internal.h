@@ -168,13 +168,28 @@ struct DiffArgs {
   nabla_strides o2_st;  // backward
   float *dlam;
 };
-int diff_fwd_splits(const CrossShape &s, nabla_dtype dt);
+// Runs of states: `runs` of every row, or (packed: the tcgen05 kernel's units of 128 rows)
+// `whole` units in one and the `rest` in `runs`.
+struct DiffPlan {
+  long whole, rest;
+  int runs;
+  bool packed;
+};
+DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt);
 size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt);
-// [nsplit, 2, B, h, Sq, D] and [nsplit, 2, B, h, Sq]; none for one run
-CrossRuns diff_runs(const DiffArgs &a, int nsplit);
-cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, int nsplit, cudaStream_t st);
+struct DiffRuns {  // partial results: [runs, 2, rows, D] and [runs, 2, rows]; none for one run
+  DiffPlan plan;
+  long rows;
+  float *po, *plse;
+};
+DiffRuns diff_runs(const DiffArgs &a, nabla_dtype dt);
+cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, const DiffRuns &r,
+                             cudaStream_t st);
 // K12: bf16, tcgen05.  K12f: fp32, CUDA cores.
 cudaError_t launch_diff_attn_tc(const DiffArgs &a, cudaStream_t st);
+// K12s: at most four packed rows a key head.
+bool diff_few_rows(const CrossShape &s);
+cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st);
 cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st);
 // K13: the backward.  Workspace: the packed rows' numbers (five), what lam's gradient is
 // summed from, the runs' sums of dK and dV and of dQ.

@@ -183,6 +183,12 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (2, 900, 64, 14, 2, 128, [64, 50], False),
     (3, 6, 2300, 4, 4, 128, [2300, 700, 0], True),   # few rows, runs of states
     (2, 2100, 200, 12, 12, 128, [199, 64], False),   # several units a CTA
+    (1, 2, 1300, 3, 3, 64, [1290], True),            # two rows a key head
+    (3, 4, 700, 2, 2, 64, [700, 0, 3], "heads"),     # four
+    (2, 2, 1100, 4, 2, 128, [1100, 513], True),      # two tokens of two heads
+    (70, 1, 600, 3, 1, 128, None, False),            # three
+    (2, 4900, 1100, 2, 2, 64, [1100, 70], False),    # 156 units, the last four in runs
+    (1, 9800, 1030, 2, 2, 128, None, False),         # 154, the last two in runs
 ]
 
 
