@@ -4,9 +4,9 @@
 //   o = o1 - lam o2,   o_m = softmax(scale q_m k_m^T) v
 //
 //  * Work unit = 128 packed query rows (two 64-row subtiles, cross_common.cuh) of one
-//    (batch, key head), over the batch's state tiles or one of `nsplit` runs of them
-//    (diff_join joins the runs): those of the last round, which would leave SMs idle.
-//    Persistent CTAs (one per SM).
+//    (batch, key head) over the batch's state tiles, or a part of them: persistent CTAs (one
+//    per SM) take units in turn and, in the end, equal shares of the rest (diff_common.cuh;
+//    diff_stream_join joins the parts).
 //  * A step covers 64 states.  For each map m: S_m = Q_m K_m^T is one SS MMA (M = 128,
 //    N = 64, depth D / 2), O_m += P_m V a TS MMA with P_m (bf16) over the scores.  The maps
 //    share K's tile (each its half of the columns) and V's.
@@ -65,7 +65,16 @@ struct FCfg {
   static constexpr int kOffSync = kOffL + 4 * 128 * 4;
 };
 
+// n state tiles of unit (b, j, qt) from t0 on; `part`: the CTA's place for the results of a
+// part, or -1: all of the unit; `more` 0: there are no more units.
+struct alignas(16) FUnit {
+  int b, j, qt, len, t0, n, part, more;
+};
+constexpr int kUnits = 4;  // of the ring
+
 struct FSync {
+  FUnit units[kUnits];
+  uint64_t unit_full[kUnits], unit_empty[kUnits];
   uint64_t q_full[2], q_empty[2], k_full[3], k_empty[3], v_full[3], v_empty[3], v_raw;
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // [map][buffer]
   uint64_t o_free, l_full, l_empty, drain;
@@ -82,60 +91,94 @@ static_assert(f_smem_bytes<128>() <= 232448, "shared memory budget");
 struct FParams {
   __nv_bfloat16 *o, *o2;  // [B, Sq, h, D]; o2 or null
   float *lse;             // [B, h, 2, Sq] or null
-  float *po, *plse;       // runs: [nsplit, 2, rows, D] and [nsplit, 2, rows], 128 rows a unit
+  float *po, *plse;       // parts: [kCtas, 2 places, 2 maps, 128, D] and [.., 128]
   const float *lam;
   const int32_t *kv_len;
   int lam_step;  // 1: a weight for each head; 0: one
-  int B, Sq, Sk, h, hk, G, tq, nqt, nsplit;
-  uint32_t units, whole;  // units and runs; the first `whole` are not split, the others in nsplit
-  size_t rows;            // of the split ones
+  int B, Sq, Sk, h, hk, G, tq, nqt;
+  uint32_t whole;  // units that go round; those from there on are cut
+  bool cut;        // there are such
   float scale_log2;  // of |scale|, never 0
   uint32_t neg;      // kIdescNegA for a negative scale: the scores come negated
   int *status;
 };
 
-struct FUnit {
-  int b, j, qt, sp, len, t0, n;  // n state tiles from t0
-  int part;                      // index among the split units, or -1
+// The CTA's way through its units: the thread that runs furthest ahead (Q's and K's loader)
+// finds the next one and leaves it in a ring for the other roles, whose registers and
+// instructions are scarce (as a function that each of them calls it took 489 us against
+// 412 for 8192 x 8192 states, 12 heads).
+struct FWalk {
+  uint32_t i;      // of the units that go round
+  int b, unit, t;  // of the piece
+  long left;
+  int seen;        // parts of the piece so far
 };
-// Query tiles of 128 packed rows first, then key heads, batches; of split ones the runs first.
-__device__ __noinline__ FUnit f_unit(const FParams &P, uint32_t i) {
+__device__ __forceinline__ FUnit f_next(const FParams &P, FWalk &w) {
   FUnit r;
-  uint32_t v = i;
-  r.sp = 0;
-  r.part = -1;
-  if (i >= P.whole) {
-    r.part = (int)((i - P.whole) / (uint32_t)P.nsplit);
-    r.sp = (int)(i - P.whole) - r.part * P.nsplit;
-    v = P.whole + (uint32_t)r.part;
+  if (w.i < P.whole) {
+    const uint32_t bj = w.i / (uint32_t)P.nqt;
+    r.qt = (int)(w.i - bj * (uint32_t)P.nqt);
+    r.b = (int)(bj / (uint32_t)P.hk);
+    r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
+    r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
+    r.t0 = 0;
+    r.n = (r.len + kStates - 1) / kStates;
+    r.part = -1;
+    r.more = 1;
+    w.i += gridDim.x;
+    return r;
   }
-  const uint32_t bj = v / (uint32_t)P.nqt;
-  r.qt = (int)(v - bj * (uint32_t)P.nqt);
-  r.b = (int)(bj / (uint32_t)P.hk);
-  r.j = (int)(bj - (uint32_t)r.b * (uint32_t)P.hk);
-  r.len = cross::batch_len(P.kv_len, r.b, P.Sk);
-  const int nt = (r.len + kStates - 1) / kStates;
-  r.t0 = 0;
-  r.n = nt;
-  if (r.part >= 0) {
-    r.t0 = (int)((long)nt * r.sp / P.nsplit);
-    r.n = (int)((long)nt * (r.sp + 1) / P.nsplit) - r.t0;
-  }
+  r.more = w.left > 0;
+  if (!r.more) return r;
+  r.len = cross::batch_len(P.kv_len, w.b, P.Sk);
+  const int tiles = (r.len + kStates - 1) / kStates, all = tiles > 0 ? tiles : 1;
+  const int n = w.left < all - w.t ? (int)w.left : all - w.t;
+  r.b = w.b;
+  r.j = w.unit / P.nqt;
+  r.qt = w.unit - r.j * P.nqt;
+  r.t0 = w.t;
+  r.n = tiles > 0 ? n : 0;
+  r.part = n == all ? -1 : w.seen > 0;
+  ++w.seen;
+  w.left -= n;
+  w.t = 0;
+  if (++w.unit == P.nqt * P.hk) w.unit = 0, ++w.b;
   return r;
+}
+// The next unit, for one thread (kWarp false) or a whole warp; false at the end, or when the
+// wait gave up.
+template <bool kWarp>
+__device__ __forceinline__ bool f_get(const FParams &P, FSync *sy, Ring<kUnits> &r, FUnit &u,
+                                      volatile int *abort) {
+  bool ok = cross::thread_wait(&sy->unit_full[r.slot], r.phase, abort, P.status);
+  if (kWarp) ok = __all_sync(0xffffffffu, ok);
+  if (!ok) return false;
+  u = sy->units[r.slot];
+  if (kWarp) __syncwarp();
+  if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive(&sy->unit_empty[r.slot]);
+  r.next();
+  return u.more != 0;
 }
 
 // Warp 0, lane 0: Q of every unit and K of every step, as far ahead as the rings allow.
 template <int D>
 __device__ void f_load_qk(const FParams &P, const CUtensorMap *mq, const CUtensorMap *mk,
-                          uint8_t *smem, FSync *sy, volatile int *abort) {
+                          uint8_t *smem, FSync *sy, FWalk w, volatile int *abort) {
   using C = FCfg<D>;
   Ring<2> q;
   Ring<C::kKBufs> k;
   uint32_t g = 0, kq = 0;
   bool go = true;
   const uint32_t qbytes = (uint32_t)(P.G * P.tq) * 128 * 2 * C::kBoxes;
-  for (uint32_t i = blockIdx.x; i < P.units && go && !*abort; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  while (go && !*abort) {
+    const FUnit u = f_next(P, w);
+    go = cross::thread_wait(&sy->unit_empty[ur.slot], ur.phase ^ 1u, abort, P.status);
+    if (!go) break;
+    sy->units[ur.slot] = u;
+    mbar_arrive(&sy->unit_full[ur.slot]);
+    ur.next();
+    if (!u.more) break;
     cross::check_len(P.kv_len, u.b, P.Sk, P.status);
     if (u.n == 0) continue;
     go = cross::thread_wait(&sy->q_empty[q.slot], q.phase ^ 1u, abort, P.status);
@@ -178,8 +221,8 @@ __device__ void f_load_v(const FParams &P, const CUtensorMap *mv, uint8_t *smem,
   Ring<C::kVBufs> v;
   uint32_t g = 0, raw = 0;
   bool go = true;
-  for (uint32_t i = blockIdx.x; i < P.units && go; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  for (FUnit u; go && f_get<true>(P, sy, ur, u, abort);) {
     for (int s = 0; s < u.n && go; ++s, ++g, v.next()) {
       const int t = u.t0 + s;
       const int rows = u.len - t * kStates, end = diff::steps16(u.len, t) * 16;
@@ -222,8 +265,8 @@ __device__ void f_qk(const FParams &P, uint8_t *smem, FSync *sy, uint32_t tmem,
   Ring<2> sb, q;
   Ring<C::kKBufs> k;
   bool ok = true;
-  for (uint32_t i = blockIdx.x; i < P.units && ok; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  for (FUnit u; ok && f_get<false>(P, sy, ur, u, abort);) {
     if (u.n == 0) continue;
     ok = cross::thread_wait(&sy->q_full[q.slot], q.phase, abort, P.status);
     const uint64_t qd = q_desc + (uint64_t)((q.slot * C::kQTile) >> 4);
@@ -266,8 +309,8 @@ __device__ void f_pv(const FParams &P, uint8_t *smem, FSync *sy, uint32_t tmem,
   Ring<C::kVBufs> v;
   uint32_t kq = 0;
   bool ok = true;
-  for (uint32_t i = blockIdx.x; i < P.units && ok; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  for (FUnit u; ok && f_get<false>(P, sy, ur, u, abort);) {
     if (u.n == 0) continue;
     // the previous unit's O must have been read before the first product overwrites it
     if (kq > 0) ok = cross::thread_wait(&sy->o_free, (kq - 1) & 1u, abort, P.status);
@@ -336,8 +379,8 @@ __device__ void f_softmax(const FParams &P, uint8_t *smem, FSync *sy, uint32_t t
   Ring<2> sb;
   uint32_t kq = 0;
   bool live = true;  // false after a wait gave up: keep meeting the barriers, do no work
-  for (uint32_t i = blockIdx.x; i < P.units; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  for (FUnit u; f_get<true>(P, sy, ur, u, abort);) {
     if (u.n == 0) continue;
     float m_run = 0.f, l_run = 0.f;
     for (int s = 0; s < u.n; ++s, sb.next()) {
@@ -412,6 +455,16 @@ __device__ void f_softmax(const FParams &P, uint8_t *smem, FSync *sy, uint32_t t
 
 // The four output warps.
 __device__ __forceinline__ void f_out_sync() { asm volatile("bar.sync 13, 128;" ::: "memory"); }
+__device__ __forceinline__ bool f_out_all(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.and.pred q, 13, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"(ok ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t d;
@@ -439,12 +492,13 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
   Ring<2> sb;   // of the next step
   uint32_t kq = 0;
   bool live = true;  // false after a wait gave up: keep meeting the barrier, do no work
-  for (uint32_t i = blockIdx.x; i < P.units; i += gridDim.x) {
-    const FUnit u = f_unit(P, i);
+  Ring<kUnits> ur;
+  // the four warps meet at barriers, so they go on together or not at all
+  for (FUnit u; f_out_all(f_get<true>(P, sy, ur, u, abort));) {
     const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok, hh = u.j * P.G + head;
     const bool row_ok = tok < P.tq && token < P.Sq;
     const bool split = u.part >= 0;
-    const size_t prow = (size_t)u.sp * 2 * P.rows + (size_t)u.part * 128 + row;  // of a run's
+    const size_t prow = ((size_t)blockIdx.x * 2 + (split ? u.part : 0)) * 256 + row;  // of a part
     float l1 = 0.f, m1 = 0.f, l2 = 0.f, m2 = 0.f;
     const float lam = row_ok ? __ldg(P.lam + hh * P.lam_step) : 0.f;
     if (u.n > 0) {
@@ -485,7 +539,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
               *reinterpret_cast<float4 *>(run + x * 32 + e) = make_float4(
                   __uint_as_float(a[e]) * inv1, __uint_as_float(a[e + 1]) * inv1,
                   __uint_as_float(a[e + 2]) * inv1, __uint_as_float(a[e + 3]) * inv1);
-              *reinterpret_cast<float4 *>(run + P.rows * D + x * 32 + e) = make_float4(
+              *reinterpret_cast<float4 *>(run + 128 * D + x * 32 + e) = make_float4(
                   __uint_as_float(c[e]) * inv2, __uint_as_float(c[e + 1]) * inv2,
                   __uint_as_float(c[e + 2]) * inv2, __uint_as_float(c[e + 3]) * inv2);
             }
@@ -496,7 +550,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
           // 16-byte piece of the row's 128 bytes in box x / 2, swizzled by the row
           const int piece = (x & 1) * 4 + e;
           uint8_t *to = tile + (x >> 1) * C::kQBox + row * 128 + ((piece ^ (row & 7)) << 4);
-          uint32_t w[4], w2[4];
+          uint32_t v1[4], v2[4];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int at2 = 8 * e + 2 * y;
@@ -504,13 +558,13 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
             float x0, x1;
             unf2(fma2(f2(__uint_as_float(a[at2]), __uint_as_float(a[at2 + 1])), i1, mul2(c2, b2)),
                  x0, x1);
-            w[y] = pack_bf16x2(x0, x1);
+            v1[y] = pack_bf16x2(x0, x1);
             unf2(mul2(c2, i2), x0, x1);
-            w2[y] = pack_bf16x2(x0, x1);
+            v2[y] = pack_bf16x2(x0, x1);
           }
-          *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4 *>(to) = make_uint4(v1[0], v1[1], v1[2], v1[3]);
           if (P.o2)
-            *reinterpret_cast<uint4 *>(to + C::kQTile) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+            *reinterpret_cast<uint4 *>(to + C::kQTile) = make_uint4(v2[0], v2[1], v2[2], v2[3]);
         }
       }
       fence_async_smem();
@@ -538,7 +592,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
       if (split) {
         float *to = P.plse + prow;
         to[0] = f_lse(l1, m1);
-        to[P.rows] = f_lse(l2, m2);
+        to[128] = f_lse(l2, m2);
       } else if (P.lse) {
         float *to = P.lse + ((size_t)u.b * P.h + hh) * 2 * P.Sq + token;
         to[0] = f_lse(l1, m1);
@@ -585,6 +639,10 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&sy->v_full[i], 1);
       mbar_init(&sy->v_empty[i], 1);
     }
+    for (int i = 0; i < kUnits; ++i) {
+      mbar_init(&sy->unit_full[i], 1);
+      mbar_init(&sy->unit_empty[i], 3 + 8 + 4);  // V's loader, the products', softmax, output
+    }
     mbar_init(&sy->v_raw, 1);
     mbar_init(&sy->o_free, 4);  // output warps
     mbar_init(&sy->l_full, 8);  // softmax warps
@@ -606,24 +664,38 @@ __global__ void __launch_bounds__(512, 1)
   }
   fence_async_smem();
   if (warp == 1) tmem_alloc(&sy->tmem_slot, C::kTmemCols);
+  pdl_wait();  // the inputs are written; no earlier kernel still reads o
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sy->tmem_slot;
-  pdl_wait();  // the inputs are written; no earlier kernel still reads o
 
-  if (warp == 0) {
-    if (lane == 0) f_load_qk<D>(P, &mq, &mk, smem, sy, abort);
-    __syncwarp();
-  } else if (warp == 1) {
-    if (elect_one()) f_qk<D>(P, smem, sy, tmem, abort);
-    __syncwarp();
-  } else if (warp == 2) {
-    if (elect_one()) f_pv<D>(P, smem, sy, tmem, abort);
-    __syncwarp();
-  } else if (warp == 3) {
-    f_load_v<D>(P, &mv, smem, sy, abort);
-    __syncwarp();
+  if (warp < 4) {
+    if (warp == 0) {
+      FWalk w{blockIdx.x, 0, 0, 0, 0, 0};
+      if (P.cut) {  // the CTA's piece
+        const int per = P.nqt * P.hk;
+        const long p0 = diff::span_of_unit(P.kv_len, P.Sk, per, P.whole);
+        const long n = diff::span_total(P.kv_len, P.B, P.Sk, per) - p0;
+        const long from = diff::piece(p0, n, blockIdx.x);
+        w.left = diff::piece(p0, n, blockIdx.x + 1) - from;
+        if (w.left > 0) {
+          const diff::Span at = diff::span_find(P.kv_len, P.B, P.Sk, per, from);
+          w.b = at.b, w.unit = at.unit, w.t = at.t;
+        }
+      }
+      if (lane == 0) f_load_qk<D>(P, &mq, &mk, smem, sy, w, abort);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (elect_one()) f_qk<D>(P, smem, sy, tmem, abort);
+      __syncwarp();
+    } else if (warp == 2) {
+      if (elect_one()) f_pv<D>(P, smem, sy, tmem, abort);
+      __syncwarp();
+    } else if (warp == 3) {
+      f_load_v<D>(P, &mv, smem, sy, abort);
+      __syncwarp();
+    }
   } else if (warp < 12) {
     f_softmax<D>(P, smem, sy, tmem, abort);
   } else {
@@ -654,10 +726,6 @@ cudaError_t launch_f(const DiffArgs &a, cudaStream_t st) {
       !cross::cross_map(enc, &mo, a.x.o, s.B, s.Sq, s.h, D, o_st, pk.G, pk.tq) ||
       !cross::cross_map(enc, &mo2, a.o2 ? a.o2 : a.x.o, s.B, s.Sq, s.h, D, o_st, pk.G, pk.tq))
     return cudaErrorInvalidValue;
-  int dev = 0, sms = 0;
-  if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
-  if ((err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-    return err;
   auto kern = diff_attn_tc_kernel<D>;
   if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   f_smem_bytes<D>())) != cudaSuccess)
@@ -675,16 +743,16 @@ cudaError_t launch_f(const DiffArgs &a, cudaStream_t st) {
   p.scale_log2 = a.x.scale == 0.f ? 1e-30f : fabsf(a.x.scale) * 1.4426950408889634f;
   p.neg = a.x.scale < 0.f ? kIdescNegA : 0u;
   p.status = a.x.status;
-  const DiffRuns runs = diff_runs(a, NABLA_BF16);
-  p.nsplit = runs.plan.runs, p.rows = (size_t)runs.rows;
-  p.po = runs.po, p.plse = runs.plse;
-  p.whole = (uint32_t)runs.plan.whole;
-  p.units = (uint32_t)(runs.plan.whole + runs.plan.rest * runs.plan.runs);
-  const unsigned grid = p.units < (unsigned)sms ? p.units : (unsigned)sms;
+  const DiffPlan plan = diff_fwd_plan(s, NABLA_BF16);
+  p.whole = (uint32_t)plan.whole, p.cut = plan.cut;
+  const DiffRuns parts = diff_runs(a, NABLA_BF16);
+  p.po = parts.po, p.plse = parts.plse;
+  const unsigned grid =
+      plan.cut || plan.whole > diff::kCtas ? (unsigned)diff::kCtas : (unsigned)plan.whole;
   err = launch_pdl(kern, dim3(grid), dim3(C::kThreads), f_smem_bytes<D>(), st, mq, mk, mv, mo,
                    mo2, p);
-  if (err != cudaSuccess || p.nsplit == 1) return err;
-  return launch_diff_join(a, NABLA_BF16, runs, st);
+  if (err != cudaSuccess || !plan.cut) return err;
+  return launch_diff_stream_join(a, parts, st);
 }
 
 }  // namespace

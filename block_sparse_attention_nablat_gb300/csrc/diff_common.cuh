@@ -33,5 +33,71 @@ __device__ __forceinline__ uint64_t k_step(int kk, int box) {
   return (uint64_t)(((kk >> 2) * box + (kk & 3) * 32) >> 4);
 }
 
+// ---- How the forward's units (128 packed rows of a batch and key head, `per` of them a
+// batch) are dealt out.  The first `whole` go round the CTAs, so that those at work share a
+// few heads' states in L2.  The others, a round or two of them, are laid end to end, every
+// unit as long as its batch has state tiles (one, where it has none), and cut into kCtas
+// equal pieces: however the lengths differ, every CTA gets the same.  A CTA's piece begins and
+// ends inside a unit; those parts' results go to its two places in the workspace.
+constexpr int kCtas = 152;  // GB300's SMs
+
+__device__ __forceinline__ int weight(const int32_t *kv_len, int b, int Sk) {
+  const int n = (cross::batch_len(kv_len, b, Sk) + kStates - 1) / kStates;
+  return n > 0 ? n : 1;
+}
+
+struct Span {  // tile t of unit `unit` of batch b
+  int b, unit, t;
+};
+
+// All of a warp: the length of all units, and where position `at` lies.
+__device__ __forceinline__ long span_total(const int32_t *kv_len, int B, int Sk, int per) {
+  if (!kv_len) return (long)B * per * weight(nullptr, 0, Sk);
+  long n = 0;
+  for (int b = threadIdx.x & 31; b < B; b += 32) n += weight(kv_len, b, Sk);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * per;
+}
+__device__ __forceinline__ Span span_find(const int32_t *kv_len, int B, int Sk, int per, long at) {
+  if (!kv_len) {
+    const int w = weight(nullptr, 0, Sk);
+    const long u = at / w;
+    return Span{(int)(u / per), (int)(u % per), (int)(at - u * w)};
+  }
+  const int lane = threadIdx.x & 31;
+  long base = 0;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const int w = b0 + lane < B ? weight(kv_len, b0 + lane, Sk) : 0;
+    long end = (long)w * per;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    const uint32_t in = __ballot_sync(0xffffffffu, at < base + end);
+    if (in) {
+      const int l = __ffs(in) - 1, wl = __shfl_sync(0xffffffffu, w, l);
+      const long rest = at - base - __shfl_sync(0xffffffffu, end - (long)w * per, l);
+      return Span{b0 + l, (int)(rest / wl), (int)(rest % wl)};
+    }
+    base += __shfl_sync(0xffffffffu, end, 31);
+  }
+  return Span{B, 0, 0};  // the end
+}
+// The position of unit `u`.
+__device__ __forceinline__ long span_of_unit(const int32_t *kv_len, int Sk, int per, long u) {
+  const int b = (int)(u / per), lane = threadIdx.x & 31;
+  if (!kv_len) return u * weight(nullptr, 0, Sk);
+  long n = 0;
+  for (int i = lane; i < b; i += 32) n += weight(kv_len, i, Sk);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  const long in = u - (long)b * per;
+  return n * per + (in ? in * weight(kv_len, b, Sk) : 0);
+}
+// Where the piece of CTA c begins, of `n` positions from p0 on.
+__device__ __forceinline__ long piece(long p0, long n, int c) { return p0 + n * c / kCtas; }
+
 }  // namespace diff
 }  // namespace nabla

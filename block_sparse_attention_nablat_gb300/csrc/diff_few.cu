@@ -356,7 +356,7 @@ cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
   p.scale_log2 = a.x.scale * 1.4426950408889634f;
   p.status = a.x.status;
   const DiffRuns runs = diff_runs(a, dt);
-  p.nsplit = runs.plan.runs, p.po = runs.po, p.plse = runs.plse;
+  p.nsplit = runs.runs, p.po = runs.po, p.plse = runs.plse;
   cudaError_t e;
   if (dt == NABLA_BF16)
     e = s.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, st) : launch_rows<__nv_bfloat16, 128>(p, st);

@@ -16,14 +16,13 @@ struct JoinParams {
   const float *lam;
   T *o, *o2;
   float *lse;  // [B, h, 2, Sq]
-  long rows;   // B h Sq, in that order, or (packed) the packed rows of the units from `first`
-  long first;
-  int Sq, h, hk, nsplit, lam_step, G, tq, nqt;
+  long rows;   // B h Sq
+  int Sq, h, nsplit, lam_step;
 };
 
 // o_m = sum_i 2^(lse_mi - lse_m) o_mi, o = o_1 - lam o_2.  A warp per row, 16 bytes a lane
 // (at D 64 half of them have none); four runs are read at a time.
-template <typename T, int D, bool kPacked>
+template <typename T, int D>
 __global__ void __launch_bounds__(256)
     diff_join_kernel(const __grid_constant__ JoinParams<T> P) {
   const int lane = threadIdx.x & 31, col = lane * 4;
@@ -31,20 +30,7 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= P.rows) return;
-  long b, hh, token;
-  if (kPacked) {
-    const long unit = P.first + (row >> 7), bj = unit / P.nqt, qt = unit - bj * P.nqt;
-    const int r = (int)(row & 127), t = (r & 63) / P.G;
-    b = bj / P.hk;
-    hh = (bj - b * P.hk) * P.G + (r & 63) - t * P.G;
-    token = (qt * 2 + (r >> 6)) * P.tq + t;
-    if (t >= P.tq || token >= P.Sq) return;  // none
-  } else {
-    const long bh = row / P.Sq;
-    token = row - bh * P.Sq;
-    b = bh / P.h;
-    hh = bh - b * P.h;
-  }
+  const long bh = row / P.Sq, token = row - bh * P.Sq, b = bh / P.h, hh = bh - b * P.h;
   float4 o[2];
   float lse[2];
 #pragma unroll
@@ -103,61 +89,134 @@ __global__ void __launch_bounds__(256)
 template <typename T, int D>
 cudaError_t launch_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st) {
   const CrossShape &s = a.x.s;
-  const cross::Packing pk = cross::packing(s);
-  JoinParams<T> p{};
-  p.po = r.po, p.plse = r.plse, p.lam = a.lam;
-  p.o = static_cast<T *>(a.x.o), p.o2 = static_cast<T *>(a.o2), p.lse = a.x.lse;
-  p.rows = r.rows, p.first = r.plan.whole;
-  p.Sq = s.Sq, p.h = s.h, p.hk = s.hk, p.nsplit = r.plan.runs, p.lam_step = a.lam_n > 1 ? 1 : 0;
-  p.G = pk.G, p.tq = pk.tq, p.nqt = (pk.nsub + 1) / 2;
-  const dim3 grid((unsigned)((r.rows + 7) / 8));
-  return r.plan.packed ? launch_pdl(diff_join_kernel<T, D, true>, grid, dim3(256), 0, st, p)
-                       : launch_pdl(diff_join_kernel<T, D, false>, grid, dim3(256), 0, st, p);
+  const long rows = (long)s.B * s.h * s.Sq;
+  const JoinParams<T> p{r.po, r.plse, a.lam, static_cast<T *>(a.x.o), static_cast<T *>(a.o2),
+                        a.x.lse, rows, s.Sq, s.h, r.runs, a.lam_n > 1 ? 1 : 0};
+  return launch_pdl(diff_join_kernel<T, D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, p);
+}
+
+// The parts of the tcgen05 kernel's units: blockIdx.y = c - 1 joins the unit that the pieces
+// of CTAs c - 1 and c share, if c is the first to go on with it; a warp per packed row.
+struct StreamParams {
+  const float *po, *plse;  // [kCtas, 2 places, 2 maps, 128, D] and [.., 128]
+  const float *lam;
+  __nv_bfloat16 *o, *o2;
+  float *lse;
+  const int32_t *kv_len;
+  int lam_step, B, Sq, Sk, h, hk, G, tq, nqt;
+  long whole;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) diff_stream_join_kernel(const __grid_constant__ StreamParams P) {
+  const int lane = threadIdx.x & 31, col = lane * 4, c = blockIdx.y + 1;
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), t = (r & 63) / P.G;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int per = P.nqt * P.hk;
+  const long p0 = diff::span_of_unit(P.kv_len, P.Sk, per, P.whole);
+  const long n = diff::span_total(P.kv_len, P.B, P.Sk, per) - p0;
+  const long from = diff::piece(p0, n, c), prev = diff::piece(p0, n, c - 1);
+  if (from >= p0 + n || from == prev) return;
+  const diff::Span at = diff::span_find(P.kv_len, P.B, P.Sk, per, from);
+  const long begin = from - at.t, end = begin + diff::weight(P.kv_len, at.b, P.Sk);
+  if (at.t == 0 || prev > begin) return;  // begins there; joined by an earlier block
+  const int j = at.unit / P.nqt, qt = at.unit - j * P.nqt;
+  const int token = (qt * 2 + (r >> 6)) * P.tq + t, hh = j * P.G + (r & 63) - t * P.G;
+  if (t >= P.tq || token >= P.Sq) return;  // none
+  int last = c;
+  while (last + 1 < diff::kCtas && diff::piece(p0, n, last + 1) < end) ++last;
+  float4 o[2];
+  float lse[2];
+#pragma unroll
+  for (int map = 0; map < 2; ++map) {
+    float m = -INFINITY, l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a CTA's second place, where its piece began before this unit
+    auto place = [&](int i) {
+      return ((size_t)i * 2 + (diff::piece(p0, n, i) < begin)) * 256 + map * 128 + r;
+    };
+    for (int i = c - 1; i <= last; ++i) {
+      if (i > c - 1 && diff::piece(p0, n, i) == diff::piece(p0, n, i + 1)) continue;  // empty
+      m = fmaxf(m, P.plse[place(i)]);
+    }
+    for (int i = c - 1; i <= last; ++i) {
+      if (i > c - 1 && diff::piece(p0, n, i) == diff::piece(p0, n, i + 1)) continue;
+      const float li = P.plse[place(i)], w = li == -INFINITY ? 0.f : exp2f(li - m);
+      if (col < D) {
+        const float4 x = *reinterpret_cast<const float4 *>(P.po + place(i) * D + col);
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
+      }
+      l += w;
+    }
+    const float inv = l > 0.f ? 1.0f / l : l;  // NaN stays
+    o[map] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    lse[map] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+  }
+  if (P.lse && lane < 2)
+    P.lse[(((size_t)at.b * P.h + hh) * 2 + lane) * P.Sq + token] = lane ? lse[1] : lse[0];
+  if (col >= D) return;
+  const float lam = P.lam[hh * P.lam_step];
+  const size_t to = (((size_t)at.b * P.Sq + token) * P.h + hh) * D + col;
+  auto put = [](__nv_bfloat16 *p, const float4 &v) {
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
+  };
+  put(P.o + to, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
+                            fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
+  if (P.o2) put(P.o2 + to, o[1]);
 }
 
 }  // namespace
 
-// How the forward's states are split into runs.  Sized for GB300's 152 SMs, so that the
-// workspace depends on the shape alone.
+// How the forward is split.  Sized for GB300's 152 SMs, so that the workspace depends on the
+// shape alone.
 //
-// bf16: units of 128 packed rows go on the SMs in rounds; those of the last one, where they
-// leave SMs idle, are split into as many runs as fill them (512 states each at least: a run
-// costs some 2 us and the join 4).  8192 x 8192 states, 12 heads: 768 units, the last 8 in 19
-// runs.  Few rows: runs of 512 states, or longer ones where those are many.  fp32: as in the
-// cross attention, whose tiles' costs have the same proportions.
+// bf16: units of 128 packed rows that go round the SMs, and from 1024 states on a last round
+// or two cut into equal pieces (below that a unit costs less than joining its parts).  Few
+// rows: runs of 512 states, or longer ones where those are many.  fp32: runs as in the cross
+// attention, whose tiles' costs have the same proportions.
 DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt) {
   if (diff_few_rows(s)) {
     const long runs = (s.Sk + 511) / 512, room = 152L * 16 / ((long)s.B * s.hk);
-    return {0, 0, runs <= 1 || room <= 1 ? 1 : (int)(runs < room ? runs : room), false};
+    return {0, runs <= 1 || room <= 1 ? 1 : (int)(runs < room ? runs : room), false};
   }
-  if (dt == NABLA_F32) return {0, 0, cross_simt_plan(s).nsplit, false};
+  if (dt == NABLA_F32) return {0, cross_simt_plan(s).nsplit, false};
   const long units = (long)s.B * s.hk * ((cross::packing(s).nsub + 1) / 2);
-  const long tiles = (s.Sk + diff::kStates - 1) / diff::kStates;
-  const long rest = units % 152, room = rest ? 152 / rest : 1;
-  const long n = room < tiles / 8 ? room : tiles / 8;
-  return n < 2 ? DiffPlan{units, 0, 1, true} : DiffPlan{units - rest, rest, (int)n, true};
-}
-
-namespace {
-// Rows of a run's partial results.
-long run_rows(const CrossShape &s, const DiffPlan &p) {
-  return p.packed ? p.rest * 128 : (long)s.B * s.h * s.Sq;
-}
-}  // namespace
-
-size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
-  const DiffPlan p = diff_fwd_plan(s, dt);
-  return p.runs > 1 ? (size_t)p.runs * 2 * run_rows(s, p) * (s.D + 1) * sizeof(float) : 0;
+  if (s.Sk < 1024) return {units, 1, false};
+  return {units < 2 * diff::kCtas ? 0 : (units / diff::kCtas - 1) * diff::kCtas, 1, true};
 }
 
 DiffRuns diff_runs(const DiffArgs &a, nabla_dtype dt) {
-  DiffRuns r{};
-  r.plan = diff_fwd_plan(a.x.s, dt);
-  if (r.plan.runs == 1) return r;
-  r.rows = run_rows(a.x.s, r.plan);
+  const CrossShape &s = a.x.s;
+  const DiffPlan p = diff_fwd_plan(s, dt);
+  DiffRuns r{p.runs, nullptr, nullptr};
+  if (p.runs == 1 && !p.cut) return r;
+  const size_t rows = p.cut ? diff::kCtas * 2 * 256 : (size_t)p.runs * 2 * s.B * s.h * s.Sq;
   r.po = static_cast<float *>(a.x.workspace);
-  r.plse = r.po + (size_t)r.plan.runs * 2 * r.rows * a.x.s.D;
+  r.plse = r.po + rows * s.D;
   return r;
+}
+
+size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
+  const DiffPlan p = diff_fwd_plan(s, dt);
+  if (p.cut) return (size_t)diff::kCtas * 2 * 256 * (s.D + 1) * sizeof(float);
+  return p.runs > 1 ? (size_t)p.runs * 2 * s.B * s.h * s.Sq * (s.D + 1) * sizeof(float) : 0;
+}
+
+cudaError_t launch_diff_stream_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st) {
+  const CrossShape &s = a.x.s;
+  const cross::Packing pk = cross::packing(s);
+  const StreamParams p{r.po, r.plse, a.lam, static_cast<__nv_bfloat16 *>(a.x.o),
+                       static_cast<__nv_bfloat16 *>(a.o2), a.x.lse, a.x.kv_len,
+                       a.lam_n > 1 ? 1 : 0, s.B, s.Sq, s.Sk, s.h, s.hk, pk.G, pk.tq,
+                       (pk.nsub + 1) / 2, diff_fwd_plan(s, NABLA_BF16).whole};
+  const dim3 grid(16, diff::kCtas - 1);
+  return s.D == 64 ? launch_pdl(diff_stream_join_kernel<64>, grid, dim3(256), 0, st, p)
+                   : launch_pdl(diff_stream_join_kernel<128>, grid, dim3(256), 0, st, p);
 }
 
 cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, const DiffRuns &r,

@@ -495,7 +495,7 @@ cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st) {
   p.x.lse_out = a.x.lse;
   p.o2 = static_cast<float *>(a.o2);
   const DiffRuns runs = diff_runs(a, NABLA_F32);
-  p.x.nsplit = runs.plan.runs, p.x.po = runs.po, p.x.plse = runs.plse;
+  p.x.nsplit = runs.runs, p.x.po = runs.po, p.x.plse = runs.plse;
   const long subs = (long)a.x.s.B * a.x.s.hk * p.x.nsub;
   const int A = cross_simt_plan(a.x.s).A;
   const cudaError_t e =

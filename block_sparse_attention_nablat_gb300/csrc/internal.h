@@ -168,23 +168,23 @@ struct DiffArgs {
   nabla_strides o2_st;  // backward
   float *dlam;
 };
-// Runs of states: `runs` of every row, or (packed: the tcgen05 kernel's units of 128 rows)
-// `whole` units in one and the `rest` in `runs`.
+// How it is split: `runs` of the states of every row, or (tcgen05 kernel) `whole` units in one
+// and, where `cut`, the others in equal pieces.
 struct DiffPlan {
-  long whole, rest;
+  long whole;
   int runs;
-  bool packed;
+  bool cut;
 };
 DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt);
 size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt);
-struct DiffRuns {  // partial results: [runs, 2, rows, D] and [runs, 2, rows]; none for one run
-  DiffPlan plan;
-  long rows;
+struct DiffRuns {  // partial results: [runs, 2, B, h, Sq, D] and [runs, 2, B, h, Sq], or of pieces
+  int runs;
   float *po, *plse;
 };
 DiffRuns diff_runs(const DiffArgs &a, nabla_dtype dt);
 cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, const DiffRuns &r,
                              cudaStream_t st);
+cudaError_t launch_diff_stream_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st);
 // K12: bf16, tcgen05.  K12f: fp32, CUDA cores.
 cudaError_t launch_diff_attn_tc(const DiffArgs &a, cudaStream_t st);
 // K12s: at most four packed rows a key head.

@@ -187,8 +187,11 @@ CASES = [  # B, Sq, Sk, h, hk, D, lens, packed
     (3, 4, 700, 2, 2, 64, [700, 0, 3], "heads"),     # four
     (2, 2, 1100, 4, 2, 128, [1100, 513], True),      # two tokens of two heads
     (70, 1, 600, 3, 1, 128, None, False),            # three
-    (2, 4900, 1100, 2, 2, 64, [1100, 70], False),    # 156 units, the last four in runs
-    (1, 9800, 1030, 2, 2, 128, None, False),         # 154, the last two in runs
+    (2, 4900, 1100, 2, 2, 64, [1100, 70], False),    # 156 units in 152 pieces
+    (1, 9800, 1030, 2, 2, 128, None, False),         # 154
+    (2, 10000, 1030, 2, 2, 64, [1030, 800], False),  # 316: 152 go round, the others are cut
+    (40, 3, 1100, 4, 2, 128, [1100, 0, 5, 700, 64] * 8, False),  # 80 units of all lengths
+    (3, 40, 5000, 4, 2, 64, [5000, 0, 4321], True),  # few long units, each in many parts
 ]
 
 
