@@ -860,7 +860,7 @@ nabla_status nabla_diff_attn_fwd(const void *q, const nabla_strides *q_st, const
   cudaError_t e;
   a.x.status = device_status_ptr(&e);
   if (!a.x.status) return NABLA_ERR_CUDA;
-  if (diff_few_rows(a.x.s)) return from_cuda(launch_diff_few(a, dt, st));
+  if (diff_few_rows(a.x.s, dt)) return from_cuda(launch_diff_few(a, dt, st));
   return from_cuda(dt == NABLA_BF16 ? launch_diff_attn_tc(a, st) : launch_diff_attn_simt(a, st));
 }
 

@@ -1,5 +1,5 @@
-// K12s -- differential attention forward of few rows: at most four packed rows a key head
-// (single tokens of grouped heads), bf16 and fp32.
+// K12s -- differential attention forward of few rows: a single packed row a key head (one token)
+// in bf16, up to four in fp32.
 //
 // Bound by the bytes of K and V.  D columns of a state lie over the lanes of a group, 16
 // bytes a lane (bf16, D 128: 16 lanes, two states a warp and load), the first half of the
@@ -10,8 +10,7 @@
 // lane's columns, added up over the half group; then every lane has its own map's P, takes
 // the other's from the other half, and adds both times its columns of V.  The groups of a CTA
 // are joined in shared memory at the end, CTAs (runs of a batch's states) by diff_join.
-// At most four rows: their arithmetic (some 100 instructions for two states and three rows)
-// stays behind the loads.
+// 16 x 1000 states at most, half of them there, 16 heads, D 128, bf16: 21 us, 3.2 TB/s.
 #include <cuda_bf16.h>
 
 #include <cfloat>
@@ -331,18 +330,24 @@ cudaError_t launch_few(const FewParams &p, cudaStream_t st) {
   return launch_pdl(kern, dim3((unsigned)((long)p.B * p.hk * p.nsplit)), dim3(256), smem, st, p);
 }
 
-template <typename T, int D>
-cudaError_t launch_rows(const FewParams &p, cudaStream_t st) {
+template <int D>
+cudaError_t launch_rows(const FewParams &p, cudaStream_t st) {  // fp32
   const int rows = p.Sq * p.G;
-  return rows == 1   ? launch_few<T, D, 1>(p, st)
-         : rows == 2 ? launch_few<T, D, 2>(p, st)
-         : rows == 3 ? launch_few<T, D, 3>(p, st)
-                     : launch_few<T, D, 4>(p, st);
+  return rows == 1   ? launch_few<float, D, 1>(p, st)
+         : rows == 2 ? launch_few<float, D, 2>(p, st)
+         : rows == 3 ? launch_few<float, D, 3>(p, st)
+                     : launch_few<float, D, 4>(p, st);
 }
 
 }  // namespace
 
-bool diff_few_rows(const CrossShape &s) { return (long)s.Sq * (s.h / s.hk) <= 4; }
+// fp32: up to four rows (24 heads on 8, 16 x 1000 states: 29 us, 118 in the general form).
+// bf16: a single row; the tensor cores' form takes two and more in the time of one, and its
+// pieces are equal (D 128, us here and there: 1 row, 1 x 8192 states, 8 heads 21, 28; 16 x 1000,
+// 16 heads 21, 23; 4 x 100 3.7, 5.8; 3 rows, 16 x 4096, 24 heads 56, 44; 16 x 128 8.0, 7.1).
+bool diff_few_rows(const CrossShape &s, nabla_dtype dt) {
+  return (long)s.Sq * (s.h / s.hk) <= (dt == NABLA_F32 ? 4 : 1);
+}
 
 cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) {
   const CrossShape &s = a.x.s;
@@ -359,9 +364,10 @@ cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
   p.nsplit = runs.runs, p.po = runs.po, p.plse = runs.plse;
   cudaError_t e;
   if (dt == NABLA_BF16)
-    e = s.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, st) : launch_rows<__nv_bfloat16, 128>(p, st);
+    e = s.D == 64 ? launch_few<__nv_bfloat16, 64, 1>(p, st)
+                  : launch_few<__nv_bfloat16, 128, 1>(p, st);
   else
-    e = s.D == 64 ? launch_rows<float, 64>(p, st) : launch_rows<float, 128>(p, st);
+    e = s.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
   if (e != cudaSuccess || p.nsplit == 1) return e;
   return launch_diff_join(a, dt, runs, st);
 }

@@ -108,59 +108,85 @@ struct StreamParams {
 };
 
 template <int D>
-__global__ void __launch_bounds__(256) diff_stream_join_kernel(const __grid_constant__ StreamParams P) {
+__global__ void __launch_bounds__(256)
+    diff_stream_join_kernel(const __grid_constant__ StreamParams P) {
+  __shared__ int place[diff::kCtas];  // of the parts: CTA * 2 + its place
+  __shared__ int count, batch, unit;
   const int lane = threadIdx.x & 31, col = lane * 4, c = blockIdx.y + 1;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5), t = (r & 63) / P.G;
   pdl_launch_dependents();
   pdl_wait();
-  const int per = P.nqt * P.hk;
-  const long p0 = diff::span_of_unit(P.kv_len, P.Sk, per, P.whole);
-  const long n = diff::span_total(P.kv_len, P.B, P.Sk, per) - p0;
-  const long from = diff::piece(p0, n, c), prev = diff::piece(p0, n, c - 1);
-  if (from >= p0 + n || from == prev) return;
-  const diff::Span at = diff::span_find(P.kv_len, P.B, P.Sk, per, from);
-  const long begin = from - at.t, end = begin + diff::weight(P.kv_len, at.b, P.Sk);
-  if (at.t == 0 || prev > begin) return;  // begins there; joined by an earlier block
-  const int j = at.unit / P.nqt, qt = at.unit - j * P.nqt;
+  if (threadIdx.x < 32) {  // the unit and its parts
+    const int per = P.nqt * P.hk;
+    const long p0 = diff::span_of_unit(P.kv_len, P.Sk, per, P.whole);
+    const long n = diff::span_total(P.kv_len, P.B, P.Sk, per) - p0;
+    const long from = diff::piece(p0, n, c), prev = diff::piece(p0, n, c - 1);
+    int parts = 0;
+    if (from < p0 + n && from != prev) {
+      const diff::Span at = diff::span_find(P.kv_len, P.B, P.Sk, per, from);
+      const long begin = from - at.t, end = begin + diff::weight(P.kv_len, at.b, P.Sk);
+      // (one that begins here has no part before; or an earlier block joins it)
+      if (at.t > 0 && prev <= begin) {
+        for (int i0 = c - 1; i0 < diff::kCtas; i0 += 32) {
+          const int i = i0 + lane;
+          const long a = i < diff::kCtas ? diff::piece(p0, n, i) : end;
+          const bool in = a < end, some = in && a != diff::piece(p0, n, i + 1);
+          const uint32_t mask = __ballot_sync(0xffffffffu, some);
+          // its second place, where the CTA's piece began before this unit
+          if (some) place[parts + __popc(mask & ((1u << lane) - 1u))] = i * 2 + (a < begin);
+          parts += __popc(mask);
+          if (!__any_sync(0xffffffffu, in && i == i0 + 31)) break;
+        }
+        batch = at.b;
+        unit = at.unit;
+      }
+    }
+    if (lane == 0) count = parts;
+  }
+  __syncthreads();
+  if (count == 0) return;
+  const int j = unit / P.nqt, qt = unit - j * P.nqt;
   const int token = (qt * 2 + (r >> 6)) * P.tq + t, hh = j * P.G + (r & 63) - t * P.G;
   if (t >= P.tq || token >= P.Sq) return;  // none
-  int last = c;
-  while (last + 1 < diff::kCtas && diff::piece(p0, n, last + 1) < end) ++last;
   float4 o[2];
   float lse[2];
 #pragma unroll
   for (int map = 0; map < 2; ++map) {
+    auto row = [&](int i) { return (size_t)place[i] * 256 + map * 128 + r; };
     float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < count; i += 32) m = fmaxf(m, P.plse[row(i)]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    // a CTA's second place, where its piece began before this unit
-    auto place = [&](int i) {
-      return ((size_t)i * 2 + (diff::piece(p0, n, i) < begin)) * 256 + map * 128 + r;
-    };
-    for (int i = c - 1; i <= last; ++i) {
-      if (i > c - 1 && diff::piece(p0, n, i) == diff::piece(p0, n, i + 1)) continue;  // empty
-      m = fmaxf(m, P.plse[place(i)]);
-    }
-    for (int i = c - 1; i <= last; ++i) {
-      if (i > c - 1 && diff::piece(p0, n, i) == diff::piece(p0, n, i + 1)) continue;
-      const float li = P.plse[place(i)], w = li == -INFINITY ? 0.f : exp2f(li - m);
-      if (col < D) {
-        const float4 x = *reinterpret_cast<const float4 *>(P.po + place(i) * D + col);
-        acc.x = fmaf(w, x.x, acc.x);
-        acc.y = fmaf(w, x.y, acc.y);
-        acc.z = fmaf(w, x.z, acc.z);
-        acc.w = fmaf(w, x.w, acc.w);
+    for (int i0 = 0; i0 < count; i0 += 4) {
+      float li[4];
+      float4 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        li[e] = i0 + e < count ? P.plse[row(i0 + e)] : -INFINITY;
+        x[e] = i0 + e < count && col < D
+                   ? *reinterpret_cast<const float4 *>(P.po + row(i0 + e) * D + col)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      l += w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = li[e] == -INFINITY ? 0.f : exp2f(li[e] - m);
+        l += w;
+        acc.x = fmaf(w, x[e].x, acc.x);
+        acc.y = fmaf(w, x[e].y, acc.y);
+        acc.z = fmaf(w, x[e].z, acc.z);
+        acc.w = fmaf(w, x[e].w, acc.w);
+      }
     }
     const float inv = l > 0.f ? 1.0f / l : l;  // NaN stays
     o[map] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     lse[map] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
   }
   if (P.lse && lane < 2)
-    P.lse[(((size_t)at.b * P.h + hh) * 2 + lane) * P.Sq + token] = lane ? lse[1] : lse[0];
+    P.lse[(((size_t)batch * P.h + hh) * 2 + lane) * P.Sq + token] = lane ? lse[1] : lse[0];
   if (col >= D) return;
   const float lam = P.lam[hh * P.lam_step];
-  const size_t to = (((size_t)at.b * P.Sq + token) * P.h + hh) * D + col;
+  const size_t to = (((size_t)batch * P.Sq + token) * P.h + hh) * D + col;
   auto put = [](__nv_bfloat16 *p, const float4 &v) {
     *reinterpret_cast<uint2 *>(p) =
         make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
@@ -180,7 +206,7 @@ __global__ void __launch_bounds__(256) diff_stream_join_kernel(const __grid_cons
 // rows: runs of 512 states, or longer ones where those are many.  fp32: runs as in the cross
 // attention, whose tiles' costs have the same proportions.
 DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt) {
-  if (diff_few_rows(s)) {
+  if (diff_few_rows(s, dt)) {
     const long runs = (s.Sk + 511) / 512, room = 152L * 16 / ((long)s.B * s.hk);
     return {0, runs <= 1 || room <= 1 ? 1 : (int)(runs < room ? runs : room), false};
   }
@@ -214,7 +240,9 @@ cudaError_t launch_diff_stream_join(const DiffArgs &a, const DiffRuns &r, cudaSt
                        static_cast<__nv_bfloat16 *>(a.o2), a.x.lse, a.x.kv_len,
                        a.lam_n > 1 ? 1 : 0, s.B, s.Sq, s.Sk, s.h, s.hk, pk.G, pk.tq,
                        (pk.nsub + 1) / 2, diff_fwd_plan(s, NABLA_BF16).whole};
-  const dim3 grid(16, diff::kCtas - 1);
+  // blocks of eight packed rows, as many as a unit can have
+  const int used = s.Sq < pk.tq ? s.Sq * pk.G : s.Sq < 2 * pk.tq ? 64 + (s.Sq - pk.tq) * pk.G : 128;
+  const dim3 grid((unsigned)((used + 7) / 8), diff::kCtas - 1);
   return s.D == 64 ? launch_pdl(diff_stream_join_kernel<64>, grid, dim3(256), 0, st, p)
                    : launch_pdl(diff_stream_join_kernel<128>, grid, dim3(256), 0, st, p);
 }

@@ -187,8 +187,8 @@ cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, const DiffRuns &
 cudaError_t launch_diff_stream_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st);
 // K12: bf16, tcgen05.  K12f: fp32, CUDA cores.
 cudaError_t launch_diff_attn_tc(const DiffArgs &a, cudaStream_t st);
-// K12s: at most four packed rows a key head.
-bool diff_few_rows(const CrossShape &s);
+// K12s: a packed row a key head (fp32: four at most).
+bool diff_few_rows(const CrossShape &s, nabla_dtype dt);
 cudaError_t launch_diff_few(const DiffArgs &a, nabla_dtype dt, cudaStream_t st);
 cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st);
 // K13: the backward.  Workspace: the packed rows' numbers (five), what lam's gradient is
