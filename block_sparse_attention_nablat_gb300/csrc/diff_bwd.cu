@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kRowsArrays = 5;
 
-// -lse_1, -lse_2, -delta_1, -delta_2 and lam of the packed rows [B, hk, nsub, 64], with
+// -lse_1, -lse_2, -delta_1, -delta_2 and -lam of the packed rows [B, hk, nsub, 64], with
 // delta_2 = <dout, o2> and delta_1 = <dout, o> + lam delta_2; -inf and 0 where a row is none
 // or has no states, so that its P is 0.  A block takes a 64-row subtile, D / 8 lanes a row;
 // HBM-bound (o, o2 and dout read once), so a thread's rows are all in flight at once.
@@ -79,15 +79,16 @@ __global__ void __launch_bounds__(256) diff_prep_kernel(const __grid_constant__ 
                       : lane == 1 ? n[i][1]
                       : lane == 2 ? -fmaf(n[i][2], s2, s)
                       : lane == 3 ? -s2
-                                  : n[i][2];
+                                  : -n[i][2];
       P.rows[lane * P.nrows + (size_t)blockIdx.x * 64 + r0 + i * kPass] = v;
     }
   }
 }
 
 // lam's gradient: minus the sum of the rows' numbers t2 ([runs][nrows]; 0 where a row is
-// none), over all rows or over each head's.  Block (i, c): chunk c of gradient i; one chunk:
-// straight to dlam, else to part [i][chunks], which lam_sum_kernel adds up.
+// none).  Block (j, c): chunk c of key head j's subtiles, four at a time; lane r of a subtile
+// adds up the numbers of head r % G.  One chunk and a weight for each head: straight to dlam,
+// else to part [h][chunks], which lam_sum_kernel adds up.
 struct LamParams {
   const float *t2;
   size_t nrows;
@@ -95,49 +96,55 @@ struct LamParams {
   float *part, *dlam;
 };
 
-__device__ __forceinline__ float block_sum(float v) {
+__global__ void __launch_bounds__(256) lam_part_kernel(const LamParams P) {
+  __shared__ float sums[256];
+  const int j = blockIdx.x, chunk = blockIdx.y, chunks = gridDim.y, r = threadIdx.x & 63;
+  pdl_launch_dependents();
+  const long n = (long)P.B * P.nsub, e0 = n * chunk / chunks, e1 = n * (chunk + 1) / chunks;
+  pdl_wait();
+  const long count = (e1 - e0) * P.runs;
+  float v = 0.f;
+  for (long k0 = threadIdx.x >> 6; k0 < count; k0 += 4 * 8) {
+    float x[8];  // under way together
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t k = (uint32_t)k0 + 4 * i, run = k % (uint32_t)P.runs;
+      const uint32_t e = (uint32_t)e0 + k / (uint32_t)P.runs, b = e / (uint32_t)P.nsub;
+      const size_t row = ((size_t)(b * P.hk + j) * P.nsub + e - b * P.nsub) * 64 + r;
+      x[i] = k < count ? P.t2[run * P.nrows + row] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += x[i];
+  }
+  sums[threadIdx.x] = v;
+  __syncthreads();
+  if ((int)threadIdx.x >= P.G) return;  // head threadIdx.x of the group
+  v = 0.f;
+  for (int q = 0; q < 4; ++q)
+    for (int t = 0; t < P.tq; ++t) v += sums[q * 64 + t * P.G + threadIdx.x];
+  const int head = j * P.G + threadIdx.x;
+  if (P.each && chunks == 1)
+    P.dlam[head] = -v;
+  else
+    P.part[(size_t)head * chunks + chunk] = v;
+}
+
+// Block i: gradient i, minus the sum of n of the parts.
+__global__ void __launch_bounds__(256) lam_sum_kernel(const LamParams P, int n) {
   __shared__ float sums[8];
+  pdl_launch_dependents();
+  pdl_wait();
+  float v = 0.f;
+  for (int i = threadIdx.x; i < n; i += 256) v += P.part[(size_t)blockIdx.x * n + i];
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
   __syncthreads();
+  if (threadIdx.x) return;
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v += sums[i];
-  return v;
-}
-
-__global__ void __launch_bounds__(256) lam_part_kernel(const LamParams P) {
-  const uint32_t i = blockIdx.x, chunk = blockIdx.y, chunks = gridDim.y;
-  pdl_launch_dependents();
-  const uint32_t j = i / (uint32_t)P.G, in = i - j * P.G;  // key head, head in its group
-  const size_t n = P.each ? (size_t)P.B * P.nsub * P.tq : P.nrows;
-  const size_t e0 = n * chunk / chunks, e1 = n * (chunk + 1) / chunks;
-  pdl_wait();
-  float v = 0.f;
-  for (size_t e = e0 + threadIdx.x; e < e1; e += 256) {
-    size_t row = e;
-    if (P.each) {
-      const size_t bs = e / P.tq, t = e - bs * P.tq, b = bs / P.nsub, sub = bs - b * P.nsub;
-      row = ((b * P.hk + j) * P.nsub + sub) * 64 + t * P.G + in;
-    }
-    for (int r = 0; r < P.runs; ++r) v += P.t2[(size_t)r * P.nrows + row];
-  }
-  v = block_sum(v);
-  if (threadIdx.x == 0) {
-    if (chunks == 1)
-      P.dlam[i] = -v;
-    else
-      P.part[(size_t)i * chunks + chunk] = v;
-  }
-}
-
-__global__ void __launch_bounds__(256) lam_sum_kernel(const LamParams P, int chunks) {
-  pdl_launch_dependents();
-  pdl_wait();
-  float v = (int)threadIdx.x < chunks ? P.part[(size_t)blockIdx.x * chunks + threadIdx.x] : 0.f;
-  v = block_sum(v);
-  if (threadIdx.x == 0) P.dlam[blockIdx.x] = -v;
+  P.dlam[blockIdx.x] = -v;
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -148,17 +155,16 @@ struct BwdLayout {
   int nsplit, qsplit, truns, chunks;
   size_t rows, t2, part, qpart, lam, total;
 };
-BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt, int lam_n) {
+BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
   w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
   w.nrows = (size_t)s.B * s.hk * w.nsub * 64;
   w.nsplit = cross_dkv_splits(s, dt);
   w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : 1;
   w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : 1;
-  // a chunk of 8192 numbers takes a block about as long as starting one more kernel does
-  const size_t numbers = w.nrows * w.truns / (lam_n > 1 ? s.h : 1);
-  const size_t chunks = (numbers + 8191) / 8192;
-  w.chunks = chunks > 256 ? 256 : (int)chunks;
+  // 64 subtiles a chunk: sixteen loads a thread and run
+  const size_t chunks = ((size_t)s.B * w.nsub + 63) / 64;
+  w.chunks = chunks > 64 ? 64 : (int)chunks;
   w.rows = 0;
   w.t2 = round_up(kRowsArrays * w.nrows * sizeof(float));
   w.part = w.t2 + round_up(w.truns * w.nrows * sizeof(float));
@@ -168,7 +174,7 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt, int lam_n) {
   w.lam = w.qpart + (w.qsplit > 1 ? round_up((size_t)w.qsplit * s.B * s.Sq * s.h * s.D *
                                              sizeof(float))
                                   : 0);
-  w.total = w.lam + round_up((size_t)(lam_n > 1 ? s.h : 1) * 256 * sizeof(float));
+  w.total = w.lam + round_up((size_t)s.h * w.chunks * sizeof(float));
   return w;
 }
 
@@ -189,15 +195,11 @@ cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, cudaS
 
 }  // namespace
 
-size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt) {
-  // one weight or one a head: the larger of the two
-  const size_t a = bwd_layout(s, dt, 1).total, b = bwd_layout(s, dt, s.h).total;
-  return a > b ? a : b;
-}
+size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt) { return bwd_layout(s, dt).total; }
 
 cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) {
   const CrossShape &s = a.x.s;
-  const BwdLayout w = bwd_layout(s, dt, a.lam_n);
+  const BwdLayout w = bwd_layout(s, dt);
   char *ws = static_cast<char *>(a.x.workspace);
   auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
   const DiffRows r{at(w.rows), w.nrows, at(w.t2), w.nsub};
@@ -217,10 +219,10 @@ cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
   const bool each = a.lam_n > 1;
   const LamParams p{r.t2, w.nrows, w.truns, s.B, s.hk, pk.G, pk.tq, w.nsub, each ? 1 : 0,
                     at(w.lam), a.dlam};
-  const unsigned n = each ? (unsigned)s.h : 1u;
-  e = launch_pdl(lam_part_kernel, dim3(n, (unsigned)w.chunks), dim3(256), 0, st, p);
-  if (e != cudaSuccess || w.chunks == 1) return e;
-  return launch_pdl(lam_sum_kernel, dim3(n), dim3(256), 0, st, p, w.chunks);
+  e = launch_pdl(lam_part_kernel, dim3((unsigned)s.hk, (unsigned)w.chunks), dim3(256), 0, st, p);
+  if (e != cudaSuccess || (each && w.chunks == 1)) return e;
+  return launch_pdl(lam_sum_kernel, dim3(each ? (unsigned)s.h : 1u), dim3(256), 0, st, p,
+                    each ? w.chunks : s.h * w.chunks);
 }
 
 }  // namespace nabla

@@ -51,7 +51,7 @@ using tcattn::fma2;
 using tcattn::Ring;
 using tcattn::unf2;
 
-constexpr int kRowsArrays = 5;  // -lse_1, -lse_2, -delta_1, -delta_2, lam of the packed rows
+constexpr int kRowsArrays = 5;  // -lse_1, -lse_2, -delta_1, -delta_2, -lam of the packed rows
 
 template <int D>
 struct BCfg {
@@ -362,6 +362,12 @@ __device__ __forceinline__ uint32_t acc_col(int map, int c) {
   return D == 128 ? (uint32_t)c : (uint32_t)(map * 64 + c);
 }
 
+// Nothing for a state that is none, whatever was computed.
+__device__ __forceinline__ void none(bool act, uint32_t (&v)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = act ? v[e] : 0u;
+}
+
 // Warps 4-11: W^T and dz^T of every step, then the unit's rows of dK and dV.  Thread =
 // state, columns = query rows, whose numbers come with dO.
 template <int D>
@@ -380,12 +386,16 @@ __device__ void k_softmax(const BParams &P, uint8_t *smem, KSync *sy, uint32_t t
   for (uint32_t i0 = blockIdx.x; i0 < P.units; i0 += gridDim.x, cross::walk_next(P.walk, w)) {
     const KUnit u = k_unit(P, w);
     const int state = u.kt * kTile + row;
-    const bool act = state < u.len;
+    const bool act = state < u.len, all_act = __all_sync(0xffffffffu, act);
     for (int i = 0; i < u.n; ++i, ++g, r.next()) {
-      cross::warp_wait(live, &sy->g_full[r.slot], r.phase, abort, P.status);
-      cross::warp_wait(live, &sy->x_full, g & 1u, abort, P.status);
+      const bool g_over = diff::is_over(&sy->g_full[r.slot], r.phase);
+      const bool x_over = diff::is_over(&sy->x_full, g & 1u);
+      // the product of two steps before has read W's buffer
+      const bool w_over = diff::is_over(&sy->dv_done[g & 1u], ((g >> 1) & 1u) ^ 1u);
+      diff::wait_unless(g_over, live, &sy->g_full[r.slot], r.phase, abort, P.status);
+      diff::wait_unless(x_over, live, &sy->x_full, g & 1u, abort, P.status);
       tc_fence_after();
-      // per query row, 64 apart: -lse_1, -lse_2, -delta_1, -delta_2, lam
+      // per query row, 64 apart: -lse_1, -lse_2, -delta_1, -delta_2, -lam
       const float *num = reinterpret_cast<const float *>(smem + C::kOffL + r.slot * C::kNums) +
                          grp * 32;
       uint32_t x1[32], x2[32];
@@ -396,7 +406,7 @@ __device__ void k_softmax(const BParams &P, uint8_t *smem, KSync *sy, uint32_t t
       reg_fence(x2);
       tc_fence_before();
       b_arrive(&sy->x_free, lane);
-      uint64_t p1[16], p2[16];  // P_1, lam P_2
+      uint64_t p1[16], p2[16];  // P_1, -lam P_2
       uint32_t pk[16];
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
@@ -407,18 +417,19 @@ __device__ void k_softmax(const BParams &P, uint8_t *smem, KSync *sy, uint32_t t
         p1[e / 2 + 1] = ex2_pair(fma2(pair(x1 + e + 2), sc2, l1.y));
         p2[e / 2] = mul2(ex2_pair(fma2(pair(x2 + e), sc2, l2.x)), lm.x);
         p2[e / 2 + 1] = mul2(ex2_pair(fma2(pair(x2 + e + 2), sc2, l2.y)), lm.y);
-        const uint64_t minus = f2(-1.f, -1.f);
-        pk[e / 2] = act ? pack_pair(fma2(p2[e / 2], minus, p1[e / 2])) : 0u;
-        pk[e / 2 + 1] = act ? pack_pair(fma2(p2[e / 2 + 1], minus, p1[e / 2 + 1])) : 0u;
+        pk[e / 2] = pack_pair(add2(p1[e / 2], p2[e / 2]));
+        pk[e / 2 + 1] = pack_pair(add2(p1[e / 2 + 1], p2[e / 2 + 1]));
       }
-      // the product of two steps before has read this buffer
-      cross::warp_wait(live, &sy->dv_done[g & 1u], ((g >> 1) & 1u) ^ 1u, abort, P.status);
+      if (!all_act) none(act, pk);
+      const bool y_over = diff::is_over(&sy->y_full, g & 1u);
+      diff::wait_unless(w_over, live, &sy->dv_done[g & 1u], ((g >> 1) & 1u) ^ 1u, abort,
+                        P.status);
       tc_fence_after();
       tmem_st16(at + C::kW + (g & 1u) * 32 + grp * 16, pk);
       tmem_wait_st();
       tc_fence_before();
       b_arrive(&sy->w_full[g & 1u], lane);
-      cross::warp_wait(live, &sy->y_full, g & 1u, abort, P.status);
+      diff::wait_unless(y_over, live, &sy->y_full, g & 1u, abort, P.status);
       tc_fence_after();
       tmem_ld32(ya, x1);
       tmem_wait_ld();
@@ -429,11 +440,14 @@ __device__ void k_softmax(const BParams &P, uint8_t *smem, KSync *sy, uint32_t t
         const ulonglong2 d1 = *reinterpret_cast<const ulonglong2 *>(num + 128 + e);
         const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(num + 192 + e);
         const uint64_t y0 = pair(x1 + e), y1 = pair(x1 + e + 2);
-        pk[e / 2] = act ? pack_pair(mul2(p1[e / 2], add2(y0, d1.x))) : 0u;
-        pk[e / 2 + 1] = act ? pack_pair(mul2(p1[e / 2 + 1], add2(y1, d1.y))) : 0u;
-        // the sign of dz_2: both halves of the packed pair
-        z2[e / 2] = act ? pack_pair(mul2(p2[e / 2], add2(y0, d2.x))) ^ 0x80008000u : 0u;
-        z2[e / 2 + 1] = act ? pack_pair(mul2(p2[e / 2 + 1], add2(y1, d2.y))) ^ 0x80008000u : 0u;
+        pk[e / 2] = pack_pair(mul2(p1[e / 2], add2(y0, d1.x)));
+        pk[e / 2 + 1] = pack_pair(mul2(p1[e / 2 + 1], add2(y1, d1.y)));
+        z2[e / 2] = pack_pair(mul2(p2[e / 2], add2(y0, d2.x)));
+        z2[e / 2 + 1] = pack_pair(mul2(p2[e / 2 + 1], add2(y1, d2.y)));
+      }
+      if (!all_act) {
+        none(act, pk);
+        none(act, z2);
       }
       tmem_st16(ya, pk);  // over columns of Y that this thread has read
       tmem_st16(ya + 16, z2);
@@ -822,7 +836,7 @@ __device__ void q_softmax(const BParams &P, uint8_t *smem, QSync *sy, uint32_t t
   const uint64_t sc2 = f2(P.scale_log2, P.scale_log2);
   const int tok = r64 / P.G, head = r64 - tok * P.G;
   uint32_t g = 0, ku = 0;
-  bool live = true;
+  bool live = true, x_over = false;
   QUnit last{};  // unit ku - 1
   auto write_rows = [&]() {  // of unit ku - 1, over its Q; a run's sums to their part
     cross::warp_wait(live, &sy->acc_full, (ku - 1) & 1u, abort, P.status);
@@ -873,10 +887,10 @@ __device__ void q_softmax(const BParams &P, uint8_t *smem, QSync *sy, uint32_t t
 #pragma unroll
       for (int i = 0; i < kRowsArrays; ++i) n[i] = __ldg(P.rows + i * P.nrows + prow);
       const uint64_t l1 = f2(n[0], n[0]), l2 = f2(n[1], n[1]), d1 = f2(n[2], n[2]),
-                     d2 = f2(n[3], n[3]), by = f2(-n[4], -n[4]);
+                     d2 = f2(n[3], n[3]), by = f2(n[4], n[4]);
       for (int t = 0; t < c.n; ++t, ++g) {
         const int mine = c.len - (c.t0 + t) * kStates - grp * 32;  // own columns that are states
-        cross::warp_wait(live, &sy->x_full, g & 1u, abort, P.status);
+        diff::wait_unless(x_over, live, &sy->x_full, g & 1u, abort, P.status);
         tc_fence_after();
         uint32_t x1[32], x2[32];
         tmem_ld32(at + C::kX2 + grp * 32, x1);
@@ -892,14 +906,17 @@ __device__ void q_softmax(const BParams &P, uint8_t *smem, QSync *sy, uint32_t t
           p1[e] = ex2_pair(fma2(pair(x1 + 2 * e), sc2, l1));
           p2[e] = ex2_pair(fma2(pair(x2 + 2 * e), sc2, l2));
         }
+        const bool y_over = diff::is_over(&sy->y_full, g & 1u);
         if (t == 0 && ku > 0) write_rows();
-        cross::warp_wait(live, &sy->y_full, g & 1u, abort, P.status);
+        diff::wait_unless(y_over, live, &sy->y_full, g & 1u, abort, P.status);
         tc_fence_after();
         tmem_ld32(at + C::kY2 + grp * 32, x1);
         tmem_wait_ld();
         reg_fence(x1);
         tc_fence_before();
         b_arrive(&sy->y_free, lane);
+        // the next step's scores, asked for ahead of this one's products
+        x_over = diff::is_over(&sy->x_full, (g & 1u) ^ 1u);
         if (mine < 32) {  // past the length: nothing, whatever was computed there
 #pragma unroll
           for (int e = 0; e < 16; ++e) {

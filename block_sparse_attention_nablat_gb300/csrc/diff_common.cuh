@@ -28,6 +28,24 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int box, int rows, int 
   __syncwarp();
 }
 
+// Whether a barrier's phase is over, for one thread.  A wait costs some 130 cycles even where
+// it is; asked for several barriers at once, or ahead of other work, the answers come together.
+__device__ __forceinline__ bool is_over(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(ok)
+      : "r"(tc::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// A whole warp's wait, `over` saying whether it was asked already and is.
+__device__ __forceinline__ void wait_unless(bool over, bool &live, uint64_t *bar, uint32_t parity,
+                                            volatile int *abort, int *status) {
+  if (!__all_sync(0xffffffffu, over)) cross::warp_wait(live, bar, parity, abort, status);
+}
+
 // 16-column step kk (of all D columns) of a K-major tile of `box` bytes a box.
 __device__ __forceinline__ uint64_t k_step(int kk, int box) {
   return (uint64_t)(((kk >> 2) * box + (kk & 3) * 32) >> 4);

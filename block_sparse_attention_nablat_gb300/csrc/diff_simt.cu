@@ -28,7 +28,7 @@ struct DiffSimt {
   const float *lam;
   int lam_step;
   float *o2;                // forward, or null
-  const float *rows;        // backward: -lse_1, -lse_2, -delta_1, -delta_2 of the packed rows
+  const float *rows;        // backward: -lse_1, -lse_2, -delta_1, -delta_2 (and -lam) of the packed rows
   size_t nrows;             // rows of each
   float *t2;                // [packed rows]: sum of P_2 (dout v^T)
 };

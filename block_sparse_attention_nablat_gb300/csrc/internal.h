@@ -194,7 +194,7 @@ cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st);
 // K13: the backward.  Workspace: the packed rows' numbers (five), what lam's gradient is
 // summed from, the runs' sums of dK and dV and of dQ.
 struct DiffRows {
-  const float *rows;  // -lse_1, -lse_2, -delta_1, -delta_2, lam: [5][nrows]
+  const float *rows;  // -lse_1, -lse_2, -delta_1, -delta_2, -lam: [5][nrows]
   size_t nrows;
   float *t2;  // [runs][nrows]
   int nsub;
