@@ -737,6 +737,7 @@ __global__ void __launch_bounds__(1024)
   if (!weights && t0 == t1) return;  // seen whole
   float a[3] = {0.f, 0.f, 0.f};
   if (c < P.C)
+#pragma unroll 4
     for (int t = t0 + ty; t <= t1; t += lanes) {
       const float *p = weights ? P.wpart + (size_t)t * 2 * P.C
                                : P.part + ((size_t)t * 2 + ((long)t * P.L >= g0 ? 0 : 1)) * 3 * P.C;

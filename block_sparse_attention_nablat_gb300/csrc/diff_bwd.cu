@@ -23,19 +23,23 @@ struct PrepParams {
   const float *lse, *lam;  // [B, h, 2, Sq]
   float *rows;
   size_t nrows;
+  unsigned *counter;
   int lam_step, Sq, h, hk, G, tq, nsub;
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(256) diff_prep_kernel(const __grid_constant__ PrepParams<T> P) {
   constexpr int kLanes = D / 8, kPass = 256 / kLanes, kRows = 64 / kPass;
+  __shared__ float out[kRowsArrays][64];
   const int lane = threadIdx.x % kLanes, r0 = threadIdx.x / kLanes;
   pdl_launch_dependents();
-  const uint32_t bj = blockIdx.x / (uint32_t)P.nsub, sub = blockIdx.x - bj * P.nsub;
-  const uint32_t b = bj / (uint32_t)P.hk, j = bj - b * P.hk;
+  // blocks side by side take the heads of the same tokens, which lie side by side
+  const uint32_t bs = blockIdx.x / (uint32_t)P.hk, j = blockIdx.x - bs * P.hk;
+  const uint32_t b = bs / (uint32_t)P.nsub, sub = bs - b * P.nsub;
   const T *o = P.o + b * P.o_st.batch + lane * 8, *o2 = P.o2 + b * P.o2_st.batch + lane * 8;
   const T *g = P.dout + b * P.g_st.batch + lane * 8;
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.counter = 0;  // of lam_kernel's blocks
   Raw<T> a[kRows], c[kRows], d[kRows];
   float n[kRows][3];  // -lse_1, -lse_2, lam
 #pragma unroll
@@ -80,25 +84,32 @@ __global__ void __launch_bounds__(256) diff_prep_kernel(const __grid_constant__ 
                       : lane == 2 ? -fmaf(n[i][2], s2, s)
                       : lane == 3 ? -s2
                                   : -n[i][2];
-      P.rows[lane * P.nrows + (size_t)blockIdx.x * 64 + r0 + i * kPass] = v;
+      out[lane][r0 + i * kPass] = v;
     }
   }
+  __syncthreads();
+  const size_t row0 = ((size_t)(b * P.hk + j) * P.nsub + sub) * 64;
+  for (int e = threadIdx.x; e < kRowsArrays * 64; e += 256)
+    P.rows[(e >> 6) * P.nrows + row0 + (e & 63)] = out[e >> 6][e & 63];
 }
 
 // lam's gradient: minus the sum of the rows' numbers t2 ([runs][nrows]; 0 where a row is
 // none).  Block (j, c): chunk c of key head j's subtiles, four at a time; lane r of a subtile
-// adds up the numbers of head r % G.  One chunk and a weight for each head: straight to dlam,
-// else to part [h][chunks], which lam_sum_kernel adds up.
+// adds up the numbers of head r % G, to part [h][chunks].  The block that is done last adds
+// those up, in order, so that the sum is the same whichever it is.
 struct LamParams {
   const float *t2;
   size_t nrows;
-  int runs, B, hk, G, tq, nsub, each;
+  int runs, B, h, hk, G, tq, nsub, each;
   float *part, *dlam;
+  unsigned *counter;
 };
 
-__global__ void __launch_bounds__(256) lam_part_kernel(const LamParams P) {
+__global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
   __shared__ float sums[256];
+  __shared__ bool last;
   const int j = blockIdx.x, chunk = blockIdx.y, chunks = gridDim.y, r = threadIdx.x & 63;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_launch_dependents();
   const long n = (long)P.B * P.nsub, e0 = n * chunk / chunks, e1 = n * (chunk + 1) / chunks;
   pdl_wait();
@@ -118,33 +129,36 @@ __global__ void __launch_bounds__(256) lam_part_kernel(const LamParams P) {
   }
   sums[threadIdx.x] = v;
   __syncthreads();
-  if ((int)threadIdx.x >= P.G) return;  // head threadIdx.x of the group
-  v = 0.f;
-  for (int q = 0; q < 4; ++q)
-    for (int t = 0; t < P.tq; ++t) v += sums[q * 64 + t * P.G + threadIdx.x];
-  const int head = j * P.G + threadIdx.x;
-  if (P.each && chunks == 1)
-    P.dlam[head] = -v;
-  else
-    P.part[(size_t)head * chunks + chunk] = v;
-}
-
-// Block i: gradient i, minus the sum of n of the parts.
-__global__ void __launch_bounds__(256) lam_sum_kernel(const LamParams P, int n) {
-  __shared__ float sums[8];
-  pdl_launch_dependents();
-  pdl_wait();
-  float v = 0.f;
-  for (int i = threadIdx.x; i < n; i += 256) v += P.part[(size_t)blockIdx.x * n + i];
+  if ((int)threadIdx.x < P.G) {  // head threadIdx.x of the group
+    v = 0.f;
+    for (int q = 0; q < 4; ++q)
+      for (int t = 0; t < P.tq; ++t) v += sums[q * 64 + t * P.G + threadIdx.x];
+    P.part[(size_t)(j * P.G + threadIdx.x) * chunks + chunk] = v;
+    __threadfence();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(P.counter, 1u) + 1u == gridDim.x * gridDim.y;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  // a warp for each head, the lanes along its chunks; one weight: the heads' sums in order
+  float all = 0.f;
+  for (int i = warp; i < P.h; i += 8) {
+    v = 0.f;
+    for (int c = lane; c < chunks; c += 32) v += __ldcg(P.part + (size_t)i * chunks + c);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    all += v;
+    if (P.each && lane == 0) P.dlam[i] = -v;
+  }
+  if (P.each) return;
+  if (lane == 0) sums[warp] = all;
   __syncthreads();
   if (threadIdx.x) return;
   v = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) v += sums[i];
-  P.dlam[blockIdx.x] = -v;
+  P.dlam[0] = -v;
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -153,7 +167,7 @@ struct BwdLayout {
   int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
   size_t nrows;
   int nsplit, qsplit, truns, chunks;
-  size_t rows, t2, part, qpart, lam, total;
+  size_t rows, t2, part, qpart, lam, counter, total;
 };
 BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
@@ -162,8 +176,8 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   w.nsplit = cross_dkv_splits(s, dt);
   w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : 1;
   w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : 1;
-  // 64 subtiles a chunk: sixteen loads a thread and run
-  const size_t chunks = ((size_t)s.B * w.nsub + 63) / 64;
+  // 16 subtiles a chunk: four loads a thread and run
+  const size_t chunks = ((size_t)s.B * w.nsub + 15) / 16;
   w.chunks = chunks > 64 ? 64 : (int)chunks;
   w.rows = 0;
   w.t2 = round_up(kRowsArrays * w.nrows * sizeof(float));
@@ -174,12 +188,14 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   w.lam = w.qpart + (w.qsplit > 1 ? round_up((size_t)w.qsplit * s.B * s.Sq * s.h * s.D *
                                              sizeof(float))
                                   : 0);
-  w.total = w.lam + round_up((size_t)s.h * w.chunks * sizeof(float));
+  w.counter = w.lam + round_up((size_t)s.h * w.chunks * sizeof(float));
+  w.total = w.counter + 256;
   return w;
 }
 
 template <typename T, int D>
-cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, cudaStream_t st) {
+cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, unsigned *counter,
+                        cudaStream_t st) {
   const CrossShape &s = a.x.s;
   const cross::Packing pk = cross::packing(s);
   PrepParams<T> p{};
@@ -187,7 +203,7 @@ cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, cudaS
   p.dout = static_cast<const T *>(a.x.dout);
   p.o_st = a.x.o_st, p.o2_st = a.o2_st, p.g_st = a.x.dout_st;
   p.lse = a.x.lse, p.lam = a.lam, p.lam_step = a.lam_n > 1 ? 1 : 0;
-  p.rows = rows, p.nrows = r.nrows;
+  p.rows = rows, p.nrows = r.nrows, p.counter = counter;
   p.Sq = s.Sq, p.h = s.h, p.hk = s.hk, p.G = pk.G, p.tq = pk.tq, p.nsub = r.nsub;
   return launch_pdl(diff_prep_kernel<T, D>, dim3((unsigned)((long)s.B * s.hk * r.nsub)), dim3(256),
                     0, st, p);
@@ -202,27 +218,24 @@ cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
   const BwdLayout w = bwd_layout(s, dt);
   char *ws = static_cast<char *>(a.x.workspace);
   auto at = [&](size_t off) { return reinterpret_cast<float *>(ws + off); };
+  unsigned *counter = reinterpret_cast<unsigned *>(ws + w.counter);
   const DiffRows r{at(w.rows), w.nrows, at(w.t2), w.nsub};
   cudaError_t e;
   if (dt == NABLA_BF16)
-    e = s.D == 64 ? launch_prep<__nv_bfloat16, 64>(a, r, at(w.rows), st)
-                  : launch_prep<__nv_bfloat16, 128>(a, r, at(w.rows), st);
+    e = s.D == 64 ? launch_prep<__nv_bfloat16, 64>(a, r, at(w.rows), counter, st)
+                  : launch_prep<__nv_bfloat16, 128>(a, r, at(w.rows), counter, st);
   else
-    e = s.D == 64 ? launch_prep<float, 64>(a, r, at(w.rows), st)
-                  : launch_prep<float, 128>(a, r, at(w.rows), st);
+    e = s.D == 64 ? launch_prep<float, 64>(a, r, at(w.rows), counter, st)
+                  : launch_prep<float, 128>(a, r, at(w.rows), counter, st);
   if (e != cudaSuccess) return e;
   e = dt == NABLA_BF16
           ? launch_diff_bwd_tc(a, r, at(w.part), w.nsplit, at(w.qpart), w.qsplit, st)
           : launch_diff_bwd_simt(a, r, at(w.part), w.nsplit, st);
   if (e != cudaSuccess) return e;
   const cross::Packing pk = cross::packing(s);
-  const bool each = a.lam_n > 1;
-  const LamParams p{r.t2, w.nrows, w.truns, s.B, s.hk, pk.G, pk.tq, w.nsub, each ? 1 : 0,
-                    at(w.lam), a.dlam};
-  e = launch_pdl(lam_part_kernel, dim3((unsigned)s.hk, (unsigned)w.chunks), dim3(256), 0, st, p);
-  if (e != cudaSuccess || (each && w.chunks == 1)) return e;
-  return launch_pdl(lam_sum_kernel, dim3(each ? (unsigned)s.h : 1u), dim3(256), 0, st, p,
-                    each ? w.chunks : s.h * w.chunks);
+  const LamParams p{r.t2, w.nrows, w.truns, s.B, s.h, s.hk, pk.G, pk.tq, w.nsub,
+                    a.lam_n > 1 ? 1 : 0, at(w.lam), a.dlam, counter};
+  return launch_pdl(lam_kernel, dim3((unsigned)s.hk, (unsigned)w.chunks), dim3(256), 0, st, p);
 }
 
 }  // namespace nabla
