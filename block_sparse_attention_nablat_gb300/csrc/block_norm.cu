@@ -50,7 +50,9 @@ constexpr int kTeamBlock = 128;  // backward: threads of a block of several team
 // lane holds eight vectors of both x and u (with 128 it spills 350 bytes).
 template <int N, bool kU>
 constexpr int kFwdBlock = N == 8 && kU ? 192 : 256;
-// Blocks of 256 threads on an SM: rows of few vectors need more of them under way.
+// Blocks of 256 threads on an SM: rows of few vectors need more of them under way (16.8 M
+// elements, two blocks against four: C 256 41 us against 29; against three: C 512 28.6
+// against 25.3).
 template <int N>
 constexpr int kFwdPerSm = N == 1 ? 4 : N == 2 ? 3 : 2;
 constexpr int kMaxStages = 4;    // rows of the backward's ring
@@ -802,9 +804,11 @@ Runs bwd_runs(const NormShape &s, long n) {
   const int per = f.team ? f.threads / f.team : 1;  // teams of a block
   const long most = 152L * (512 / f.threads) * per;
   long L = (T + most - 1) / most;
-  if (L < 4) L = 4;  // shorter ones would have more partial sums than rows
-  // whole rows of the modulations where that changes little: nothing to join then
-  if (n * 4 <= L) L = (L + n - 1) / n * n;
+  // Whole rows of the modulations where that changes little: nothing to join then.  Teams of
+  // a warp or less: up to a run's length (65536 x 256, fp32 modulations, 16 tokens a row: 94 us
+  // against 118; 8: 103 against 126), a block a row: to a quarter of it (32768 x 1536, 16
+  // tokens: 208 against 221 us, 8: 224 against 231, but 64: 217 against 206).
+  if (n * (f.team ? 1 : 4) <= L) L = (L + n - 1) / n * n;
   return {(T + L - 1) / L, (int)L};
 }
 
@@ -822,12 +826,14 @@ NormLayout norm_layout(const NormShape &s) {
   return w;
 }
 
-// Tokens of a row of the modulations from which on it is worth laying out in shared memory.
-constexpr int kSharedFrom = 16;
+// Tokens of a row of the modulations from which on it is worth laying out in shared memory
+// (8192 rows, 4 tokens each: C 1536 41.5 us against 56.5, C 5120 133 against 156, but C 512
+// 20.4 against 17.4; 8 tokens, C 512: 14.1 against 17.4; 2, C 1536: 67 against 58).
+constexpr int shared_from(int C) { return C > 512 ? 4 : 8; }
 
 template <typename T, int kTeam, int N, bool kSpread, bool kU>
 cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
-  const bool shared = !kSpread && p.n >= kSharedFrom;
+  const bool shared = !kSpread && p.n >= shared_from(p.C);
   const size_t smem = shared ? (size_t)3 * p.C * sizeof(float) : 0;
   // as many warps an SM as their registers allow, if shared memory holds their modulations
   int per_sm = kSpread ? 2048 / f.threads : kFwdPerSm<N> * kFwdBlock<N, kU> / f.threads;
@@ -877,8 +883,11 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
 
 template <typename T>
 cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st) {
-  // Few rows: what counts is how long one takes.
-  if (p.C > 256 && p.T <= 304) {
+  // Few rows: what counts is how long one takes (C 1536: 16 rows 3.0 us against 3.7, 608 3.6
+  // against 4.6, 1216 6.8 against 4.8; C 4096: 152 3.6 against 10.7, 608 11.7 against 12.2,
+  // 1216 20 against 16; C 5120, two vectors a thread: 304 8.6 against 10.8, 456 11.5 against
+  // 10.9).
+  if (p.C > 256 && p.T <= (p.C <= 4096 ? 608 : 304)) {
     const int vecs = p.C <= 4096 ? 1 : 2;
     const Form g{0, vecs, (p.C + vecs * 256 - 1) / (vecs * 256) * 32};
     return vecs == 1 ? launch_fwd<T, 0, 1, true>(p, g, st) : launch_fwd<T, 0, 2, true>(p, g, st);
@@ -906,7 +915,8 @@ cudaError_t launch_bwd_form(const NormParams &p, const Form &f, long teams, cuda
     case 32: return launch_bwd<T, 32, 1, kTeamBlock>(p, f, teams, st);
   }
   if (f.vecs == 1) return launch_bwd<T, 0, 1, 512>(p, f, teams, st);
-  // two vectors a thread want more than the 128 registers that 512 threads have
+  // two vectors a thread want more than the 128 registers that 512 threads have (16384 x 5120:
+  // 341 us against 510)
   return f.threads <= 384 ? launch_bwd<T, 0, 2, 384>(p, f, teams, st)
                           : launch_bwd<T, 0, 2, 512>(p, f, teams, st);
 }
@@ -956,7 +966,9 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
     return launch_pdl(block_norm_join_kernel, dim3(nx, y), dim3(threads), 0, st, p, (int)r.teams,
                       (int)borders, (long)a.rows, a.dw, a.dpw);
   };
-  if (ny > 0 && p.n <= 4L * p.L) {  // a row of them lies in few runs: small blocks
+  // a row of them lies in few runs: small blocks (16384 x 1536, 5 runs: 106 us against 120;
+  // 4096 x 1536, 18 runs: 41.4 against 39.9)
+  if (ny > 0 && p.n <= 10L * p.L) {
     const cudaError_t e2 = join((unsigned)ny, 128, ny);
     if (e2 != cudaSuccess) return e2;
     ny = 0;
