@@ -91,7 +91,7 @@ static_assert(f_smem_bytes<128>() <= 232448, "shared memory budget");
 struct FParams {
   __nv_bfloat16 *o, *o2;  // [B, Sq, h, D]; o2 or null
   float *lse;             // [B, h, 2, Sq] or null
-  float *po, *plse;       // parts: [kCtas, 2 places, 2 maps, 128, D] and [.., 128]
+  float *po, *plse;       // parts: [kCtas, 2 places, 2 maps, D / 4, 128, 4], [.., 128]
   const float *lam;
   const int32_t *kv_len;
   int lam_step;  // 1: a weight for each head; 0: one
@@ -498,7 +498,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
     const int token = (u.qt * 2 + (row >> 6)) * P.tq + tok, hh = u.j * P.G + head;
     const bool row_ok = tok < P.tq && token < P.Sq;
     const bool split = u.part >= 0;
-    const size_t prow = ((size_t)blockIdx.x * 2 + (split ? u.part : 0)) * 256 + row;  // of a part
+    const size_t place = (size_t)blockIdx.x * 2 + (split ? u.part : 0);  // of a part
     float l1 = 0.f, m1 = 0.f, l2 = 0.f, m2 = 0.f;
     const float lam = row_ok ? __ldg(P.lam + hh * P.lam_step) : 0.f;
     if (u.n > 0) {
@@ -519,7 +519,8 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
       ++kq;
       const float inv1 = f_inv(l1), inv2 = f_inv(l2), by2 = -lam * inv2;
       const uint64_t i1 = f2(inv1, inv1), i2 = f2(inv2, inv2), b2 = f2(by2, by2);
-      float *run = P.po + prow * D;
+      // a part's rows lie side by side, four columns at a time: 512 bytes a warp and store
+      float4 *run = reinterpret_cast<float4 *>(P.po) + place * 2 * (D / 4) * 128 + row;
 #pragma unroll 1
       for (int x = 0; x < D / 32; ++x) {
         uint32_t a[32], c[32];
@@ -536,12 +537,13 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
           if (row_ok && live)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              *reinterpret_cast<float4 *>(run + x * 32 + e) = make_float4(
-                  __uint_as_float(a[e]) * inv1, __uint_as_float(a[e + 1]) * inv1,
-                  __uint_as_float(a[e + 2]) * inv1, __uint_as_float(a[e + 3]) * inv1);
-              *reinterpret_cast<float4 *>(run + 128 * D + x * 32 + e) = make_float4(
-                  __uint_as_float(c[e]) * inv2, __uint_as_float(c[e + 1]) * inv2,
-                  __uint_as_float(c[e + 2]) * inv2, __uint_as_float(c[e + 3]) * inv2);
+              float4 *to = run + (x * 8 + e / 4) * 128;
+              *to = make_float4(__uint_as_float(a[e]) * inv1, __uint_as_float(a[e + 1]) * inv1,
+                                __uint_as_float(a[e + 2]) * inv1,
+                                __uint_as_float(a[e + 3]) * inv1);
+              to[D / 4 * 128] =
+                  make_float4(__uint_as_float(c[e]) * inv2, __uint_as_float(c[e + 1]) * inv2,
+                              __uint_as_float(c[e + 2]) * inv2, __uint_as_float(c[e + 3]) * inv2);
             }
           continue;
         }
@@ -590,7 +592,7 @@ __device__ void f_output(const FParams &P, const CUtensorMap *mo, const CUtensor
     }
     if (row_ok && live) {
       if (split) {
-        float *to = P.plse + prow;
+        float *to = P.plse + place * 256 + row;
         to[0] = f_lse(l1, m1);
         to[128] = f_lse(l2, m2);
       } else if (P.lse) {
@@ -743,7 +745,7 @@ cudaError_t launch_f(const DiffArgs &a, cudaStream_t st) {
   p.scale_log2 = a.x.scale == 0.f ? 1e-30f : fabsf(a.x.scale) * 1.4426950408889634f;
   p.neg = a.x.scale < 0.f ? kIdescNegA : 0u;
   p.status = a.x.status;
-  const DiffPlan plan = diff_fwd_plan(s, NABLA_BF16);
+  const DiffPlan plan = diff_fwd_plan(s, NABLA_BF16, a.x.kv_len != nullptr);
   p.whole = (uint32_t)plan.whole, p.cut = plan.cut;
   const DiffRuns parts = diff_runs(a, NABLA_BF16);
   p.po = parts.po, p.plse = parts.plse;

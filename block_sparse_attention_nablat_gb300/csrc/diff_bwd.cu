@@ -5,6 +5,7 @@
 #include "diff_common.cuh"
 #include "internal.h"
 #include "pdl.cuh"
+#include "tc_ptx.cuh"
 #include "vec8.cuh"
 
 namespace nabla {
@@ -93,6 +94,34 @@ __global__ void __launch_bounds__(256) diff_prep_kernel(const __grid_constant__ 
     P.rows[(e >> 6) * P.nrows + row0 + (e & 63)] = out[e >> 6][e & 63];
 }
 
+// dQ of runs of state tiles: their sums added up in order, scaled and rounded.  A thread per
+// four columns.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    diff_dq_sum_kernel(const float *part, int nsplit, int Sq, int Sk, const int32_t *kv_len,
+                       float scale, long n4, int row, T *dq) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  const long e = i * 4;
+  const int b = (int)(e / row / Sq);
+  const int tiles = (cross::batch_len(kv_len, b, Sk) + diff::kStates - 1) / diff::kStates;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int sp = 0; sp < nsplit; ++sp) {
+    if ((long)tiles * sp / nsplit == (long)tiles * (sp + 1) / nsplit) continue;  // no states
+    const float4 x = *reinterpret_cast<const float4 *>(part + (size_t)sp * n4 * 4 + e);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+  s = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4 *>(dq + e) = s;
+  else
+    *reinterpret_cast<uint2 *>(dq + e) =
+        make_uint2(tc::pack_bf16x2(s.x, s.y), tc::pack_bf16x2(s.z, s.w));
+}
+
 // lam's gradient: minus the sum of the rows' numbers t2 ([runs][nrows]; 0 where a row is
 // none).  Block (j, c): chunk c of key head j's subtiles, four at a time; lane r of a subtile
 // adds up the numbers of head r % G, to part [h][chunks].  The block that is done last adds
@@ -163,6 +192,26 @@ __global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
+// Runs of state tiles the fp32 dQ units (64 packed rows) are split into.  Cost in steps of a
+// 64 x 64 tile, about 6 us, in which 24 MB move: as cross_dkv_splits.  (Whole backward, D 64,
+// us, in runs and whole: 512 x 2048, 2 heads 92, 281; 256 x 1024, 4 heads 55, 148; 2048 x 256,
+// 2 heads 57, 66.)
+int simt_dq_splits(const CrossShape &s, int nsub) {
+  const long units = (long)s.B * s.hk * nsub;
+  const int tiles = (s.Sk + 63) / 64;
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= tiles && n <= 64; ++n) {
+    double cost = (double)((units * n + 151) / 152) * ((tiles + n - 1) / n + 0.5);
+    if (n > 1) cost += 1.0 + (double)units * n * 64 * s.D * 4 * 2 / 24.0e6;
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 struct BwdLayout {
   int nsub;  // subtiles per (batch, key head), a whole number of 128-row tiles
   size_t nrows;
@@ -174,8 +223,8 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
   w.nrows = (size_t)s.B * s.hk * w.nsub * 64;
   w.nsplit = cross_dkv_splits(s, dt);
-  w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : 1;
-  w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : 1;
+  w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : simt_dq_splits(s, w.nsub);
+  w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : w.qsplit;
   // 16 subtiles a chunk: four loads a thread and run
   const size_t chunks = ((size_t)s.B * w.nsub + 15) / 16;
   w.chunks = chunks > 64 ? 64 : (int)chunks;
@@ -211,6 +260,19 @@ cudaError_t launch_prep(const DiffArgs &a, const DiffRows &r, float *rows, unsig
 
 }  // namespace
 
+cudaError_t launch_diff_dq_sum(const DiffArgs &a, nabla_dtype dt, const float *part, int nsplit,
+                               cudaStream_t st) {
+  const CrossShape &s = a.x.s;
+  const long n4 = (long)s.B * s.Sq * s.h * (s.D / 4);
+  const dim3 grid((unsigned)((n4 + 255) / 256));
+  if (dt == NABLA_BF16)
+    return launch_pdl(diff_dq_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, part, nsplit,
+                      s.Sq, s.Sk, a.x.kv_len, a.x.scale, n4, s.h * s.D,
+                      static_cast<__nv_bfloat16 *>(a.x.dq));
+  return launch_pdl(diff_dq_sum_kernel<float>, grid, dim3(256), 0, st, part, nsplit, s.Sq, s.Sk,
+                    a.x.kv_len, a.x.scale, n4, s.h * s.D, static_cast<float *>(a.x.dq));
+}
+
 size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt) { return bwd_layout(s, dt).total; }
 
 cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) {
@@ -230,7 +292,7 @@ cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
   if (e != cudaSuccess) return e;
   e = dt == NABLA_BF16
           ? launch_diff_bwd_tc(a, r, at(w.part), w.nsplit, at(w.qpart), w.qsplit, st)
-          : launch_diff_bwd_simt(a, r, at(w.part), w.nsplit, st);
+          : launch_diff_bwd_simt(a, r, at(w.part), w.nsplit, at(w.qpart), w.qsplit, st);
   if (e != cudaSuccess) return e;
   const cross::Packing pk = cross::packing(s);
   const LamParams p{r.t2, w.nrows, w.truns, s.B, s.h, s.hk, pk.G, pk.tq, w.nsub,

@@ -1043,27 +1043,6 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-// dQ of runs: their sums added up in order, scaled and rounded.  A thread per four columns.
-__global__ void __launch_bounds__(256)
-    diff_dq_sum_kernel(const __grid_constant__ BParams P, long n4, int row) {
-  pdl_launch_dependents();
-  pdl_wait();
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const long e = i * 4;
-  const int b = (int)(e / row / P.Sq);
-  const int tiles = (cross::batch_len(P.kv_len, b, P.Sk) + kStates - 1) / kStates;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int sp = 0; sp < P.nsplit; ++sp) {
-    if ((long)tiles * sp / P.nsplit == (long)tiles * (sp + 1) / P.nsplit) continue;  // no states
-    const float4 x = *reinterpret_cast<const float4 *>(P.part + (size_t)sp * n4 * 4 + e);
-    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-  }
-  *reinterpret_cast<uint2 *>(P.dq + e) = make_uint2(pack_bf16x2(s.x * P.scale, s.y * P.scale),
-                                                    pack_bf16x2(s.z * P.scale, s.w * P.scale));
-}
-
 template <int D>
 cudaError_t launch_b(const DiffArgs &a, const DiffRows &r, float *part, int nsplit, float *qpart,
                      int qsplit, cudaStream_t st) {
@@ -1126,9 +1105,7 @@ cudaError_t launch_b(const DiffArgs &a, const DiffRows &r, float *part, int nspl
   err = launch_pdl(kern2, dim3(grid), dim3(C::kThreads), b_smem_bytes<D, true>(), st, mq, mk64,
                    mv64, mg, mo, p);
   if (err != cudaSuccess || p.nsplit == 1) return err;
-  const long n4 = (long)s.B * s.Sq * s.h * (D / 4);
-  return launch_pdl(diff_dq_sum_kernel, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, st, p,
-                    n4, s.h * D);
+  return launch_diff_dq_sum(a, NABLA_BF16, qpart, qsplit, st);
 }
 
 }  // namespace

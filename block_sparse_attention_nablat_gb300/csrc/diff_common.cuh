@@ -115,7 +115,10 @@ __device__ __forceinline__ long span_of_unit(const int32_t *kv_len, int Sk, int 
   return n * per + (in ? in * weight(kv_len, b, Sk) : 0);
 }
 // Where the piece of CTA c begins, of `n` positions from p0 on.
-__device__ __forceinline__ long piece(long p0, long n, int c) { return p0 + n * c / kCtas; }
+__device__ __forceinline__ long piece(long p0, long n, int c) {
+  // (a division of 64 bits takes several times as long, and they come one after another)
+  return p0 + (n < (1L << 24) ? (long)((uint32_t)n * (uint32_t)c / kCtas) : n * c / kCtas);
+}
 
 }  // namespace diff
 }  // namespace nabla

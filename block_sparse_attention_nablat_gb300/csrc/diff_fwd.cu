@@ -96,24 +96,28 @@ cudaError_t launch_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st) {
 }
 
 // The parts of the tcgen05 kernel's units: blockIdx.y = c - 1 joins the unit that the pieces
-// of CTAs c - 1 and c share, if c is the first to go on with it; a warp per packed row.
+// of CTAs c - 1 and c share, if c is the first to go on with it.  A thread takes kQ times four
+// columns of one of the first `rows` packed rows, kE parts at a time; lanes have rows, which
+// the parts hold four columns at a time side by side, so a warp reads 512 bytes at once.
 struct StreamParams {
-  const float *po, *plse;  // [kCtas, 2 places, 2 maps, 128, D] and [.., 128]
+  const float *po, *plse;  // [kCtas, 2 places, 2 maps, D / 4, 128, 4] and [.., 2 maps, 128]
   const float *lam;
   __nv_bfloat16 *o, *o2;
   float *lse;
   const int32_t *kv_len;
-  int lam_step, B, Sq, Sk, h, hk, G, tq, nqt;
+  int lam_step, B, Sq, Sk, h, hk, G, tq, nqt, rows;
   long whole;
 };
 
-template <int D>
-__global__ void __launch_bounds__(256)
+template <int D, int kQ, int kE>
+__global__ void __launch_bounds__(256, 2)
     diff_stream_join_kernel(const __grid_constant__ StreamParams P) {
   __shared__ int place[diff::kCtas];  // of the parts: CTA * 2 + its place
   __shared__ int count, batch, unit;
-  const int lane = threadIdx.x & 31, col = lane * 4, c = blockIdx.y + 1;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5), t = (r & 63) / P.G;
+  const int lane = threadIdx.x & 31, c = blockIdx.y + 1;
+  const int teams = 256 / P.rows, team = threadIdx.x / P.rows;
+  const int r = threadIdx.x - team * P.rows, t = (r & 63) / P.G;
+  const int quad = (blockIdx.x * teams + team) * kQ;  // of the columns
   pdl_launch_dependents();
   pdl_wait();
   if (threadIdx.x < 32) {  // the unit and its parts
@@ -147,53 +151,71 @@ __global__ void __launch_bounds__(256)
   if (count == 0) return;
   const int j = unit / P.nqt, qt = unit - j * P.nqt;
   const int token = (qt * 2 + (r >> 6)) * P.tq + t, hh = j * P.G + (r & 63) - t * P.G;
-  if (t >= P.tq || token >= P.Sq) return;  // none
-  float4 o[2];
-  float lse[2];
+  if (team >= teams || quad >= D / 4 || t >= P.tq || token >= P.Sq) return;  // none
+  const float lam = P.lam[hh * P.lam_step];
+  float o[2][4 * kQ], lse[2];
 #pragma unroll
   for (int map = 0; map < 2; ++map) {
-    auto row = [&](int i) { return (size_t)place[i] * 256 + map * 128 + r; };
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < count; i += 32) m = fmaxf(m, P.plse[row(i)]);
+    auto log_sum = [&](int i) { return P.plse[(size_t)place[i] * 256 + map * 128 + r]; };
+    float4 x[kE][kQ];
+    auto load = [&](int i0) {
 #pragma unroll
-    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < count; i0 += 4) {
-      float li[4];
-      float4 x[4];
+      for (int e = 0; e < kE; ++e) {
+        const int i = i0 + e < count ? i0 + e : count - 1;
+        const float4 *from = reinterpret_cast<const float4 *>(P.po) +
+                             (((size_t)place[i] * 2 + map) * (D / 4) + quad) * 128 + r;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        li[e] = i0 + e < count ? P.plse[row(i0 + e)] : -INFINITY;
-        x[e] = i0 + e < count && col < D
-                   ? *reinterpret_cast<const float4 *>(P.po + row(i0 + e) * D + col)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int y = 0; y < kQ; ++y) x[e][y] = from[y * 128];
       }
+    };
+    load(0);
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < count; ++i) m = fmaxf(m, log_sum(i));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float w = li[e] == -INFINITY ? 0.f : exp2f(li[e] - m);
+    for (int y = 0; y < 4 * kQ; ++y) o[map][y] = 0.f;
+    for (int i0 = 0; i0 < count; i0 += kE) {
+      if (i0) load(i0);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const float li = i0 + e < count ? log_sum(i0 + e) : -INFINITY;
+        if (li == -INFINITY) continue;
+        const float w = exp2f(li - m);
         l += w;
-        acc.x = fmaf(w, x[e].x, acc.x);
-        acc.y = fmaf(w, x[e].y, acc.y);
-        acc.z = fmaf(w, x[e].z, acc.z);
-        acc.w = fmaf(w, x[e].w, acc.w);
+#pragma unroll
+        for (int y = 0; y < kQ; ++y) {
+          o[map][4 * y] = fmaf(w, x[e][y].x, o[map][4 * y]);
+          o[map][4 * y + 1] = fmaf(w, x[e][y].y, o[map][4 * y + 1]);
+          o[map][4 * y + 2] = fmaf(w, x[e][y].z, o[map][4 * y + 2]);
+          o[map][4 * y + 3] = fmaf(w, x[e][y].w, o[map][4 * y + 3]);
+        }
       }
     }
     const float inv = l > 0.f ? 1.0f / l : l;  // NaN stays
-    o[map] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+#pragma unroll
+    for (int y = 0; y < 4 * kQ; ++y) o[map][y] *= inv;
     lse[map] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
   }
-  if (P.lse && lane < 2)
-    P.lse[(((size_t)batch * P.h + hh) * 2 + lane) * P.Sq + token] = lane ? lse[1] : lse[0];
-  if (col >= D) return;
-  const float lam = P.lam[hh * P.lam_step];
-  const size_t to = (((size_t)batch * P.Sq + token) * P.h + hh) * D + col;
-  auto put = [](__nv_bfloat16 *p, const float4 &v) {
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
+  if (P.lse && quad == 0) {
+    float *to = P.lse + ((size_t)batch * P.h + hh) * 2 * P.Sq + token;
+    to[0] = lse[0];
+    to[P.Sq] = lse[1];
+  }
+  const size_t to = (((size_t)batch * P.Sq + token) * P.h + hh) * D + quad * 4;
+  auto put = [](__nv_bfloat16 *p, const float (&v)[4 * kQ]) {
+    uint32_t w[2 * kQ];
+#pragma unroll
+    for (int y = 0; y < 2 * kQ; ++y) w[y] = tc::pack_bf16x2(v[2 * y], v[2 * y + 1]);
+    if constexpr (kQ == 1)
+      *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else
+#pragma unroll
+      for (int y = 0; y < 2 * kQ; y += 4)
+        *reinterpret_cast<uint4 *>(p + 2 * y) = make_uint4(w[y], w[y + 1], w[y + 2], w[y + 3]);
   };
-  put(P.o + to, make_float4(fmaf(-lam, o[1].x, o[0].x), fmaf(-lam, o[1].y, o[0].y),
-                            fmaf(-lam, o[1].z, o[0].z), fmaf(-lam, o[1].w, o[0].w)));
   if (P.o2) put(P.o2 + to, o[1]);
+#pragma unroll
+  for (int y = 0; y < 4 * kQ; ++y) o[0][y] = fmaf(-lam, o[1][y], o[0][y]);
+  put(P.o + to, o[0]);
 }
 
 }  // namespace
@@ -201,24 +223,38 @@ __global__ void __launch_bounds__(256)
 // How the forward is split.  Sized for GB300's 152 SMs, so that the workspace depends on the
 // shape alone.
 //
-// bf16: units of 128 packed rows that go round the SMs, and from 1024 states on a last round
-// or two cut into equal pieces (below that a unit costs less than joining its parts).  Few
-// rows: runs of 512 states, or longer ones where those are many.  fp32: runs as in the cross
-// attention, whose tiles' costs have the same proportions.
-DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt) {
+// bf16: units of 128 packed rows that go round the SMs; the last round or two are cut into
+// equal pieces where that spares every SM at least 28 tiles of 64 states, 18 us, about what
+// the parts and their join cost.  (us, whole and cut; D 128: 8192 tokens, 12 heads, 1536
+// states 99, 101, 2048 states 128, 126; 64 tokens, 24 heads on 8, 2048 states 24.3, 25.0,
+// 4096 states 44, 27.)  Where lengths differ they are taken to be half of Sk on average.  (One
+// token of 24 heads on 8, 16 ragged batches: 2048 states 25.0, 26.3, 4096 states 45.6, 42.0,
+// 8192 states 85, 66.)
+//
+// Few rows: runs of 512 states, longer ones where those would be more than eight to an SM (16
+// ragged batches of up to 4096 states, 24 heads: 74.5 us, with 16 an SM 85, with 4 80), and
+// twice as long where the heads alone fill the SMs (16 x 1024 states, 16 heads, one run: 24.9
+// us, two: 29.9; but 1 x 1024, one: 13.1, two: 11.7).  fp32: runs as in the cross attention,
+// whose tiles' costs have the same proportions.
+DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt, bool ragged) {
   if (diff_few_rows(s, dt)) {
-    const long runs = (s.Sk + 511) / 512, room = 152L * 16 / ((long)s.B * s.hk);
+    const long heads = (long)s.B * s.hk, room = 152L * 8 / heads;
+    const long runs = heads < 152 ? (s.Sk + 511) / 512 : (s.Sk + 1023) / 1024;
     return {0, runs <= 1 || room <= 1 ? 1 : (int)(runs < room ? runs : room), false};
   }
   if (dt == NABLA_F32) return {0, cross_simt_plan(s).nsplit, false};
   const long units = (long)s.B * s.hk * ((cross::packing(s).nsub + 1) / 2);
-  if (s.Sk < 1024) return {units, 1, false};
+  const long tiles = (s.Sk + diff::kStates - 1) / diff::kStates;
+  const long over = units % diff::kCtas;  // of a round: the others idle meanwhile
+  double idle = over ? 1.0 - (double)over / diff::kCtas : 0.0;
+  if (ragged && idle < 0.5) idle = 0.5;
+  if (idle * (double)tiles < 28.0) return {units, 1, false};
   return {units < 2 * diff::kCtas ? 0 : (units / diff::kCtas - 1) * diff::kCtas, 1, true};
 }
 
 DiffRuns diff_runs(const DiffArgs &a, nabla_dtype dt) {
   const CrossShape &s = a.x.s;
-  const DiffPlan p = diff_fwd_plan(s, dt);
+  const DiffPlan p = diff_fwd_plan(s, dt, a.x.kv_len != nullptr);
   DiffRuns r{p.runs, nullptr, nullptr};
   if (p.runs == 1 && !p.cut) return r;
   const size_t rows = p.cut ? diff::kCtas * 2 * 256 : (size_t)p.runs * 2 * s.B * s.h * s.Sq;
@@ -228,7 +264,7 @@ DiffRuns diff_runs(const DiffArgs &a, nabla_dtype dt) {
 }
 
 size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
-  const DiffPlan p = diff_fwd_plan(s, dt);
+  const DiffPlan p = diff_fwd_plan(s, dt, true);  // cut wherever equal lengths are
   if (p.cut) return (size_t)diff::kCtas * 2 * 256 * (s.D + 1) * sizeof(float);
   return p.runs > 1 ? (size_t)p.runs * 2 * s.B * s.h * s.Sq * (s.D + 1) * sizeof(float) : 0;
 }
@@ -236,15 +272,20 @@ size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt) {
 cudaError_t launch_diff_stream_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st) {
   const CrossShape &s = a.x.s;
   const cross::Packing pk = cross::packing(s);
+  // few rows: more threads for each
+  const int used = s.Sq <= pk.tq ? s.Sq * pk.G : 128, rows = used <= 32 ? used : 128;
   const StreamParams p{r.po, r.plse, a.lam, static_cast<__nv_bfloat16 *>(a.x.o),
                        static_cast<__nv_bfloat16 *>(a.o2), a.x.lse, a.x.kv_len,
                        a.lam_n > 1 ? 1 : 0, s.B, s.Sq, s.Sk, s.h, s.hk, pk.G, pk.tq,
-                       (pk.nsub + 1) / 2, diff_fwd_plan(s, NABLA_BF16).whole};
-  // blocks of eight packed rows, as many as a unit can have
-  const int used = s.Sq < pk.tq ? s.Sq * pk.G : s.Sq < 2 * pk.tq ? 64 + (s.Sq - pk.tq) * pk.G : 128;
-  const dim3 grid((unsigned)((used + 7) / 8), diff::kCtas - 1);
-  return s.D == 64 ? launch_pdl(diff_stream_join_kernel<64>, grid, dim3(256), 0, st, p)
-                   : launch_pdl(diff_stream_join_kernel<128>, grid, dim3(256), 0, st, p);
+                       (pk.nsub + 1) / 2, rows,
+                       diff_fwd_plan(s, NABLA_BF16, a.x.kv_len != nullptr).whole};
+  const int threads = s.D / (rows < 128 ? 4 : 16), teams = 256 / rows;  // of a row, a block's
+  const dim3 grid((unsigned)((threads + teams - 1) / teams), diff::kCtas - 1);
+  auto kern = s.D == 64 ? (rows < 128 ? diff_stream_join_kernel<64, 1, 8>
+                                      : diff_stream_join_kernel<64, 4, 2>)
+                        : (rows < 128 ? diff_stream_join_kernel<128, 1, 8>
+                                      : diff_stream_join_kernel<128, 4, 2>);
+  return launch_pdl(kern, grid, dim3(256), 0, st, p);
 }
 
 cudaError_t launch_diff_join(const DiffArgs &a, nabla_dtype dt, const DiffRuns &r,

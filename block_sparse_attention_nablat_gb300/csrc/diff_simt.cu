@@ -30,7 +30,7 @@ struct DiffSimt {
   float *o2;                // forward, or null
   const float *rows;        // backward: -lse_1, -lse_2, -delta_1, -delta_2 (and -lam) of the packed rows
   size_t nrows;             // rows of each
-  float *t2;                // [packed rows]: sum of P_2 (dout v^T)
+  float *t2;                // [runs][packed rows]: sums of P_2 (dout v^T)
 };
 
 // s[a][c] = <X row ty + 16 a, Y row tx + 16 c> over the d columns from X and Y on.
@@ -250,34 +250,39 @@ __global__ void __launch_bounds__(256, A == 4 && D == 128 ? 1 : 2)
 
 // ---------------------------------------------------------------- backward
 
-template <int D, int A>
+template <int D>
 constexpr int dq_smem() {  // q, dout, K, V, dz of both maps
-  return ((2 * 16 * A + 2 * kCols) * (D + 4) + 2 * 16 * A * (kCols + 4)) * (int)sizeof(float);
+  return ((2 * 64 + 2 * kCols) * (D + 4) + 2 * 64 * (kCols + 4)) * (int)sizeof(float);
 }
 
-template <int D, int A>
+// CTA: run `sp` of a batch's state tiles over a subtile of 64 packed rows.
+template <int D>
 __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant__ DiffSimt S) {
-  constexpr int M = 16 * A, LD = D + 4, LP = kCols + 4, E = D / 64;
+  constexpr int A = 4, M = 64, LD = D + 4, LP = kCols + 4, E = D / 64;
   const SimtParams &P = S.x;
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm, *Gs = Qs + M * LD, *Ks = Gs + M * LD, *Vs = Ks + kCols * LD,
         *Z1 = Vs + kCols * LD, *Z2 = Z1 + M * LP;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int parts = 64 / M, part = (int)(blockIdx.x % parts);
-  const long su = blockIdx.x / parts;
+  const int sp = (int)(blockIdx.x % P.nsplit);
+  const long su = blockIdx.x / P.nsplit;
   const int sub = (int)(su % P.nsub);
   const long bj = su / P.nsub;
   const int b = (int)(bj / P.hk), j = (int)(bj - (long)b * P.hk);
   pdl_launch_dependents();
   pdl_wait();
-  const size_t row0 = (size_t)(bj * P.nsub + sub) * 64 + part * M;
-  if (!packed_row(P, j, sub, part * M).ok) {  // nor is any later row of the tile
-    if (tid < M) S.t2[row0 + tid] = 0.f;
+  const size_t row0 = (size_t)(bj * P.nsub + sub) * 64;
+  float *sums = S.t2 + sp * S.nrows + row0;
+  const int len = batch_len(P.kv_len, b, P.Sk), tiles = (len + kCols - 1) / kCols;
+  const int u0 = (int)((long)tiles * sp / P.nsplit) * kCols;
+  const int u1 = (int)((long)tiles * (sp + 1) / P.nsplit) * kCols;
+  // no rows, or a run without states, whose dQ is not read
+  if (sub * P.tq >= P.Sq || (P.nsplit > 1 && u0 == u1)) {
+    if (tid < M) sums[tid] = 0.f;
     return;
   }
-  const int len = batch_len(P.kv_len, b, P.Sk);
-  load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, part * M);
-  load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, part * M);
+  load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, 0);
+  load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, 0);
   copy_commit();
   float n[4][A], lam[A], t2[A];
   uint64_t acc[A][E][2];
@@ -285,13 +290,13 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
   for (int a = 0; a < A; ++a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) n[i][a] = S.rows[i * S.nrows + row0 + ty + 16 * a];
-    const PackedRow r = packed_row(P, j, sub, part * M + ty + 16 * a);
+    const PackedRow r = packed_row(P, j, sub, ty + 16 * a);
     lam[a] = r.ok ? S.lam[r.head * S.lam_step] : 0.f;
     t2[a] = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[a][e][0] = acc[a][e][1] = 0ull;
   }
-  for (int k0 = 0; k0 < len; k0 += kCols) {
+  for (int k0 = u0; k0 < u1; k0 += kCols) {
     __syncthreads();
     load_states<D>(Ks, static_cast<const float *>(P.k), P.k_st, b, j, k0, len);
     load_states<D>(Vs, static_cast<const float *>(P.v), P.v_st, b, j, k0, len);
@@ -326,21 +331,23 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
     add_maps<D, A>(Z1, Z2, Ks, ty, tx, acc);
   }
   copy_wait<0>();  // q's and dout's, where there were no states
+  const float scale = P.nsplit > 1 ? 1.f : P.scale;  // parts are scaled when they are joined
+  float *out = P.out + (P.nsplit > 1 ? sp * (size_t)P.B * P.Sq * P.h * D : 0);
 #pragma unroll
   for (int a = 0; a < A; ++a) {
 #pragma unroll
     for (int o = 8; o; o >>= 1) t2[a] += __shfl_xor_sync(0xffffffffu, t2[a], o);
-    const PackedRow r = packed_row(P, j, sub, part * M + ty + 16 * a);
-    if (tx == 0) S.t2[row0 + ty + 16 * a] = r.ok ? t2[a] : 0.f;
+    const PackedRow r = packed_row(P, j, sub, ty + 16 * a);
+    if (tx == 0) sums[ty + 16 * a] = r.ok ? t2[a] : 0.f;
     if (!r.ok) continue;
-    float *o = P.out + (((size_t)b * P.Sq + r.token) * P.h + r.head) * D + 4 * tx;
+    float *o = out + (((size_t)b * P.Sq + r.token) * P.h + r.head) * D + 4 * tx;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       float4 w;
       unf2(acc[a][e][0], w.x, w.y);
       unf2(acc[a][e][1], w.z, w.w);
       *reinterpret_cast<float4 *>(o + 64 * e) =
-          make_float4(w.x * P.scale, w.y * P.scale, w.z * P.scale, w.w * P.scale);
+          make_float4(w.x * scale, w.y * scale, w.z * scale, w.w * scale);
     }
   }
 }
@@ -462,8 +469,8 @@ cudaError_t launch_fwd(const DiffSimt &p, int A, long subs, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t launch_bwd(const DiffArgs &a, DiffSimt p, float *part, int nsplit, long subs,
-                       cudaStream_t st) {
+cudaError_t launch_bwd(const DiffArgs &a, DiffSimt p, float *part, int nsplit, float *qpart,
+                       int qsplit, cudaStream_t st) {
   const int nkt = (a.x.s.Sk + kCols - 1) / kCols;
   p.x.nsplit = nsplit;
   p.x.out = nsplit > 1 ? part : static_cast<float *>(a.x.dk);
@@ -472,11 +479,11 @@ cudaError_t launch_bwd(const DiffArgs &a, DiffSimt p, float *part, int nsplit, l
                               dkv_smem<D>(), p, st);
   if (e == cudaSuccess && nsplit > 1) e = launch_cross_dkv_join(a.x, NABLA_F32, part, nsplit, st);
   if (e != cudaSuccess) return e;
-  p.x.nsplit = 1;
-  p.x.out = static_cast<float *>(a.x.dq);
-  // 16 rows a CTA where 64 would leave SMs idle
-  return subs < 152 ? launch_with(diff_dq_simt_kernel<D, 1>, subs * 4, dq_smem<D, 1>(), p, st)
-                    : launch_with(diff_dq_simt_kernel<D, 4>, subs, dq_smem<D, 4>(), p, st);
+  p.x.nsplit = qsplit;
+  p.x.out = qsplit > 1 ? qpart : static_cast<float *>(a.x.dq);
+  e = launch_with(diff_dq_simt_kernel<D>, (long)a.x.s.B * a.x.s.hk * p.x.nsub * qsplit,
+                  dq_smem<D>(), p, st);
+  return e != cudaSuccess || qsplit == 1 ? e : launch_diff_dq_sum(a, NABLA_F32, qpart, qsplit, st);
 }
 
 DiffSimt diff_simt(const DiffArgs &a) {
@@ -505,15 +512,14 @@ cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st) {
 }
 
 cudaError_t launch_diff_bwd_simt(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,
-                                 cudaStream_t st) {
+                                 float *qpart, int qsplit, cudaStream_t st) {
   DiffSimt p = diff_simt(a);
   p.rows = r.rows;
   p.nrows = r.nrows;
   p.t2 = r.t2;
   p.x.nsub = r.nsub;  // of the rows' layout; a subtile past the last token is skipped
-  const long subs = (long)a.x.s.B * a.x.s.hk * p.x.nsub;
-  return a.x.s.D == 64 ? launch_bwd<64>(a, p, part, nsplit, subs, st)
-                       : launch_bwd<128>(a, p, part, nsplit, subs, st);
+  return a.x.s.D == 64 ? launch_bwd<64>(a, p, part, nsplit, qpart, qsplit, st)
+                       : launch_bwd<128>(a, p, part, nsplit, qpart, qsplit, st);
 }
 
 }  // namespace nabla

@@ -175,7 +175,7 @@ struct DiffPlan {
   int runs;
   bool cut;
 };
-DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt);
+DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt, bool ragged);  // ragged: kv_len given
 size_t diff_fwd_workspace(const CrossShape &s, nabla_dtype dt);
 struct DiffRuns {  // partial results: [runs, 2, B, h, Sq, D] and [runs, 2, B, h, Sq], or of pieces
   int runs;
@@ -204,7 +204,9 @@ cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st);
 cudaError_t launch_diff_bwd_tc(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,
                                float *qpart, int qsplit, cudaStream_t st);
 cudaError_t launch_diff_bwd_simt(const DiffArgs &a, const DiffRows &r, float *part, int nsplit,
-                                 cudaStream_t st);
+                                 float *qpart, int qsplit, cudaStream_t st);
+cudaError_t launch_diff_dq_sum(const DiffArgs &a, nabla_dtype dt, const float *part, int nsplit,
+                               cudaStream_t st);
 
 size_t qk_norm_bwd_workspace(int D);
 cudaError_t launch_qk_norm(const QkNormArgs &a, cudaStream_t st);
