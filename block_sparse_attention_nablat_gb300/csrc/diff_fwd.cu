@@ -20,19 +20,21 @@ struct JoinParams {
   int Sq, h, nsplit, lam_step;
 };
 
-// o_m = sum_i 2^(lse_mi - lse_m) o_mi, o = o_1 - lam o_2.  A warp per row, 16 bytes a lane
-// (at D 64 half of them have none); four runs are read at a time.
-template <typename T, int D>
+// o_m = sum_i 2^(lse_mi - lse_m) o_mi, o = o_1 - lam o_2.  kG warps per row, 16 bytes a lane
+// (at D 64 half of them have none), each of them every kG-th run, four at a time.
+template <typename T, int D, int kG>
 __global__ void __launch_bounds__(256)
     diff_join_kernel(const __grid_constant__ JoinParams<T> P) {
-  const int lane = threadIdx.x & 31, col = lane * 4;
+  __shared__ float4 part[kG > 1 ? kG : 1][2][32];
+  __shared__ float part_l[kG > 1 ? kG : 1][2];
+  const int lane = threadIdx.x & 31, col = lane * 4, g = (threadIdx.x >> 5) % kG;
   pdl_launch_dependents();
   pdl_wait();
-  const long row = (long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long row = (long)blockIdx.x * (8 / kG) + (threadIdx.x >> 5) / kG;
   if (row >= P.rows) return;
   const long bh = row / P.Sq, token = row - bh * P.Sq, b = bh / P.h, hh = bh - b * P.h;
   float4 o[2];
-  float lse[2];
+  float lse[2], top[2], sum[2];
 #pragma unroll
   for (int map = 0; map < 2; ++map) {
     float m = -INFINITY;
@@ -42,19 +44,20 @@ __global__ void __launch_bounds__(256)
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int i0 = 0; i0 < P.nsplit; i0 += 4) {
+    for (int i0 = g; i0 < P.nsplit; i0 += 4 * kG) {
       float li[4];
       float4 src[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        li[x] = i0 + x < P.nsplit ? P.plse[((size_t)(i0 + x) * 2 + map) * P.rows + row]
-                                  : -INFINITY;
+      for (int x = 0; x < 4; ++x) {
+        const int i = i0 + x * kG;
+        li[x] = i < P.nsplit ? P.plse[((size_t)i * 2 + map) * P.rows + row] : -INFINITY;
+      }
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         src[x] = li[x] == -INFINITY || col >= D  // no states in this run: nothing was written
                      ? make_float4(0.f, 0.f, 0.f, 0.f)
                      : *reinterpret_cast<const float4 *>(
-                           P.po + (((size_t)(i0 + x) * 2 + map) * P.rows + row) * D + col);
+                           P.po + (((size_t)(i0 + x * kG) * 2 + map) * P.rows + row) * D + col);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const float w = li[x] == -INFINITY ? 0.f : exp2f(li[x] - m);
@@ -65,9 +68,29 @@ __global__ void __launch_bounds__(256)
         acc.w = fmaf(w, src[x].w, acc.w);
       }
     }
-    const float inv = l > 0.f ? 1.0f / l : l;  // 0 for no states; NaN stays
-    o[map] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    lse[map] = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+    o[map] = acc, sum[map] = l, top[map] = m;
+    if constexpr (kG > 1) {
+      part[g][map][lane] = acc;
+      if (lane == 0) part_l[g][map] = l;
+    }
+  }
+  if constexpr (kG > 1) {
+    __syncthreads();
+    if (g > 0) return;
+#pragma unroll
+    for (int map = 0; map < 2; ++map)
+#pragma unroll
+      for (int i = 1; i < kG; ++i) {
+        const float4 x = part[i][map][lane];
+        o[map].x += x.x, o[map].y += x.y, o[map].z += x.z, o[map].w += x.w;
+        sum[map] += part_l[i][map];
+      }
+  }
+#pragma unroll
+  for (int map = 0; map < 2; ++map) {
+    const float l = sum[map], inv = l > 0.f ? 1.0f / l : l;  // 0 for no states; NaN stays
+    o[map] = make_float4(o[map].x * inv, o[map].y * inv, o[map].z * inv, o[map].w * inv);
+    lse[map] = l > 0.f ? top[map] + log2f(l) : l == 0.f ? -INFINITY : l;
   }
   if (P.lse && lane < 2) P.lse[((b * P.h + hh) * 2 + lane) * P.Sq + token] = lane ? lse[1] : lse[0];
   if (col >= D) return;
@@ -92,7 +115,12 @@ cudaError_t launch_join(const DiffArgs &a, const DiffRuns &r, cudaStream_t st) {
   const long rows = (long)s.B * s.h * s.Sq;
   const JoinParams<T> p{r.po, r.plse, a.lam, static_cast<T *>(a.x.o), static_cast<T *>(a.o2),
                         a.x.lse, rows, s.Sq, s.h, r.runs, a.lam_n > 1 ? 1 : 0};
-  return launch_pdl(diff_join_kernel<T, D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st, p);
+  // A block a row where the SMs hold them all at once (one token of 24 heads on 8, 8192
+  // states: 11.2 us, a warp a row 20.6; but 64 x 32 rows 41 against 35).
+  if (rows <= 152 * 8)
+    return launch_pdl(diff_join_kernel<T, D, 8>, dim3((unsigned)rows), dim3(256), 0, st, p);
+  return launch_pdl(diff_join_kernel<T, D, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st,
+                    p);
 }
 
 // The parts of the tcgen05 kernel's units: blockIdx.y = c - 1 joins the unit that the pieces
@@ -231,16 +259,20 @@ __global__ void __launch_bounds__(256, 2)
 // token of 24 heads on 8, 16 ragged batches: 2048 states 25.0, 26.3, 4096 states 45.6, 42.0,
 // 8192 states 85, 66.)
 //
-// Few rows: runs of 512 states, longer ones where those would be more than eight to an SM (16
-// ragged batches of up to 4096 states, 24 heads: 74.5 us, with 16 an SM 85, with 4 80), and
-// twice as long where the heads alone fill the SMs (16 x 1024 states, 16 heads, one run: 24.9
-// us, two: 29.9; but 1 x 1024, one: 13.1, two: 11.7).  fp32: runs as in the cross attention,
-// whose tiles' costs have the same proportions.
+// Few rows: runs of 256 states above 512 (one batch, 16 heads, us: 512 states whole 6.9, in two
+// 8.7; 1024 in four 8.4, in two 10.3), longer ones where two CTAs an SM are all there is room
+// for (16 batches, 16 heads, 1024 states: whole 23.1, in two 29.3; 4 batches, 8 heads, 4096
+// states: in 9 12.6, in 16 15.9).  Where lengths differ, runs of 2048 or eight CTAs an SM at
+// least, so that the longest batch holds up no one (8 batches of up to 32768, 12 heads: in 12
+// 133 us, in 3 153; 64 of up to 2048, 4 heads: whole 28.9, in two 35).  fp32 of more rows: runs
+// as in the cross attention, whose tiles' costs have the same proportions.
 DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt, bool ragged) {
   if (diff_few_rows(s, dt)) {
-    const long heads = (long)s.B * s.hk, room = 152L * 8 / heads;
-    const long runs = heads < 152 ? (s.Sk + 511) / 512 : (s.Sk + 1023) / 1024;
-    return {0, runs <= 1 || room <= 1 ? 1 : (int)(runs < room ? runs : room), false};
+    const long heads = (long)s.B * s.hk, least = (s.Sk + 255) / 256;
+    long runs = s.Sk <= 512 ? 1 : least < 304 / heads ? least : 304 / heads;
+    const long more = s.Sk / 2048 < 1216 / heads ? s.Sk / 2048 : 1216 / heads;
+    if (ragged && runs < more) runs = more;
+    return {0, runs < 1 ? 1 : (int)runs, false};
   }
   if (dt == NABLA_F32) return {0, cross_simt_plan(s).nsplit, false};
   const long units = (long)s.B * s.hk * ((cross::packing(s).nsub + 1) / 2);

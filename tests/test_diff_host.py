@@ -79,8 +79,8 @@ def test_workspaces(lib):
                 (0, 1, 1, 1, 3, 2, 64)):
         assert f(*bad) == b(*bad) == 0
     assert f(1, 2, 32768, 512, 12, 12, 128) == 0         # many rows: no runs
-    n = f(1, 1, 1, 8192, 2, 2, 128)                      # few: runs of 512 states
-    assert n == 16 * 2 * 2 * 129 * 4
+    n = f(1, 1, 1, 8192, 2, 2, 128)                      # few: runs of 256 states
+    assert n == 32 * 2 * 2 * 129 * 4
     for dt in (0, 1):
         assert b(dt, 2, 100, 300, 6, 2, 128) >= 5 * 2 * 2 * 6 * 64 * 4
         assert bwd(lib, dt=dt, ws_bytes=b(dt, 2, 8, 10, 4, 2, 64) - 1) == INVALID

@@ -19,7 +19,7 @@ CASES = [
     (2, 64, 3584, 1, 1, 64, [0, 0]),
     (4, 200, 5000, 3, 3, 128, [5000, 4999, 4993, 1]),
     (1, 3600, 2100, 11, 11, 64, None),                  # 319 units: one round of whole ones
-    (160, 3, 3584, 2, 2, 128, [3584 if i % 40 == 7 else i % 5 for i in range(160)]),
+    (160, 9, 3584, 2, 2, 128, [3584 if i % 40 == 7 else i % 5 for i in range(160)]),
 ]
 
 
