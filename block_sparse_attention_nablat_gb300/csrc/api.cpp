@@ -658,6 +658,7 @@ struct NormCheck {
     if (!p) return true;
     if (a.rows == 1) st = a.shape.C;
     if (st < a.shape.C || st > (int64_t)1 << 38 || st * msz % 16 != 0) return false;
+    if ((double)(a.rows - 1) * (double)st > 4.0e12) return false;  // nor do its bytes wrap
     return array(p, (uintptr_t)((a.rows - 1) * st + a.shape.C) * msz);
   }
   bool common() {

@@ -92,6 +92,17 @@ def test_more_that_is_refused(lib):
                dw=None, dsum=None) == INVALID                                # nothing upstream
 
 
+def test_modulations_whose_extent_wraps_are_refused(lib):
+    """2^30 rows 2^34 elements apart: 2^64 elements, 0 if their number is taken modulo that."""
+    far = dict(B=1, S=1 << 30, C=8, rows=1 << 30, mdt=1, u=None, post=0, w=None, pw=None,
+               gate=None, scale=None)
+    assert fwd(lib, xo=None, x=1 << 50, y=2 << 50, shift=3 << 50, shift_st=1 << 34,
+               **far) == INVALID
+    far.update(scale=3 << 50, scale_st=1 << 34)
+    assert bwd(lib, s=1 << 50, dy=2 << 50, dsum=None, dx=4 << 50, du=None, dgate=None, dscale=None,
+               dshift=None, dw=None, dpw=None, **far) == INVALID
+
+
 def test_workspace(lib):
     size = lib.nabla_block_norm_bwd_workspace_bytes
     assert size(1, 1000, 60) == size(0, 8, 64) == size(1, 1, 8200) == 0
