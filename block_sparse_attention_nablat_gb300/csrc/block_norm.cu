@@ -29,8 +29,8 @@
 // their sums once a norm.  Sums over tokens: every team adds up its run's, a modulation row
 // at a time.  A row whose tokens all lie in the run is finished there, the others' parts (of
 // the run's first and last row of modulations) go to the workspace and are added up in
-// order by a second kernel, as are the teams' sums for the weights.  65536 x 2048: 293 us,
-// 5.5 TB/s (81%); instructions are issued in 54% of the cycles, which it shares the bound with.
+// order by a second kernel, as are the teams' sums for the weights.  65536 x 2048: 284 us,
+// 5.7 TB/s (84%); instructions are issued in 54% of the cycles, which it shares the bound with.
 #include <cuda_bf16.h>
 
 #include "attn_common.cuh"
@@ -57,6 +57,10 @@ constexpr int kFwdBlock = N == 8 && kU ? 192 : 256;
 // against 25.3).
 template <int N>
 constexpr int kFwdPerSm = N == 1 ? 4 : N == 2 ? 3 : 2;
+// Blocks of a row each on an SM, with up to 256 threads or up to 512: registers that let one
+// more of them in (304 rows of 4096, bf16: 4.2 us against 6.5).
+template <int N, int kSpread>
+constexpr int kSpreadPerSm = N == 2 ? 1 : kSpread == 256 ? 3 : 2;
 constexpr int kMaxStages = 4;    // rows of the backward's ring
 
 struct Mod {  // a modulation: `rows` rows, `st` elements apart
@@ -187,24 +191,21 @@ struct Team {
     Sums *b = box->of[turn][which];
     if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
     __syncthreads();
-    // a lane per warp, in both halves of the warp
+    // A lane per warp, in both halves of the warp.  First about warp 0's mean, from which the
+    // others' differ little: four sums at once, two in each half, whose eighths share them out.
     const int l = threadIdx.x & 15;
-    const bool hi = threadIdx.x & 16;
+    const bool hi = threadIdx.x & 16, odd = threadIdx.x & 8;
     const Sums a = l < warps ? b[l] : Sums{0.f, 0.f, 0.f, 0.f};
-    const float n = l < warps ? box->cols[l] : 0.f;
-    Sums r{sum16(a.mean * n) * inv, 0.f, 0.f, 0.f};
-    const float off = a.mean - r.mean;
-    r.sq = sum16(fmaf(n * off, off, a.sq));
-    const float dd = sum16(hi ? fmaf(off, a.d, a.dt) : a.d);
-    r.d = __shfl_sync(0xffffffffu, dd, 0);
-    r.dt = __shfl_sync(0xffffffffu, dd, 16);
-    return r;
-  }
-  // The sum of 16 lanes' values, in all of them.
-  static __device__ __forceinline__ float sum16(float v) {
+    const float n = l < warps ? box->cols[l] : 0.f, mean0 = b[0].mean, off = a.mean - mean0;
+    const float x = hi ? a.d : n * off;
+    const float y = fmaf(off, x, hi ? a.dt : a.sq);
+    float z = (odd ? y : x) + __shfl_xor_sync(0xffffffffu, odd ? x : y, 8);
 #pragma unroll
-    for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = 4; o; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    const float first = __shfl_sync(0xffffffffu, z, 0), sq = __shfl_sync(0xffffffffu, z, 8);
+    const float d = __shfl_sync(0xffffffffu, z, 16), dt = __shfl_sync(0xffffffffu, z, 24);
+    const float by = first * inv;  // then about the row's
+    return Sums{mean0 + by, fmaf(-by, first, sq), d, fmaf(-by, d, dt)};
   }
 
   // Takes this warp's mean (layer; else 0) off v, whose columns that do not exist stay 0,
@@ -320,10 +321,11 @@ __device__ __forceinline__ void load_mods(const NormParams &P, const Tm &tm, lon
 
 // kShared: the modulations of a block's rows in shared memory, [up, by, add][C], halves of
 // every eight columns apart.
-// kSpread: few rows; a block a row, with as many threads as that takes.
+// kSpread: few rows; a block a row, with as many threads as that takes, up to kSpread.
 // kU: there is a branch's output.
-template <typename T, int kTeam, int N, bool kShared, bool kSpread, bool kU>
-__global__ void __launch_bounds__(kSpread ? 512 : kFwdBlock<N, kU>, kSpread ? 1 : kFwdPerSm<N>)
+template <typename T, int kTeam, int N, bool kShared, int kSpread, bool kU>
+__global__ void __launch_bounds__(kSpread ? kSpread : kFwdBlock<N, kU>,
+                                  kSpread ? kSpreadPerSm<N, kSpread> : kFwdPerSm<N>)
     block_norm_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   extern __shared__ __align__(16) float mods[];
@@ -833,7 +835,7 @@ NormLayout norm_layout(const NormShape &s) {
 // 20.4 against 17.4; 8 tokens, C 512: 14.1 against 17.4; 2, C 1536: 67 against 58).
 constexpr int shared_from(int C) { return C > 512 ? 4 : 8; }
 
-template <typename T, int kTeam, int N, bool kSpread, bool kU>
+template <typename T, int kTeam, int N, int kSpread, bool kU>
 cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
   const bool shared = !kSpread && p.n >= shared_from(p.C);
   const size_t smem = shared ? (size_t)3 * p.C * sizeof(float) : 0;
@@ -853,7 +855,7 @@ cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
   return launch_pdl(kern, grid, block, smem, st, p);
 }
 
-template <typename T, int kTeam, int N, bool kSpread = false>
+template <typename T, int kTeam, int N, int kSpread = 0>
 cudaError_t launch_fwd(const NormParams &p, const Form &f, cudaStream_t st) {
   return p.u ? launch_fwd_u<T, kTeam, N, kSpread, true>(p, f, st)
              : launch_fwd_u<T, kTeam, N, kSpread, false>(p, f, st);
@@ -886,13 +888,14 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
 template <typename T>
 cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st) {
   // Few rows: what counts is how long one takes (C 1536: 16 rows 3.0 us against 3.7, 608 3.6
-  // against 4.6, 1216 6.8 against 4.8; C 4096: 152 3.6 against 10.7, 608 11.7 against 12.2,
-  // 1216 20 against 16; C 5120, two vectors a thread: 304 8.6 against 10.8, 456 11.5 against
+  // against 4.6, 1216 6.8 against 4.8; C 4096: 152 3.5 against 10.7, 608 7.8 against 12.2,
+  // 1216 20 against 15; C 5120, two vectors a thread: 304 8.6 against 10.8, 456 11.5 against
   // 10.9).
   if (p.C > 256 && p.T <= (p.C <= 4096 ? 608 : 304)) {
     const int vecs = p.C <= 4096 ? 1 : 2;
     const Form g{0, vecs, (p.C + vecs * 256 - 1) / (vecs * 256) * 32};
-    return vecs == 1 ? launch_fwd<T, 0, 1, true>(p, g, st) : launch_fwd<T, 0, 2, true>(p, g, st);
+    if (vecs == 2) return launch_fwd<T, 0, 2, 512>(p, g, st);
+    return g.threads <= 256 ? launch_fwd<T, 0, 1, 256>(p, g, st) : launch_fwd<T, 0, 1, 512>(p, g, st);
   }
   if (f.team == 8) return launch_fwd<T, 8, 1>(p, f, st);
   if (f.team == 16) return launch_fwd<T, 16, 1>(p, f, st);
