@@ -456,10 +456,11 @@ struct Ring {
 
 // The gradient.  Dynamic shared memory: where a weight's is wanted the teams' dw and dpw,
 // [teams of the block][2][C], every column of them one thread's own; then (a team that is a
-// block) the ring, [stages][s, dy, dsum, u: those there are][columns of the team].  kMost: threads at most; kU: there is a
-// branch's output; kPost: it is normed.
-template <typename T, int kTeam, int N, int kMost, bool kU, bool kPost>
-__global__ void __launch_bounds__(kMost)
+// block) the ring, [stages][s, dy, dsum, u: those there are][columns of the team].  kMost,
+// kPerSm: threads at most, blocks an SM at least; kU: there is a branch's output; kPost: it is
+// normed.
+template <typename T, int kTeam, int N, int kMost, int kPerSm, bool kU, bool kPost>
+__global__ void __launch_bounds__(kMost, kPerSm)
     block_norm_bwd_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
   __shared__ Ring ring;
@@ -796,17 +797,25 @@ Form fwd_form(int C, nabla_dtype dt, bool u) {
   return {warps == 1 ? 32 : 0, vecs, warps == 1 ? threads : warps * 32};
 }
 
+// bf16 rows of up to 2560 columns: two blocks of up to 320 threads on an SM, at 96 registers,
+// with some of them spilled (16384 rows, norms before and after: 2152 columns 157 us against 183,
+// 2560 154 against 182).  In fp32 or with 384 threads more spill (fp32, 2560 242 against 209).
+bool bwd_pair(const Form &f, nabla_dtype dt) {
+  return dt == NABLA_BF16 && f.vecs == 1 && f.threads > 256 && f.threads <= 320;
+}
+int bwd_per_sm(const Form &f, nabla_dtype dt) { return bwd_pair(f, dt) ? 2 : 512 / f.threads; }
+
 // Teams and rows of a run of the backward.  Sized for GB300's 152 SMs, so that the workspace
-// depends on the shape alone: 512 threads an SM.  n: tokens of a row of the modulations.
+// depends on the shape alone: 512 threads an SM or two blocks.  n: tokens of a row of the modulations.
 struct Runs {
   long teams;
   int L;
 };
-Runs bwd_runs(const NormShape &s, long n) {
+Runs bwd_runs(const NormShape &s, long n, nabla_dtype dt) {
   const Form f = bwd_form(s.C);
   const long T = (long)s.B * s.S;
   const int per = f.team ? f.threads / f.team : 1;  // teams of a block
-  const long most = 152L * (512 / f.threads) * per;
+  const long most = 152L * bwd_per_sm(f, dt) * per;
   long L = (T + most - 1) / most;
   // Whole rows of the modulations where that changes little: nothing to join then.  Teams of
   // a warp or less: up to a run's length (65536 x 256, fp32 modulations, 16 tokens a row: 94 us
@@ -822,7 +831,7 @@ struct NormLayout {
   size_t part, wpart, total;
 };
 NormLayout norm_layout(const NormShape &s) {
-  const Runs r = bwd_runs(s, s.B * (long)s.S);  // the most runs
+  const Runs r = bwd_runs(s, s.B * (long)s.S, NABLA_BF16);  // the most runs
   NormLayout w;
   w.part = 0;
   w.wpart = round_up((size_t)r.teams * 6 * s.C * sizeof(float));
@@ -861,7 +870,7 @@ cudaError_t launch_fwd(const NormParams &p, const Form &f, cudaStream_t st) {
              : launch_fwd_u<T, kTeam, N, kSpread, false>(p, f, st);
 }
 
-template <typename T, int kTeam, int N, int kMost>
+template <typename T, int kTeam, int N, int kMost, int kPerSm = 1>
 cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st) {
   const int per = kTeam ? f.threads / (kTeam ? kTeam : 1) : 1;
   const dim3 grid((unsigned)((teams + per - 1) / per)), block(f.threads);
@@ -869,14 +878,15 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
   if (!kTeam) {  // as many rows as fit the SM's share of shared memory
     const size_t row =
         ((p.norm ? 2 : 0) + (p.dsum ? 1 : 0) + (p.u ? 1 : 0)) * f.threads * 8 * N * sizeof(T);
-    const size_t room = (size_t)220 * 1024 / (512 / f.threads) - 2048;
+    const int per_sm = bwd_per_sm(f, sizeof(T) == 2 ? NABLA_BF16 : NABLA_F32);
+    const size_t room = (size_t)220 * 1024 / per_sm - 2048;
     p.stages = smem + row < room ? (int)((room - smem) / row) : 1;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     smem += p.stages * row;
   }
-  auto kern = p.post ? block_norm_bwd_kernel<T, kTeam, N, kMost, true, true>
-              : p.u  ? block_norm_bwd_kernel<T, kTeam, N, kMost, true, false>
-                     : block_norm_bwd_kernel<T, kTeam, N, kMost, false, false>;
+  auto kern = p.post ? block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, true, true>
+              : p.u  ? block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, true, false>
+                     : block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, false, false>;
   if (smem > 40000) {
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -895,7 +905,8 @@ cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st)
     const int vecs = p.C <= 4096 ? 1 : 2;
     const Form g{0, vecs, (p.C + vecs * 256 - 1) / (vecs * 256) * 32};
     if (vecs == 2) return launch_fwd<T, 0, 2, 512>(p, g, st);
-    return g.threads <= 256 ? launch_fwd<T, 0, 1, 256>(p, g, st) : launch_fwd<T, 0, 1, 512>(p, g, st);
+    return g.threads <= 256 ? launch_fwd<T, 0, 1, 256>(p, g, st)
+                            : launch_fwd<T, 0, 1, 512>(p, g, st);
   }
   if (f.team == 8) return launch_fwd<T, 8, 1>(p, f, st);
   if (f.team == 16) return launch_fwd<T, 16, 1>(p, f, st);
@@ -919,6 +930,8 @@ cudaError_t launch_bwd_form(const NormParams &p, const Form &f, long teams, cuda
     case 16: return launch_bwd<T, 16, 1, kTeamBlock>(p, f, teams, st);
     case 32: return launch_bwd<T, 32, 1, kTeamBlock>(p, f, teams, st);
   }
+  if constexpr (sizeof(T) == 2)
+    if (bwd_pair(f, NABLA_BF16)) return launch_bwd<T, 0, 1, 320, 2>(p, f, teams, st);
   if (f.vecs == 1) return launch_bwd<T, 0, 1, 512>(p, f, teams, st);
   // two vectors a thread want more than the 128 registers that 512 threads have (16384 x 5120:
   // 341 us against 510)
@@ -954,7 +967,7 @@ cudaError_t launch_block_norm(const NormArgs &a, cudaStream_t st) {
     return a.dt == NABLA_BF16 ? launch_fwd_form<__nv_bfloat16>(p, fwd_form(p.C, a.dt, p.u), st)
                               : launch_fwd_form<float>(p, fwd_form(p.C, a.dt, p.u), st);
   const Form f = bwd_form(p.C);
-  const Runs r = bwd_runs(a.shape, p.n);
+  const Runs r = bwd_runs(a.shape, p.n, a.dt);
   p.L = r.L;
   const NormLayout w = norm_layout(a.shape);
   char *ws = static_cast<char *>(a.workspace);

@@ -177,6 +177,11 @@ CASES = [  # B, S, C, dtype, norm, post, modulations, their type, weights, branc
     (1, 700, 1536, "bf16", "layer", None, "batch", "bf16", False, False),  # the norm alone
     (2, 310, 2048, "bf16", "layer", None, "batch", "bf16", False, True),
     (1, 64, 2056, "bf16", "rms", "layer", "one", "f32", True, True),   # the last warp nearly empty
+    (2, 350, 2152, "bf16", "layer", "rms", 5, "bf16", True, True),     # several rows a block
+    (1, 640, 2560, "bf16", "rms", "layer", "batch", "f32", True, True),
+    (1, 640, 2560, "f32", "layer", "layer", "batch", "bf16", True, True),
+    (2, 200, 512, "bf16", "layer", None, 25, "f32", True, True),       # 4 to 16 tokens a row
+    (2, 640, 1024, "bf16", "rms", "rms", 160, "f32", True, True),
     (1, 19, 4096, "f32", "rms", "rms", None, "f32", True, True),
     (2, 9, 4104, "bf16", "layer", "rms", 3, "f32", True, True),        # two vectors a thread
     (1, 11, 8192, "f32", "layer", "layer", "batch", "f32", True, True),
