@@ -844,6 +844,23 @@ NormLayout norm_layout(const NormShape &s) {
 // 20.4 against 17.4; 8 tokens, C 512: 14.1 against 17.4; 2, C 1536: 67 against 58).
 constexpr int shared_from(int C) { return C > 512 ? 4 : 8; }
 
+constexpr int kMostColumns = 8192;
+// Dynamic shared memory of the backward's blocks on an SM.
+constexpr int kBwdRoom = 220 * 1024;
+
+// A kernel's limit of dynamic shared memory is one for all host threads, and calls of several
+// widths share a kernel: `limit` is what the kernel may need at any of them, so that no thread's
+// call takes from another's, about to be launched.
+cudaError_t launch_with_room(void (*kern)(NormParams), int limit, dim3 grid, dim3 block,
+                             size_t smem, cudaStream_t st, const NormParams &p) {
+  if (smem > 40000) {  // with less (and 48 KB in all) a kernel needs no limit of its own
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, limit);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, grid, block, smem, st, p);
+}
+
 template <typename T, int kTeam, int N, int kSpread, bool kU>
 cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
   const bool shared = !kSpread && p.n >= shared_from(p.C);
@@ -856,12 +873,8 @@ cudaError_t launch_fwd_u(NormParams p, const Form &f, cudaStream_t st) {
   const dim3 grid((unsigned)((p.T + p.L - 1) / p.L)), block(f.threads);
   auto kern = shared ? block_norm_kernel<T, kTeam, N, !kSpread, kSpread, kU>
                      : block_norm_kernel<T, kTeam, N, false, kSpread, kU>;
-  if (smem > 40000) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kern, grid, block, smem, st, p);
+  constexpr int limit = 3 * (kTeam ? kTeam * 8 * N : kMostColumns) * (int)sizeof(float);
+  return launch_with_room(kern, limit, grid, block, smem, st, p);
 }
 
 template <typename T, int kTeam, int N, int kSpread = 0>
@@ -879,7 +892,7 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
     const size_t row =
         ((p.norm ? 2 : 0) + (p.dsum ? 1 : 0) + (p.u ? 1 : 0)) * f.threads * 8 * N * sizeof(T);
     const int per_sm = bwd_per_sm(f, sizeof(T) == 2 ? NABLA_BF16 : NABLA_F32);
-    const size_t room = (size_t)220 * 1024 / per_sm - 2048;
+    const size_t room = (size_t)kBwdRoom / per_sm - 2048;
     p.stages = smem + row < room ? (int)((room - smem) / row) : 1;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     smem += p.stages * row;
@@ -887,12 +900,7 @@ cudaError_t launch_bwd(NormParams p, const Form &f, long teams, cudaStream_t st)
   auto kern = p.post ? block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, true, true>
               : p.u  ? block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, true, false>
                      : block_norm_bwd_kernel<T, kTeam, N, kMost, kPerSm, false, false>;
-  if (smem > 40000) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_pdl(kern, grid, block, smem, st, p);
+  return launch_with_room(kern, kBwdRoom, grid, block, smem, st, p);
 }
 
 template <typename T>
