@@ -36,6 +36,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <cfloat>
+
 #include "attn_common.cuh"
 #include "diff_common.cuh"
 #include "internal.h"
@@ -413,7 +415,8 @@ __device__ void f_softmax(const FParams &P, uint8_t *smem, FSync *sy, uint32_t t
           cross::x_mask(mine - 32, r1);
         }
         if (s == 0) {
-          m_run = f_max(r0, r1) * sl2;
+          // (finite even if no score is: a later step's can still raise it)
+          m_run = fmaxf(f_max(r0, r1) * sl2, -FLT_MAX);
         } else if (again) {
           const float mh = f_max(r0, r1) * sl2;
           const float m_new = sum > kFMost ? fmaxf(m_run, mh) : m_run, alpha = ex2(m_run - m_new);

@@ -492,7 +492,9 @@ nabla_status nabla_cross_attn_bwd(const void *q, const nabla_strides *q_st, cons
  *   o = o_1 - lam[i] o_2,   o2 = o_2,   u = 0 .. kv_len[b] - 1;
  *   lse[((b*h + i)*2 + m)*Sq + s] = log2( sum_u 2^(scale * log2(e) * <q_m, k_m,u>) ).
  * A batch with kv_len[b] = 0 gets o = o2 = 0 and lse = -INFINITY.  k and v from kv_len[b] on
- * are padding: nothing they hold (NaN, infinities) reaches o, o2 or lse.
+ * are padding: nothing they hold (NaN, infinities) reaches o, o2 or lse.  A state whose score
+ * is -INFINITY in fp32 weighs nothing, and a map all of whose scores are gives a row what a
+ * batch without states does.
  * bf16: the products run on the tcgen05 tensor cores with fp32 accumulators (P is rounded to
  * bf16 before its product with v; o_1 and o_2 are subtracted in fp32 and o rounded once);
  * f32: fp32 arithmetic on CUDA cores.  Repeated calls on the same inputs give the same bits.
