@@ -36,6 +36,7 @@
 #include "attn_common.cuh"
 #include "internal.h"
 #include "pdl.cuh"
+#include "row_ring.cuh"
 #include "tc_ptx.cuh"
 #include "vec8.cuh"
 
@@ -61,7 +62,6 @@ constexpr int kFwdPerSm = N == 1 ? 4 : N == 2 ? 3 : 2;
 // more of them in (304 rows of 4096, bf16: 4.2 us against 6.5).
 template <int N, int kSpread>
 constexpr int kSpreadPerSm = N == 2 ? 1 : kSpread == 256 ? 3 : 2;
-constexpr int kMaxStages = 4;    // rows of the backward's ring
 
 struct Mod {  // a modulation: `rows` rows, `st` elements apart
   const void *p;
@@ -448,12 +448,6 @@ __global__ void __launch_bounds__(kSpread ? kSpread : kFwdBlock<N, kU>,
   }
 }
 
-// What a block of the backward waits with: the rows that have arrived.
-struct Ring {
-  uint64_t full[kMaxStages];
-  int abort;
-};
-
 // The gradient.  Dynamic shared memory: where a weight's is wanted the teams' dw and dpw,
 // [teams of the block][2][C], every column of them one thread's own; then (a team that is a
 // block) the ring, [stages][s, dy, dsum, u: those there are][columns of the team].  kMost,
@@ -463,7 +457,7 @@ template <typename T, int kTeam, int N, int kMost, int kPerSm, bool kU, bool kPo
 __global__ void __launch_bounds__(kMost, kPerSm)
     block_norm_bwd_kernel(const __grid_constant__ NormParams P) {
   __shared__ Box box;
-  __shared__ Ring ring;
+  __shared__ RowRing ring;
   extern __shared__ __align__(16) float wsum[];
   pdl_launch_dependents();
   const Team<kTeam, N, kTeamBlock> tm(P.C, &box);
@@ -489,6 +483,7 @@ __global__ void __launch_bounds__(kMost, kPerSm)
     if (threadIdx.x == 0) {
       for (int i = 0; i < P.stages; ++i) tc::mbar_init(&ring.full[i], 1);
       ring.abort = 0;
+      ring.stages = P.stages;
       tc::fence_barrier_init();
     }
     __syncthreads();
@@ -534,7 +529,8 @@ __global__ void __launch_bounds__(kMost, kPerSm)
       ahead.next(P.S);
       return;
     }
-    tc::mbar_wait_small(&ring.full[stage], phase, &ring.abort, P.status, kDevTimeout);
+    if (!tc::mbar_try_wait(&ring.full[stage], phase))
+      wait_for_row(&ring.full[stage], phase, &ring, P.status);
     const T *from = reinterpret_cast<const T *>(rows + stage * tensors * pitch);
     auto take = [&](Raw<T> (&r)[N]) {
 #pragma unroll
