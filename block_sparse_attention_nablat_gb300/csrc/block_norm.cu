@@ -782,7 +782,8 @@ Form bwd_form(int C) {
   if (C <= 4096) return {0, 1, (C + 255) / 256 * 32};
   return {0, 2, (C + 511) / 512 * 32};
 }
-// bf16: up to 8 vectors a lane, fp32 (twice the registers): 4.
+// bf16: up to 8 vectors a lane, fp32 (twice the registers): 4.  A row of several warps has 6 or 8
+// of them, or 4.
 Form fwd_form(int C, nabla_dtype dt, bool u) {
   if (C <= 64) return {8, 1, 256};
   if (C <= 128) return {16, 1, 256};
@@ -914,17 +915,18 @@ cudaError_t launch_fwd_form(const NormParams &p, const Form &f, cudaStream_t st)
   }
   if (f.team == 8) return launch_fwd<T, 8, 1>(p, f, st);
   if (f.team == 16) return launch_fwd<T, 16, 1>(p, f, st);
-  const bool warp = f.team == 32;
-  switch (f.vecs) {
-    case 1: return launch_fwd<T, 32, 1>(p, f, st);
-    case 2: return launch_fwd<T, 32, 2>(p, f, st);
-    case 4: return warp ? launch_fwd<T, 32, 4>(p, f, st) : launch_fwd<T, 0, 4>(p, f, st);
+  constexpr bool kWide = sizeof(T) == 4;
+  if (f.team == 32) {
+    if (f.vecs == 1) return launch_fwd<T, 32, 1>(p, f, st);
+    if (f.vecs == 2) return launch_fwd<T, 32, 2>(p, f, st);
+    if (kWide || f.vecs == 4) return launch_fwd<T, 32, 4>(p, f, st);
+    if constexpr (!kWide)
+      return f.vecs == 6 ? launch_fwd<T, 32, 6>(p, f, st) : launch_fwd<T, 32, 8>(p, f, st);
   }
-  if constexpr (sizeof(T) == 2) {
-    if (f.vecs == 6) return warp ? launch_fwd<T, 32, 6>(p, f, st) : launch_fwd<T, 0, 6>(p, f, st);
-    return warp ? launch_fwd<T, 32, 8>(p, f, st) : launch_fwd<T, 0, 8>(p, f, st);
-  }
-  return cudaErrorInvalidValue;
+  if constexpr (kWide)
+    return launch_fwd<T, 0, 4>(p, f, st);
+  else
+    return f.vecs == 6 ? launch_fwd<T, 0, 6>(p, f, st) : launch_fwd<T, 0, 8>(p, f, st);
 }
 
 template <typename T>
