@@ -193,9 +193,10 @@ __global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Runs of state tiles the fp32 dQ units (64 packed rows) are split into.  Cost in steps of a
-// 64 x 64 tile, about 6 us, in which 24 MB move: as cross_dkv_splits.  (Whole backward, D 64,
-// us, in runs and whole: 512 x 2048, 2 heads 92, 281; 256 x 1024, 4 heads 55, 148; 2048 x 256,
-// 2 heads 57, 66.)
+// 64 x 64 tile, about 6 us (12 at D 128), in which 24 MB move: as cross_dkv_splits.  (Whole
+// backward, D 64, us, in runs and whole: 512 x 2048, 2 heads 92, 281; 256 x 1024, 4 heads 55,
+// 148; 2048 x 256, 2 heads 57, 66; D 128: 1024 x 1024, 4 heads 254, 349.  Furthest from the best
+// of those tried: 64 x 4096, 4 heads of 64, in 16 runs 72, in 32 65.)
 int simt_dq_splits(const CrossShape &s, int nsub) {
   const long units = (long)s.B * s.hk * nsub;
   const int tiles = (s.Sk + 63) / 64;
@@ -222,6 +223,12 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   BwdLayout w;
   w.nsub = (cross::packing(s).nsub + 1) / 2 * 2;
   w.nrows = (size_t)s.B * s.hk * w.nsub * 64;
+  // Runs of dK / dV, and of dQ in bf16, as in the cross attention's backward: its units' steps
+  // and sums are in about the same proportions.  (Whole backward, us, as chosen, then with
+  // others.  dK / dV: 32768 x 512, 12 heads of 128, 3 runs 472, 2 564, 6 483; 8192 x 8192 whole
+  // 1550, 2 1599; 65536 x 128, 1 head of 64, 64 runs 67, 32 77; 8 x 3000 x 200, 5 heads of 64,
+  // whole 110, 3 104, the furthest from the best of those tried; fp32: 2 x 500 x 77, 6 heads on 2
+  // of 128, 12 79, 8 95, 20 97.  dQ: 500 x 4000, 4 heads of 128, 8 runs 51, whole 85, 12 64.)
   w.nsplit = cross_dkv_splits(s, dt);
   w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : simt_dq_splits(s, w.nsub);
   w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : w.qsplit;

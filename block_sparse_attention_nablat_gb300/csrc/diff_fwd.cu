@@ -264,8 +264,12 @@ __global__ void __launch_bounds__(256, 2)
 // for (16 batches, 16 heads, 1024 states: whole 23.1, in two 29.3; 4 batches, 8 heads, 4096
 // states: in 9 12.6, in 16 15.9).  Where lengths differ, runs of 2048 or eight CTAs an SM at
 // least, so that the longest batch holds up no one (8 batches of up to 32768, 12 heads: in 12
-// 133 us, in 3 153; 64 of up to 2048, 4 heads: whole 28.9, in two 35).  fp32 of more rows: runs
-// as in the cross attention, whose tiles' costs have the same proportions.
+// 133 us, in 3 153; 64 of up to 2048, 4 heads: whole 28.9, in two 35).
+//
+// fp32 of more rows: rows a CTA and runs as in the cross attention.  (us, as chosen, then
+// otherwise: 1024 x 257, 2 heads of 64, in 5 runs 24, in 3 27; 4096 x 512, 4 heads of 128, whole
+// 184, in 4 199; 8192 x 128, 2 heads of 64, whole 30, in two 48.  At D 128 an SM holds one CTA of
+// 64 rows, where those costs count on two: 2 x 500 x 77, 6 heads on 2, in two 36, whole 26.)
 DiffPlan diff_fwd_plan(const CrossShape &s, nabla_dtype dt, bool ragged) {
   if (diff_few_rows(s, dt)) {
     const long heads = (long)s.B * s.hk, least = (s.Sk + 255) / 256;
