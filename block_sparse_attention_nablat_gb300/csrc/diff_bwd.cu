@@ -122,20 +122,47 @@ __global__ void __launch_bounds__(256)
         make_uint2(tc::pack_bf16x2(s.x, s.y), tc::pack_bf16x2(s.z, s.w));
 }
 
-// lam's gradient: minus the sum of the rows' numbers t2 ([runs][nrows]; 0 where a row is
+// A sum in two floats, the second holding what the additions to the first rounded off (Knuth's
+// two-sum): the rows' numbers cancel, and 64-bit additions take 2 to 6 us more here.
+struct Sum {
+  float hi, lo;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, t = s - hi;
+    lo += (hi - (s - t)) + (x - t);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum &o) {
+    lo += o.lo;
+    add(o.hi);
+  }
+  __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+  __device__ __forceinline__ void over_warp() {
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+      add(Sum{__shfl_xor_sync(0xffffffffu, hi, o), __shfl_xor_sync(0xffffffffu, lo, o)});
+  }
+};
+
+// lam's gradient: `sign` times the sum of the rows' numbers ([runs][nrows]; 0 where a row is
 // none).  Block (j, c): chunk c of key head j's subtiles, four at a time; lane r of a subtile
-// adds up the numbers of head r % G, to part [h][chunks].  The block that is done last adds
-// those up, in order, so that the sum is the same whichever it is.
+// adds up the numbers of head r % G, a warp a head's lanes, to part [h][chunks].  The block that
+// is done last adds those up, in order, so that the sum is the same whichever it is.
+//
+// bf16: minus the sums of P_2 Y from the dQ kernel, since o2 is rounded.  fp32: the rows'
+// -delta_2 = -<dout, o2>, where P_2 rebuilt from an fp32 log-sum-exp is off by 2e-7 in a whole
+// row at once (2 x 500 x 77, 6 heads on 2 of 128: the gradient off by 2.2e-7 of the rows' norm
+// against 4.6e-7; with sums in fp32 3.2e-7).
 struct LamParams {
-  const float *t2;
+  const float *rows;
   size_t nrows;
   int runs, B, h, hk, G, tq, nsub, each;
-  float *part, *dlam;
+  Sum *part;
+  float *dlam, sign;
   unsigned *counter;
 };
 
 __global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
-  __shared__ float sums[256];
+  __shared__ Sum sums[256];
   __shared__ bool last;
   const int j = blockIdx.x, chunk = blockIdx.y, chunks = gridDim.y, r = threadIdx.x & 63;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -143,7 +170,7 @@ __global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
   const long n = (long)P.B * P.nsub, e0 = n * chunk / chunks, e1 = n * (chunk + 1) / chunks;
   pdl_wait();
   const long count = (e1 - e0) * P.runs;
-  float v = 0.f;
+  Sum v{0.f, 0.f};
   for (long k0 = threadIdx.x >> 6; k0 < count; k0 += 4 * 8) {
     float x[8];  // under way together
 #pragma unroll
@@ -151,43 +178,45 @@ __global__ void __launch_bounds__(256) lam_kernel(const LamParams P) {
       const uint32_t k = (uint32_t)k0 + 4 * i, run = k % (uint32_t)P.runs;
       const uint32_t e = (uint32_t)e0 + k / (uint32_t)P.runs, b = e / (uint32_t)P.nsub;
       const size_t row = ((size_t)(b * P.hk + j) * P.nsub + e - b * P.nsub) * 64 + r;
-      x[i] = k < count ? P.t2[run * P.nrows + row] : 0.f;
+      x[i] = k < count ? P.rows[run * P.nrows + row] : 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v += x[i];
+    for (int i = 0; i < 8; ++i) v.add(x[i]);
   }
   sums[threadIdx.x] = v;
   __syncthreads();
-  if ((int)threadIdx.x < P.G) {  // head threadIdx.x of the group
-    v = 0.f;
-    for (int q = 0; q < 4; ++q)
-      for (int t = 0; t < P.tq; ++t) v += sums[q * 64 + t * P.G + threadIdx.x];
-    P.part[(size_t)(j * P.G + threadIdx.x) * chunks + chunk] = v;
-    __threadfence();
+  for (int i = warp; i < P.G; i += 8) {  // head i of the group
+    v = Sum{0.f, 0.f};
+    for (int t = lane; t < 4 * P.tq; t += 32) v.add(sums[(t & 3) * 64 + (t >> 2) * P.G + i]);
+    v.over_warp();
+    if (lane == 0) P.part[(size_t)(j * P.G + i) * chunks + chunk] = v;
   }
+  __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(P.counter, 1u) + 1u == gridDim.x * gridDim.y;
   __syncthreads();
   if (!last) return;
   __threadfence();
   // a warp for each head, the lanes along its chunks; one weight: the heads' sums in order
-  float all = 0.f;
+  Sum all{0.f, 0.f};
   for (int i = warp; i < P.h; i += 8) {
-    v = 0.f;
-    for (int c = lane; c < chunks; c += 32) v += __ldcg(P.part + (size_t)i * chunks + c);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    all += v;
-    if (P.each && lane == 0) P.dlam[i] = -v;
+    v = Sum{0.f, 0.f};
+    for (int c = lane; c < chunks; c += 32) {
+      const float2 p = __ldcg(reinterpret_cast<const float2 *>(P.part + (size_t)i * chunks + c));
+      v.add(Sum{p.x, p.y});
+    }
+    v.over_warp();
+    all.add(v);
+    if (P.each && lane == 0) P.dlam[i] = P.sign * v.value();
   }
   if (P.each) return;
   if (lane == 0) sums[warp] = all;
   __syncthreads();
   if (threadIdx.x) return;
-  v = 0.f;
+  v = Sum{0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v += sums[i];
-  P.dlam[0] = -v;
+  for (int i = 0; i < 8; ++i) v.add(sums[i]);
+  P.dlam[0] = P.sign * v.value();
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -231,7 +260,7 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   // of 128, 12 79, 8 95, 20 97.  dQ: 500 x 4000, 4 heads of 128, 8 runs 51, whole 85, 12 64.)
   w.nsplit = cross_dkv_splits(s, dt);
   w.qsplit = dt == NABLA_BF16 ? cross_dq_splits(s) : simt_dq_splits(s, w.nsub);
-  w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : w.qsplit;
+  w.truns = dt == NABLA_BF16 ? 2 * w.qsplit : 0;
   // 16 subtiles a chunk: four loads a thread and run
   const size_t chunks = ((size_t)s.B * w.nsub + 15) / 16;
   w.chunks = chunks > 64 ? 64 : (int)chunks;
@@ -244,7 +273,7 @@ BwdLayout bwd_layout(const CrossShape &s, nabla_dtype dt) {
   w.lam = w.qpart + (w.qsplit > 1 ? round_up((size_t)w.qsplit * s.B * s.Sq * s.h * s.D *
                                              sizeof(float))
                                   : 0);
-  w.counter = w.lam + round_up((size_t)s.h * w.chunks * sizeof(float));
+  w.counter = w.lam + round_up((size_t)s.h * w.chunks * sizeof(Sum));
   w.total = w.counter + 256;
   return w;
 }
@@ -302,8 +331,10 @@ cudaError_t launch_diff_bwd(const DiffArgs &a, nabla_dtype dt, cudaStream_t st) 
           : launch_diff_bwd_simt(a, r, at(w.part), w.nsplit, at(w.qpart), w.qsplit, st);
   if (e != cudaSuccess) return e;
   const cross::Packing pk = cross::packing(s);
-  const LamParams p{r.t2, w.nrows, w.truns, s.B, s.h, s.hk, pk.G, pk.tq, w.nsub,
-                    a.lam_n > 1 ? 1 : 0, at(w.lam), a.dlam, counter};
+  LamParams p{r.t2, w.nrows, w.truns, s.B, s.h, s.hk, pk.G, pk.tq, w.nsub,
+              a.lam_n > 1 ? 1 : 0, reinterpret_cast<Sum *>(ws + w.lam), a.dlam, -1.f,
+              counter};
+  if (dt == NABLA_F32) p.rows = r.rows + 3 * w.nrows, p.runs = 1, p.sign = 1.f;  // -delta_2
   return launch_pdl(lam_kernel, dim3((unsigned)s.hk, (unsigned)w.chunks), dim3(256), 0, st, p);
 }
 

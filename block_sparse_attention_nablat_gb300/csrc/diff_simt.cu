@@ -6,8 +6,7 @@
 //    tile's scores of both maps are formed, each has its running maximum and sum; P_1, then
 //    P_2 lie over K's tile for O_m += P_m V.  The two O are subtracted at the end.
 //  * dQ: dz_1 = P_1 (dout v^T - delta_1), dz_2 = -lam P_2 (dout v^T - delta_2); a thread's
-//    columns of q lie in one map's half, so one product with K serves both.  The rows' sums
-//    of P_2 (dout v^T), whose negative sum is lam's gradient, are kept beside it.
+//    columns of q lie in one map's half, so one product with K serves both.
 //  * dK, dV: the same with the axes exchanged; dV takes P_1 - lam P_2.
 // A tile's sums of the backward are added up apart and then to the total.
 //
@@ -35,7 +34,6 @@ struct DiffSimt {
   float *o2;                // forward, or null
   const float *rows;        // backward: -lse_1, -lse_2, -delta_1, -delta_2 (and -lam) of the packed rows
   size_t nrows;             // rows of each
-  float *t2;                // [runs][packed rows]: sums of P_2 (dout v^T)
 };
 
 // s[a][c] = <X row ty + 16 a, Y row tx + 16 c> over the d columns from X and Y on.
@@ -277,19 +275,15 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
   pdl_launch_dependents();
   pdl_wait();
   const size_t row0 = (size_t)(bj * P.nsub + sub) * 64;
-  float *sums = S.t2 + sp * S.nrows + row0;
   const int len = batch_len(P.kv_len, b, P.Sk), tiles = (len + kCols - 1) / kCols;
   const int u0 = (int)((long)tiles * sp / P.nsplit) * kCols;
   const int u1 = (int)((long)tiles * (sp + 1) / P.nsplit) * kCols;
   // no rows, or a run without states, whose dQ is not read
-  if (sub * P.tq >= P.Sq || (P.nsplit > 1 && u0 == u1)) {
-    if (tid < M) sums[tid] = 0.f;
-    return;
-  }
+  if (sub * P.tq >= P.Sq || (P.nsplit > 1 && u0 == u1)) return;
   load_rows<D, M>(Qs, Side{static_cast<const float *>(P.q), P.q_st}, P, b, j, sub, 0);
   load_rows<D, M>(Gs, Side{static_cast<const float *>(P.dout), P.dout_st}, P, b, j, sub, 0);
   copy_commit();
-  float n[4][A], lam[A], t2[A];
+  float n[4][A], lam[A];
   uint64_t acc[A][E][2];
 #pragma unroll
   for (int a = 0; a < A; ++a) {
@@ -297,7 +291,6 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
     for (int i = 0; i < 4; ++i) n[i][a] = S.rows[i * S.nrows + row0 + ty + 16 * a];
     const PackedRow r = packed_row(P, j, sub, ty + 16 * a);
     lam[a] = r.ok ? S.lam[r.head * S.lam_step] : 0.f;
-    t2[a] = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[a][e][0] = acc[a][e][1] = 0ull;
   }
@@ -321,17 +314,13 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
       }
     dot_half<D, A>(Qs + D / 2, Ks + D / 2, ty, tx, s);
 #pragma unroll
-    for (int a = 0; a < A; ++a) {
-      float t = 0.f;
+    for (int a = 0; a < A; ++a)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const float p =
             k0 + tx + 16 * c < len ? exp2f(fmaf(s[a][c], P.scale_log2, n[1][a])) : 0.f;
-        t = fmaf(p, dp[a][c], t);
         Z2[(ty + 16 * a) * LP + tx + 16 * c] = -lam[a] * p * (dp[a][c] + n[3][a]);
       }
-      t2[a] += t;
-    }
     __syncwarp();  // a row's dz comes from the 16 lanes that use it
     add_maps<D, A>(Z1, Z2, Ks, ty, tx, acc);
   }
@@ -340,10 +329,7 @@ __global__ void __launch_bounds__(256) diff_dq_simt_kernel(const __grid_constant
   float *out = P.out + (P.nsplit > 1 ? sp * (size_t)P.B * P.Sq * P.h * D : 0);
 #pragma unroll
   for (int a = 0; a < A; ++a) {
-#pragma unroll
-    for (int o = 8; o; o >>= 1) t2[a] += __shfl_xor_sync(0xffffffffu, t2[a], o);
     const PackedRow r = packed_row(P, j, sub, ty + 16 * a);
-    if (tx == 0) sums[ty + 16 * a] = r.ok ? t2[a] : 0.f;
     if (!r.ok) continue;
     float *o = out + (((size_t)b * P.Sq + r.token) * P.h + r.head) * D + 4 * tx;
 #pragma unroll
@@ -521,7 +507,6 @@ cudaError_t launch_diff_bwd_simt(const DiffArgs &a, const DiffRows &r, float *pa
   DiffSimt p = diff_simt(a);
   p.rows = r.rows;
   p.nrows = r.nrows;
-  p.t2 = r.t2;
   p.x.nsub = r.nsub;  // of the rows' layout; a subtile past the last token is skipped
   return a.x.s.D == 64 ? launch_bwd<64>(a, p, part, nsplit, qpart, qsplit, st)
                        : launch_bwd<128>(a, p, part, nsplit, qpart, qsplit, st);

@@ -196,7 +196,7 @@ cudaError_t launch_diff_attn_simt(const DiffArgs &a, cudaStream_t st);
 struct DiffRows {
   const float *rows;  // -lse_1, -lse_2, -delta_1, -delta_2, -lam: [5][nrows]
   size_t nrows;
-  float *t2;  // [runs][nrows]
+  float *t2;  // [runs][nrows]; bf16
   int nsub;
 };
 size_t diff_bwd_workspace(const CrossShape &s, nabla_dtype dt);

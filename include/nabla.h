@@ -530,9 +530,9 @@ nabla_status nabla_diff_attn_fwd(const void *q, const nabla_strides *q_st, const
  *   dq_m = scale sum_u dz_m k_m,u,   dk_m = scale sum_s dz_m q_m,s,
  *   dv_u = sum_s (P_1 - lam P_2) dout_s,   dlam = - sum_s,u P_2 <dout_s, v_u>,
  * the sums over s running over the tokens of all the heads that share the key head, those of
- * dlam over a head's rows, or all heads' (lam_n = 1).  A batch without states gets dq = 0;
- * states from kv_len[b] on get dk = dv = 0, whatever k and v hold there.  o and o2 must be the
- * forward's.  bf16: the products run on tcgen05 with fp32 accumulators, P and dz enter them as
+ * dlam over a head's rows, or all heads' (lam_n = 1; f32 forms the same number as the sum of
+ * -delta_2).  A batch without states gets dq = 0; states from kv_len[b] on get dk = dv = 0,
+ * whatever k and v hold there.  o and o2 must be the forward's.  bf16: the products run on tcgen05 with fp32 accumulators, P and dz enter them as
  * bf16; f32: fp32 arithmetic on CUDA cores.  No value is added up by atomics: repeated calls give
  * the same bits.  delta_1 takes the rounding of o and o2 as they are stored, the latter's times
  * lam: with |lam| well above 1 it shows in dq_1 and dk_1 (bf16: off by 2.6e-3 of their norm at
