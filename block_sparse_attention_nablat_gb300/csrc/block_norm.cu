@@ -15,7 +15,7 @@
 // written).  Variances are summed about each warp's own mean and joined exactly, so a large
 // mean cancels no digits of the squares.  The mean itself is an fp32 number: a normed value is
 // off by some 2^-24 |mean| / deviation, as it is in elementary fp32 operations (2048 columns, a
-// mean of 1000 deviations: 2.3e-5 on average and 9e-5 at most; those 2.3e-5 and 8e-5).
+// mean of 1000 deviations: 2.3e-5 on average, 9e-5 at most; there 2.3e-5 and 8e-5).
 //
 // Forward: a warp holds a row (up to 8 vectors of 8 columns a lane; few columns: 8 or 16
 // lanes, many: two to eight warps), so its norms need no barrier, and an SM's 16 warps have

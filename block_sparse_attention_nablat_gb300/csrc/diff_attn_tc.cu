@@ -11,8 +11,9 @@
 //    N = 64, depth D / 2), O_m += P_m V a TS MMA with P_m (bf16) over the scores.  The maps
 //    share K's tile (each its half of the columns) and V's.
 //  * TMEM: O_1, O_2 (D columns each, 128 apart) and two 64-column score buffers a map: all 512
-//    columns at D 128, while 64 beside each O stay unused at D 64.  The maps could only be subtracted before the product with V if their sums were known, so
-//    the forward takes two products where the definition has one.
+//    columns at D 128, while 64 beside each O stay unused at D 64.  The maps could only be
+//    subtracted before the product with V if their sums were known, so the forward takes two
+//    products where the definition has one.
 //  * Each map has four softmax warps, thread = row: a row's maximum and sum never leave its
 //    thread, and the two maps' chains (S, softmax, P V) fill each other's gaps, as do the
 //    two buffers of a chain.

@@ -31,9 +31,9 @@
 //
 // Bound by a step's chain, scores, dz, product with dz (dK / dV 2340 cycles for 128 x 64, of
 // which the tensor pipe works 1280; dQ 2100): one set of scores is in work at a time, and a
-// second one, 192 columns, would have to share those of dz.  (dK / dV hold all 512
-// columns at D 128, dQ 448.)  32768 tokens, 512 states, 12 heads, D 128: 208 us, tensor pipe active in 45% of the
-// cycles, and 177 us, 39%.  Sixteen softmax warps: dK / dV 217 us, dQ 172, and the whole
+// second one, 192 columns, would have to share those of dz.  (dK / dV hold all 512 columns at
+// D 128, dQ 448.)  32768 tokens, 512 states, 12 heads, D 128: 208 us, tensor pipe active in 45%
+// of the cycles, and 177 us, 39%.  Sixteen softmax warps: dK / dV 217 us, dQ 172, and the whole
 // backward slower (525 us against 478).
 // Every mbarrier wait is bounded (1 s), as in the forward.
 #include <cuda.h>

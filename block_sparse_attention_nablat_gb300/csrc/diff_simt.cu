@@ -11,8 +11,9 @@
 // A tile's sums of the backward are added up apart and then to the total.
 //
 // Bound by shared memory: a step of 64 x 64 takes 6.7 us in dQ and 10 in dK / dV at D 64, 12
-// and 16 at D 128, and loads what it needs before it begins.  So few rows have their states (dQ) or their rows (dK, dV) split
-// over CTAs; 16 rows a CTA in place of 64 took 4.8 us a step and four times the steps.
+// and 16 at D 128, and loads what it needs before it begins.  So few rows have their states (dQ)
+// or their rows (dK, dV) split over CTAs; 16 rows a CTA in place of 64 took 4.8 us a step and
+// four times the steps.
 // 512 x 2048, 2 heads, D 64: backward 92 us; 1024 x 1024, 4 heads: 162 us, D 128: 255 us.
 #include <cfloat>
 

@@ -178,7 +178,7 @@ def test_gradients_along_directions_against_differences(nabla, norm, branch):
             return (loss(hi) - loss(lo)) / (2 * step)
 
         near, far = difference(2.0 ** -10), difference(2.0 ** -9)
-        room = (np.abs(d) * (2.0 ** -24 * np.abs(value) + 2.0 ** plain.TOLERANCE[grad] * size)).sum()
-        room += abs(near - far)
+        room = 2.0 ** -24 * np.abs(value) + 2.0 ** plain.TOLERANCE[grad] * size
+        room = (np.abs(d) * room).sum() + abs(near - far)
         assert abs((g * d).sum() - near) <= room, grad
         assert room < abs(near) / 8, grad

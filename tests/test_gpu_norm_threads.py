@@ -68,7 +68,8 @@ class Program:
             return t[i].data_ptr() if t is not None and on else None
 
         self.call = NormCall(
-            (vp * 4)(*(t.data_ptr() for t in self.ins)), (vp * 2)(*(t.data_ptr() for t in self.outs)),
+            (vp * 4)(*(t.data_ptr() for t in self.ins)),
+            (vp * 2)(*(t.data_ptr() for t in self.outs)),
             at(w, 0), at(w, 1), at(self.small, 0, weights and grad),
             at(self.small, 1, weights and grad), self.ws.data_ptr(), self.ws.numel(),
             self.stream.cuda_stream, S, C,
