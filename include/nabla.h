@@ -534,9 +534,10 @@ nabla_status nabla_diff_attn_fwd(const void *q, const nabla_strides *q_st, const
  * -delta_2).  A batch without states gets dq = 0; states from kv_len[b] on get dk = dv = 0,
  * whatever k and v hold there.  o and o2 must be the forward's.  bf16: the products run on
  * tcgen05 with fp32 accumulators, P and dz enter them as bf16; f32: fp32 arithmetic on CUDA
- * cores.  No value is added up by atomics: repeated calls give the same bits.  delta_1 takes the rounding of o and o2 as they are stored, the latter's times
- * lam: with |lam| well above 1 it shows in dq_1 and dk_1 (bf16: off by 2.6e-3 of their norm at
- * lam = 1, 4e-3 at 4, 1.3e-2 at 16, 5.6e-2 at 64), not in the other gradients.
+ * cores.  No value is added up by atomics: repeated calls give the same bits.  delta_1 takes the
+ * rounding of o and o2 as they are stored, the latter's times lam: with |lam| well above 1 it
+ * shows in dq_1 and dk_1 (bf16: off by 2.6e-3 of their norm at lam = 1, 4e-3 at 4, 1.3e-2 at 16,
+ * 5.6e-2 at 64), not in the other gradients.
  *
  *   q, k, v, lam, kv_len, scale  as given to nabla_diff_attn_fwd.
  *   o, o2, dout [B, Sq, h, D] device, element type dt, strides o_st, o2_st and dout_st.
